@@ -1,0 +1,385 @@
+"""What the layer's training operators are measured on: cases, inputs, and their plain forms.
+
+Operators: products of rows grouped by expert (``moe_grouped_matmul``), the experts' SwiGLU
+gradient (``moe_swiglu_backward``), the router's gradient (``moe_route_backward``) and the
+norms around the layer with their gate and residual scale (``moe_block_norm``,
+``moe_block_norm_backward``). ``run`` computes a case in elementary torch operations in
+32 bits, rounded once at the end, or (``own``) through the framework's entry points.
+``exact`` computes it in 64 bits: products expert by expert, gradients by differentiating
+the forward definition.
+"""
+import torch
+
+own = False
+
+BF16, FP32 = "bf16", "fp32"
+TYPES = {BF16: torch.bfloat16, FP32: torch.float32}
+SIZE = {BF16: 2, FP32: 4}
+DEV = "cuda"
+EPS = 1e-6
+
+
+# ---- the cases -----------------------------------------------------------------------
+def listed():
+    return [
+        # one decoding step: 8 sequences, top-2 of 8, the Mixtral layer's gate projection;
+        # its weights are the work, and each expert has a row or a few
+        _matmul("matmul_nn_decode", form="nn", T=8, k=2, E=8, K=4096, N=14336, skew=0.0, gather=True),
+        # the tiny layer's gradient with respect to its rows, fp32
+        _matmul("matmul_nt_tiny_fp32", form="nt", T=256, k=2, E=8, K=128, N=64, dtype=FP32, skew=1.0, out=FP32),
+        # the mid-size layer's gate projection recomputed for the backward pass (rows of x)
+        _matmul("matmul_nn_mid", form="nn", T=4096, k=2, E=8, K=1024, N=4096, skew=1.0, gather=True),
+        # the Mixtral-size layer, skewed router: the hidden gradient dy W_down^T
+        _matmul("matmul_nt_mixtral", form="nt", T=16384, k=2, E=8, K=4096, N=14336, skew=1.0, gather=True),
+        # 64 fine-grained experts, an odd token count: the weight gradient x^T dg, fp32 sums out
+        _matmul("matmul_tn_fine", form="tn", T=8191, k=4, E=64, K=2048, N=1408, skew=0.5, gather=True, out=FP32),
+        # a short ragged step of fp32 rows and one of the mid-size layer's hidden gradients
+        _swiglu("swiglu_short_fp32", R=37, f=1408, dtype=FP32),
+        _swiglu("swiglu_mid", R=8192, f=4096),
+        # the router's gradient with both training losses: mid-size, and 64 experts with the
+        # gradients of the experts' rows added to dx
+        _route("route_mid", T=4096, d=1024, E=8, k=2, rows=False),
+        _route("route_fine", T=8191, d=2048, E=64, k=4, rows=True),
+        # before the layer, one decoding step of 8 tokens; after it and before the next
+        # block at the Mixtral width; the gradient of both at an odd token count
+        _norm("norm_decode", T=8, d=4096, y=False, u=True, gate="none", back=False),
+        _norm("norm_mixtral", T=16384, d=4096, y=True, u=True, gate="channel", back=False),
+        _norm("norm_back_fine", T=8191, d=2048, y=True, u=True, gate="token", back=True),
+    ]
+
+
+def _matmul(name, *, form, T, k, E, K, N, dtype=BF16, skew=0.0, gather=False, out=None):
+    return dict(name=name, op="matmul", form=form, T=T, k=k, E=E, K=K, N=N, dtype=dtype, skew=skew,
+                gather=gather, out=out or dtype)
+
+
+def _swiglu(name, *, R, f, dtype=BF16):
+    return dict(name=name, op="swiglu", R=R, f=f, dtype=dtype)
+
+
+def _route(name, *, T, d, E, k, rows, dtype=BF16, renormalize=True):
+    return dict(name=name, op="route", T=T, d=d, E=E, k=k, rows=rows, dtype=dtype,
+                renormalize=renormalize)
+
+
+def _norm(name, *, T, d, y, u, gate, back, dtype=BF16):
+    return dict(name=name, op="norm", T=T, d=d, y=y, u=u, gate=gate, back=back, dtype=dtype)
+
+
+def draw(rng):
+    """One more case: sizes log-uniform over the listed range, odd token counts, widths that
+    are whole 16-byte chunks, no more work than the largest listed case of its operator."""
+    def size(lo, hi, step=1):
+        v = lo * (hi / lo) ** rng.random()
+        return max(lo, min(hi, int(v / step) * step))
+
+    op = rng.choice(["matmul", "matmul", "matmul", "swiglu", "route", "norm", "norm"])
+    dtype = FP32 if rng.random() < 0.2 else BF16
+    if op == "matmul":
+        form = rng.choice(["nn", "nt", "tn"])
+        E = rng.choice([1, 4, 8, 16, 40, 64])
+        k = rng.randint(1, min(E, 4))
+        K, N = size(64, 4096, 8), size(64, 8192, 8)
+        T = size(1, 16384)
+        if dtype == FP32:
+            K, N = min(K, 1024), min(N, 2048)
+        while E * K * N > 8 * 4096 * 14336 or T * k * K * N > 32768 * 4096 * 14336 // 2:
+            N, T = max(64, N // 16 * 8), max(1, T // 2)
+        return dict(_matmul("", form=form, T=T, k=k, E=E, K=K, N=N, dtype=dtype,
+                            skew=rng.choice([0.0, 0.5, 1.0]), gather=rng.random() < 0.6,
+                            out=FP32 if dtype == FP32 or rng.random() < 0.3 else BF16))
+    if op == "swiglu":
+        f = size(64, 8192, 8)
+        return _swiglu("", R=min(size(1, 16384), 8192 * 4096 // f), f=f, dtype=dtype)
+    if op == "route":
+        E = rng.choice([2, 5, 8, 16, 33, 64])
+        d = size(64, 4096, 64)
+        T = min(size(1, 16384), 8191 * 2048 // d)
+        return _route("", T=T, d=d, E=E, k=rng.randint(1, min(E, 4)), rows=rng.random() < 0.5,
+                      dtype=dtype, renormalize=rng.random() < 0.7)
+    y = rng.random() < 0.7
+    u = True if not y else rng.random() < 0.6
+    d = size(64, 8192, 8)
+    return _norm("", T=min(size(1, 16384), 16384 * 4096 // d // 2), d=d, y=y, u=u,
+                 gate=rng.choice(["none", "channel", "token"]) if y else "none",
+                 back=rng.random() < 0.5, dtype=dtype)
+
+
+def work(case):
+    c = dict(case)
+    b = SIZE[c["dtype"]]
+    if c["op"] == "matmul":
+        R, E, K, N = c["T"] * c["k"], c["E"], c["K"], c["N"]
+        rows = c["T"] if c["gather"] else R
+        if c["form"] == "tn":
+            moved = (rows * K + R * N) * b + E * K * N * SIZE[c["out"]]
+        else:  # an expert without rows has its weights left unread
+            moved = (rows * K + min(E, R) * K * N) * b + R * N * SIZE[c["out"]]
+        return {"bytes": moved, "flops": 2.0 * R * K * N}
+    if c["op"] == "swiglu":
+        return {"bytes": c["R"] * (6 * c["f"] * b + 8), "flops": 16.0 * c["R"] * c["f"]}
+    if c["op"] == "route":
+        T, d, E, k = c["T"], c["d"], c["E"], c["k"]
+        rows = T * k * d * b if c["rows"] else 0
+        return {"bytes": 2 * T * d * b + rows + 2 * d * E * b + 8 * T * E + 16 * T * k,
+                "flops": 4.0 * T * d * E}
+    T, d = c["T"], c["d"]
+    if not c["back"]:
+        per = b + ((4 + b) if c["y"] else 0) + (b if c["u"] else 0)
+    else:  # d_out, dx; d_u and x; y and dy
+        per = 2 * b + (2 * b if c["u"] else 0) + ((4 + b) if c["y"] else 0)
+    return {"bytes": T * d * per + 12 * d, "flops": 12.0 * T * d}
+
+
+# ---- inputs --------------------------------------------------------------------------
+def prepare(case, seed):
+    c = dict(case)
+    gen = torch.Generator(device=DEV).manual_seed(int(seed))
+    dt = TYPES[c["dtype"]]
+
+    def normal(*shape, std=1.0, dtype=dt):
+        return torch.randn(*shape, generator=gen, device=DEV, dtype=dtype).mul_(std)
+
+    s = {"case": c}
+    if c["op"] == "matmul":
+        T, k, E, K, N = c["T"], c["k"], c["E"], c["K"], c["N"]
+        R = T * k
+        # a router's choices, some experts favoured (skew): the rows sorted by expert
+        bias = normal(E, std=c["skew"], dtype=torch.float32)
+        expert = torch.topk(normal(T, E, dtype=torch.float32) + bias, k).indices.reshape(-1)
+        counts = torch.bincount(expert, minlength=E)
+        s["offsets"] = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).int()
+        s["counts"] = counts.tolist()  # the host's own knowledge of the groups, for the plain forms
+        src = (torch.argsort(expert, stable=True) // k).int()
+        s["gather"] = src if c["gather"] else None
+        s["a"] = normal(T if c["gather"] else R, K)
+        if c["form"] == "tn":
+            s["b"] = normal(R, N, std=0.1)
+        else:
+            s["b"] = normal(E, *((K, N) if c["form"] == "nn" else (N, K)), std=0.02)
+    elif c["op"] == "swiglu":
+        R, f = c["R"], c["f"]
+        s["g"], s["u"], s["dh"] = normal(R, f, std=1.5), normal(R, f), normal(R, f, std=0.1)
+        s["w"] = torch.rand(R, generator=gen, device=DEV)
+    elif c["op"] == "route":
+        T, d, E, k = c["T"], c["d"], c["E"], c["k"]
+        s["x"], s["W_g"] = normal(T, d), normal(d, E, std=0.02)
+        s["b_g"] = normal(E, std=0.5, dtype=torch.float32)
+        p = torch.softmax(s["x"].double() @ s["W_g"].double() + s["b_g"].double(), 1)
+        top = torch.topk(p, k)
+        w = top.values / top.values.sum(1, keepdim=True) if c["renormalize"] else top.values
+        s["probs"], s["idx"], s["w"] = p.float(), top.indices.int(), w.float()
+        s["f"] = (torch.bincount(top.indices.reshape(-1), minlength=E).double() / T).float()
+        s["dw"] = normal(T, k, dtype=torch.float32)
+        s["rows"] = s["pos"] = None
+        if c["rows"]:
+            s["rows"] = normal(T * k, d, std=0.1)
+            order = torch.argsort(top.indices.reshape(-1), stable=True)
+            pos = torch.empty(T * k, dtype=torch.int32, device=DEV)
+            pos[order] = torch.arange(T * k, dtype=torch.int32, device=DEV)
+            s["pos"] = pos.view(T, k)
+        s["loss_grad"], s["z_loss_grad"] = 0.01 * T, 0.001 * T  # coefficients of a loss summed over tokens
+    else:
+        T, d = c["T"], c["d"]
+        s["x"] = normal(T, d)
+        s["y"] = normal(T, d, std=0.5, dtype=torch.float32) if c["y"] else None
+        s["gamma_post"] = 1 + normal(d, std=0.1, dtype=torch.float32) if c["y"] else None
+        s["gamma"] = 1 + normal(d, std=0.1, dtype=torch.float32) if c["u"] else None
+        s["gate"] = {"none": None, "channel": normal(d, std=0.5, dtype=torch.float32),
+                     "token": torch.rand(T, generator=gen, device=DEV)}[c["gate"]]
+        s["scale"] = 0.75 if c["y"] else 1.0
+        if c["back"]:  # what the forward pass left
+            s["d_out"] = normal(T, d, std=0.1)
+            s["d_u"] = normal(T, d, std=0.1) if c["u"] else None
+            s["rstd"] = _rstd(s["x"].double()).float() if c["u"] else None
+            s["rstd_post"] = _rstd(s["y"].double()).float() if c["y"] else None
+    return s
+
+
+def _rstd(v):
+    return ((v * v).mean(1) + EPS).rsqrt()
+
+
+# ---- one pass ------------------------------------------------------------------------
+def run(s):
+    c = s["case"]
+    return {"matmul": _run_matmul, "swiglu": _run_swiglu, "route": _run_route,
+            "norm": _run_norm_backward if c.get("back") else _run_norm}[c["op"]](s, c)
+
+
+def _run_matmul(s, c):
+    if own:
+        import sparse_mixture_experts_sum_amd as moe
+        return moe.moe_grouped_matmul(s["a"], s["b"], s["offsets"], form=c["form"],
+                                      gather_a=s["gather"], out_dtype=TYPES[c["out"]])
+    # every group padded to the longest one, as one batched product in fp32
+    E, longest = c["E"], max(s["counts"])
+    first = s["offsets"][:-1].long()
+    length = s["offsets"][1:].long() - first
+    at = torch.arange(longest, device=DEV)
+    real = at[None, :] < length[:, None]                                      # [E, longest]
+    row = torch.where(real, first[:, None] + at[None, :], torch.zeros_like(first)[:, None])
+    a_row = row if s["gather"] is None else s["gather"].long()[row]
+    a = s["a"].float()[a_row] * real[:, :, None]
+    if c["form"] == "tn":
+        b = s["b"].float()[row] * real[:, :, None]
+        return torch.bmm(a.transpose(1, 2), b).to(TYPES[c["out"]])
+    b = s["b"].float()
+    o = torch.bmm(a, b if c["form"] == "nn" else b.transpose(1, 2))
+    r = torch.arange(c["T"] * c["k"], device=DEV)
+    e = torch.searchsorted(s["offsets"][1:].long(), r, right=True)
+    return o[e, r - first[e]].to(TYPES[c["out"]])
+
+
+def _run_swiglu(s, c):
+    if own:
+        import sparse_mixture_experts_sum_amd as moe
+        return moe.moe_swiglu_backward(s["g"], s["u"], s["dh"], s["w"])
+    dt = TYPES[c["dtype"]]
+    g, u, dh, w = s["g"].float(), s["u"].float(), s["dh"].float(), s["w"][:, None]
+    sig = 1 / (1 + torch.exp(-g))
+    silu = g * sig
+    return {"dg": (w * dh * u * sig * (1 + g * (1 - sig))).to(dt), "du": (w * dh * silu).to(dt),
+            "h": (w * silu * u).to(dt), "dw": (dh * silu * u).sum(1)}
+
+
+def _run_route(s, c):
+    if own:
+        import sparse_mixture_experts_sum_amd as moe
+        return moe.moe_route_backward(s["x"], s["W_g"], s["probs"], s["idx"], s["w"], s["dw"],
+                                      b_g=s["b_g"], f=s["f"], loss_grad=s["loss_grad"],
+                                      z_loss_grad=s["z_loss_grad"], renormalize=c["renormalize"],
+                                      rows=s["rows"], pos=s["pos"])
+    T, E, k, dt = c["T"], c["E"], c["k"], TYPES[c["dtype"]]
+    x, W_g, p, idx = s["x"].float(), s["W_g"].float(), s["probs"], s["idx"].long()
+    # lse_t = log sum_e exp(s_te)
+    logits = x @ W_g + s["b_g"]
+    top = logits.max(1, keepdim=True).values
+    lse = top + torch.log(torch.exp(logits - top).sum(1, keepdim=True))
+    dw = s["dw"]
+    if c["renormalize"]:
+        dw = (dw - (dw * s["w"]).sum(1, keepdim=True)) / p.gather(1, idx).sum(1, keepdim=True)
+    dp = torch.zeros_like(p).scatter(1, idx, dw) + s["loss_grad"] * E / (k * T) * s["f"]
+    ds = p * (dp - (p * dp).sum(1, keepdim=True)) + s["z_loss_grad"] * 2 / T * lse * p
+    dx = ds @ W_g.t()
+    if s["rows"] is not None:
+        dx = dx + s["rows"].float()[s["pos"].long()].sum(1)
+    return {"dx": dx.to(dt), "dW_g": (x.t() @ ds).to(dt), "db_g": ds.sum(0), "dlogits": ds}
+
+
+def _run_norm(s, c):
+    if own:
+        import sparse_mixture_experts_sum_amd as moe
+        r = moe.moe_block_norm(s["x"], gamma=s["gamma"], y=s["y"], gamma_post=s["gamma_post"],
+                               gate=s["gate"], residual_scale=s["scale"], eps=EPS)
+        return {n: r[n] for n in (("out", "rstd_post") if c["y"] else ()) + (("u", "rstd") if c["u"] else ())}
+    dt, r, out = TYPES[c["dtype"]], {}, s["x"]
+    if c["y"]:
+        r["rstd_post"] = _rstd(s["y"])
+        v = s["y"] * r["rstd_post"][:, None] * s["gamma_post"]
+        if s["gate"] is not None:
+            v = v * (s["gate"] if c["gate"] == "channel" else s["gate"][:, None])
+        r["out"] = out = (s["scale"] * s["x"].float() + v).to(dt)
+    if c["u"]:  # the next norm reads the stored sum
+        r["rstd"] = _rstd(out.float())
+        r["u"] = (out.float() * r["rstd"][:, None] * s["gamma"]).to(dt)
+    return r
+
+
+def _run_norm_backward(s, c):
+    names = (["dy", "dgamma_post"] if c["y"] else []) + (["dgamma"] if c["u"] else []) + \
+            (["dgate"] if c["gate"] != "none" else []) + ["dx"]
+    if own:
+        import sparse_mixture_experts_sum_amd as moe
+        r = moe.moe_block_norm_backward(s["x"], d_out=s["d_out"], d_u=s["d_u"], rstd=s["rstd"],
+                                        gamma=s["gamma"], y=s["y"], rstd_post=s["rstd_post"],
+                                        gamma_post=s["gamma_post"], gate=s["gate"],
+                                        residual_scale=s["scale"])
+        return {n: r[n] for n in names}
+    dt, r = TYPES[c["dtype"]], {}
+    D = s["d_out"].float()
+    if c["u"]:
+        z = s["x"].float() * s["rstd"][:, None]
+        d_u = s["d_u"].float()
+        dz = d_u * s["gamma"]
+        D = D + s["rstd"][:, None] * (dz - z * (dz * z).mean(1, keepdim=True))
+        r["dgamma"] = (d_u * z).sum(0)
+    r["dx"] = (s["scale"] * D).to(dt)
+    if c["y"]:
+        n = s["y"] * s["rstd_post"][:, None]
+        gate = s["gate"] if c["gate"] == "channel" else s["gate"][:, None] if c["gate"] == "token" else 1.0
+        dv = gate * D
+        dn = dv * s["gamma_post"]
+        r["dy"] = (s["rstd_post"][:, None] * (dn - n * (dn * n).mean(1, keepdim=True))).to(dt)
+        r["dgamma_post"] = (dv * n).sum(0)
+        if c["gate"] != "none":
+            r["dgate"] = (D * n * s["gamma_post"]).sum(0 if c["gate"] == "channel" else 1)
+    return r
+
+
+# ---- the definition in 64 bits -------------------------------------------------------
+def exact(case, seed):
+    s = prepare(case, seed)
+    c = s["case"]
+    d = {n: v.double() if isinstance(v, torch.Tensor) and v.is_floating_point() else v for n, v in s.items()}
+    if c["op"] == "matmul":
+        a = d["a"] if s["gather"] is None else d["a"][s["gather"].long()]
+        parts, r = [], 0
+        for e, n in enumerate(s["counts"]):
+            rows = a[r:r + n]
+            if c["form"] == "tn":
+                parts.append((rows.t() @ d["b"][r:r + n])[None])
+            else:
+                parts.append(rows @ (d["b"][e] if c["form"] == "nn" else d["b"][e].t()))
+            r += n
+        return torch.cat(parts)
+    if c["op"] == "swiglu":
+        g, u, w = (d[n].requires_grad_() for n in ("g", "u", "w"))
+        h = g * torch.sigmoid(g) * u * w[:, None]
+        dg, du, dw = torch.autograd.grad(h, (g, u, w), d["dh"])
+        return {"dg": dg, "du": du, "h": h.detach(), "dw": dw}
+    if c["op"] == "route":
+        x, W_g, b_g = (d[n].requires_grad_() for n in ("x", "W_g", "b_g"))
+        logits = x @ W_g + b_g
+        logits.retain_grad()
+        p = torch.softmax(logits, 1)
+        w = p.gather(1, s["idx"].long())
+        if c["renormalize"]:
+            w = w / w.sum(1, keepdim=True)
+        total = (w * d["dw"]).sum() + s["loss_grad"] * c["E"] * (d["f"] / c["k"] * p.mean(0)).sum() \
+            + s["z_loss_grad"] * torch.logsumexp(logits, 1).square().mean()
+        total.backward()
+        dx = x.grad
+        if s["rows"] is not None:
+            dx = dx + torch.stack([d["rows"][s["pos"][:, j].long()] for j in range(c["k"])]).sum(0)
+        return {"dx": dx, "dW_g": W_g.grad, "db_g": b_g.grad, "dlogits": logits.grad}
+    if not c["back"]:
+        r, out = {}, d["x"]
+        if c["y"]:
+            r["rstd_post"] = _rstd(d["y"])
+            gate = 1.0 if s["gate"] is None else d["gate"] if c["gate"] == "channel" else d["gate"][:, None]
+            r["out"] = s["scale"] * d["x"] + gate * d["gamma_post"] * d["y"] / ((d["y"] ** 2).mean(1, keepdim=True) + EPS).sqrt()
+            out = r["out"].to(TYPES[c["dtype"]]).double()
+        if c["u"]:
+            r["rstd"] = _rstd(out)
+            r["u"] = d["gamma"] * out / ((out ** 2).mean(1, keepdim=True) + EPS).sqrt()
+        return r
+    # the forward as a function of its inputs, differentiated; `t` is what the next norm reads
+    r, D = {}, d["d_out"]
+    if c["u"]:
+        t, gamma = d["x"].requires_grad_(), d["gamma"].requires_grad_()
+        u = gamma * t / ((t ** 2).mean(1, keepdim=True) + EPS).sqrt()
+        dt, r["dgamma"] = torch.autograd.grad(u, (t, gamma), d["d_u"])
+        D = D + dt
+    r["dx"] = s["scale"] * D
+    if c["y"]:
+        leaves = {"dy": d["y"], "dgamma_post": d["gamma_post"]}
+        if s["gate"] is not None:
+            leaves["dgate"] = d["gate"]
+        for v in leaves.values():
+            v.requires_grad_()
+        gate = 1.0 if s["gate"] is None else d["gate"] if c["gate"] == "channel" else d["gate"][:, None]
+        v = gate * d["gamma_post"] * d["y"] / ((d["y"] ** 2).mean(1, keepdim=True) + EPS).sqrt()
+        for n, grad in zip(leaves, torch.autograd.grad(v, list(leaves.values()), D)):
+            r[n] = grad
+    return r
