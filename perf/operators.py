@@ -186,7 +186,7 @@ def prepare(case, seed):
         s["gamma_post"] = 1 + normal(d, std=0.1, dtype=torch.float32) if c["y"] else None
         s["gamma"] = 1 + normal(d, std=0.1, dtype=torch.float32) if c["u"] else None
         s["gate"] = {"none": None, "channel": normal(d, std=0.5, dtype=torch.float32),
-                     "token": torch.rand(T, generator=gen, device=DEV)}[c["gate"]]
+                     "token": torch.rand(T, 1, generator=gen, device=DEV)}[c["gate"]]
         s["scale"] = 0.75 if c["y"] else 1.0
         if c["back"]:  # what the forward pass left
             s["d_out"] = normal(T, d, std=0.1)
@@ -278,7 +278,7 @@ def _run_norm(s, c):
         r["rstd_post"] = _rstd(s["y"])
         v = s["y"] * r["rstd_post"][:, None] * s["gamma_post"]
         if s["gate"] is not None:
-            v = v * (s["gate"] if c["gate"] == "channel" else s["gate"][:, None])
+            v = v * s["gate"]
         r["out"] = out = (s["scale"] * s["x"].float() + v).to(dt)
     if c["u"]:  # the next norm reads the stored sum
         r["rstd"] = _rstd(out.float())
@@ -307,13 +307,14 @@ def _run_norm_backward(s, c):
     r["dx"] = (s["scale"] * D).to(dt)
     if c["y"]:
         n = s["y"] * s["rstd_post"][:, None]
-        gate = s["gate"] if c["gate"] == "channel" else s["gate"][:, None] if c["gate"] == "token" else 1.0
+        gate = 1.0 if s["gate"] is None else s["gate"]
         dv = gate * D
         dn = dv * s["gamma_post"]
         r["dy"] = (s["rstd_post"][:, None] * (dn - n * (dn * n).mean(1, keepdim=True))).to(dt)
         r["dgamma_post"] = (dv * n).sum(0)
         if c["gate"] != "none":
-            r["dgate"] = (D * n * s["gamma_post"]).sum(0 if c["gate"] == "channel" else 1)
+            dgate = D * n * s["gamma_post"]
+            r["dgate"] = dgate.sum(0) if c["gate"] == "channel" else dgate.sum(1, keepdim=True)
     return r
 
 
@@ -357,7 +358,7 @@ def exact(case, seed):
         r, out = {}, d["x"]
         if c["y"]:
             r["rstd_post"] = _rstd(d["y"])
-            gate = 1.0 if s["gate"] is None else d["gate"] if c["gate"] == "channel" else d["gate"][:, None]
+            gate = 1.0 if s["gate"] is None else d["gate"]
             r["out"] = s["scale"] * d["x"] + gate * d["gamma_post"] * d["y"] / ((d["y"] ** 2).mean(1, keepdim=True) + EPS).sqrt()
             out = r["out"].to(TYPES[c["dtype"]]).double()
         if c["u"]:
@@ -378,7 +379,7 @@ def exact(case, seed):
             leaves["dgate"] = d["gate"]
         for v in leaves.values():
             v.requires_grad_()
-        gate = 1.0 if s["gate"] is None else d["gate"] if c["gate"] == "channel" else d["gate"][:, None]
+        gate = 1.0 if s["gate"] is None else d["gate"]
         v = gate * d["gamma_post"] * d["y"] / ((d["y"] ** 2).mean(1, keepdim=True) + EPS).sqrt()
         for n, grad in zip(leaves, torch.autograd.grad(v, list(leaves.values()), D)):
             r[n] = grad
