@@ -288,6 +288,169 @@ moe_status moe_profile_enable(int32_t on);
 moe_status moe_profile_read(double* total_ms, int64_t* launches, int32_t n);
 const char* moe_stage_name(int32_t stage);
 
+/* ---- Training: the products, gradients and norms around the forward ------------------
+ * The entry points below follow the conventions above (device memory, the caller's buffers
+ * and stream, host checks before any HIP call, deterministic results) with these limits:
+ * 1 <= E <= 64, row counts below 2^31. Index values read on the device (offsets, gathers,
+ * idx, pos) that lie outside their range never move an access out of a buffer: each
+ * function says what such a value is taken for. No output may overlap an input or another
+ * output unless it says so. They record no stage timing. */
+
+/* Products of rows grouped by expert: group e is rows [offsets[e], offsets[e+1]).
+ *   MOE_MATMUL_NN  out[r] = a[r] b_e      a [R, K], b [E, K, N] -> out [R, N]
+ *   MOE_MATMUL_NT  out[r] = a[r] b_e^T    a [R, K], b [E, N, K] -> out [R, N]
+ *   MOE_MATMUL_TN  out_e = sum over the group's rows r of a[r]^T b[r]
+ *                                         a [R, K], b [R, N]    -> out [E, K, N]
+ * With a forward product y = x W (NN), NT with W is the gradient of x and TN of W. */
+typedef enum moe_matmul_form {
+  MOE_MATMUL_NN = 0,
+  MOE_MATMUL_NT = 1,
+  MOE_MATMUL_TN = 2
+} moe_matmul_form;
+
+typedef struct moe_matmul_shape {
+  int64_t R;          /* rows of the grouped problem; groups end at or before R */
+  int64_t rows_a;     /* rows of a: R without gather_a */
+  int64_t rows_b;     /* TN: rows of b, R without gather_b; ignored otherwise */
+  int64_t K;          /* width of a */
+  int64_t N;          /* width of out */
+  int32_t E;          /* groups */
+  int32_t form;       /* moe_matmul_form */
+  int32_t dtype;      /* moe_dtype of a and b */
+  int32_t out_dtype;  /* moe_dtype of out: fp32, or bf16 where dtype is bf16 */
+  int32_t accumulate; /* 1: the product is added to out's values (fp32 out only); 0: stored */
+} moe_matmul_shape;
+
+/*   offsets   [E+1] int32 on the device, ascending from 0 (offsets of moe_forward's
+ *             workspace, MOE_WS_OFFSETS, as they are). A bound is taken for the largest of
+ *             itself, the bounds before it and 0, and at most R.
+ *   gather_a  [R] int32 or NULL: row r of the problem is row gather_a[r] of a (the same row
+ *             any number of times); values are clamped into [0, rows_a)
+ *   gather_b  TN only: the same for b
+ * Sums are fp32 (bf16 products are exact in it); bf16 outputs are rounded once. NN and NT
+ * leave the rows of out at and past offsets[E] as they are; a TN group without rows
+ * gives zeros (accumulate: leaves its matrix as it is). K and N at most 2^20 and multiples of 8
+ * (bf16) or 4 (fp32): rows are read in 16-byte pieces (otherwise MOE_ERR_UNSUPPORTED). a, b
+ * and out must be 16-byte aligned. gather_b in NN or NT, and accumulate or a bf16 dtype's
+ * opposite that out_dtype does not allow, return MOE_ERR_UNSUPPORTED. */
+moe_status moe_grouped_matmul(const moe_matmul_shape* shape, const void* a, const void* b,
+                              const int32_t* offsets, const int32_t* gather_a,
+                              const int32_t* gather_b, void* out, hipStream_t stream);
+
+/* Gradient of the experts' activation h = silu(g) * u and of the row's gate weight, for
+ * y = sum over rows of w_r (h_r W_down): with dh = dy W_down^T (unweighted) and
+ * s = 1 / (1 + e^-g), element by element,
+ *   dg = w dh u s (1 + g (1 - s)),  du = w dh g s,  hw = w g s u,  dw_r = sum_f dh g s u
+ * (hw^T dy is then the gradient of W_down). All rows' values are computed in fp32.
+ *   g, u, dh     [R, f] dtype      dg, du, hw  [R, f] dtype (each may be the input of its
+ *                                  place: dg = g, du = u, hw = dh), NULL to skip
+ *   w            the gate weights, NULL for 1: [R] by row when pos is NULL; otherwise by
+ *                slot, [T, k]: row r belongs to token src[r] and to the slot j of that token
+ *                with pos[src[r], j] = r (MOE_WS_SRC, MOE_WS_POS), and a row that no slot of
+ *                its token names has weight 0
+ *   dw           [R] fp32 by row, NULL to skip
+ *   offsets      NULL, or the [E+1] bounds: rows at and past offsets[E] are neither read
+ *                nor written
+ * f at most 2^20 and a multiple of 8 (bf16) or 4 (fp32), else MOE_ERR_UNSUPPORTED. Tensors
+ * of R rows must be 16-byte aligned. */
+typedef struct moe_swiglu_shape {
+  int64_t R;      /* rows */
+  int64_t f;      /* width */
+  int64_t T;      /* tokens (rows of pos), with pos */
+  int32_t k;      /* slots per token, with pos: 1 .. 8 */
+  int32_t E;      /* groups, with offsets */
+  int32_t dtype;  /* moe_dtype */
+} moe_swiglu_shape;
+moe_status moe_swiglu_backward(const moe_swiglu_shape* shape, const void* g, const void* u,
+                               const void* dh, const float* w, const int32_t* src,
+                               const int32_t* pos, const int32_t* offsets, void* dg, void* du,
+                               void* hw, float* dw, hipStream_t stream);
+
+/* Gradient of the token-choice router (both token-choice modes, without training noise):
+ * of its weights w, the load-balancing loss and the z-loss, with respect to x, W_g and b_g.
+ * Per token, over the slots the forward kept (w != 0; the others' dw is not looked at),
+ * S = sum of their probabilities:
+ *   dp_e  = (dw_j - sum_i dw_i w_i) / S for e = idx_j (renormalize = 1), dw_j (= 0),
+ *           plus loss_grad * E f_e / (k T) for every e
+ *   ds_e  = p_e (dp_e - sum_c p_c dp_c) + z_loss_grad * 2 lse p_e / T
+ *   db_g = sum_t ds,  dW_g = x^T ds,  dx = ds W_g^T (+ sum_j rows[pos[t, j]])
+ * lse, the token's log sum_e exp(s_e), is s - log p at its most probable expert, from one
+ * dot product in fp32 (z_loss_grad != 0 only); the counts behind f carry no gradient. */
+typedef struct moe_route_upstream {
+  const float* dw;        /* gradient of w, NULL for none: [T, k], or [R] by row (dw_by_row) */
+  int32_t dw_by_row;      /* 1: dw of slot (t, j) is dw[pos[t, j]] */
+  float loss_grad;        /* gradient of the load-balancing loss */
+  float z_loss_grad;      /* gradient of the z-loss */
+  const float* f;         /* [E] the forward's f; required when loss_grad != 0 */
+  const void* rows;       /* [R, d_model] dtype, NULL for none: gradients of the routed rows */
+  const int32_t* pos;     /* [T, k] row of each slot (MOE_WS_POS); values outside [0, R) add
+                             nothing. Required with rows or dw_by_row */
+  int64_t R;              /* rows of rows / by-row dw */
+} moe_route_upstream;
+
+/* Bytes of workspace moe_route_backward needs. Host only. */
+moe_status moe_route_backward_workspace_size(const moe_shape* shape, size_t* bytes);
+
+/*   x, W_g, b_g     as in moe_route
+ *   probs, idx, w   moe_route's or moe_forward's outputs for them (an idx outside [0, E) is
+ *                   taken for the nearest end)
+ *   dx      [T, d_model] dtype, dW_g [d_model, E] dtype, db_g [E] fp32: NULL to skip
+ *   dlogits [T, E] fp32, the ds above: always written
+ * d_ff is ignored. Expert-choice shapes return MOE_ERR_UNSUPPORTED. x, W_g, rows, dx, dW_g
+ * and the workspace must be 16-byte aligned. With T = 0 dW_g and db_g are zero. */
+moe_status moe_route_backward(const moe_shape* shape, const void* x, const void* W_g,
+                              const float* b_g, const float* probs, const int32_t* idx,
+                              const float* w, const moe_route_upstream* up, void* dx, void* dW_g,
+                              float* db_g, float* dlogits, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
+
+/* RMS norms after a block and before the next one, with the block's gate and the residual
+ * scale, in one pass. With rms(v) = sqrt(mean v^2 + eps) over the row:
+ *   after   (y given)      out = residual_scale * x + gate * (y / rms(y) * gamma_post)
+ *                          (out = x without y)
+ *   before  (gamma given)  u = out / rms(out) * gamma
+ * One or both parts run. `out` is rounded to dtype and `u` is computed from the rounded
+ * values, so that both parts in one call give the bits of two calls. */
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
+typedef struct moe_norm_shape {
+  int64_t T;             /* rows */
+  int64_t d;             /* width: at most 16384 (a row is held in registers) and a multiple of 8 */
+  int32_t dtype;         /* moe_dtype of x, out, u and their gradients, and of dy */
+  int32_t gate;          /* gate: none (1), [d] per channel, or [T] per token */
+  float eps;             /* > 0, finite */
+  float residual_scale;  /* finite; only with y */
+} moe_norm_shape;
+
+/*   x [T, d] dtype, y [T, d] fp32 (moe_forward's output) or NULL, gamma_post [d] fp32 and
+ *   gate fp32 (with y), gamma [d] fp32 or NULL
+ *   out [T, d] dtype (with y; may be x), u [T, d] dtype (with gamma)
+ *   rstd_post, rstd [T] fp32 = 1 / rms(y), 1 / rms(out): for the gradient, NULL to skip
+ * Neither y nor gamma: MOE_ERR_NULL_ARG. All tensors but the [T] ones 16-byte aligned. */
+moe_status moe_block_norm(const moe_norm_shape* shape, const void* x, const float* y,
+                          const float* gamma_post, const float* gate, const float* gamma,
+                          void* out, void* u, float* rstd_post, float* rstd, hipStream_t stream);
+
+/* Bytes of workspace moe_block_norm_backward needs. Host only. */
+moe_status moe_block_norm_backward_workspace_size(const moe_norm_shape* shape, size_t* bytes);
+
+/* Its gradient. d_out, d_u [T, d] dtype: gradients of out and u; either may be NULL (the part
+ * before runs with d_u, the part after with y).
+ *   D  = d_out + r (dz - z mean(dz z)),  dz = d_u gamma, z = out r, r = rstd
+ *   dx = residual_scale D (with y, else D),  dgamma = sum_t d_u z
+ *   n = y q, q = rstd_post, dn = gate D gamma_post:  dy = q (dn - n mean(dn n)),
+ *   dgamma_post = sum_t gate D n,  dgate = sum of D n gamma_post over t (per channel) or
+ *   over the row (per token)
+ *   out, rstd, gamma: with d_u (out: the forward's rounded sum; x where y was NULL)
+ *   y, rstd_post, gamma_post, gate: with y
+ *   dx, dy [T, d] dtype; dgamma, dgamma_post [d], dgate [d] or [T] fp32: NULL to skip. dx may
+ *   be d_out or d_u. */
+moe_status moe_block_norm_backward(const moe_norm_shape* shape, const void* d_out,
+                                   const void* d_u, const void* out, const float* rstd,
+                                   const float* gamma, const float* y, const float* rstd_post,
+                                   const float* gamma_post, const float* gate, void* dx, void* dy,
+                                   float* dgamma, float* dgamma_post, float* dgate, void* ws,
+                                   size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

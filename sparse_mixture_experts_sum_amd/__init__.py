@@ -20,6 +20,8 @@ __all__ = [
     "workspace_size", "capacity",
     "workspace_offset", "profile_enable", "profile_read", "stage_names", "SparseMoE",
     "MoEError", "load_library", "LIB_PATH",
+    "moe_grouped_matmul", "moe_swiglu_backward", "moe_route_backward", "moe_block_norm",
+    "moe_block_norm_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_hip.so")
@@ -36,6 +38,9 @@ EXPORTS = (
     "moe_status_string", "moe_capacity", "moe_workspace_size", "moe_workspace_offset",
     "moe_route", "moe_forward", "moe_aux_loss", "moe_profile_enable", "moe_profile_read",
     "moe_stage_name", "moe_forward_noalloc",
+    "moe_grouped_matmul", "moe_swiglu_backward", "moe_route_backward_workspace_size",
+    "moe_route_backward", "moe_block_norm", "moe_block_norm_backward_workspace_size",
+    "moe_block_norm_backward",
 )
 
 
@@ -111,6 +116,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "moe_forward", "moe_forward_noalloc", "moe_aux_loss", "moe_profile_enable",
                  "moe_profile_read"):
         getattr(lib, name).restype = I32
+    training.declare(lib, S)
     _lib = lib
     return lib
 
@@ -398,6 +404,11 @@ def profile_read() -> dict:
     n = (ctypes.c_int64 * NUM_STAGES)()
     _check("moe_profile_read", load_library().moe_profile_read(ms, n, NUM_STAGES))
     return {nm: (ms[i], n[i]) for i, nm in enumerate(stage_names())}
+
+
+from . import training  # noqa: E402  (its bindings use the helpers above)
+from .training import (moe_block_norm, moe_block_norm_backward,  # noqa: E402
+                       moe_grouped_matmul, moe_route_backward, moe_swiglu_backward)
 
 
 class SparseMoE:
