@@ -24,7 +24,6 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kStages = 4;    // LDS ring
-constexpr int kTable = 2048;  // TN: rows of the summed axis whose indices are in LDS at once
 
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
@@ -34,18 +33,17 @@ __device__ __forceinline__ void wait_vmcnt() {
 __device__ __forceinline__ void wait_lgkmcnt0() {
   __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));
 }
-// s_waitcnt vmcnt(n * PER) for a runtime n, 3 or more taken for 3
-template <int PER>
-__device__ __forceinline__ void wait_stages(int n) {
-  if (n >= 3) wait_vmcnt<3 * PER>();
-  else if (n == 2) wait_vmcnt<2 * PER>();
-  else if (n == 1) wait_vmcnt<PER>();
-  else wait_vmcnt<0>();
-}
 __device__ __forceinline__ void sync_point() {
   __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
+}
+
+// The value, hidden from the compiler: what depends on it is computed where it is used, and
+// not kept in registers (which the 256-row tiles do not have) from before the tile loop.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
 }
 
 // One operand's stage in LDS: X rows (its output axis) by BK of the summed axis.
@@ -109,55 +107,57 @@ struct Geo {
   typedef Operand<FORM != MOE_MATMUL_NT, BN, BK, 4> B;
   static constexpr int WM = BM / WGM, WN = BN / WGN, MB = WM / 32, NB = WN / 32;
   static constexpr int STAGE = A::BYTES + B::BYTES, LPS = A::PW + B::PW;
+  // LDS of each wave for its output: 32 rows of its columns in bf16 (the 32-row tiles have
+  // none left, and little to store)
+  static constexpr int OUT_BYTES = BM >= 128 ? 32 * WN * 2 : 0;
 };
 
 // Sources of a tile's direct loads. NN, NT: one pointer per load, advancing by a fixed step
-// per stage. TN: the rows are the summed axis, so each load takes its row's index from a
-// table in LDS (the gather, or the rows themselves; past the end the last row again).
+// per stage. TN: the rows are the summed axis, and each load takes its row's index (the
+// gather's, or the row itself) from the turn's indices.
 template <class G>
 struct Loader {
   const bf16* pa[G::A::PW];
   const bf16* pb[G::B::PW];
   size_t step_a, step_b;  // elements per stage (TN: per row)
-  const int *ta, *tb;     // TN tables, this segment's first row at 0
   int len, wave, ln;
 
-  template <class Op>
-  __device__ __forceinline__ const bf16* at(const bf16* const* p, size_t step, const int* tab, int j,
-                                            int kt) const {
-    if constexpr (G::TN) return p[j] + (size_t)tab[kt * G::BK + Op::row(j, wave, ln)] * step;
-    else return p[j] + (size_t)kt * step;
-  }
-  // NN, NT, a stage that ends past len: the last chunk (or row) again
-  template <class Op>
-  __device__ __forceinline__ const bf16* at_tail(const bf16* const* p, size_t step, int j, int kt) const {
-    const int k = kt * G::BK + (Op::KS ? Op::row(j, wave, ln) : Op::chunk(j, wave, ln) * 8);
-    const int back = min(0, len - (Op::KS ? 1 : 8) - k);
-    return p[j] + (size_t)kt * step + (Op::KS ? (int64_t)back * (int64_t)(step / G::BK) : (int64_t)back);
-  }
-  // load j (A's, then B's; a constant at every call) of stage kt into st
-  template <bool TAIL>
-  __device__ __forceinline__ void issue(int j, int kt, char* st) const {
-    if (j < G::A::PW) {
-      const bf16* p = TAIL ? at_tail<typename G::A>(pa, step_a, j, kt)
-                           : at<typename G::A>(pa, step_a, ta, j, kt);
-      __builtin_amdgcn_global_load_lds(p, (lds_void*)(st + (wave * G::A::PW + j) * 1024), 16, 0, 0);
-    } else {
-      const int i = j - G::A::PW;
-      const bf16* p = TAIL ? at_tail<typename G::B>(pb, step_b, i, kt)
-                           : at<typename G::B>(pb, step_b, tb, i, kt);
-      __builtin_amdgcn_global_load_lds(
-          p, (lds_void*)(st + G::A::BYTES + (wave * G::B::PW + i) * 1024), 16, 0, 0);
+  // Stages may end past len where CLAMP: the last chunk (or row) is then read again.
+  template <class Op, bool CLAMP>
+  __device__ __forceinline__ const bf16* at(const bf16* const* p, size_t step, int j, int kt) const {
+    const bf16* q = p[j] + (size_t)kt * step;
+    if constexpr (CLAMP) {
+      const int l = here(ln);
+      const int k = kt * G::BK + (Op::KS ? Op::row(j, wave, l) : Op::chunk(j, wave, l) * 8);
+      const int back = min(0, len - (Op::KS ? 1 : 8) - k);
+      q += Op::KS ? (int64_t)back * (int64_t)(step / G::BK) : (int64_t)back;
     }
+    return q;
   }
-  __device__ __forceinline__ void issue_stage(int kt, char* st) const {
-    if (G::TN || (kt + 1) * G::BK <= len) {
+  // load j (A's, then B's; a constant at every call) of stage kt into st; TN: of the rows
+  // that `turn` holds for ring place q
+  template <bool CLAMP>
+  __device__ __forceinline__ void issue(int j, int kt, int turn, int q, char* st) const {
+    const bool is_a = j < G::A::PW;
+    const int i = is_a ? j : j - G::A::PW;
+    const bf16* p;
+    if constexpr (G::TN) {
+      // the rows of one load instruction are consecutive lanes of `turn`
+      constexpr int RPI = 8 / G::A::PW;
+      static_assert(G::A::RPI == RPI && G::B::RPI == RPI, "eight rows per wave and stage");
+      const int l0 = (is_a ? 0 : 32) + q * 8 + i * RPI, mine = ln / (64 / RPI);
+      int row = __builtin_amdgcn_readlane(turn, l0);
 #pragma unroll
-      for (int j = 0; j < G::LPS; ++j) issue<false>(j, kt, st);
+      for (int r = 1; r < RPI; ++r) {
+        const int v = __builtin_amdgcn_readlane(turn, l0 + r);
+        row = mine >= r ? v : row;
+      }
+      p = is_a ? pa[i] + (int64_t)row * (int64_t)step_a : pb[i] + (int64_t)row * (int64_t)step_b;
     } else {
-#pragma unroll
-      for (int j = 0; j < G::LPS; ++j) issue<true>(j, kt, st);
+      p = is_a ? at<typename G::A, CLAMP>(pa, step_a, i, kt) : at<typename G::B, CLAMP>(pb, step_b, i, kt);
     }
+    char* to = is_a ? st + (wave * G::A::PW + i) * 1024 : st + G::A::BYTES + (wave * G::B::PW + i) * 1024;
+    __builtin_amdgcn_global_load_lds(p, (lds_void*)to, 16, 0, 0);
   }
 };
 
@@ -204,207 +204,177 @@ __device__ __forceinline__ void mask_frags(Frags<G>& F, int left, int ln) {
 }
 
 // Stage kt (J = kt % kStages). On entry its fragments are in Fc and the loads of the next
-// kStages - 1 stages are in flight. Wait for this wave's loads of stage kt + 1 and its own LDS
-// reads of stage kt, then the barrier: after it stage kt + 1 is whole in LDS and stage kt's
-// buffer is free. Then the stage's MFMAs, with the reads of stage kt + 1 into Fn and the
-// refill of stage kt's buffer (with stage kt + kStages) spread between them. FULL: both happen
-// and the next stage and the refill lie inside len; otherwise they are tested.
-template <class G, int J, bool FULL>
+// kStages - 1 stages are in flight. Wait for this wave's loads of the next stage and its own
+// LDS reads of this one, then the barrier: after it the next stage is whole in LDS and this
+// stage's buffer is free. Then the stage's MFMAs, with the reads of the next stage into Fn and
+// the refill of this buffer (stage `rs` of ld) spread between them.
+// Every step loads and reads the same amounts, so that the loads in flight are known at
+// every wait: past an item's last stage the refills are the next item's first stages, and an
+// item is a whole number of ring turns, whose spare stages (CALC false) skip the MFMAs.
+template <class G, int J, bool CLAMP>
 struct Step {
-  static __device__ __forceinline__ void run(int kt, int nk, char* const (&ring)[kStages],
-                                             const Loader<G>& ld, Wave<G>& w, Frags<G>& Fc,
-                                             Frags<G>& Fn) {
+  template <bool CALC>
+  static __device__ __forceinline__ void body(int rs, int turn, char* const (&ring)[kStages],
+                                              const Loader<G>& ld, Wave<G>& w, Frags<G>& Fc,
+                                              Frags<G>& Fn) {
     constexpr int NM = G::SUB * G::NB * G::MB, NR = G::SUB * (G::MB + G::NB), NG = G::LPS;
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (FULL) wait_vmcnt<(kStages - 2) * G::LPS>();
-    else wait_stages<G::LPS>(min(kStages - 2, max(nk - 2 - kt, 0)));
-    wait_lgkmcnt0();
-    sync_point();
-    const bool more = FULL || kt + 1 < nk, refill = FULL || kt + kStages < nk;
     const char* src = ring[(J + 1) % kStages];
     char* const dst = ring[J];
-    const bool tail = !FULL && !G::TN && (kt + kStages + 1) * G::BK > ld.len;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
+      if constexpr (CALC) {
 #pragma unroll
-      for (int m = NM * g / NG; m < NM * (g + 1) / NG; ++m) w.mfma(m, Fc);
-      if (more) {
+        for (int m = NM * g / NG; m < NM * (g + 1) / NG; ++m) w.mfma(m, Fc);
+      }
 #pragma unroll
-        for (int r = NR * g / NG; r < NR * (g + 1) / NG; ++r) w.read(r, src, Fn);
-      }
-      if (refill) {
-        if (!tail) ld.template issue<false>(g, kt + kStages, dst);
-        else if constexpr (!FULL && !G::TN) ld.template issue<true>(g, kt + kStages, dst);
-      }
+      for (int r = NR * g / NG; r < NR * (g + 1) / NG; ++r) w.read(r, src, Fn);
+      ld.template issue<CLAMP>(g, rs, turn, J, dst);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (!FULL) {
-      if (more && (kt + 2) * G::BK > ld.len) mask_frags<G>(Fn, ld.len - (kt + 1) * G::BK, ld.ln);
-    }
+  }
+  static __device__ __forceinline__ void wait() {
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<(kStages - 2) * G::LPS>();
+    wait_lgkmcnt0();
+    sync_point();
   }
 };
 
-// All stages of a tile (or of a TN segment): nk = ceil(len / BK) > 0.
+// Fragments of the first stage of an item of length len, once read.
 template <class G>
-__device__ __forceinline__ void run_stages(char* const (&ring)[kStages], const Loader<G>& ld,
-                                           Wave<G>& w) {
-  const int nk = (ld.len + G::BK - 1) / G::BK, whole = ld.len / G::BK;
-  Frags<G> F0, F1;
-  int kt = 0;
-#define MOE_STEP(J, FULL, KT) \
-  Step<G, J, FULL>::run(KT, nk, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1)
-  // Prologue and the whole stages in one branch, so that the compiler sees the same loads in
-  // flight on every path into the loop.
-  if (whole >= 2 * kStages) {
-#pragma unroll
-    for (int i = 0; i < kStages; ++i)
-#pragma unroll
-      for (int j = 0; j < G::LPS; ++j) ld.template issue<false>(j, i, ring[i]);
-    wait_vmcnt<(kStages - 1) * G::LPS>();
-    sync_point();
-#pragma unroll
-    for (int r = 0; r < G::SUB * (G::MB + G::NB); ++r) w.read(r, ring[0], F0);
-    for (; kt + 2 * kStages <= whole; kt += kStages) {
-      MOE_STEP(0, true, kt);
-      MOE_STEP(1, true, kt + 1);
-      MOE_STEP(2, true, kt + 2);
-      MOE_STEP(3, true, kt + 3);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kStages; ++i)
-      if (i < nk) ld.issue_stage(i, ring[i]);
-    wait_stages<G::LPS>(min(kStages, nk) - 1);
-    sync_point();
-#pragma unroll
-    for (int r = 0; r < G::SUB * (G::MB + G::NB); ++r) w.read(r, ring[0], F0);
-    if (ld.len < G::BK) mask_frags<G>(F0, ld.len, ld.ln);
-  }
-  // at most 2 * kStages left
-  if (kt < nk) { MOE_STEP(0, false, kt); }
-  if (kt + 1 < nk) { MOE_STEP(1, false, kt + 1); }
-  if (kt + 2 < nk) { MOE_STEP(2, false, kt + 2); }
-  if (kt + 3 < nk) { MOE_STEP(3, false, kt + 3); }
-  if (kt + 4 < nk) { MOE_STEP(0, false, kt + 4); }
-  if (kt + 5 < nk) { MOE_STEP(1, false, kt + 5); }
-  if (kt + 6 < nk) { MOE_STEP(2, false, kt + 6); }
-  if (kt + 7 < nk) { MOE_STEP(3, false, kt + 7); }
-#undef MOE_STEP
+__device__ __forceinline__ void mask_first(Frags<G>& F, int len, int ln) {
+  if (len < G::BK) mask_frags<G>(F, len, ln);
 }
 
-// A workgroup's tile: group e, its rows [r0, r1), output tile (mt, nt) of it.
-struct TileAt {
+// A workgroup's work: output tile (mt, nt) of group e, whose rows are [r0, r1).
+struct Item {
   int e, r0, r1, mt, nt;
 };
 
 constexpr int kXcds = 8;
+constexpr int kCus = 256;
 constexpr int kColBlock = 4;  // columns of tiles walked together
+// TN: what a tile costs beside its stages (its stores, the pipeline's ends), in stages
+constexpr int kTileCost = 12;
 
-// Tile `slot` of XCD `xcd`'s share; false past its end. The tiles of all groups are listed
-// group after group and each XCD takes a contiguous eighth of the list; within a group,
-// blocks of kColBlock tile columns, rows outer and the block's columns inner, so that the
-// tiles an XCD runs together share rows of a and columns of b in its L2.
+// The groups' bounds and tile counts (inclusive sums), and the XCD's share of the tiles. The
+// tiles of all groups are listed group after group and each XCD takes a contiguous eighth of
+// the list, by count, or, in TN, where a tile's work goes with its group's rows, by work;
+// within a group, blocks of kColBlock tile columns, rows outer and the block's columns
+// inner, so that the tiles an XCD runs together share rows of a and columns of b in its L2.
+struct Groups {  // lane e: group e
+  int start, end, incl;
+};
+
 template <class G>
-__device__ __forceinline__ bool locate(const MatmulArgs& a, int64_t bid, TileAt& t) {
+__device__ __forceinline__ void make_groups(const MatmulArgs& a, int xcd, Groups& g, int& lo, int& hi) {
   const int lane = threadIdx.x & 63;
   const int NT = (int)((a.N + G::BN - 1) / G::BN);
   int start, end;
   group_bounds(a.offsets, a.E, (int)a.R, start, end);
-  const int mts = G::TN ? (lane < a.E ? (int)((a.K + G::BM - 1) / G::BM) : 0) : (end - start + G::BM - 1) / G::BM;
-  int64_t incl = (int64_t)mts * NT;
+  const int mts = G::TN ? (lane < a.E ? (int)((a.K + G::BM - 1) / G::BM) : 0)
+                        : (end - start + G::BM - 1) / G::BM;
+  const int tiles = mts * NT;
+  const int64_t cost = G::TN ? (end - start + G::BK - 1) / G::BK + kTileCost : 1;
+  int incl = tiles;
+  int64_t work = tiles * cost;  // inclusive sum
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int64_t v = __shfl_up(incl, o);
-    if (lane >= o) incl += v;
+    const int v = __shfl_up(incl, o);
+    const int64_t u = __shfl_up(work, o);
+    if (lane >= o) {
+      incl += v;
+      work += u;
+    }
   }
-  const int64_t total = __shfl(incl, 63);
-  const int xcd = (int)(bid % kXcds);
-  const int64_t lo = total * xcd / kXcds, hi = total * (xcd + 1) / kXcds;
-  const int64_t i = lo + bid / kXcds;
-  if (i >= hi) return false;
-  const uint64_t past = __ballot(incl > i);
+  const int64_t all = __shfl(work, 63), before = work - tiles * cost;
+  // tiles that begin before the x-th eighth of the work
+  auto first = [&](int x) {
+    const int64_t left = all * x / kXcds - before;
+    int n = left <= 0 ? 0 : (int)min((int64_t)tiles, (left + cost - 1) / cost);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
+    return n;
+  };
+  lo = __builtin_amdgcn_readfirstlane(first(xcd));
+  hi = __builtin_amdgcn_readfirstlane(first(xcd + 1));
+  g = Groups{start, end, incl};
+}
+
+template <class G>
+__device__ __forceinline__ Item locate(const MatmulArgs& a, const Groups& g, int i) {
+  Item t;
+  const int NT = (int)((a.N + G::BN - 1) / G::BN);
+  const uint64_t past = __ballot(g.incl > i);
   t.e = __ffsll((unsigned long long)past) - 1;
-  const int m = __shfl(mts, t.e);
-  const int in = (int)(i - (__shfl(incl, t.e) - (int64_t)m * NT));
-  t.r0 = __shfl(start, t.e);
-  t.r1 = __shfl(end, t.e);
+  t.r0 = __builtin_amdgcn_readlane(g.start, t.e);
+  t.r1 = __builtin_amdgcn_readlane(g.end, t.e);
+  const int m = G::TN ? (int)((a.K + G::BM - 1) / G::BM) : (t.r1 - t.r0 + G::BM - 1) / G::BM;
+  const int in = i - (__builtin_amdgcn_readlane(g.incl, t.e) - m * NT);
   const int blk = in / (m * kColBlock), cols = min(kColBlock, NT - blk * kColBlock);
   const int at = in - blk * m * kColBlock;
   t.mt = at / cols;
   t.nt = blk * kColBlock + at % cols;
-  return true;
+  return t;
 }
 
-__device__ __forceinline__ int64_t gathered(const int32_t* g, int64_t r, int64_t rows) {
-  return g ? min(max((int64_t)g[r], (int64_t)0), rows - 1) : r;
+// TN: row indices of a ring turn (four stages, 128 rows) of a group: a wave loads 8 of each
+// stage's 32 rows, so lane l < 32 holds a's row of stage l / 8, place l % 8, and lane 32 + l
+// b's. Rows past the group's end give its last one again.
+template <class G>
+__device__ __forceinline__ int fetch_turn(const MatmulArgs& a, const Item& t, int turn, int wave, int lane) {
+  if constexpr (G::TN) {
+    static_assert(G::BK == 32, "32 rows per stage");
+    const int64_t at = (int64_t)t.r0 + (int64_t)turn * 128 + (lane & 31) / 8 * 32 + wave * 8 + (lane & 7);
+    const int64_t r = max(min(at, (int64_t)t.r1 - 1), (int64_t)0);
+    const bool is_a = lane < 32;
+    const int32_t* g = is_a ? a.gather_a : a.gather_b;
+    const int64_t rows = is_a ? a.rows_a : a.rows_b;
+    return (int)(g ? min(max((int64_t)g[r], (int64_t)0), rows - 1) : r);
+  }
+  return 0;
 }
 
-template <class G, typename TO>
-__global__ __launch_bounds__(256, 1) void matmul_bf16_kernel(MatmulArgs a) {
-  // (an array of its own for each stage: the compiler then sees that the reads of one stage
-  // do not wait for the loads into another)
-  __shared__ __attribute__((aligned(1024))) char s0[G::STAGE], s1[G::STAGE], s2[G::STAGE], s3[G::STAGE];
-  __shared__ int tab[G::TN ? 2 * kTable : 1];
-  char* const ring[kStages] = {s0, s1, s2, s3};
-  TileAt t;
-  if (!locate<G>(a, blockIdx.x, t)) return;
-  t.e = __builtin_amdgcn_readfirstlane(t.e);
-  t.r0 = __builtin_amdgcn_readfirstlane(t.r0);
-  t.r1 = __builtin_amdgcn_readfirstlane(t.r1);
-  t.mt = __builtin_amdgcn_readfirstlane(t.mt);
-  t.nt = __builtin_amdgcn_readfirstlane(t.nt);
-  const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / G::WGN, wn = wave % G::WGN;
-  const int K = (int)a.K, N = (int)a.N;
-  const int m0 = t.mt * G::BM + (G::TN ? 0 : t.r0), n0 = t.nt * G::BN;
-  const int mend = G::TN ? K : t.r1;
+// NN, NT: the rows of a that this lane's loads of a tile read (fetched long before their use).
+template <class G>
+__device__ __forceinline__ void fetch_rows(const MatmulArgs& a, const Item& t, int wave, int lane,
+                                           int (&rows)[G::A::PW]) {
+  if constexpr (!G::TN) {
+    const int ln = here(lane), m0 = t.r0 + t.mt * G::BM;
+#pragma unroll
+    for (int j = 0; j < G::A::PW; ++j) {
+      const int r = min(m0 + G::A::row(j, wave, ln), t.r1 - 1);
+      rows[j] = a.gather_a ? a.gather_a[r] : r;
+    }
+  }
+}
+
+// The item's sources, in `ld`.
+template <class G>
+__device__ __forceinline__ void make_loader(const MatmulArgs& a, const Item& t, int wave, int lane,
+                                            const int (&rows)[G::A::PW], Loader<G>& ld) {
+  const int K = (int)a.K, N = (int)a.N, n0 = t.nt * G::BN;
   const bf16* A = static_cast<const bf16*>(a.a);
   const bf16* B = static_cast<const bf16*>(a.b);
-
-  Wave<G> w;
-#pragma unroll
-  for (int i = 0; i < G::MB; ++i) w.a_at[i] = G::A::frag(wm * G::WM + i * 32, ln);
-#pragma unroll
-  for (int i = 0; i < G::NB; ++i) w.b_at[i] = G::B::frag(wn * G::WN + i * 32, ln);
-#pragma unroll
-  for (int nb = 0; nb < G::NB; ++nb)
-#pragma unroll
-    for (int mb = 0; mb < G::MB; ++mb)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) w.acc[nb][mb][r] = 0.f;
-
-  Loader<G> ld;
+  const int ln = here(lane);
   ld.wave = wave;
-  ld.ln = ln;
+  ld.ln = lane;
   if constexpr (G::TN) {
+    const int m0 = t.mt * G::BM;
+    ld.len = t.r1 - t.r0;
     ld.step_a = K;
     ld.step_b = N;
-    ld.ta = tab;
-    ld.tb = tab + kTable;
 #pragma unroll
     for (int j = 0; j < G::A::PW; ++j) ld.pa[j] = A + min(m0 + G::A::chunk(j, wave, ln) * 8, K - 8);
 #pragma unroll
     for (int j = 0; j < G::B::PW; ++j) ld.pb[j] = B + min(n0 + G::B::chunk(j, wave, ln) * 8, N - 8);
-    for (int r = t.r0; r < t.r1; r += kTable) {
-      __syncthreads();  // the last segment's table is no longer read
-      ld.len = min(kTable, t.r1 - r);
-      const int fill = (ld.len + G::BK - 1) / G::BK * G::BK;
-      for (int i = threadIdx.x; i < fill; i += 256) {
-        const int64_t at = r + min(i, ld.len - 1);
-        tab[i] = (int)gathered(a.gather_a, at, a.rows_a);
-        tab[kTable + i] = (int)gathered(a.gather_b, at, a.rows_b);
-      }
-      __syncthreads();
-      run_stages<G>(ring, ld, w);
-    }
   } else {
     const bf16* Be = B + (size_t)t.e * K * N;
     ld.len = K;
     ld.step_a = G::BK;
 #pragma unroll
     for (int j = 0; j < G::A::PW; ++j)
-      ld.pa[j] = A + (size_t)gathered(a.gather_a, min(m0 + G::A::row(j, wave, ln), t.r1 - 1), a.rows_a) * K +
-                 G::A::chunk(j, wave, ln) * 8;
+      ld.pa[j] = A + (size_t)min(max((int64_t)rows[j], (int64_t)0), a.rows_a - 1) * K + G::A::chunk(j, wave, ln) * 8;
     if constexpr (G::FORM == MOE_MATMUL_NT) {
       ld.step_b = G::BK;
 #pragma unroll
@@ -416,33 +386,185 @@ __global__ __launch_bounds__(256, 1) void matmul_bf16_kernel(MatmulArgs a) {
       for (int j = 0; j < G::B::PW; ++j)
         ld.pb[j] = Be + (size_t)G::B::row(j, wave, ln) * N + min(n0 + G::B::chunk(j, wave, ln) * 8, N - 8);
     }
-    run_stages<G>(ring, ld, w);
   }
+}
 
-  // acc[nb][mb][4 q + i]: row m = lane % 32 of block mb, column 8 q + 4 (lane / 32) + i of
-  // block nb
+// Output. acc[nb][mb][4 q + i] is row lane % 32 of block mb, column 8 q + 4 (lane / 32) + i of
+// block nb: stored from there, an instruction would touch 32 rows with 8 or 16 bytes each,
+// and the writes, not their bytes, would bound the tile's end. The 128- and 256-row tiles
+// pass 32 rows at a time through a piece of LDS of the wave's own (16-byte chunk c of a row
+// at c ^ (row % chunks)) and store whole row segments.
+template <class G, typename TO>
+__device__ __forceinline__ void store_tile(const MatmulArgs& a, const Item& t, int wm, int wn, int lane,
+                                           char* buf, const Wave<G>& w) {
+  const int ln = here(lane);
+  const int K = (int)a.K, N = (int)a.N;
+  const int m0 = t.mt * G::BM + (G::TN ? 0 : t.r0) + wm * G::WM, mend = G::TN ? K : t.r1;
+  const int n0 = t.nt * G::BN + wn * G::WN;
   TO* out = static_cast<TO*>(a.out) + (G::TN ? (size_t)t.e * K * N : 0);
+  auto vec = [&](int mb, int nb, int q) {
+    return f32x4{w.acc[nb][mb][4 * q], w.acc[nb][mb][4 * q + 1], w.acc[nb][mb][4 * q + 2],
+                 w.acc[nb][mb][4 * q + 3]};
+  };
+  if constexpr (G::OUT_BYTES == 0) {
 #pragma unroll
-  for (int mb = 0; mb < G::MB; ++mb) {
-    const int m = m0 + wm * G::WM + mb * 32 + (ln & 31);
-    if (m >= mend) continue;
-    TO* row = out + (size_t)m * N;
+    for (int mb = 0; mb < G::MB; ++mb) {
+      const int m = m0 + mb * 32 + (ln & 31);
+      if (m >= mend) continue;
 #pragma unroll
-    for (int nb = 0; nb < G::NB; ++nb)
+      for (int nb = 0; nb < G::NB; ++nb)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = n0 + wn * G::WN + nb * 32 + 8 * q + 4 * (ln >> 5);
-        if (n >= N) continue;  // (N is a multiple of 8)
-        f32x4 v = {w.acc[nb][mb][4 * q], w.acc[nb][mb][4 * q + 1], w.acc[nb][mb][4 * q + 2],
-                   w.acc[nb][mb][4 * q + 3]};
-        if constexpr (sizeof(TO) == 2) {
-          *reinterpret_cast<bf16x4*>(row + n) = __builtin_convertvector(v, bf16x4);
-        } else {
-          if (a.accumulate) v += *reinterpret_cast<const f32x4*>(row + n);
-          *reinterpret_cast<f32x4*>(row + n) = v;
+        for (int q = 0; q < 4; ++q) {
+          const int n = n0 + nb * 32 + 8 * q + 4 * (ln >> 5);
+          if (n >= N) continue;  // (N is a multiple of 4)
+          TO* p = out + (size_t)m * N + n;
+          f32x4 v = vec(mb, nb, q);
+          if constexpr (sizeof(TO) == 2) {
+            *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(v, bf16x4);
+          } else {
+            if (a.accumulate) v += *reinterpret_cast<const f32x4*>(p);
+            *reinterpret_cast<f32x4*>(p) = v;
+          }
+        }
+    }
+  } else {
+    constexpr int SEG = G::OUT_BYTES / 32, CHUNKS = SEG / 16;       // of a row, per pass
+    constexpr int COLS = SEG / (int)sizeof(TO), BLOCKS = COLS / 32; // columns, 32-column blocks
+    constexpr int RPS = 64 / CHUNKS;                                // rows per store instruction
+#pragma unroll
+    for (int mb = 0; mb < G::MB; ++mb)
+#pragma unroll
+      for (int nb0 = 0; nb0 < G::NB; nb0 += BLOCKS) {
+        __builtin_amdgcn_sched_barrier(0);  // (one pass's registers at a time)
+        const int r = ln & 31;
+#pragma unroll
+        for (int nb = 0; nb < BLOCKS; ++nb)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int at = (nb * 32 + 8 * q + 4 * (ln >> 5)) * (int)sizeof(TO);
+            char* p = buf + r * SEG + (((at >> 4) ^ (r % CHUNKS)) << 4) + (at & 15);
+            const f32x4 v = vec(mb, nb0 + nb, q);
+            if constexpr (sizeof(TO) == 2) *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(v, bf16x4);
+            else *reinterpret_cast<f32x4*>(p) = v;
+          }
+#pragma unroll
+        for (int i = 0; i < 32 / RPS; ++i) {
+          const int row = i * RPS + ln / CHUNKS, c = ln % CHUNKS;
+          const int m = m0 + mb * 32 + row, n = n0 + nb0 * 32 + c * (16 / (int)sizeof(TO));
+          u32x4 v = *reinterpret_cast<const u32x4*>(buf + row * SEG + ((c ^ (row % CHUNKS)) << 4));
+          if (m >= mend || n >= N) continue;  // (N is a multiple of a chunk)
+          TO* p = out + (size_t)m * N + n;
+          if constexpr (sizeof(TO) == 4) {
+            if (a.accumulate)
+              v = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, v) + *reinterpret_cast<const f32x4*>(p));
+          }
+          *reinterpret_cast<u32x4*>(p) = v;
         }
       }
   }
+}
+
+// Workgroups take their XCD's tiles in strides of the XCD's workgroups, as one stream of
+// stages: the last ring turn of an item loads the first one of the next.
+template <class G, typename TO>
+__global__ __launch_bounds__(256, 1) void matmul_bf16_kernel(MatmulArgs a) {
+  // (an array of its own for each stage: the compiler then sees that the reads of one stage
+  // do not wait for the loads into another)
+  __shared__ __attribute__((aligned(1024))) char s0[G::STAGE], s1[G::STAGE], s2[G::STAGE], s3[G::STAGE];
+  __shared__ __attribute__((aligned(1024))) char outs[G::OUT_BYTES ? 4 * G::OUT_BYTES : 16];
+  char* const ring[kStages] = {s0, s1, s2, s3};
+  const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / G::WGN, wn = wave % G::WGN;
+  const int slots = gridDim.x / kXcds;
+  Groups groups;
+  int lo, hi;
+  make_groups<G>(a, blockIdx.x % kXcds, groups, lo, hi);
+  int i = lo + blockIdx.x / kXcds;
+  if (i >= hi) return;
+
+  Wave<G> w;
+#pragma unroll
+  for (int j = 0; j < G::MB; ++j) w.a_at[j] = G::A::frag(wm * G::WM + j * 32, ln);
+#pragma unroll
+  for (int j = 0; j < G::NB; ++j) w.b_at[j] = G::B::frag(wn * G::WN + j * 32, ln);
+  Loader<G> ld;
+  int rows[G::A::PW];  // NN, NT: rows of a of the next tile's loads
+  Item t = locate<G>(a, groups, i);
+  fetch_rows<G>(a, t, wave, ln, rows);
+  make_loader<G>(a, t, wave, ln, rows, ld);
+  Frags<G> F0, F1;
+  // TN: row indices of the turn whose loads come next, and of the next tile's first turn
+  int turn = fetch_turn<G>(a, t, 0, wave, ln), turn_first = 0;
+#pragma unroll
+  for (int q = 0; q < kStages; ++q)
+#pragma unroll
+    for (int j = 0; j < G::LPS; ++j) ld.template issue<true>(j, q, turn, q, ring[q]);
+  wait_vmcnt<(kStages - 1) * G::LPS>();
+  sync_point();
+#pragma unroll
+  for (int r = 0; r < G::SUB * (G::MB + G::NB); ++r) w.read(r, ring[0], F0);
+  turn = fetch_turn<G>(a, t, 1, wave, ln);
+
+  for (;;) {
+#pragma unroll
+    for (int nb = 0; nb < G::NB; ++nb)
+#pragma unroll
+      for (int mb = 0; mb < G::MB; ++mb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) w.acc[nb][mb][r] = 0.f;
+    const Item cur = t;
+    const int len = ld.len, nk = (len + G::BK - 1) / G::BK, whole = len / G::BK;
+    const int end = max((nk + kStages - 1) / kStages, 1) * kStages;  // whole ring turns
+    i += slots;
+    const bool more = i < hi;
+    if (more) t = locate<G>(a, groups, i);
+    fetch_rows<G>(a, t, wave, ln, rows);
+    turn_first = fetch_turn<G>(a, t, 0, wave, ln);
+
+    mask_first<G>(F0, len, ln);
+    int kt = 0;
+#define MOE_STEP(J, CLAMP, RS)                                                                   \
+  Step<G, J, CLAMP>::wait();                                                                     \
+  Step<G, J, CLAMP>::template body<true>(RS, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1)
+    for (; kt + 2 * kStages <= whole && kt + kStages < end; kt += kStages) {
+      const int now = turn;
+      turn = fetch_turn<G>(a, cur, kt / kStages + 2, wave, ln);
+      MOE_STEP(0, false, kt + 4);
+      MOE_STEP(1, false, kt + 5);
+      MOE_STEP(2, false, kt + 6);
+      MOE_STEP(3, false, kt + 7);
+    }
+    if (kt + kStages < end) {  // the refills end past len
+      const int now = turn;
+      MOE_STEP(0, true, kt + 4);
+      MOE_STEP(1, true, kt + 5);
+      MOE_STEP(2, true, kt + 6);
+      MOE_STEP(3, true, kt + 7);
+      kt += kStages;
+      if ((kt + 1) * G::BK > len) mask_frags<G>(F0, len - kt * G::BK, ln);
+    }
+    // the last turn: the next item's first stages (without one, this item's, never used)
+    if (more) make_loader<G>(a, t, wave, ln, rows, ld);
+    const int now = turn_first;
+    turn = fetch_turn<G>(a, t, 1, wave, ln);
+#define MOE_LAST(J)                                                                              \
+  Step<G, J, true>::wait();                                                                      \
+  if (kt + J < nk)                                                                               \
+    Step<G, J, true>::template body<true>(J, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1); \
+  else                                                                                           \
+    Step<G, J, true>::template body<false>(J, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1); \
+  if (J < 3 && kt + J + 1 < nk && (kt + J + 2) * G::BK > len)                                    \
+    mask_frags<G>((J) % 2 ? F0 : F1, len - (kt + J + 1) * G::BK, ln);
+    MOE_LAST(0)
+    MOE_LAST(1)
+    MOE_LAST(2)
+    MOE_LAST(3)
+#undef MOE_STEP
+#undef MOE_LAST
+    store_tile<G, TO>(a, cur, wm, wn, ln, outs + wave * G::OUT_BYTES, w);
+    if (!more) break;
+  }
+  wait_vmcnt<0>();  // the loads that nobody reads have landed before the LDS is given back
 }
 
 // ---- fp32 ------------------------------------------------------------------------------
@@ -534,11 +656,12 @@ __global__ __launch_bounds__(256) void matmul_kernel(MatmulArgs a, int mtiles, i
 
 template <class G, typename TO>
 hipError_t launch_bf16(const MatmulArgs& a, hipStream_t s) {
+  // at most as many workgroups as are resident together, a multiple of the XCDs
+  constexpr int64_t resident = kCus * (G::BM == 256 ? 1 : 2);
   const int64_t nt = (a.N + G::BN - 1) / G::BN;
-  // an upper bound of the tiles, and a multiple of the XCDs: every XCD's eighth (rounded up)
   const int64_t mt = G::TN ? a.E * ((a.K + G::BM - 1) / G::BM) : a.R / G::BM + a.E;
   const int64_t blocks = (mt * nt + kXcds - 1) / kXcds * kXcds;
-  matmul_bf16_kernel<G, TO><<<(unsigned)blocks, 256, 0, s>>>(a);
+  matmul_bf16_kernel<G, TO><<<(unsigned)(blocks < resident ? blocks : resident), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
