@@ -254,16 +254,16 @@ struct Item {
 constexpr int kXcds = 8;
 constexpr int kCus = 256;
 constexpr int kColBlock = 4;  // columns of tiles walked together
-// TN: what a tile costs beside its stages (its stores, the pipeline's ends), in stages
-constexpr int kTileCost = 12;
-
-// The groups' bounds and tile counts (inclusive sums), and the XCD's share of the tiles. The
-// tiles of all groups are listed group after group and each XCD takes a contiguous eighth of
-// the list, by count, or, in TN, where a tile's work goes with its group's rows, by work;
-// within a group, blocks of kColBlock tile columns, rows outer and the block's columns
+// The XCD's share of the tiles, lo .. hi of a list.
+// NN, NT (every tile has the same work): the tiles of all groups group after group, of which
+// each XCD takes a contiguous eighth.
+// TN (a tile's work goes with its group's rows): the XCD takes an eighth of every group's
+// tiles, the groups by falling length, so that all XCDs have the same work and the long
+// tiles come first; `list` deals them in alternating order.
+// Within a group, blocks of kColBlock tile columns, rows outer and the block's columns
 // inner, so that the tiles an XCD runs together share rows of a and columns of b in its L2.
-struct Groups {  // lane e: group e
-  int start, end, incl;
+struct Groups {  // lane i: the i-th group of the list
+  int e, start, end, first, incl;  // first: the share's first tile in the group; incl: tiles so far
 };
 
 template <class G>
@@ -272,45 +272,47 @@ __device__ __forceinline__ void make_groups(const MatmulArgs& a, int xcd, Groups
   const int NT = (int)((a.N + G::BN - 1) / G::BN);
   int start, end;
   group_bounds(a.offsets, a.E, (int)a.R, start, end);
-  const int mts = G::TN ? (lane < a.E ? (int)((a.K + G::BM - 1) / G::BM) : 0)
-                        : (end - start + G::BM - 1) / G::BM;
-  const int tiles = mts * NT;
-  const int64_t cost = G::TN ? (end - start + G::BK - 1) / G::BK + kTileCost : 1;
-  int incl = tiles;
-  int64_t work = tiles * cost;  // inclusive sum
+  g = Groups{lane, start, end, 0, 0};
+  int tiles;
+  if constexpr (G::TN) {
+    const int len = lane < a.E ? end - start : -1;
+    int rank = 0;
+    for (int j = 0; j < 64; ++j) {
+      const int other = __builtin_amdgcn_readlane(len, j);
+      rank += other > len || (other == len && j < lane);
+    }
+    g.e = __builtin_amdgcn_ds_permute(4 * rank, lane);
+    g.start = __builtin_amdgcn_ds_permute(4 * rank, start);
+    g.end = __builtin_amdgcn_ds_permute(4 * rank, end);
+    const int64_t n = lane < a.E ? (a.K + G::BM - 1) / G::BM * NT : 0;
+    const int x = (xcd + lane) % kXcds;  // (a group of few tiles: another XCD's for each)
+    g.first = (int)(n * x / kXcds);
+    tiles = (int)(n * (x + 1) / kXcds) - g.first;
+  } else {
+    tiles = (end - start + G::BM - 1) / G::BM * NT;
+  }
+  g.incl = tiles;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(incl, o);
-    const int64_t u = __shfl_up(work, o);
-    if (lane >= o) {
-      incl += v;
-      work += u;
-    }
+    const int v = __shfl_up(g.incl, o);
+    if (lane >= o) g.incl += v;
   }
-  const int64_t all = __shfl(work, 63), before = work - tiles * cost;
-  // tiles that begin before the x-th eighth of the work
-  auto first = [&](int x) {
-    const int64_t left = all * x / kXcds - before;
-    int n = left <= 0 ? 0 : (int)min((int64_t)tiles, (left + cost - 1) / cost);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
-    return n;
-  };
-  lo = __builtin_amdgcn_readfirstlane(first(xcd));
-  hi = __builtin_amdgcn_readfirstlane(first(xcd + 1));
-  g = Groups{start, end, incl};
+  const int64_t all = __builtin_amdgcn_readlane(g.incl, 63);
+  lo = G::TN ? 0 : (int)(all * xcd / kXcds);
+  hi = G::TN ? (int)all : (int)(all * (xcd + 1) / kXcds);
 }
 
 template <class G>
 __device__ __forceinline__ Item locate(const MatmulArgs& a, const Groups& g, int i) {
   Item t;
   const int NT = (int)((a.N + G::BN - 1) / G::BN);
-  const uint64_t past = __ballot(g.incl > i);
-  t.e = __ffsll((unsigned long long)past) - 1;
-  t.r0 = __builtin_amdgcn_readlane(g.start, t.e);
-  t.r1 = __builtin_amdgcn_readlane(g.end, t.e);
+  const int at_group = __ffsll((unsigned long long)__ballot(g.incl > i)) - 1;
+  t.e = __builtin_amdgcn_readlane(g.e, at_group);
+  t.r0 = __builtin_amdgcn_readlane(g.start, at_group);
+  t.r1 = __builtin_amdgcn_readlane(g.end, at_group);
   const int m = G::TN ? (int)((a.K + G::BM - 1) / G::BM) : (t.r1 - t.r0 + G::BM - 1) / G::BM;
-  const int in = i - (__builtin_amdgcn_readlane(g.incl, t.e) - m * NT);
+  const int before = at_group ? __builtin_amdgcn_readlane(g.incl, at_group - 1) : 0;
+  const int in = i - before + __builtin_amdgcn_readlane(g.first, at_group);
   const int blk = in / (m * kColBlock), cols = min(kColBlock, NT - blk * kColBlock);
   const int at = in - blk * m * kColBlock;
   t.mt = at / cols;
@@ -458,7 +460,7 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const Item& t, i
             if (a.accumulate)
               v = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, v) + *reinterpret_cast<const f32x4*>(p));
           }
-          *reinterpret_cast<u32x4*>(p) = v;
+          __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
         }
       }
   }
@@ -479,7 +481,12 @@ __global__ __launch_bounds__(256, 1) void matmul_bf16_kernel(MatmulArgs a) {
   Groups groups;
   int lo, hi;
   make_groups<G>(a, blockIdx.x % kXcds, groups, lo, hi);
-  int i = lo + blockIdx.x / kXcds;
+  // this workgroup's tiles: one of every `slots`; TN: in alternating order, so that who had
+  // the longest of one round has the shortest of the next
+  const int slot = blockIdx.x / kXcds;
+  int round = 0;
+  auto place = [&](int r) { return lo + r * slots + (G::TN && r % 2 ? slots - 1 - slot : slot); };
+  int i = place(0);
   if (i >= hi) return;
 
   Wave<G> w;
@@ -515,7 +522,7 @@ __global__ __launch_bounds__(256, 1) void matmul_bf16_kernel(MatmulArgs a) {
     const Item cur = t;
     const int len = ld.len, nk = (len + G::BK - 1) / G::BK, whole = len / G::BK;
     const int end = max((nk + kStages - 1) / kStages, 1) * kStages;  // whole ring turns
-    i += slots;
+    i = place(++round);
     const bool more = i < hi;
     if (more) t = locate<G>(a, groups, i);
     fetch_rows<G>(a, t, wave, ln, rows);
@@ -669,6 +676,7 @@ template <int FORM, typename TO>
 hipError_t pick(const MatmulArgs& a, hipStream_t s) {
   if constexpr (FORM != MOE_MATMUL_TN) {
     if (a.R <= 32 * (int64_t)a.E) return launch_bf16<Geo<FORM, 32, 128, 64, 1>, TO>(a, s);
+    if (a.K <= 1024) return launch_bf16<Geo<FORM, 128, 128, 32, 2>, TO>(a, s);
   }
   const int64_t mt = FORM == MOE_MATMUL_TN ? a.E * ((a.K + 255) / 256) : a.R / 256 + a.E;
   if (mt * ((a.N + 255) / 256) < 256) return launch_bf16<Geo<FORM, 128, 128, 32, 2>, TO>(a, s);
