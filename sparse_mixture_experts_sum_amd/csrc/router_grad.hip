@@ -5,26 +5,67 @@
 //   dp_e = (dw_j - sum_i dw_i w_i) / S at e = idx_j (or dw_j), + loss_grad E f_e / (k T),
 //   ds_e = p_e (dp_e - sum_c p_c dp_c) + z_loss_grad 2 lse p_e / T;
 //   dx = ds W_g^T (+ the token's expert rows), dW_g = x^T ds, db = sum_t ds.
-// x, dx and the rows are read or written once each, which bounds both passes (HBM).
-// All values and sums are fp32. dW_g and db are summed per chunk of tokens into partial
-// sums and those in chunk order: no atomics, one fixed order.
+// x, dx and the rows are read or written once each (x twice with the z-loss, whose lse takes
+// a dot product first): bound by HBM, and by the launches at small sizes. Four kernels: W_g
+// transposed (z-loss only), ds, then dx and partial sums of dW_g and db side by side in one
+// launch, and the partial sums' sum in chunk order: no atomics, one fixed order.
+//
+// Both products run on the matrix cores. fp32: v_mfma_f32_32x32x2_f32 on the values. bf16:
+// v_mfma_f32_32x32x16_bf16 with ds split into two bf16 terms (ds ~ hi + lo, off by 2^-17 of
+// its size, against the 2^-8 that the bf16 results are rounded to); x and W_g are bf16
+// already. The ds kernel leaves the operands in rows of EP = 32 or 64 experts, zeros past E.
 #include "train_common.h"
 #include "train_kernels.h"
 
 namespace {
 
-constexpr int kTok = 16;     // tokens per workgroup of the ds / dx pass
-// Partial sums of dW_g and db: chunks of tokens, at least kChunk each and at most kChunks.
-constexpr int kChunk = 256, kChunks = 1024;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kTok = 16;     // tokens per workgroup of the ds kernel
+constexpr int kTile = 64;    // tokens that the dW_g workgroups take at a time
+constexpr int kSlab = 128;   // columns of x per dW_g workgroup: 32 per wave
+constexpr int kDxCols = 256; // columns of dx per workgroup: 64 per wave, 32 tokens
+// Partial sums of dW_g and db: at most kChunks chunks of whole tiles of tokens, so that
+// d / kSlab times that many workgroups cover the chip and the partial sums stay small.
+constexpr int kChunks = 32;
 __host__ __device__ inline int64_t chunk_len(int64_t T) {
-  const int64_t n = (T + kChunks - 1) / kChunks;
-  return n < kChunk ? kChunk : n;
+  const int64_t tiles = (T + kTile - 1) / kTile;
+  return (tiles + kChunks - 1) / kChunks * kTile;
+}
+int64_t chunks_of(int64_t T) { return T > 0 ? (T + chunk_len(T) - 1) / chunk_len(T) : 0; }
+int padded_experts(int E) { return E <= 32 ? 32 : 64; }
+
+// Workspace: operand rows of ds (bf16: hi rows, then lo rows; fp32: the values), W_g
+// transposed, the partial sums [chunk][d + 1][E]. Whole 256-byte pieces.
+struct Layout {
+  size_t ds, wt, partial, total;
+};
+Layout layout(int64_t T, int64_t d, int E) {
+  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  Layout l;
+  l.ds = 0;
+  l.wt = up((size_t)T * padded_experts(E) * 4);
+  l.partial = l.wt + up(T > 0 ? (size_t)d * E * 4 : 0);
+  l.total = l.partial + up((size_t)chunks_of(T) * (d + 1) * E * 4);
+  return l;
 }
 
-// ds of the workgroup's 16 tokens into LDS (row stride 64) and dlogits. 16 lanes per token,
-// lane `sub` owning experts sub + 16 i.
-template <typename TI>
-__device__ __forceinline__ void token_ds(const RouteGradArgs& a, int64_t t0, float (&ds)[kTok][64]) {
+__global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* __restrict__ w16,
+                                                        const uint32_t* __restrict__ w32, int d, int E,
+                                                        void* __restrict__ out) {
+  const int i = blockIdx.x * 256 + threadIdx.x;  // (d E <= 2^26)
+  if (i >= d * E) return;
+  const int e = i / d, c = i - e * d;
+  if (w16) static_cast<uint16_t*>(out)[i] = w16[(size_t)c * E + e];
+  else static_cast<uint32_t*>(out)[i] = w32[(size_t)c * E + e];
+}
+
+// ds of 16 tokens, 16 lanes per token, lane `sub` owning experts sub + 16 i: into dlogits
+// and the operand rows.
+template <typename TI, int EP>
+__device__ __forceinline__ void token_ds(const RouteGradArgs& a, const void* wt, int64_t t0) {
   const int tok = threadIdx.x >> 4, sub = threadIdx.x & 15;
   const int64_t t = t0 + tok < a.T ? t0 + tok : a.T - 1;  // (past the end: a copy, not stored)
   const int E = a.E, k = a.k;
@@ -96,97 +137,289 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, int64_t t0, flo
     constexpr int N = Chunk<TI>::N;
     typedef typename Chunk<TI>::vec vec;
     const TI* x = static_cast<const TI*>(a.x) + t * a.d;
-    const TI* W = static_cast<const TI*>(a.Wg) + be;
+    const TI* W = static_cast<const TI*>(wt) + (size_t)be * a.d;
     float s = 0.f;
+#pragma unroll 4
     for (int c = sub * N; c < a.d; c += 16 * N) {
-      const vec v = *reinterpret_cast<const vec*>(x + c);
+      const vec v = *reinterpret_cast<const vec*>(x + c), u = *reinterpret_cast<const vec*>(W + c);
 #pragma unroll
-      for (int i = 0; i < N; ++i) s += (float)v[i] * (float)W[(size_t)(c + i) * E];
+      for (int i = 0; i < N; ++i) s += (float)v[i] * (float)u[i];
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor(s, o);
     if (a.bias) s += a.bias[be];
     zc = a.z_loss_grad * 2.0f * inv_T * (s - logf(best));
   }
+  if (t0 + tok >= a.T) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < EP / 16; ++i) {
     const int e = sub + 16 * i;
-    const float v = p[i] * (dp[i] - mean + zc);
-    ds[tok][e] = v;
-    if (t0 + tok < a.T && e < E) a.dlogits[t * E + e] = v;
+    const float v = p[i] * (dp[i] - mean + zc);  // (0 past E: p is)
+    if (e < E) a.dlogits[t * E + e] = v;
+    if constexpr (sizeof(TI) == 2) {
+      const bf16 hi = (bf16)v, lo = (bf16)(v - (float)hi);
+      static_cast<bf16*>(a.ds)[t * EP + e] = hi;
+      static_cast<bf16*>(a.ds)[(a.T + t) * EP + e] = lo;
+    } else {
+      static_cast<float*>(a.ds)[t * EP + e] = v;
+    }
   }
-  __syncthreads();
 }
 
-template <typename TI>
-__global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
-  __shared__ float ds[kTok][64];
-  for (int64_t t0 = (int64_t)blockIdx.x * kTok; t0 < a.T; t0 += (int64_t)gridDim.x * kTok) {
-  token_ds<TI>(a, t0, ds);
-  if (a.dx) {
-  constexpr int N = Chunk<TI>::N;
-  typedef typename Chunk<TI>::vec vec;
+template <typename TI, int EP>
+__global__ __launch_bounds__(256) void ds_kernel(RouteGradArgs a) {
+  for (int64_t t0 = (int64_t)blockIdx.x * kTok; t0 < a.T; t0 += (int64_t)gridDim.x * kTok)
+    token_ds<TI, EP>(a, a.wt, t0);
+}
+
+// Operands of the two products. A fragment covers 32 indices (lane % 32) and a piece of the
+// summed axis: bf16 16 deep, lanes below 32 the first eight; fp32 two deep, lane / 32 the
+// place. Accumulator value 4 q + i: first operand's index 8 q + 4 (lane / 32) + i, second
+// operand's index lane % 32.
+__device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(float a, float b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 v;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = 0.f;
+  return v;
+}
+
+// dx of 32 tokens (t0 ..) and 64 columns (c0 ..), one wave: ds W_g^T with the columns as the
+// first operand, then through the wave's piece of LDS, so that rows, dx go in whole 16-byte
+// pieces of 32 to 128 contiguous bytes per row.
+template <typename TI, int EP>
+__device__ __forceinline__ void dx_tile(const RouteGradArgs& a, int64_t t0, int c0, float* buf) {
+  const int ln = threadIdx.x & 63, x = ln & 31, h = ln >> 5, E = a.E;
   const TI* W = static_cast<const TI*>(a.Wg);
-  for (int c = threadIdx.x * N; c < a.d; c += 256 * N) {
-    float acc[kTok][N] = {};
-    for (int e = 0; e < a.E; ++e) {
-      float w[N];
+  const int64_t t = min(t0 + x, a.T - 1);
+  f32x16 acc[2] = {zero16(), zero16()};
+  if constexpr (sizeof(TI) == 2) {
+    const bf16* hi = static_cast<const bf16*>(a.ds) + t * EP + 8 * h;
+    const bf16* lo = hi + a.T * EP;
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = (float)W[(size_t)(c + i) * a.E + e];
+    for (int s = 0; s < EP / 16; ++s) {
+      const s16x8 dh = *reinterpret_cast<const s16x8*>(hi + 16 * s);
+      const s16x8 dl = *reinterpret_cast<const s16x8*>(lo + 16 * s);
+      const int e0 = 16 * s + 8 * h;
 #pragma unroll
-      for (int q = 0; q < kTok; ++q)
+      for (int b = 0; b < 2; ++b) {
+        const TI* w = W + (size_t)min(c0 + 32 * b + x, a.d - 1) * E;
+        s16x8 f = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (E % 8 == 0) {
+          if (e0 < E) f = *reinterpret_cast<const s16x8*>(w + e0);
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[q][i] += ds[q][e] * w[i];
-    }
-#pragma unroll
-    for (int q = 0; q < kTok; ++q) {
-      const int64_t t = t0 + q;
-      if (t >= a.T) continue;
-      if (a.rows)
-        for (int j = 0; j < a.k; ++j) {
-          const int r = a.pos[t * a.k + j];
-          if (r < 0 || r >= a.R) continue;
-          const vec v = *reinterpret_cast<const vec*>(static_cast<const TI*>(a.rows) + (size_t)r * a.d + c);
-#pragma unroll
-          for (int i = 0; i < N; ++i) acc[q][i] += (float)v[i];
+          for (int i = 0; i < 8; ++i)
+            if (e0 + i < E) f[i] = reinterpret_cast<const short*>(w)[e0 + i];
         }
-      vec o;
+        acc[b] = mma(f, dh, acc[b]);
+        acc[b] = mma(f, dl, acc[b]);
+      }
+    }
+  } else {
+    // summed in the order e, EP / 2 + e: each lane's values are then consecutive
+    const float* row = static_cast<const float*>(a.ds) + t * EP + h * (EP / 2);
+#pragma unroll 8
+    for (int i = 0; i < EP / 2; ++i) {
+      const int e = h * (EP / 2) + i;
+      const float v = row[i];
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = (TI)acc[q][i];
-      *reinterpret_cast<vec*>(static_cast<TI*>(a.dx) + t * a.d + c) = o;
+      for (int b = 0; b < 2; ++b) {
+        const float f = e < E ? W[(size_t)min(c0 + 32 * b + x, a.d - 1) * E + e] : 0.f;
+        acc[b] = mma(f, v, acc[b]);
+      }
     }
   }
-  }
-  __syncthreads();  // ds is written again
+  // [32 tokens][64 columns], 16-byte piece p of token row r at p ^ (r % 16)
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int p = (32 * b + 8 * q + 4 * h) / 4;
+      *reinterpret_cast<f32x4*>(buf + x * 64 + (p ^ (x & 15)) * 4) =
+          f32x4{acc[b][4 * q], acc[b][4 * q + 1], acc[b][4 * q + 2], acc[b][4 * q + 3]};
+    }
+  constexpr int N = Chunk<TI>::N, PIECES = 64 / N, RPI = 64 / PIECES;
+  typedef typename Chunk<TI>::vec vec;
+  const int c = c0 + (ln % PIECES) * N;
+#pragma unroll
+  for (int it = 0; it < 32 / RPI; ++it) {
+    const int r = it * RPI + ln / PIECES;
+    const int64_t tt = t0 + r;
+    if (tt >= a.T || c >= a.d) continue;
+    vec rows[8];
+    int n = 0;
+    if (a.rows) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = j < a.k ? a.pos[tt * a.k + j] : -1;
+        const bool in = at >= 0 && at < a.R;
+        n |= in << j;
+        if (in) rows[j] = *reinterpret_cast<const vec*>(static_cast<const TI*>(a.rows) + (size_t)at * a.d + c);
+      }
+    }
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const int p = (ln % PIECES) * (N / 4) + i;
+      const f32x4 u = *reinterpret_cast<const f32x4*>(buf + r * 64 + (p ^ (r & 15)) * 4);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[4 * i + q] = u[q];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n >> j & 1) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += (float)rows[j][i];
+      }
+    vec o;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = (TI)v[i];
+    *reinterpret_cast<vec*>(static_cast<TI*>(a.dx) + tt * a.d + c) = o;
   }
 }
 
-// partial[chunk][d + 1][E]: x^T ds over the chunk's tokens, and (row d) the sum of ds.
-template <typename TI>
-__global__ __launch_bounds__(256) void route_wgrad_kernel(RouteGradArgs a) {
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
-  const int64_t t0 = blockIdx.y * chunk_len(a.T);
-  const int64_t t1 = t0 + chunk_len(a.T) < a.T ? t0 + chunk_len(a.T) : a.T;
-  if (c > a.d) return;
-  float acc[16] = {};
-  for (int64_t t = t0; t < t1; ++t) {
-    const float x = c < a.d ? (float)static_cast<const TI*>(a.x)[t * a.d + c] : 1.f;
+// x^T ds over a chunk's tokens for kSlab columns: a wave's 32 columns by EP experts.
+template <typename TI, int EP>
+__device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, int slab, char* lds) {
+  const int tid = threadIdx.x, ln = tid & 63, wave = tid >> 6, x = ln & 31, h = ln >> 5;
+  const int64_t t0 = chunk * chunk_len(a.T), t1 = min(t0 + chunk_len(a.T), a.T);
+  const int c0 = slab * kSlab;
+  constexpr int NE = EP / 32;
+  f32x16 acc[NE];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (part + 4 * i < a.E) acc[i] += x * a.dlogits[t * a.E + part + 4 * i];
+  for (int n = 0; n < NE; ++n) acc[n] = zero16();
+  if constexpr (sizeof(TI) == 2) {
+    // x [64][128], ds hi and lo [64][EP], bf16, read back transposed (a 16-lane group's four
+    // rows give each lane four tokens of one column); 16-byte pieces swizzled by the row
+    char* xs = lds;
+    char* dh = lds + kTile * kSlab * 2;
+    char* dl = dh + kTile * EP * 2;
+    const bf16* X = static_cast<const bf16*>(a.x);
+    const bf16* D = static_cast<const bf16*>(a.ds);
+    auto sw = [](int row, int pieces) { return ((0xCA60 >> (4 * (row & 3))) & 15) % pieces; };
+    auto frag = [&](const char* base, int width, int k0, int col0) {  // rows k0 .. + 15, 32 columns
+      const int g = ln >> 4, r = (ln & 15) >> 2, cc = ln & 3;
+      const int n = col0 + (g & 1) * 16 + 4 * cc, k = k0 + (g >> 1) * 8 + r;
+      const char* p = base + k * width * 2 + ((n >> 3) ^ sw(k, width / 8)) * 16 + ((n >> 2) & 1) * 8;
+      const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+      const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * width * 2));
+      return s16x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+    };
+    for (int64_t t = t0; t < t1; t += kTile) {
+      // tokens past the chunk's end are zeros in both operands
+      u32x4 xv[4], dv[2 * EP / 32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int p = tid + 256 * i, r = p / 16, c = c0 + (p % 16) * 8;
+        xv[i] = t + r < t1 && c < a.d ? ld16(X + (t + r) * a.d + c) : u32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * EP / 32; ++i) {
+        const int p = (tid + 256 * i) % (kTile * EP / 8), r = p / (EP / 8), lo = i >= EP / 32;
+        dv[i] = t + r < t1 ? ld16(D + ((lo ? a.T : 0) + t + r) * EP + (p % (EP / 8)) * 8)
+                           : u32x4{0, 0, 0, 0};
+      }
+      __syncthreads();  // the last tile is no longer read
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int p = tid + 256 * i, r = p / 16;
+        st16(xs + r * kSlab * 2 + ((p % 16) ^ sw(r, 16)) * 16, xv[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * EP / 32; ++i) {
+        const int p = (tid + 256 * i) % (kTile * EP / 8), r = p / (EP / 8), lo = i >= EP / 32;
+        st16((lo ? dl : dh) + r * EP * 2 + ((p % (EP / 8)) ^ sw(r, EP / 8)) * 16, dv[i]);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < kTile / 16; ++s) {
+        const s16x8 f = frag(xs, kSlab, 16 * s, wave * 32);
+#pragma unroll
+        for (int n = 0; n < NE; ++n) {
+          acc[n] = mma(frag(dh, EP, 16 * s, 32 * n), f, acc[n]);
+          acc[n] = mma(frag(dl, EP, 16 * s, 32 * n), f, acc[n]);
+        }
+      }
+    }
+  } else {
+    const float* X = static_cast<const float*>(a.x) + min(c0 + wave * 32 + x, a.d - 1);
+    const float* D = static_cast<const float*>(a.ds) + x;
+    for (int64_t t = t0; t < t1; t += 16) {
+      float xv[8], dv[8][NE];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t tt = t + 2 * i + h;
+        const bool in = tt < t1;
+        xv[i] = in ? X[tt * a.d] : 0.f;
+#pragma unroll
+        for (int n = 0; n < NE; ++n) dv[i][n] = in ? D[tt * EP + 32 * n] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int n = 0; n < NE; ++n) acc[n] = mma(dv[i][n], xv[i], acc[n]);
+    }
   }
-  float* out = a.partial + ((size_t)blockIdx.y * (a.d + 1) + c) * a.E;
+  const int c = c0 + wave * 32 + x;
+  float* out = a.partial + (size_t)chunk * (a.d + 1) * a.E;
+  if (c < a.d) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (part + 4 * i < a.E) out[part + 4 * i] = acc[i];
+    for (int n = 0; n < NE; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int e = 32 * n + 8 * (i / 4) + 4 * h + i % 4;
+        if (e < a.E) out[(size_t)c * a.E + e] = acc[n][i];
+      }
+  }
+  // db's partial sum, in the first slab's workgroup: a wave takes every fourth token
+  if (slab) return;
+  __syncthreads();
+  float* sh = reinterpret_cast<float*>(lds);
+  float v = 0.f;
+  if (ln < a.E) {
+#pragma unroll 4
+    for (int64_t t = t0 + wave; t < t1; t += 4) v += a.dlogits[t * a.E + ln];
+  }
+  sh[tid] = v;
+  __syncthreads();
+  if (tid < a.E) out[(size_t)a.d * a.E + tid] = ((sh[tid] + sh[64 + tid]) + sh[128 + tid]) + sh[192 + tid];
 }
 
+// Workgroups [0, dw_blocks): partial sums of dW_g and db, column slabs within a chunk; the
+// others: dx tiles, columns within 32 tokens.
+template <typename TI, int EP>
+__global__ __launch_bounds__(256) void route_products_kernel(RouteGradArgs a, int dw_blocks) {
+  // dx: 8 KB per wave; dW_g (bf16): x and ds tiles
+  __shared__ __attribute__((aligned(16))) char lds[32768];
+  static_assert(kTile * kSlab * 2 + 2 * kTile * EP * 2 <= 32768, "tiles");
+  if ((int)blockIdx.x < dw_blocks) {
+    const int slabs = (a.d + kSlab - 1) / kSlab;
+    dw_chunk<TI, EP>(a, blockIdx.x / slabs, blockIdx.x % slabs, lds);
+    return;
+  }
+  const int wave = threadIdx.x >> 6;
+  const int64_t cols = (a.d + kDxCols - 1) / kDxCols, tiles = (a.T + 31) / 32 * cols;
+  for (int64_t i = blockIdx.x - dw_blocks; i < tiles; i += gridDim.x - dw_blocks) {
+    const int c0 = (int)(i % cols) * kDxCols + wave * 64;
+    if (c0 < a.d) dx_tile<TI, EP>(a, i / cols * 32, c0, reinterpret_cast<float*>(lds) + wave * 2048);
+  }
+}
+
+// dW_g and db from the partial sums, chunks in order.
 template <typename TI>
-__global__ __launch_bounds__(256) void route_wgrad_sum_kernel(RouteGradArgs a, int64_t chunks) {
+__global__ __launch_bounds__(256) void route_sum_kernel(RouteGradArgs a, int chunks) {
   const size_t n = (size_t)(a.d + 1) * a.E, i = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   float v = 0.f;
-  for (int64_t c = 0; c < chunks; ++c) v += a.partial[c * n + i];
+#pragma unroll 8
+  for (int c = 0; c < chunks; ++c) v += a.partial[c * n + i];
   const size_t nw = (size_t)a.d * a.E;
   if (i < nw) {
     if (a.dWg) static_cast<TI*>(a.dWg)[i] = (TI)v;
@@ -195,33 +428,47 @@ __global__ __launch_bounds__(256) void route_wgrad_sum_kernel(RouteGradArgs a, i
   }
 }
 
-int64_t chunks_of(int64_t T) { return (T + chunk_len(T) - 1) / chunk_len(T); }
+template <typename TI, int EP>
+hipError_t launch(RouteGradArgs a, hipStream_t s) {
+  const Layout l = layout(a.T, a.d, a.E);
+  a.ds = a.ws + l.ds;
+  a.wt = a.ws + l.wt;
+  a.partial = reinterpret_cast<float*>(a.ws + l.partial);
+  const bool dw = a.dWg || a.db;
+  const int chunks = (int)chunks_of(a.T);
+  hipError_t e = hipSuccess;
+  if (a.T > 0) {
+    if (a.z_loss_grad != 0.f) {
+      const bool b16 = sizeof(TI) == 2;
+      transpose_kernel<<<(a.d * a.E + 255) / 256, 256, 0, s>>>(
+          b16 ? static_cast<const uint16_t*>(a.Wg) : nullptr,
+          b16 ? nullptr : static_cast<const uint32_t*>(a.Wg), a.d, a.E, a.wt);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    ds_kernel<TI, EP><<<capped_grid((a.T + kTok - 1) / kTok), 256, 0, s>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int dw_blocks = dw ? chunks * ((a.d + kSlab - 1) / kSlab) : 0;
+    const int64_t dx_blocks = a.dx ? (a.T + 31) / 32 * ((a.d + kDxCols - 1) / kDxCols) : 0;
+    if (dw_blocks || dx_blocks) {
+      route_products_kernel<TI, EP><<<dw_blocks + capped_grid(dx_blocks), 256, 0, s>>>(a, dw_blocks);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+  }
+  if (!dw) return hipSuccess;
+  const size_t n = (size_t)(a.d + 1) * a.E;
+  route_sum_kernel<TI><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, chunks);
+  return hipGetLastError();
+}
 
 template <typename TI>
-hipError_t launch(const RouteGradArgs& a, hipStream_t s) {
-  if (a.T > 0) {
-    route_grad_kernel<TI><<<capped_grid((a.T + kTok - 1) / kTok), 256, 0, s>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (!a.dWg && !a.db) return hipSuccess;
-  const int64_t chunks = chunks_of(a.T);
-  if (chunks > 0) {
-    route_wgrad_kernel<TI><<<dim3(a.d / 64 + 1, (unsigned)chunks), 256, 0, s>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  const size_t n = (size_t)(a.d + 1) * a.E;
-  route_wgrad_sum_kernel<TI><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, chunks);
-  return hipGetLastError();
+hipError_t launch_type(const RouteGradArgs& a, hipStream_t s) {
+  return padded_experts(a.E) == 32 ? launch<TI, 32>(a, s) : launch<TI, 64>(a, s);
 }
 
 }  // namespace
 
-size_t route_grad_workspace(int64_t T, int64_t d, int E) {
-  return (size_t)chunks_of(T) * (size_t)(d + 1) * (size_t)E;
-}
+size_t route_grad_workspace(int64_t T, int64_t d, int E) { return layout(T, d, E).total; }
 
 hipError_t launch_route_grad(const RouteGradArgs& a, hipStream_t s) {
-  return a.bf16 ? launch<bf16>(a, s) : launch<float>(a, s);
+  return a.bf16 ? launch_type<bf16>(a, s) : launch_type<float>(a, s);
 }

@@ -160,7 +160,7 @@ moe_status moe_route_backward_workspace_size(const moe_shape* shape, size_t* byt
   if (!bytes) return MOE_ERR_NULL_ARG;
   const moe_status st = check_route(shape);
   if (st != MOE_OK) return st;
-  *bytes = route_grad_workspace(shape->T, shape->d_model, shape->E) * sizeof(float);
+  *bytes = route_grad_workspace(shape->T, shape->d_model, shape->E);
   return MOE_OK;
 }
 
@@ -210,7 +210,7 @@ moe_status moe_route_backward(const moe_shape* shape, const void* x, const void*
   m.dWg = dW_g;
   m.db = db_g;
   m.dlogits = dlogits;
-  m.partial = static_cast<float*>(ws);
+  m.ws = static_cast<char*>(ws);
   return launched(launch_route_grad(m, stream));
 }
 

@@ -44,9 +44,11 @@ struct RouteGradArgs {
   float loss_grad, z_loss_grad;
   void *dx, *dWg;
   float *db, *dlogits;
-  float* partial;           // workspace: route_grad_workspace floats
+  char* ws;                 // workspace: route_grad_workspace bytes
+  void *ds, *wt;            // pieces of it (set by the launch)
+  float* partial;
 };
-// Floats of workspace: per-chunk partial sums of dW_g and db.
+// Bytes of workspace.
 size_t route_grad_workspace(int64_t T, int64_t d, int E);
 hipError_t launch_route_grad(const RouteGradArgs& a, hipStream_t s);
 
