@@ -246,17 +246,18 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_grad_kernel(
     }
 }
 
-// Column sums of the partials, groups in order: 64 columns per workgroup, four threads per
-// column on a quarter of the groups each, then the quarters in order.
-__global__ __launch_bounds__(256) void norm_grad_sum_kernel(const float* __restrict__ partial,
+// Column sums of the partials: 64 columns per workgroup, sixteen threads per column on a
+// sixteenth of the groups each, in order, then those in order.
+constexpr int kSumParts = 16;
+__global__ __launch_bounds__(64 * kSumParts) void norm_grad_sum_kernel(const float* __restrict__ partial,
                                                             int64_t groups, int d, float* o0,
                                                             float* o1, float* o2) {
-  __shared__ float sh[4][64];
+  __shared__ float sh[kSumParts][64];
   const int which = blockIdx.y;
   float* out = which == 0 ? o0 : which == 1 ? o1 : o2;
   if (!out) return;
   const int c = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
-  const int64_t per = (groups + 3) / 4, g0 = part * per;
+  const int64_t per = (groups + kSumParts - 1) / kSumParts, g0 = part * per;
   const int64_t g1 = g0 + per < groups ? g0 + per : groups;
   float v = 0.f;
   if (c < d) {
@@ -265,8 +266,11 @@ __global__ __launch_bounds__(256) void norm_grad_sum_kernel(const float* __restr
   }
   sh[part][threadIdx.x & 63] = v;
   __syncthreads();
-  if (part == 0 && c < d)
-    out[c] = ((sh[0][threadIdx.x] + sh[1][threadIdx.x]) + sh[2][threadIdx.x]) + sh[3][threadIdx.x];
+  if (part || c >= d) return;
+  v = sh[0][threadIdx.x];
+#pragma unroll
+  for (int i = 1; i < kSumParts; ++i) v += sh[i][threadIdx.x];
+  out[c] = v;
 }
 
 // Workgroups of the gradient: enough rows in flight for HBM, few enough partial sums.
@@ -303,7 +307,7 @@ hipError_t launch_bwd(const NormGradArgs& a, hipStream_t s) {
   if (e != hipSuccess) return e;
   float* chan = a.gate_kind == MOE_GATE_CHANNEL ? a.dgate : nullptr;
   if (!a.dgamma && !a.dgamma_post && !chan) return hipSuccess;
-  norm_grad_sum_kernel<<<dim3((a.d + 63) / 64, 3), 256, 0, s>>>(a.partial, groups, a.d, a.dgamma,
+  norm_grad_sum_kernel<<<dim3((a.d + 63) / 64, 3), 64 * kSumParts, 0, s>>>(a.partial, groups, a.d, a.dgamma,
                                                                a.dgamma_post, chan);
   return hipGetLastError();
 }

@@ -1,7 +1,8 @@
 // Products of rows grouped by expert, with ragged group sizes: NN (a b_e), NT (a b_e^T) and
 // TN (the group's a^T b), fp32 sums.
 //
-// bf16: one workgroup of four waves per BM x BN tile of the output, v_mfma_f32_32x32x16_bf16.
+// One workgroup of four waves per BM x BN tile of the output, v_mfma_f32_32x32x16_bf16 or
+// v_mfma_f32_32x32x2_f32.
 // The summed axis advances in stages of BK through a ring of four LDS buffers filled by
 // direct global -> LDS loads. An operand is either K-contiguous in memory (a of NN and NT,
 // b of NT), and its fragments are 16-byte LDS reads, or K-strided (b of NN, both of TN), and
@@ -51,13 +52,13 @@ __device__ __forceinline__ int here(int v) {
 //   K-strided (KS true): [BK][X], 16-byte slot s of a row stored at s ^ swz(row).
 // Both swizzles make the fragment reads free of bank conflicts. A direct load instruction
 // moves 64 lanes x 16 bytes into 1 KB of LDS, lane l into slot l.
-template <bool KS_, int X_, int BK_, int NW>
+template <typename T, bool KS_, int X_, int BK_, int NW>
 struct Operand {
   static constexpr bool KS = KS_;
-  static constexpr int X = X_, BK = BK_;
-  static constexpr int BYTES = X * BK * 2;
+  static constexpr int X = X_, BK = BK_, EB = sizeof(T), EPC = 16 / EB;  // elements per chunk
+  static constexpr int BYTES = X * BK * EB;
   static constexpr int PW = BYTES / 1024 / NW;         // loads per wave and stage
-  static constexpr int ROW = KS ? X * 2 : BK * 2;      // bytes per LDS row
+  static constexpr int ROW = (KS ? X : BK) * EB;       // bytes per LDS row
   static constexpr int SLOTS = ROW / 16;               // chunks per LDS row
   static constexpr int RPI = 1024 / ROW;               // LDS rows per load instruction
   static_assert(PW >= 1 && BYTES % (1024 * NW) == 0, "whole loads per wave");
@@ -75,36 +76,48 @@ struct Operand {
   }
   // byte offset of this lane's fragment of the 32 rows from x0 (substep 0)
   static __device__ __forceinline__ int frag(int x0, int ln) {
-    if constexpr (KS) {
+    if constexpr (!KS) {
+      const int m = x0 + (ln & 31);
+      return m * ROW + ((ln >> 5) ^ swz(m)) * 16;
+    } else if constexpr (EB == 2) {
       const int g = ln >> 4, r = (ln & 15) >> 2, c = ln & 3;
       const int n = x0 + (g & 1) * 16 + 4 * c, k = (g >> 1) * 8 + r;
       return k * ROW + ((n >> 3) ^ swz(k)) * 16 + ((n >> 2) & 1) * 8;
     } else {
-      const int m = x0 + (ln & 31);
-      return m * ROW + ((ln >> 5) ^ swz(m)) * 16;
+      return (ln >> 5) * 4 * ROW + (x0 + (ln & 31)) * 4;  // (rows 4 h + i, swizzled by i below)
     }
   }
-  // the fragment of substep s (k = 16 s + 8 (lane / 32) .. + 7)
-  static __device__ __forceinline__ s16x8 read(const char* st, int at, int s) {
-    if constexpr (KS) {
+  // The fragment of substep s, 16 bytes. bf16: k = 16 s + 8 h .. + 7 (h = lane / 32); fp32:
+  // k = 8 s + 4 h .. + 3.
+  static __device__ __forceinline__ u32x4 read(const char* st, int at, int s) {
+    if constexpr (!KS) {
+      return *reinterpret_cast<const u32x4*>(st + (at ^ (32 * s)));
+    } else if constexpr (EB == 2) {
       const char* p = st + at + 16 * s * ROW;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ROW));
-      return s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      return __builtin_bit_cast(u32x4, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
     } else {
-      return *reinterpret_cast<const s16x8*>(st + (at ^ (32 * s)));
+      u32x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = *reinterpret_cast<const uint32_t*>(st + (at ^ (swz(i) * 16)) + (8 * s + i) * ROW);
+      return v;
     }
   }
 };
 
 // BM x BN tile, WGM x (4 / WGM) waves.
-template <int FORM_, int BM_, int BN_, int BK_, int WGM>
+template <typename T, int FORM_, int BM_, int BN_, int BK_, int WGM>
 struct Geo {
+  typedef T type;
   static constexpr int FORM = FORM_, BM = BM_, BN = BN_, BK = BK_;
   static constexpr bool TN = FORM == MOE_MATMUL_TN;
-  static constexpr int WGN = 4 / WGM, SUB = BK / 16;
-  typedef Operand<TN, BM, BK, 4> A;
-  typedef Operand<FORM != MOE_MATMUL_NT, BN, BK, 4> B;
+  static constexpr int EPC = 16 / sizeof(T);
+  static constexpr int WGN = 4 / WGM, SUB = BK / (2 * EPC);
+  static constexpr int RW = BK / 4;  // TN: rows of the summed axis that a wave loads per stage
+  typedef Operand<T, TN, BM, BK, 4> A;
+  typedef Operand<T, FORM != MOE_MATMUL_NT, BN, BK, 4> B;
   static constexpr int WM = BM / WGM, WN = BN / WGN, MB = WM / 32, NB = WN / 32;
   static constexpr int STAGE = A::BYTES + B::BYTES, LPS = A::PW + B::PW;
   // LDS of each wave for its output: 32 rows of its columns in bf16 (the 32-row tiles have
@@ -117,53 +130,66 @@ struct Geo {
 // gather's, or the row itself) from the turn's indices.
 template <class G>
 struct Loader {
-  const bf16* pa[G::A::PW];
-  const bf16* pb[G::B::PW];
+  typedef typename G::type T;
+  const T* pa[G::A::PW];
+  const T* pb[G::B::PW];
   size_t step_a, step_b;  // elements per stage (TN: per row)
   int len, wave, ln;
 
-  // Stages may end past len where CLAMP: the last chunk (or row) is then read again.
-  template <class Op, bool CLAMP>
-  __device__ __forceinline__ const bf16* at(const bf16* const* p, size_t step, int j, int kt) const {
-    const bf16* q = p[j] + (size_t)kt * step;
+};
+
+// One operand's address of load j of stage kt (NN, NT). Stages may end past len where CLAMP:
+// the last chunk (or row) is then read again. (Class templates: hipcc's host pass rejects
+// later calls of these as function templates once they are instantiated from two callers.)
+template <class G, class Op, bool CLAMP>
+struct Source {
+  typedef typename G::type T;
+  static __device__ __forceinline__ const T* at(const Loader<G>& ld, const T* p, size_t step, int j, int kt) {
+    const T* q = p + (size_t)kt * step;
     if constexpr (CLAMP) {
-      const int l = here(ln);
-      const int k = kt * G::BK + (Op::KS ? Op::row(j, wave, l) : Op::chunk(j, wave, l) * 8);
-      const int back = min(0, len - (Op::KS ? 1 : 8) - k);
+      const int l = here(ld.ln);
+      const int k = kt * G::BK + (Op::KS ? Op::row(j, ld.wave, l) : Op::chunk(j, ld.wave, l) * G::EPC);
+      const int back = min(0, ld.len - (Op::KS ? 1 : G::EPC) - k);
       q += Op::KS ? (int64_t)back * (int64_t)(step / G::BK) : (int64_t)back;
     }
     return q;
   }
-  // load j (A's, then B's; a constant at every call) of stage kt into st; TN: of the rows
-  // that `turn` holds for ring place q
-  template <bool CLAMP>
-  __device__ __forceinline__ void issue(int j, int kt, int turn, int q, char* st) const {
+};
+
+// Load j (A's, then B's; a constant at every call) of stage kt into st; TN: of the rows that
+// `turn` holds for ring place q.
+template <class G, bool CLAMP>
+struct Issue {
+  typedef typename G::type T;
+  static __device__ __forceinline__ void run(const Loader<G>& ld, int j, int kt, int turn, int q, char* st) {
     const bool is_a = j < G::A::PW;
     const int i = is_a ? j : j - G::A::PW;
-    const bf16* p;
+    const T* p;
     if constexpr (G::TN) {
       // the rows of one load instruction are consecutive lanes of `turn`
-      constexpr int RPI = 8 / G::A::PW;
-      static_assert(G::A::RPI == RPI && G::B::RPI == RPI, "eight rows per wave and stage");
-      const int l0 = (is_a ? 0 : 32) + q * 8 + i * RPI, mine = ln / (64 / RPI);
+      constexpr int RPI = G::A::RPI;
+      static_assert(RPI * G::A::PW == G::RW && G::B::RPI == RPI && G::B::PW == G::A::PW, "rows per wave");
+      const int l0 = (is_a ? 0 : 32) + q * G::RW + i * RPI, mine = ld.ln / (64 / RPI);
       int row = __builtin_amdgcn_readlane(turn, l0);
 #pragma unroll
       for (int r = 1; r < RPI; ++r) {
         const int v = __builtin_amdgcn_readlane(turn, l0 + r);
         row = mine >= r ? v : row;
       }
-      p = is_a ? pa[i] + (int64_t)row * (int64_t)step_a : pb[i] + (int64_t)row * (int64_t)step_b;
+      p = is_a ? ld.pa[i] + (int64_t)row * (int64_t)ld.step_a : ld.pb[i] + (int64_t)row * (int64_t)ld.step_b;
     } else {
-      p = is_a ? at<typename G::A, CLAMP>(pa, step_a, i, kt) : at<typename G::B, CLAMP>(pb, step_b, i, kt);
+      p = is_a ? Source<G, typename G::A, CLAMP>::at(ld, ld.pa[i], ld.step_a, i, kt)
+               : Source<G, typename G::B, CLAMP>::at(ld, ld.pb[i], ld.step_b, i, kt);
     }
-    char* to = is_a ? st + (wave * G::A::PW + i) * 1024 : st + G::A::BYTES + (wave * G::B::PW + i) * 1024;
+    char* to = is_a ? st + (ld.wave * G::A::PW + i) * 1024
+                    : st + G::A::BYTES + (ld.wave * G::B::PW + i) * 1024;
     __builtin_amdgcn_global_load_lds(p, (lds_void*)to, 16, 0, 0);
   }
 };
 
 template <class G>
 struct Frags {
-  s16x8 a[G::SUB][G::MB], b[G::SUB][G::NB];
+  u32x4 a[G::SUB][G::MB], b[G::SUB][G::NB];
 };
 
 template <class G>
@@ -177,11 +203,19 @@ struct Wave {
     if (i < G::MB) F.a[s][i] = G::A::read(st, a_at[i], s);
     else F.b[s][i - G::MB] = G::B::read(st + G::A::BYTES, b_at[i - G::MB], s);
   }
+  // one fragment of each operand (fp32: four instructions, two deep each)
   __device__ __forceinline__ void mfma(int i, const Frags<G>& F) {
     const int s = i / (G::NB * G::MB), nb = i / G::MB % G::NB, mb = i % G::MB;
-    acc[nb][mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-        __builtin_bit_cast(bf16x8, F.b[s][nb]), __builtin_bit_cast(bf16x8, F.a[s][mb]), acc[nb][mb],
-        0, 0, 0);
+    if constexpr (sizeof(typename G::type) == 2) {
+      acc[nb][mb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+          __builtin_bit_cast(bf16x8, F.b[s][nb]), __builtin_bit_cast(bf16x8, F.a[s][mb]), acc[nb][mb],
+          0, 0, 0);
+    } else {
+      const f32x4 b = __builtin_bit_cast(f32x4, F.b[s][nb]), a = __builtin_bit_cast(f32x4, F.a[s][mb]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[nb][mb] = __builtin_amdgcn_mfma_f32_32x32x2f32(b[j], a[j], acc[nb][mb], 0, 0, 0);
+    }
   }
 };
 
@@ -190,16 +224,17 @@ template <class G>
 __device__ __forceinline__ void mask_frags(Frags<G>& F, int left, int ln) {
 #pragma unroll
   for (int s = 0; s < G::SUB; ++s) {
-    const int v = left - 16 * s - 8 * (ln >> 5);  // of this lane's 8
+    const int v = left - G::EPC * (2 * s + (ln >> 5));  // of this lane's EPC
     u32x4 m;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m[j] = v >= 2 * j + 2 ? ~0u : v == 2 * j + 1 ? 0xffffu : 0u;
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (G::EPC == 8) m[j] = v >= 2 * j + 2 ? ~0u : v == 2 * j + 1 ? 0xffffu : 0u;
+      else m[j] = v > j ? ~0u : 0u;
+    }
 #pragma unroll
-    for (int i = 0; i < G::MB; ++i)
-      F.a[s][i] = __builtin_bit_cast(s16x8, __builtin_bit_cast(u32x4, F.a[s][i]) & m);
+    for (int i = 0; i < G::MB; ++i) F.a[s][i] &= m;
 #pragma unroll
-    for (int i = 0; i < G::NB; ++i)
-      F.b[s][i] = __builtin_bit_cast(s16x8, __builtin_bit_cast(u32x4, F.b[s][i]) & m);
+    for (int i = 0; i < G::NB; ++i) F.b[s][i] &= m;
   }
 }
 
@@ -211,12 +246,20 @@ __device__ __forceinline__ void mask_frags(Frags<G>& F, int left, int ln) {
 // Every step loads and reads the same amounts, so that the loads in flight are known at
 // every wait: past an item's last stage the refills are the next item's first stages, and an
 // item is a whole number of ring turns, whose spare stages (CALC false) skip the MFMAs.
-template <class G, int J, bool CLAMP>
+template <class G>
+struct Wait {
+  static __device__ __forceinline__ void run() {
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<(kStages - 2) * G::LPS>();
+    wait_lgkmcnt0();
+    sync_point();
+  }
+};
+template <class G, int J, bool CLAMP, bool CALC>
 struct Step {
-  template <bool CALC>
-  static __device__ __forceinline__ void body(int rs, int turn, char* const (&ring)[kStages],
-                                              const Loader<G>& ld, Wave<G>& w, Frags<G>& Fc,
-                                              Frags<G>& Fn) {
+  static __device__ __forceinline__ void run(int rs, int turn, char* const (&ring)[kStages],
+                                             const Loader<G>& ld, Wave<G>& w, Frags<G>& Fc,
+                                             Frags<G>& Fn) {
     constexpr int NM = G::SUB * G::NB * G::MB, NR = G::SUB * (G::MB + G::NB), NG = G::LPS;
     const char* src = ring[(J + 1) % kStages];
     char* const dst = ring[J];
@@ -228,15 +271,9 @@ struct Step {
       }
 #pragma unroll
       for (int r = NR * g / NG; r < NR * (g + 1) / NG; ++r) w.read(r, src, Fn);
-      ld.template issue<CLAMP>(g, rs, turn, J, dst);
+      Issue<G, CLAMP>::run(ld, g, rs, turn, J, dst);
       __builtin_amdgcn_sched_barrier(0);
     }
-  }
-  static __device__ __forceinline__ void wait() {
-    __builtin_amdgcn_sched_barrier(0);
-    wait_vmcnt<(kStages - 2) * G::LPS>();
-    wait_lgkmcnt0();
-    sync_point();
   }
 };
 
@@ -320,14 +357,16 @@ __device__ __forceinline__ Item locate(const MatmulArgs& a, const Groups& g, int
   return t;
 }
 
-// TN: row indices of a ring turn (four stages, 128 rows) of a group: a wave loads 8 of each
-// stage's 32 rows, so lane l < 32 holds a's row of stage l / 8, place l % 8, and lane 32 + l
-// b's. Rows past the group's end give its last one again.
+// TN: row indices of a ring turn (four stages) of a group: a wave loads RW of each stage's BK
+// rows, so lane l < 4 RW holds a's row of stage l / RW, place l % RW, and lane 32 + l b's.
+// Rows past the group's end give its last one again.
 template <class G>
 __device__ __forceinline__ int fetch_turn(const MatmulArgs& a, const Item& t, int turn, int wave, int lane) {
   if constexpr (G::TN) {
-    static_assert(G::BK == 32, "32 rows per stage");
-    const int64_t at = (int64_t)t.r0 + (int64_t)turn * 128 + (lane & 31) / 8 * 32 + wave * 8 + (lane & 7);
+    static_assert(kStages * G::RW <= 32, "a turn's rows in half a wave");
+    const int l = (lane & 31) % (kStages * G::RW);
+    const int64_t at = (int64_t)t.r0 + (int64_t)turn * (kStages * G::BK) + l / G::RW * G::BK +
+                       wave * G::RW + l % G::RW;
     const int64_t r = max(min(at, (int64_t)t.r1 - 1), (int64_t)0);
     const bool is_a = lane < 32;
     const int32_t* g = is_a ? a.gather_a : a.gather_b;
@@ -356,8 +395,10 @@ template <class G>
 __device__ __forceinline__ void make_loader(const MatmulArgs& a, const Item& t, int wave, int lane,
                                             const int (&rows)[G::A::PW], Loader<G>& ld) {
   const int K = (int)a.K, N = (int)a.N, n0 = t.nt * G::BN;
-  const bf16* A = static_cast<const bf16*>(a.a);
-  const bf16* B = static_cast<const bf16*>(a.b);
+  typedef typename G::type T;
+  constexpr int C = G::EPC;
+  const T* A = static_cast<const T*>(a.a);
+  const T* B = static_cast<const T*>(a.b);
   const int ln = here(lane);
   ld.wave = wave;
   ld.ln = lane;
@@ -367,26 +408,26 @@ __device__ __forceinline__ void make_loader(const MatmulArgs& a, const Item& t, 
     ld.step_a = K;
     ld.step_b = N;
 #pragma unroll
-    for (int j = 0; j < G::A::PW; ++j) ld.pa[j] = A + min(m0 + G::A::chunk(j, wave, ln) * 8, K - 8);
+    for (int j = 0; j < G::A::PW; ++j) ld.pa[j] = A + min(m0 + G::A::chunk(j, wave, ln) * C, K - C);
 #pragma unroll
-    for (int j = 0; j < G::B::PW; ++j) ld.pb[j] = B + min(n0 + G::B::chunk(j, wave, ln) * 8, N - 8);
+    for (int j = 0; j < G::B::PW; ++j) ld.pb[j] = B + min(n0 + G::B::chunk(j, wave, ln) * C, N - C);
   } else {
-    const bf16* Be = B + (size_t)t.e * K * N;
+    const T* Be = B + (size_t)t.e * K * N;
     ld.len = K;
     ld.step_a = G::BK;
 #pragma unroll
     for (int j = 0; j < G::A::PW; ++j)
-      ld.pa[j] = A + (size_t)min(max((int64_t)rows[j], (int64_t)0), a.rows_a - 1) * K + G::A::chunk(j, wave, ln) * 8;
+      ld.pa[j] = A + (size_t)min(max((int64_t)rows[j], (int64_t)0), a.rows_a - 1) * K + G::A::chunk(j, wave, ln) * C;
     if constexpr (G::FORM == MOE_MATMUL_NT) {
       ld.step_b = G::BK;
 #pragma unroll
       for (int j = 0; j < G::B::PW; ++j)
-        ld.pb[j] = Be + (size_t)min(n0 + G::B::row(j, wave, ln), N - 1) * K + G::B::chunk(j, wave, ln) * 8;
+        ld.pb[j] = Be + (size_t)min(n0 + G::B::row(j, wave, ln), N - 1) * K + G::B::chunk(j, wave, ln) * C;
     } else {
       ld.step_b = (size_t)G::BK * N;
 #pragma unroll
       for (int j = 0; j < G::B::PW; ++j)
-        ld.pb[j] = Be + (size_t)G::B::row(j, wave, ln) * N + min(n0 + G::B::chunk(j, wave, ln) * 8, N - 8);
+        ld.pb[j] = Be + (size_t)G::B::row(j, wave, ln) * N + min(n0 + G::B::chunk(j, wave, ln) * C, N - C);
     }
   }
 }
@@ -469,7 +510,7 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const Item& t, i
 // Workgroups take their XCD's tiles in strides of the XCD's workgroups, as one stream of
 // stages: the last ring turn of an item loads the first one of the next.
 template <class G, typename TO>
-__global__ __launch_bounds__(256, 1) void matmul_bf16_kernel(MatmulArgs a) {
+__global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
   // (an array of its own for each stage: the compiler then sees that the reads of one stage
   // do not wait for the loads into another)
   __shared__ __attribute__((aligned(1024))) char s0[G::STAGE], s1[G::STAGE], s2[G::STAGE], s3[G::STAGE];
@@ -505,7 +546,7 @@ __global__ __launch_bounds__(256, 1) void matmul_bf16_kernel(MatmulArgs a) {
 #pragma unroll
   for (int q = 0; q < kStages; ++q)
 #pragma unroll
-    for (int j = 0; j < G::LPS; ++j) ld.template issue<true>(j, q, turn, q, ring[q]);
+    for (int j = 0; j < G::LPS; ++j) Issue<G, true>::run(ld, j, q, turn, q, ring[q]);
   wait_vmcnt<(kStages - 1) * G::LPS>();
   sync_point();
 #pragma unroll
@@ -530,9 +571,9 @@ __global__ __launch_bounds__(256, 1) void matmul_bf16_kernel(MatmulArgs a) {
 
     mask_first<G>(F0, len, ln);
     int kt = 0;
-#define MOE_STEP(J, CLAMP, RS)                                                                   \
-  Step<G, J, CLAMP>::wait();                                                                     \
-  Step<G, J, CLAMP>::template body<true>(RS, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1)
+#define MOE_STEP(J, CLAMP, RS) \
+  Wait<G>::run();              \
+  Step<G, J, CLAMP, true>::run(RS, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1)
     for (; kt + 2 * kStages <= whole && kt + kStages < end; kt += kStages) {
       const int now = turn;
       turn = fetch_turn<G>(a, cur, kt / kStages + 2, wave, ln);
@@ -554,13 +595,13 @@ __global__ __launch_bounds__(256, 1) void matmul_bf16_kernel(MatmulArgs a) {
     if (more) make_loader<G>(a, t, wave, ln, rows, ld);
     const int now = turn_first;
     turn = fetch_turn<G>(a, t, 1, wave, ln);
-#define MOE_LAST(J)                                                                              \
-  Step<G, J, true>::wait();                                                                      \
-  if (kt + J < nk)                                                                               \
-    Step<G, J, true>::template body<true>(J, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1); \
-  else                                                                                           \
-    Step<G, J, true>::template body<false>(J, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1); \
-  if (J < 3 && kt + J + 1 < nk && (kt + J + 2) * G::BK > len)                                    \
+#define MOE_LAST(J)                                                                             \
+  Wait<G>::run();                                                                               \
+  if (kt + J < nk)                                                                              \
+    Step<G, J, true, true>::run(J, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1);     \
+  else                                                                                          \
+    Step<G, J, true, false>::run(J, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1);    \
+  if (J < 3 && kt + J + 1 < nk && (kt + J + 2) * G::BK > len)                                   \
     mask_frags<G>((J) % 2 ? F0 : F1, len - (kt + J + 1) * G::BK, ln);
     MOE_LAST(0)
     MOE_LAST(1)
@@ -574,141 +615,42 @@ __global__ __launch_bounds__(256, 1) void matmul_bf16_kernel(MatmulArgs a) {
   wait_vmcnt<0>();  // the loads that nobody reads have landed before the LDS is given back
 }
 
-// ---- fp32 ------------------------------------------------------------------------------
-// One workgroup per 64 x 64 tile of the output, 16 of the summed axis at a time through LDS.
-constexpr int kT = 64, kK = 16;
-
-// The tile of a workgroup: group e, summed range / output rows.
-template <typename TI, typename TO, int FORM>
-__global__ __launch_bounds__(256) void matmul_kernel(MatmulArgs a, int mtiles, int ntiles) {
-  __shared__ float As[kK][kT + 1], Bs[kK][kT + 1];
-  __shared__ int sh[4];
-  const int tid = threadIdx.x, R = (int)a.R, K = (int)a.K, N = (int)a.N;
-  const int nt = blockIdx.x % ntiles, mt = blockIdx.x / ntiles;
-  int start, end;
-  group_bounds(a.offsets, a.E, R, start, end);
-  if (FORM == MOE_MATMUL_TN) {
-    if (tid == mt / mtiles) { sh[0] = start; sh[1] = end; }
-  } else {
-    // tile mt of the groups' row tiles, group after group
-    const int tiles = (end - start + kT - 1) / kT;
-    int incl = tiles;
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o);
-      if ((tid & 63) >= o) incl += v;
-    }
-    if (tid == 0) sh[2] = -1;
-    __syncthreads();
-    if (tid < a.E && mt >= incl - tiles && mt < incl) {
-      sh[0] = start + (mt - (incl - tiles)) * kT;
-      sh[1] = end;
-      sh[2] = tid;
-    }
-  }
-  __syncthreads();
-  const int e = FORM == MOE_MATMUL_TN ? mt / mtiles : sh[2];
-  if (e < 0) return;
-  const int r0 = sh[0], r1 = sh[1], n0 = nt * kT;
-  const int m0 = FORM == MOE_MATMUL_TN ? (mt % mtiles) * kT : r0;  // first output row
-  const int len = FORM == MOE_MATMUL_TN ? r1 - r0 : K;             // summed
-  const int mend = FORM == MOE_MATMUL_TN ? K : r1;
-  const TI* A = static_cast<const TI*>(a.a);
-  const TI* B = static_cast<const TI*>(a.b) + (FORM == MOE_MATMUL_TN ? 0 : (size_t)e * K * N);
-  auto arow = [&](int r) -> int64_t {
-    return a.gather_a ? min(max((int64_t)a.gather_a[r], (int64_t)0), a.rows_a - 1) : r;
-  };
-  auto brow = [&](int r) -> int64_t {
-    return a.gather_b ? min(max((int64_t)a.gather_b[r], (int64_t)0), a.rows_b - 1) : r;
-  };
-  float acc[4][4] = {};
-  const int tx = tid % 16, ty = tid / 16;
-  for (int k0 = 0; k0 < len; k0 += kK) {
-    for (int i = tid; i < kK * kT; i += 256) {
-      if (FORM == MOE_MATMUL_TN) {
-        const int kk = i / kT, m = i % kT;
-        const bool in = k0 + kk < len;
-        As[kk][m] = in && m0 + m < K ? (float)A[arow(r0 + k0 + kk) * K + m0 + m] : 0.f;
-        Bs[kk][m] = in && n0 + m < N ? (float)B[brow(r0 + k0 + kk) * N + n0 + m] : 0.f;
-      } else {
-        const int kk = i % kK, m = i / kK;
-        const bool in = k0 + kk < len;
-        As[kk][m] = in && m0 + m < r1 ? (float)A[arow(m0 + m) * K + k0 + kk] : 0.f;
-        if (FORM == MOE_MATMUL_NT) {
-          Bs[kk][m] = in && n0 + m < N ? (float)B[(size_t)(n0 + m) * K + k0 + kk] : 0.f;
-        } else {
-          const int kb = i / kT, n = i % kT;
-          Bs[kb][n] = k0 + kb < len && n0 + n < N ? (float)B[(size_t)(k0 + kb) * N + n0 + n] : 0.f;
-        }
-      }
-    }
-    __syncthreads();
-    for (int kk = 0; kk < kK; ++kk)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += As[kk][ty + 16 * i] * Bs[kk][tx + 16 * j];
-    __syncthreads();
-  }
-  TO* out = static_cast<TO*>(a.out) + (FORM == MOE_MATMUL_TN ? (size_t)e * K * N : 0);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= mend || n >= N) continue;
-      TO* o = out + (size_t)m * N + n;
-      *o = (TO)(a.accumulate ? (float)*o + acc[i][j] : acc[i][j]);
-    }
-}
-
 template <class G, typename TO>
-hipError_t launch_bf16(const MatmulArgs& a, hipStream_t s) {
+hipError_t launch_tile(const MatmulArgs& a, hipStream_t s) {
   // at most as many workgroups as are resident together, a multiple of the XCDs
   constexpr int64_t resident = kCus * (G::BM == 256 ? 1 : 2);
   const int64_t nt = (a.N + G::BN - 1) / G::BN;
   const int64_t mt = G::TN ? a.E * ((a.K + G::BM - 1) / G::BM) : a.R / G::BM + a.E;
   const int64_t blocks = (mt * nt + kXcds - 1) / kXcds * kXcds;
-  matmul_bf16_kernel<G, TO><<<(unsigned)(blocks < resident ? blocks : resident), 256, 0, s>>>(a);
+  grouped_matmul_kernel<G, TO><<<(unsigned)(blocks < resident ? blocks : resident), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <int FORM, typename TO>
+template <typename T, int FORM, typename TO>
 hipError_t pick(const MatmulArgs& a, hipStream_t s) {
-  if constexpr (FORM != MOE_MATMUL_TN) {
-    if (a.R <= 32 * (int64_t)a.E) return launch_bf16<Geo<FORM, 32, 128, 64, 1>, TO>(a, s);
-    if (a.K <= 1024) return launch_bf16<Geo<FORM, 128, 128, 32, 2>, TO>(a, s);
+  constexpr bool TN = FORM == MOE_MATMUL_TN;
+  constexpr int BK = 64 / sizeof(T);  // 64 bytes
+  if constexpr (!TN) {
+    if (a.R <= 32 * (int64_t)a.E) return launch_tile<Geo<T, FORM, 32, 128, 2 * BK, 1>, TO>(a, s);
   }
-  const int64_t mt = FORM == MOE_MATMUL_TN ? a.E * ((a.K + 255) / 256) : a.R / 256 + a.E;
-  if (mt * ((a.N + 255) / 256) < 256) return launch_bf16<Geo<FORM, 128, 128, 32, 2>, TO>(a, s);
-  return launch_bf16<Geo<FORM, 256, 256, 32, 2>, TO>(a, s);
+  if constexpr (sizeof(T) == 2) {
+    const int64_t mt = TN ? a.E * ((a.K + 255) / 256) : a.R / 256 + a.E;
+    if ((TN || a.K > 1024) && mt * ((a.N + 255) / 256) >= 256)
+      return launch_tile<Geo<T, FORM, 256, 256, BK, 2>, TO>(a, s);
+  }
+  return launch_tile<Geo<T, FORM, 128, 128, BK, 2>, TO>(a, s);
 }
 
-template <typename TO>
+template <typename T, typename TO>
 hipError_t launch_forms(const MatmulArgs& a, hipStream_t s) {
-  if (a.form == MOE_MATMUL_NN) return pick<MOE_MATMUL_NN, TO>(a, s);
-  if (a.form == MOE_MATMUL_NT) return pick<MOE_MATMUL_NT, TO>(a, s);
-  return pick<MOE_MATMUL_TN, TO>(a, s);
-}
-
-template <typename TI, typename TO>
-hipError_t launch(const MatmulArgs& a, hipStream_t s) {
-  const int ntiles = (int)((a.N + kT - 1) / kT);
-  const int mtiles = (int)((a.K + kT - 1) / kT);
-  if (a.form == MOE_MATMUL_TN) {
-    matmul_kernel<TI, TO, MOE_MATMUL_TN><<<a.E * mtiles * ntiles, 256, 0, s>>>(a, mtiles, ntiles);
-  } else {
-    const int64_t mt = a.R / kT + a.E;
-    if (a.form == MOE_MATMUL_NN)
-      matmul_kernel<TI, TO, MOE_MATMUL_NN><<<(unsigned)(mt * ntiles), 256, 0, s>>>(a, 0, ntiles);
-    else
-      matmul_kernel<TI, TO, MOE_MATMUL_NT><<<(unsigned)(mt * ntiles), 256, 0, s>>>(a, 0, ntiles);
-  }
-  return hipGetLastError();
+  if (a.form == MOE_MATMUL_NN) return pick<T, MOE_MATMUL_NN, TO>(a, s);
+  if (a.form == MOE_MATMUL_NT) return pick<T, MOE_MATMUL_NT, TO>(a, s);
+  return pick<T, MOE_MATMUL_TN, TO>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_grouped_matmul(const MatmulArgs& a, hipStream_t s) {
-  if (!a.bf16_in) return launch<float, float>(a, s);
-  return a.bf16_out ? launch_forms<bf16>(a, s) : launch_forms<float>(a, s);
+  if (!a.bf16_in) return launch_forms<float, float>(a, s);
+  return a.bf16_out ? launch_forms<bf16, bf16>(a, s) : launch_forms<bf16, float>(a, s);
 }

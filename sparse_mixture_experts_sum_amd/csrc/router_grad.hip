@@ -139,7 +139,7 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const void* wt,
     const TI* x = static_cast<const TI*>(a.x) + t * a.d;
     const TI* W = static_cast<const TI*>(wt) + (size_t)be * a.d;
     float s = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int c = sub * N; c < a.d; c += 16 * N) {
       const vec v = *reinterpret_cast<const vec*>(x + c), u = *reinterpret_cast<const vec*>(W + c);
 #pragma unroll
@@ -190,14 +190,56 @@ __device__ __forceinline__ f32x16 zero16() {
   return v;
 }
 
+// The routed rows of a dx tile: 32 tokens of up to KM slots, 64 columns, in passes of 32 /
+// PASSES tokens whose loads are all in flight together.
+template <typename TI, int KM>
+struct RowTile {
+  static constexpr int N = Chunk<TI>::N, PIECES = 64 / N, RPI = 64 / PIECES;  // tokens per load
+  static constexpr int ITS = 32 / RPI, PASSES = KM > 4 ? ITS : ITS > 4 ? ITS / 4 : 1;
+  static constexpr int PER = ITS / PASSES;
+  typedef typename Chunk<TI>::vec vec;
+  vec v[PER][KM ? KM : 1];
+  uint32_t in[PER];  // bit j: slot j has a row
+
+  // pass p; pos: the 32 tokens' rows in LDS, KM per token
+  __device__ __forceinline__ void load(const RouteGradArgs& a, int p, const int* pos, int c, int ln) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int r = (p * PER + i) * RPI + ln / PIECES;
+      in[i] = 0;
+#pragma unroll
+      for (int j = 0; j < KM; ++j) {
+        const int at = pos[r * KM + j];
+        in[i] |= (at >= 0 ? 1u : 0u) << j;
+        // (a slot without a row reads row 0 and drops it: no branch between the loads)
+        v[i][j] = *reinterpret_cast<const vec*>(static_cast<const TI*>(a.rows) + (size_t)max(at, 0) * a.d + c);
+      }
+    }
+  }
+};
+
 // dx of 32 tokens (t0 ..) and 64 columns (c0 ..), one wave: ds W_g^T with the columns as the
-// first operand, then through the wave's piece of LDS, so that rows, dx go in whole 16-byte
-// pieces of 32 to 128 contiguous bytes per row.
-template <typename TI, int EP>
-__device__ __forceinline__ void dx_tile(const RouteGradArgs& a, int64_t t0, int c0, float* buf) {
+// first operand, then through the wave's piece of LDS, so that rows and dx move in 16-byte
+// pieces, 128 or 256 contiguous bytes per row. The rows' loads go out first.
+template <typename TI, int EP, int KM>
+__device__ __forceinline__ void dx_tile(const RouteGradArgs& a, int64_t t0, int c0, float* buf, int* pos) {
   const int ln = threadIdx.x & 63, x = ln & 31, h = ln >> 5, E = a.E;
   const TI* W = static_cast<const TI*>(a.Wg);
   const int64_t t = min(t0 + x, a.T - 1);
+  typedef RowTile<TI, KM> Rows;
+  constexpr int N = Rows::N, PIECES = Rows::PIECES, RPI = Rows::RPI;
+  const int c = c0 + (ln % PIECES) * N, c_in = min(c, a.d - N);
+  Rows rows;
+  if constexpr (KM > 0) {
+#pragma unroll
+    for (int i = 0; i < (32 * KM + 63) / 64; ++i) {
+      const int at = ln + 64 * i, j = at % KM;  // token at / KM, slot j
+      const int64_t tt = t0 + at / KM;
+      const int r = at < 32 * KM && tt < a.T && j < a.k ? a.pos[tt * a.k + j] : -1;
+      if (at < 32 * KM) pos[at] = r < a.R ? r : -1;
+    }
+    rows.load(a, 0, pos, c_in, ln);
+  }
   f32x16 acc[2] = {zero16(), zero16()};
   if constexpr (sizeof(TI) == 2) {
     const bf16* hi = static_cast<const bf16*>(a.ds) + t * EP + 8 * h;
@@ -245,43 +287,34 @@ __device__ __forceinline__ void dx_tile(const RouteGradArgs& a, int64_t t0, int 
       *reinterpret_cast<f32x4*>(buf + x * 64 + (p ^ (x & 15)) * 4) =
           f32x4{acc[b][4 * q], acc[b][4 * q + 1], acc[b][4 * q + 2], acc[b][4 * q + 3]};
     }
-  constexpr int N = Chunk<TI>::N, PIECES = 64 / N, RPI = 64 / PIECES;
-  typedef typename Chunk<TI>::vec vec;
-  const int c = c0 + (ln % PIECES) * N;
+  typedef typename Rows::vec vec;
 #pragma unroll
-  for (int it = 0; it < 32 / RPI; ++it) {
-    const int r = it * RPI + ln / PIECES;
-    const int64_t tt = t0 + r;
-    if (tt >= a.T || c >= a.d) continue;
-    vec rows[8];
-    int n = 0;
-    if (a.rows) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int at = j < a.k ? a.pos[tt * a.k + j] : -1;
-        const bool in = at >= 0 && at < a.R;
-        n |= in << j;
-        if (in) rows[j] = *reinterpret_cast<const vec*>(static_cast<const TI*>(a.rows) + (size_t)at * a.d + c);
-      }
-    }
-    float v[N];
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const int p = (ln % PIECES) * (N / 4) + i;
-      const f32x4 u = *reinterpret_cast<const f32x4*>(buf + r * 64 + (p ^ (r & 15)) * 4);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[4 * i + q] = u[q];
+  for (int p = 0; p < Rows::PASSES; ++p) {
+    if constexpr (KM > 0) {
+      if (p) rows.load(a, p, pos, c_in, ln);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (n >> j & 1) {
+    for (int it = 0; it < Rows::PER; ++it) {
+      const int r = (p * Rows::PER + it) * RPI + ln / PIECES;
+      float v[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += (float)rows[j][i];
+      for (int i = 0; i < N / 4; ++i) {
+        const int piece = (ln % PIECES) * (N / 4) + i;
+        const f32x4 u = *reinterpret_cast<const f32x4*>(buf + r * 64 + (piece ^ (r & 15)) * 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[4 * i + q] = u[q];
       }
-    vec o;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = (TI)v[i];
-    *reinterpret_cast<vec*>(static_cast<TI*>(a.dx) + tt * a.d + c) = o;
+      for (int j = 0; j < KM; ++j) {
+        const bool in = rows.in[it] >> j & 1;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += in ? (float)rows.v[it][j][i] : 0.f;
+      }
+      vec o;
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] = (TI)v[i];
+      if (t0 + r < a.T && c < a.d) *reinterpret_cast<vec*>(static_cast<TI*>(a.dx) + (t0 + r) * a.d + c) = o;
+    }
   }
 }
 
@@ -394,11 +427,12 @@ __device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, 
 
 // Workgroups [0, dw_blocks): partial sums of dW_g and db, column slabs within a chunk; the
 // others: dx tiles, columns within 32 tokens.
-template <typename TI, int EP>
+template <typename TI, int EP, int KM>
 __global__ __launch_bounds__(256) void route_products_kernel(RouteGradArgs a, int dw_blocks) {
   // dx: 8 KB per wave; dW_g (bf16): x and ds tiles
   __shared__ __attribute__((aligned(16))) char lds[32768];
   static_assert(kTile * kSlab * 2 + 2 * kTile * EP * 2 <= 32768, "tiles");
+  __shared__ int pos[4][KM ? 32 * KM : 1];
   if ((int)blockIdx.x < dw_blocks) {
     const int slabs = (a.d + kSlab - 1) / kSlab;
     dw_chunk<TI, EP>(a, blockIdx.x / slabs, blockIdx.x % slabs, lds);
@@ -408,7 +442,7 @@ __global__ __launch_bounds__(256) void route_products_kernel(RouteGradArgs a, in
   const int64_t cols = (a.d + kDxCols - 1) / kDxCols, tiles = (a.T + 31) / 32 * cols;
   for (int64_t i = blockIdx.x - dw_blocks; i < tiles; i += gridDim.x - dw_blocks) {
     const int c0 = (int)(i % cols) * kDxCols + wave * 64;
-    if (c0 < a.d) dx_tile<TI, EP>(a, i / cols * 32, c0, reinterpret_cast<float*>(lds) + wave * 2048);
+    if (c0 < a.d) dx_tile<TI, EP, KM>(a, i / cols * 32, c0, reinterpret_cast<float*>(lds) + wave * 2048, pos[wave]);
   }
 }
 
@@ -450,7 +484,12 @@ hipError_t launch(RouteGradArgs a, hipStream_t s) {
     const int dw_blocks = dw ? chunks * ((a.d + kSlab - 1) / kSlab) : 0;
     const int64_t dx_blocks = a.dx ? (a.T + 31) / 32 * ((a.d + kDxCols - 1) / kDxCols) : 0;
     if (dw_blocks || dx_blocks) {
-      route_products_kernel<TI, EP><<<dw_blocks + capped_grid(dx_blocks), 256, 0, s>>>(a, dw_blocks);
+      const unsigned grid = dw_blocks + (dx_blocks ? capped_grid(dx_blocks) : 0);
+      const int km = a.rows && a.R > 0 ? a.k : 0;
+      if (km == 0) route_products_kernel<TI, EP, 0><<<grid, 256, 0, s>>>(a, dw_blocks);
+      else if (km <= 2) route_products_kernel<TI, EP, 2><<<grid, 256, 0, s>>>(a, dw_blocks);
+      else if (km <= 4) route_products_kernel<TI, EP, 4><<<grid, 256, 0, s>>>(a, dw_blocks);
+      else route_products_kernel<TI, EP, 8><<<grid, 256, 0, s>>>(a, dw_blocks);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }

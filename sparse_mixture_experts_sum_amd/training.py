@@ -4,76 +4,60 @@ gradients, and the norms around the layer with their gradient.
 Bindings of the entry points in the "Training" section of ``include/moe.h``; like the
 forward's, they check tensor metadata, allocate outputs and workspaces with torch and pass
 pointers and the current HIP stream of the tensors' device.
+
+The smallest calls are bound by the host: a call checks each tensor once, in one expression,
+and only a failed check goes through the binding's full checks for its error; shape structs
+travel as packed bytes; the workspace size of a shape is asked for once.
 """
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+import functools
+import struct
 
 import torch
+
+from . import (MOE_BF16, MOE_FP32, MOE_TOKEN_CHOICE, _check, _dtype_name, _need, _shape_is,
+               load_library)
 
 MATMUL_FORMS = {"nn": 0, "nt": 1, "tn": 2}
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+_TYPES = {_BF16: MOE_BF16, _F32: MOE_FP32}
 
-class MoeMatmulShape(ctypes.Structure):
-    _fields_ = [("R", ctypes.c_int64), ("rows_a", ctypes.c_int64), ("rows_b", ctypes.c_int64),
-                ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("E", ctypes.c_int32),
-                ("form", ctypes.c_int32), ("dtype", ctypes.c_int32),
-                ("out_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+# the structs of include/moe.h, native alignment
+_MATMUL_SHAPE = struct.Struct("@qqqqqiiiii0q").pack
+_SWIGLU_SHAPE = struct.Struct("@qqqiii0q").pack
+_ROUTE_UPSTREAM = struct.Struct("@PiffPPPq0q").pack
+_NORM_SHAPE = struct.Struct("@qqiiff0q").pack
+_LAYER_SHAPE = struct.Struct("@qqqiiiii0dd").pack
 
-
-class MoeSwigluShape(ctypes.Structure):
-    _fields_ = [("R", ctypes.c_int64), ("f", ctypes.c_int64), ("T", ctypes.c_int64),
-                ("k", ctypes.c_int32), ("E", ctypes.c_int32), ("dtype", ctypes.c_int32)]
-
-
-class MoeRouteUpstream(ctypes.Structure):
-    _fields_ = [("dw", ctypes.c_void_p), ("dw_by_row", ctypes.c_int32),
-                ("loss_grad", ctypes.c_float), ("z_loss_grad", ctypes.c_float),
-                ("f", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("pos", ctypes.c_void_p),
-                ("R", ctypes.c_int64)]
-
-
-class MoeNormShape(ctypes.Structure):
-    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int64), ("dtype", ctypes.c_int32),
-                ("gate", ctypes.c_int32), ("eps", ctypes.c_float),
-                ("residual_scale", ctypes.c_float)]
+_raw_stream = torch._C._cuda_getCurrentRawStream  # (torch.cuda.current_stream builds an object)
 
 
 def declare(lib, shape_p):
-    """Argument types of the training entry points (called once by load_library)."""
-    P, SZ, B = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER
-    lib.moe_grouped_matmul.argtypes = [B(MoeMatmulShape)] + [P] * 7
-    lib.moe_swiglu_backward.argtypes = [B(MoeSwigluShape)] + [P] * 12
-    lib.moe_route_backward_workspace_size.argtypes = [shape_p, B(SZ)]
-    lib.moe_route_backward.argtypes = [shape_p] + [P] * 6 + [B(MoeRouteUpstream)] + [P] * 5 + [SZ, P]
-    lib.moe_block_norm.argtypes = [B(MoeNormShape)] + [P] * 10
-    lib.moe_block_norm_backward_workspace_size.argtypes = [B(MoeNormShape), B(SZ)]
-    lib.moe_block_norm_backward.argtypes = [B(MoeNormShape)] + [P] * 15 + [SZ, P]
+    """Argument types of the training entry points (called once by load_library). The shape
+    structs are passed as bytes."""
+    P, SZ = ctypes.c_void_p, ctypes.c_size_t
+    lib.moe_grouped_matmul.argtypes = [P] * 8
+    lib.moe_swiglu_backward.argtypes = [P] * 13
+    lib.moe_route_backward_workspace_size.argtypes = [P, ctypes.POINTER(SZ)]
+    lib.moe_route_backward.argtypes = [P] * 13 + [SZ, P]
+    lib.moe_block_norm.argtypes = [P] * 11
+    lib.moe_block_norm_backward_workspace_size.argtypes = [P, ctypes.POINTER(SZ)]
+    lib.moe_block_norm_backward.argtypes = [P] * 16 + [SZ, P]
     for name in ("moe_grouped_matmul", "moe_swiglu_backward", "moe_route_backward_workspace_size",
                  "moe_route_backward", "moe_block_norm", "moe_block_norm_backward_workspace_size",
                  "moe_block_norm_backward"):
         getattr(lib, name).restype = ctypes.c_int32
 
 
-from . import (MOE_BF16, MOE_FP32, _check, _dtype_name, _need, _shape_is,  # noqa: E402
-               load_library, make_shape)
-
-
-def _p(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _dt(t) -> int:
-    return MOE_BF16 if _dtype_name(t) == "bf16" else MOE_FP32
-
-
-def _matrix(t, name, cols=None):
+def _matrix(t, name, width="width"):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must be [rows, {cols or 'width'}], got shape {tuple(t.shape)}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, {width}], got shape {tuple(t.shape)}")
     return t.shape
 
 
@@ -85,27 +69,62 @@ def _vector(t, name):
     return t.shape[0]
 
 
+def _type(t) -> int:
+    dt = _TYPES.get(t.dtype)
+    return dt if dt is not None else _dtype_name(t)  # (raises)
+
+
+def _pointers(tensors, dev):
+    """Addresses of (tensor, name, shape, dtype) entries, None for None: every tensor of that
+    shape and type, contiguous and on dev."""
+    out = []
+    index = dev.index
+    for t, _, shape, dtype in tensors:
+        if t is None:
+            out.append(None)
+        elif (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+              and t.get_device() == index and t.is_contiguous()):
+            out.append(t.data_ptr())
+        else:
+            break
+    else:
+        if index is not None:  # (a host tensor has no index)
+            return out
+    for t, name, shape, _ in tensors:
+        _shape_is(t, name, shape)
+    for t, name, _, dtype in tensors:
+        _need(t, name, dtype, dev)
+    raise TypeError("tensors must be CUDA (HIP) tensors")
+
+
 def _call(fn: str, dev: torch.device, *args):
     """One library call on dev's current stream, with dev the current device."""
-    lib = load_library()
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        st = getattr(lib, fn)(*args, stream)
+    f = getattr(load_library(), fn)
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        st = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            st = getattr(lib, fn)(*args, stream)
+            st = f(*args, _raw_stream(index))
     if st:
         _check(fn, st)
 
 
-def _scratch(fn: str, shape, dev, workspace):
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(fn: str, shape: bytes) -> int:
     n = ctypes.c_size_t(0)
-    _check(fn, getattr(load_library(), fn)(ctypes.byref(shape), ctypes.byref(n)))
+    _check(fn, getattr(load_library(), fn)(shape, ctypes.byref(n)))
+    return n.value
+
+
+def _scratch(fn: str, shape: bytes, dev, workspace):
+    n = _workspace_bytes(fn, shape)
     if workspace is not None:
         _need(workspace, "workspace", dev=dev)
-        if workspace.numel() * workspace.element_size() >= n.value:
-            return workspace
-    return torch.empty(max(n.value, 16), dtype=torch.uint8, device=dev)
+        if workspace.numel() * workspace.element_size() >= n:
+            return workspace, workspace.numel() * workspace.element_size()
+    n = max(n, 16)
+    return torch.empty(n, dtype=torch.uint8, device=dev), n
 
 
 def moe_grouped_matmul(a, b, offsets, *, form="nn", gather_a=None, gather_b=None, out_dtype=None,
@@ -127,7 +146,7 @@ def moe_grouped_matmul(a, b, offsets, *, form="nn", gather_a=None, gather_b=None
     R = rows_a if gather_a is None else _vector(gather_a, "gather_a")
     rows_b = 0
     if form == "tn":
-        rows_b, N = _matrix(b, "b")
+        rows_b, N = b_shape = _matrix(b, "b")
         Rb = rows_b if gather_b is None else _vector(gather_b, "gather_b")
         if Rb != R:
             raise ValueError(f"a and b give {R} and {Rb} rows")
@@ -137,30 +156,31 @@ def moe_grouped_matmul(a, b, offsets, *, form="nn", gather_a=None, gather_b=None
             raise ValueError("gather_b is for form 'tn'")
         if not isinstance(b, torch.Tensor) or b.dim() != 3:
             raise ValueError("b must be [E, K, N] ('nn') or [E, N, K] ('nt')")
-        N = b.shape[2] if form == "nn" else b.shape[1]
-        _shape_is(b, "b", (E, K, N) if form == "nn" else (E, N, K))
+        if form == "nn":
+            N = b.shape[2]
+            b_shape = (E, K, N)
+        else:
+            N = b.shape[1]
+            b_shape = (E, N, K)
         shape = (R, N)
-    _shape_is(out, "out", shape)
-    dt = _dt(a)
+    dt = _type(a)
     if out_dtype is None:
-        out_dtype = a.dtype if out is None else out.dtype
-    if out_dtype not in (torch.float32, torch.bfloat16):
+        out_dtype = a.dtype if out is None or not isinstance(out, torch.Tensor) else out.dtype
+    if out_dtype not in _TYPES:
         raise TypeError(f"unsupported out_dtype {out_dtype}: bfloat16 or float32")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    dev = a.device
-    _need(a, "a", dev=dev)
-    _need(b, "b", a.dtype, dev)
-    _need(offsets, "offsets", torch.int32, dev)
-    _need(gather_a, "gather_a", torch.int32, dev)
-    _need(gather_b, "gather_b", torch.int32, dev)
-    _need(out, "out", out_dtype, dev)
+    dev, dtype = a.device, a.dtype
+    pa, pb, po, pga, pgb, pout = _pointers(
+        ((a, "a", (rows_a, K), dtype), (b, "b", b_shape, dtype), (offsets, "offsets", (E + 1,), _I32),
+         (gather_a, "gather_a", (R,), _I32), (gather_b, "gather_b", (R,), _I32),
+         (out, "out", shape, out_dtype)), dev)
     if out is None:
         out = torch.empty(shape, dtype=out_dtype, device=dev)
-    s = MoeMatmulShape(R, rows_a, rows_b, K, N, E, MATMUL_FORMS[form], dt,
-                       MOE_BF16 if out_dtype == torch.bfloat16 else MOE_FP32, 1 if accumulate else 0)
-    _call("moe_grouped_matmul", dev, ctypes.byref(s), _p(a), _p(b), _p(offsets), _p(gather_a),
-          _p(gather_b), _p(out))
+        pout = out.data_ptr()
+    s = _MATMUL_SHAPE(R, rows_a, rows_b, K, N, E, MATMUL_FORMS[form], dt, _TYPES[out_dtype],
+                      1 if accumulate else 0)
+    _call("moe_grouped_matmul", dev, s, pa, pb, po, pga, pgb, pout)
     return out
 
 
@@ -170,40 +190,28 @@ def moe_swiglu_backward(g, u, dh, w=None, *, src=None, pos=None, offsets=None, i
     [R] by row, or [T,k] by slot with src [R] and pos [T,k] (the routing of the forward's
     workspace). Rows at and past offsets[E] are left alone. inplace writes dg, du and h over
     g, u and dh."""
-    R, f = _matrix(g, "g")
-    _shape_is(u, "u", (R, f))
-    _shape_is(dh, "dh", (R, f))
-    dev = g.device
-    T = k = 0
+    R, f = rows = _matrix(g, "g")
+    T = k = E = 0
     if (src is None) != (pos is None):
         raise ValueError("src and pos come together")
+    w_shape = (R,)
     if pos is not None:
-        T, k = _matrix(pos, "pos")
+        T, k = w_shape = _matrix(pos, "pos", "k")
         if w is None:
             raise ValueError("src and pos need w")
-        _shape_is(w, "w", (T, k))
-        _shape_is(src, "src", (R,))
-    else:
-        _shape_is(w, "w", (R,))
-    E = 0
     if offsets is not None:
         E = _vector(offsets, "offsets") - 1
-    dt = _dt(g)
-    _need(g, "g", dev=dev)
-    _need(u, "u", g.dtype, dev)
-    _need(dh, "dh", g.dtype, dev)
-    _need(w, "w", torch.float32, dev)
-    _need(src, "src", torch.int32, dev)
-    _need(pos, "pos", torch.int32, dev)
-    _need(offsets, "offsets", torch.int32, dev)
+    dt, dev, dtype = _type(g), g.device, g.dtype
+    pg, pu, pdh, pw, ps, pp, po = _pointers(
+        ((g, "g", rows, dtype), (u, "u", rows, dtype), (dh, "dh", rows, dtype), (w, "w", w_shape, _F32),
+         (src, "src", (R,), _I32), (pos, "pos", w_shape, _I32), (offsets, "offsets", (E + 1,), _I32)), dev)
     if inplace:
         dg, du, h = g, u, dh
     else:
         dg, du, h = torch.empty_like(g), torch.empty_like(u), torch.empty_like(dh)
-    dw = torch.empty(R, dtype=torch.float32, device=dev)
-    s = MoeSwigluShape(R, f, T, k, E, dt)
-    _call("moe_swiglu_backward", dev, ctypes.byref(s), _p(g), _p(u), _p(dh), _p(w), _p(src),
-          _p(pos), _p(offsets), _p(dg), _p(du), _p(h), _p(dw))
+    dw = torch.empty(R, dtype=_F32, device=dev)
+    _call("moe_swiglu_backward", dev, _SWIGLU_SHAPE(R, f, T, k, E, dt), pg, pu, pdh, pw, ps, pp, po,
+          dg.data_ptr(), du.data_ptr(), h.data_ptr(), dw.data_ptr())
     return {"dg": dg, "du": du, "h": h, "dw": dw}
 
 
@@ -217,67 +225,52 @@ def moe_route_backward(x, W_g, probs, idx, w, dw=None, *, b_g=None, f=None, loss
     routed row (with pos). loss_grad and z_loss_grad are the gradients of the load-balancing
     loss (with the forward's f) and the z-loss. rows [R,d] with pos [T,k] adds each token's
     routed-row gradients to dx."""
-    T, d = _matrix(x, "x")
-    E = _matrix(W_g, "W_g")[1]
-    _shape_is(W_g, "W_g", (d, E))
-    _shape_is(b_g, "b_g", (E,))
-    _shape_is(probs, "probs", (T, E))
-    k = _matrix(idx, "idx")[1]
-    _shape_is(idx, "idx", (T, k))
-    _shape_is(w, "w", (T, k))
-    _shape_is(f, "f", (E,))
-    _shape_is(pos, "pos", (T, k))
-    R = 0
-    if rows is not None:
-        R = _matrix(rows, "rows", d)[0]
+    T, d = x_shape = _matrix(x, "x", "d_model")
+    E = _matrix(W_g, "W_g", "E")[1]
+    k = _matrix(idx, "idx", "k")[1]
+    slots = (T, k)
+    R = _matrix(rows, "rows", "d_model")[0] if rows is not None else 0
     by_row = isinstance(dw, torch.Tensor) and dw.dim() == 1
     if by_row:
         if rows is not None and dw.shape[0] != R:
             raise ValueError(f"dw has {dw.shape[0]} rows, rows {R}")
         R = dw.shape[0]
-    else:
-        _shape_is(dw, "dw", (T, k))
     if pos is None and (by_row or rows is not None):
         raise ValueError("rows, and dw by row, need pos")
     if loss_grad != 0 and f is None:
         raise ValueError("loss_grad needs f")
-    dev = x.device
-    _dtype_name(x)
-    _need(x, "x", dev=dev)
-    _need(W_g, "W_g", x.dtype, dev)
-    for t, n in ((b_g, "b_g"), (probs, "probs"), (w, "w"), (dw, "dw"), (f, "f")):
-        _need(t, n, torch.float32, dev)
-    _need(idx, "idx", torch.int32, dev)
-    _need(pos, "pos", torch.int32, dev)
-    _need(rows, "rows", x.dtype, dev)
-    shape = make_shape(T, d, 64, E, k, "tc", _dtype_name(x), renormalize)
-    ws = _scratch("moe_route_backward_workspace_size", shape, dev, workspace)
+    dt, dev, dtype = _type(x), x.device, x.dtype
+    px, pW, pb, pp, pi, pw, pdw, pf, prows, ppos = _pointers(
+        ((x, "x", x_shape, dtype), (W_g, "W_g", (d, E), dtype), (b_g, "b_g", (E,), _F32),
+         (probs, "probs", (T, E), _F32), (idx, "idx", slots, _I32), (w, "w", slots, _F32),
+         (dw, "dw", (R,) if by_row else slots, _F32), (f, "f", (E,), _F32),
+         (rows, "rows", (R, d), dtype), (pos, "pos", slots, _I32)), dev)
+    shape = _LAYER_SHAPE(T, d, 64, E, k, MOE_TOKEN_CHOICE, dt, 1 if renormalize else 0, 1.0)
+    ws, ws_bytes = _scratch("moe_route_backward_workspace_size", shape, dev, workspace)
     dx = torch.empty_like(x) if want_dx else None
     dW = torch.empty_like(W_g) if want_dW else None
-    db = torch.empty(E, dtype=torch.float32, device=dev) if want_dW else None
-    ds = torch.empty(T, E, dtype=torch.float32, device=dev)
-    up = MoeRouteUpstream(_p(dw), 1 if by_row else 0, float(loss_grad), float(z_loss_grad), _p(f),
-                          _p(rows), _p(pos), R)
-    _call("moe_route_backward", dev, ctypes.byref(shape), _p(x), _p(W_g), _p(b_g), _p(probs),
-          _p(idx), _p(w), ctypes.byref(up), _p(dx), _p(dW), _p(db), _p(ds), _p(ws),
-          ws.numel() * ws.element_size())
+    db = torch.empty(E, dtype=_F32, device=dev) if want_dW else None
+    ds = torch.empty_like(probs)
+    up = _ROUTE_UPSTREAM(pdw or 0, 1 if by_row else 0, loss_grad, z_loss_grad, pf or 0, prows or 0,
+                         ppos or 0, R)
+    _call("moe_route_backward", dev, shape, px, pW, pb, pp, pi, pw, up,
+          None if dx is None else dx.data_ptr(), None if dW is None else dW.data_ptr(),
+          None if db is None else db.data_ptr(), ds.data_ptr(), ws.data_ptr(), ws_bytes)
     return {"dx": dx, "dW_g": dW, "db_g": db, "dlogits": ds}
 
 
-def _norm_shape(T, d, dt, y, gate, eps, scale):
-    kind = GATE_NONE
-    if gate is not None:
-        if y is None:
-            raise ValueError("gate belongs to the norm after the block: it needs y")
-        if not isinstance(gate, torch.Tensor):
-            raise TypeError("gate must be a tensor")
-        if tuple(gate.shape) == (d,):
-            kind = GATE_CHANNEL
-        elif tuple(gate.shape) == (T, 1):
-            kind = GATE_TOKEN
-        else:
-            raise ValueError(f"gate has shape {tuple(gate.shape)}, expected {(d,)} or {(T, 1)}")
-    return MoeNormShape(T, d, dt, kind, float(eps), float(scale))
+def _gate_kind(gate, y, T, d):
+    if gate is None:
+        return GATE_NONE
+    if y is None:
+        raise ValueError("gate belongs to the norm after the block: it needs y")
+    if not isinstance(gate, torch.Tensor):
+        raise TypeError("gate must be a tensor")
+    if gate.shape == (d,):
+        return GATE_CHANNEL
+    if gate.shape == (T, 1):
+        return GATE_TOKEN
+    raise ValueError(f"gate has shape {tuple(gate.shape)}, expected {(d,)} or {(T, 1)}")
 
 
 def moe_block_norm(x, *, gamma=None, y=None, gamma_post=None, gate=None, residual_scale=1.0,
@@ -290,31 +283,31 @@ def moe_block_norm(x, *, gamma=None, y=None, gamma_post=None, gate=None, residua
     x [T,d] bf16 or fp32; y [T,d] fp32, moe_forward's output; gamma, gamma_post [d] fp32; gate
     fp32, [d] per channel or [T,1] per token. Returns out and u (x's type; None where the part
     did not run) and, for the gradient, rstd = 1 / rms(out) and rstd_post = 1 / rms(y), [T]."""
-    T, d = _matrix(x, "x")
+    T, d = rows = _matrix(x, "x", "d")
     if y is None and gamma is None:
         raise ValueError("moe_block_norm needs y (the norm after) or gamma (the norm before)")
-    _shape_is(y, "y", (T, d))
-    _shape_is(gamma, "gamma", (d,))
-    _shape_is(gamma_post, "gamma_post", (d,))
     if (y is None) != (gamma_post is None):
         raise ValueError("y and gamma_post come together")
-    dt = _dt(x)
-    s = _norm_shape(T, d, dt, y, gate, eps, residual_scale)
+    kind = _gate_kind(gate, y, T, d)
     dev = x.device
-    _need(x, "x", dev=dev)
-    for t, n in ((y, "y"), (gamma, "gamma"), (gamma_post, "gamma_post"), (gate, "gate")):
-        _need(t, n, torch.float32, dev)
-    out = u = rstd = rstd_post = None
+    s = _NORM_SHAPE(T, d, _type(x), kind, eps, residual_scale)
+    px, py, pgp, pgate, pg = _pointers(
+        ((x, "x", rows, x.dtype), (y, "y", rows, _F32), (gamma_post, "gamma_post", (d,), _F32),
+         (gate, "gate", (d,) if kind == GATE_CHANNEL else (T, 1), _F32), (gamma, "gamma", (d,), _F32)), dev)
+    out = u = rstd = rstd_post = pout = pu = prp = pr = None
     if y is not None:
         out = torch.empty_like(x)
+        pout = out.data_ptr()
         if want_rstd:
-            rstd_post = torch.empty(T, dtype=torch.float32, device=dev)
+            rstd_post = torch.empty(T, dtype=_F32, device=dev)
+            prp = rstd_post.data_ptr()
     if gamma is not None:
         u = torch.empty_like(x)
+        pu = u.data_ptr()
         if want_rstd:
-            rstd = torch.empty(T, dtype=torch.float32, device=dev)
-    _call("moe_block_norm", dev, ctypes.byref(s), _p(x), _p(y), _p(gamma_post), _p(gate),
-          _p(gamma), _p(out), _p(u), _p(rstd_post), _p(rstd))
+            rstd = torch.empty(T, dtype=_F32, device=dev)
+            pr = rstd.data_ptr()
+    _call("moe_block_norm", dev, s, px, py, pgp, pgate, pg, pout, pu, prp, pr)
     return {"out": x if y is None else out, "u": u, "rstd": rstd, "rstd_post": rstd_post}
 
 
@@ -325,37 +318,33 @@ def moe_block_norm_backward(out, *, d_out=None, d_u=None, rstd=None, gamma=None,
     d_u are the gradients of out and u (either may be None, u's part needs rstd and gamma).
     Returns dx and dy (out's type) and dgamma, dgamma_post, dgate (fp32, their inputs'
     shapes); None where the part did not run."""
-    T, d = _matrix(out, "out")
+    T, d = rows = _matrix(out, "out", "d")
     if d_out is None and d_u is None:
         raise ValueError("moe_block_norm_backward needs d_out or d_u")
-    for t, n in ((d_out, "d_out"), (d_u, "d_u"), (y, "y")):
-        _shape_is(t, n, (T, d))
-    _shape_is(gamma, "gamma", (d,))
-    _shape_is(gamma_post, "gamma_post", (d,))
-    _shape_is(rstd, "rstd", (T,))
-    _shape_is(rstd_post, "rstd_post", (T,))
     if d_u is not None and (rstd is None or gamma is None):
         raise ValueError("d_u needs rstd and gamma")
     if (y is None) != (rstd_post is None) or (y is None) != (gamma_post is None):
         raise ValueError("y, rstd_post and gamma_post come together")
-    s = _norm_shape(T, d, _dt(out), y, gate, 1.0, residual_scale)
-    dev = out.device
-    _need(out, "out", dev=dev)
-    _need(d_out, "d_out", out.dtype, dev)
-    _need(d_u, "d_u", out.dtype, dev)
-    for t, n in ((rstd, "rstd"), (gamma, "gamma"), (y, "y"), (rstd_post, "rstd_post"),
-                 (gamma_post, "gamma_post"), (gate, "gate")):
-        _need(t, n, torch.float32, dev)
-    ws = _scratch("moe_block_norm_backward_workspace_size", s, dev, workspace)
+    kind = _gate_kind(gate, y, T, d)
+    dev, dtype = out.device, out.dtype
+    s = _NORM_SHAPE(T, d, _type(out), kind, 1.0, residual_scale)
+    pdo, pdu, po, pr, pg, py, prp, pgp, pgate = _pointers(
+        ((d_out, "d_out", rows, dtype), (d_u, "d_u", rows, dtype), (out, "out", rows, dtype),
+         (rstd, "rstd", (T,), _F32), (gamma, "gamma", (d,), _F32), (y, "y", rows, _F32),
+         (rstd_post, "rstd_post", (T,), _F32), (gamma_post, "gamma_post", (d,), _F32),
+         (gate, "gate", (d,) if kind == GATE_CHANNEL else (T, 1), _F32)), dev)
+    ws, ws_bytes = _scratch("moe_block_norm_backward_workspace_size", s, dev, workspace)
     dx = torch.empty_like(out)
-    dy = dgamma = dgamma_post = dgate = None
+    dy = dgamma = dgamma_post = dgate = pdy = pdg = pdgp = pdgate = None
     if y is not None:
-        dy = torch.empty_like(out)
-        dgamma_post = torch.empty_like(gamma_post)
-        dgate = None if gate is None else torch.empty_like(gate)
+        dy, dgamma_post = torch.empty_like(out), torch.empty_like(gamma_post)
+        pdy, pdgp = dy.data_ptr(), dgamma_post.data_ptr()
+        if gate is not None:
+            dgate = torch.empty_like(gate)
+            pdgate = dgate.data_ptr()
     if d_u is not None:
         dgamma = torch.empty_like(gamma)
-    _call("moe_block_norm_backward", dev, ctypes.byref(s), _p(d_out), _p(d_u), _p(out), _p(rstd),
-          _p(gamma), _p(y), _p(rstd_post), _p(gamma_post), _p(gate), _p(dx), _p(dy), _p(dgamma),
-          _p(dgamma_post), _p(dgate), _p(ws), ws.numel() * ws.element_size())
+        pdg = dgamma.data_ptr()
+    _call("moe_block_norm_backward", dev, s, pdo, pdu, po, pr, pg, py, prp, pgp, pgate, dx.data_ptr(),
+          pdy, pdg, pdgp, pdgate, ws.data_ptr(), ws_bytes)
     return {"dx": dx, "dy": dy, "dgamma": dgamma, "dgamma_post": dgamma_post, "dgate": dgate}
