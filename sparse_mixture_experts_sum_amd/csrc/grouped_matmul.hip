@@ -64,7 +64,7 @@ struct Operand {
   static_assert(PW >= 1 && BYTES % (1024 * NW) == 0, "whole loads per wave");
   static __device__ __forceinline__ int swz(int row) {
     if constexpr (KS) return ((0xCA60 >> (4 * (row & 3))) & 15) % SLOTS;
-    else if constexpr (SLOTS == 4) return ((row >> 1) ^ (row >> 3)) & 3;
+    else if constexpr (SLOTS == 4) return (row >> 2) & 3;
     else return (row ^ (row >> 3)) & 7;
   }
   // LDS row of load j of a wave for this lane, and the source chunk that goes into its slot
