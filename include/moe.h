@@ -335,7 +335,12 @@ typedef struct moe_matmul_shape {
  * opposite that out_dtype does not allow, return MOE_ERR_UNSUPPORTED. */
 moe_status moe_grouped_matmul(const moe_matmul_shape* shape, const void* a, const void* b,
                               const int32_t* offsets, const int32_t* gather_a,
-                              const int32_t* gather_b, void* out, hipStream_t stream);
+                              const int32_t* gather_b, void* out, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
+
+/* Bytes of workspace moe_grouped_matmul needs for `shape`: partial sums where few output tiles
+ * share a long sum, 0 (and a NULL workspace) elsewhere. Host only. */
+moe_status moe_grouped_matmul_workspace_size(const moe_matmul_shape* shape, size_t* bytes);
 
 /* Gradient of the experts' activation h = silu(g) * u and of the row's gate weight, for
  * y = sum over rows of w_r (h_r W_down): with dh = dy W_down^T (unweighted) and

@@ -38,7 +38,8 @@ EXPORTS = (
     "moe_status_string", "moe_capacity", "moe_workspace_size", "moe_workspace_offset",
     "moe_route", "moe_forward", "moe_aux_loss", "moe_profile_enable", "moe_profile_read",
     "moe_stage_name", "moe_forward_noalloc",
-    "moe_grouped_matmul", "moe_swiglu_backward", "moe_route_backward_workspace_size",
+    "moe_grouped_matmul", "moe_grouped_matmul_workspace_size", "moe_swiglu_backward",
+    "moe_route_backward_workspace_size",
     "moe_route_backward", "moe_block_norm", "moe_block_norm_backward_workspace_size",
     "moe_block_norm_backward",
 )

@@ -283,9 +283,11 @@ __device__ __forceinline__ void mask_first(Frags<G>& F, int len, int ln) {
   if (len < G::BK) mask_frags<G>(F, len, ln);
 }
 
-// A workgroup's work: output tile (mt, nt) of group e, whose rows are [r0, r1).
+// A workgroup's work: output tile (mt, nt) of group e, whose rows are [r0, r1), over a part of
+// the summed axis: NN, NT [k0, k0 + len); TN rows [r0, r1) are that part, and `split` says
+// which.
 struct Item {
-  int e, r0, r1, mt, nt;
+  int e, r0, r1, mt, nt, k0, len, split;
 };
 
 constexpr int kXcds = 8;
@@ -310,7 +312,7 @@ __device__ __forceinline__ void make_groups(const MatmulArgs& a, int xcd, Groups
   int start, end;
   group_bounds(a.offsets, a.E, (int)a.R, start, end);
   g = Groups{lane, start, end, 0, 0};
-  int tiles;
+  int tiles;  // (with splits: each part is a tile of its own)
   if constexpr (G::TN) {
     const int len = lane < a.E ? end - start : -1;
     int rank = 0;
@@ -321,12 +323,12 @@ __device__ __forceinline__ void make_groups(const MatmulArgs& a, int xcd, Groups
     g.e = __builtin_amdgcn_ds_permute(4 * rank, lane);
     g.start = __builtin_amdgcn_ds_permute(4 * rank, start);
     g.end = __builtin_amdgcn_ds_permute(4 * rank, end);
-    const int64_t n = lane < a.E ? (a.K + G::BM - 1) / G::BM * NT : 0;
+    const int64_t n = lane < a.E ? (a.K + G::BM - 1) / G::BM * NT * a.splits : 0;
     const int x = (xcd + lane) % kXcds;  // (a group of few tiles: another XCD's for each)
     g.first = (int)(n * x / kXcds);
     tiles = (int)(n * (x + 1) / kXcds) - g.first;
   } else {
-    tiles = (end - start + G::BM - 1) / G::BM * NT;
+    tiles = (end - start + G::BM - 1) / G::BM * NT * a.splits;
   }
   g.incl = tiles;
 #pragma unroll
@@ -349,11 +351,24 @@ __device__ __forceinline__ Item locate(const MatmulArgs& a, const Groups& g, int
   t.r1 = __builtin_amdgcn_readlane(g.end, at_group);
   const int m = G::TN ? (int)((a.K + G::BM - 1) / G::BM) : (t.r1 - t.r0 + G::BM - 1) / G::BM;
   const int before = at_group ? __builtin_amdgcn_readlane(g.incl, at_group - 1) : 0;
-  const int in = i - before + __builtin_amdgcn_readlane(g.first, at_group);
+  const int part = i - before + __builtin_amdgcn_readlane(g.first, at_group);
+  const int in = part / a.splits;
+  t.split = part - in * a.splits;
   const int blk = in / (m * kColBlock), cols = min(kColBlock, NT - blk * kColBlock);
   const int at = in - blk * m * kColBlock;
   t.mt = at / cols;
   t.nt = blk * kColBlock + at % cols;
+  t.k0 = 0;
+  t.len = G::TN ? t.r1 - t.r0 : (int)a.K;
+  if (a.splits > 1) {  // whole stages per part; a part may be empty (TN)
+    const int per = ((t.len + G::BK - 1) / G::BK + a.splits - 1) / a.splits * G::BK;
+    t.k0 = min(t.split * per, t.len);
+    t.len = min(per, t.len - t.k0);
+    if constexpr (G::TN) {
+      t.r0 += t.k0;
+      t.r1 = t.r0 + t.len;
+    }
+  }
   return t;
 }
 
@@ -404,7 +419,7 @@ __device__ __forceinline__ void make_loader(const MatmulArgs& a, const Item& t, 
   ld.ln = lane;
   if constexpr (G::TN) {
     const int m0 = t.mt * G::BM;
-    ld.len = t.r1 - t.r0;
+    ld.len = t.len;
     ld.step_a = K;
     ld.step_b = N;
 #pragma unroll
@@ -413,21 +428,21 @@ __device__ __forceinline__ void make_loader(const MatmulArgs& a, const Item& t, 
     for (int j = 0; j < G::B::PW; ++j) ld.pb[j] = B + min(n0 + G::B::chunk(j, wave, ln) * C, N - C);
   } else {
     const T* Be = B + (size_t)t.e * K * N;
-    ld.len = K;
+    ld.len = t.len;
     ld.step_a = G::BK;
 #pragma unroll
     for (int j = 0; j < G::A::PW; ++j)
-      ld.pa[j] = A + (size_t)min(max((int64_t)rows[j], (int64_t)0), a.rows_a - 1) * K + G::A::chunk(j, wave, ln) * C;
+      ld.pa[j] = A + (size_t)min(max((int64_t)rows[j], (int64_t)0), a.rows_a - 1) * K + t.k0 + G::A::chunk(j, wave, ln) * C;
     if constexpr (G::FORM == MOE_MATMUL_NT) {
       ld.step_b = G::BK;
 #pragma unroll
       for (int j = 0; j < G::B::PW; ++j)
-        ld.pb[j] = Be + (size_t)min(n0 + G::B::row(j, wave, ln), N - 1) * K + G::B::chunk(j, wave, ln) * C;
+        ld.pb[j] = Be + (size_t)min(n0 + G::B::row(j, wave, ln), N - 1) * K + t.k0 + G::B::chunk(j, wave, ln) * C;
     } else {
       ld.step_b = (size_t)G::BK * N;
 #pragma unroll
       for (int j = 0; j < G::B::PW; ++j)
-        ld.pb[j] = Be + (size_t)G::B::row(j, wave, ln) * N + min(n0 + G::B::chunk(j, wave, ln) * C, N - C);
+        ld.pb[j] = Be + (size_t)(t.k0 + G::B::row(j, wave, ln)) * N + min(n0 + G::B::chunk(j, wave, ln) * C, N - C);
     }
   }
 }
@@ -444,7 +459,7 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const Item& t, i
   const int K = (int)a.K, N = (int)a.N;
   const int m0 = t.mt * G::BM + (G::TN ? 0 : t.r0) + wm * G::WM, mend = G::TN ? K : t.r1;
   const int n0 = t.nt * G::BN + wn * G::WN;
-  TO* out = static_cast<TO*>(a.out) + (G::TN ? (size_t)t.e * K * N : 0);
+  TO* out = static_cast<TO*>(a.out) + (size_t)t.split * a.split_stride + (G::TN ? (size_t)t.e * K * N : 0);
   auto vec = [&](int mb, int nb, int q) {
     return f32x4{w.acc[nb][mb][4 * q], w.acc[nb][mb][4 * q + 1], w.acc[nb][mb][4 * q + 2],
                  w.acc[nb][mb][4 * q + 3]};
@@ -615,42 +630,119 @@ __global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
   wait_vmcnt<0>();  // the loads that nobody reads have landed before the LDS is given back
 }
 
+// Parts' sums, in order, into out: n values, NN and NT up to the last group's end.
+template <typename TO>
+__global__ __launch_bounds__(256) void join_parts_kernel(MatmulArgs a, const float* __restrict__ parts) {
+  int64_t n = a.split_stride;
+  if (a.form != MOE_MATMUL_TN) {
+    int b0, b1;
+    n = (int64_t)group_bounds(a.offsets, a.E, (int)a.R, b0, b1) * a.N;
+  }
+  TO* out = static_cast<TO*>(a.out);
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(parts + i);
+    for (int p = 1; p < a.splits; ++p) v += *reinterpret_cast<const f32x4*>(parts + p * a.split_stride + i);
+    if constexpr (sizeof(TO) == 2) {
+      *reinterpret_cast<bf16x4*>(out + i) = __builtin_convertvector(v, bf16x4);
+    } else {
+      if (a.accumulate) v = *reinterpret_cast<const f32x4*>(out + i) + v;
+      *reinterpret_cast<f32x4*>(out + i) = v;
+    }
+  }
+}
+
+// Tile of a product, and in how many parts its summed axis is taken. The tiles' count is
+// bounded from the sizes alone (the groups' sizes are on the device): one part tile per group
+// that can have rows.
+struct Plan {
+  int bm, splits;
+};
+int64_t tiles_of(const MatmulArgs& a, int bm, int bn) {
+  const int64_t nt = (a.N + bn - 1) / bn;
+  if (a.form == MOE_MATMUL_TN) return a.E * ((a.K + bm - 1) / bm) * nt;
+  return (a.R / bm + (a.R < a.E ? a.R : a.E)) * nt;
+}
+Plan plan_of(const MatmulArgs& a) {
+  const bool tn = a.form == MOE_MATMUL_TN;
+  Plan p{128, 1};
+  // 32 rows: a row tile's other rows are work for nothing, or there are too few 128-row
+  // tiles to fill the chip (fp32, 512 rows of 8 groups, K 128: 12.7 -> 7.2 us; bf16, 300 rows
+  // of 4 groups, K 512, N 1024: 8.7 -> 7.8 us). 256 rows: half the operand traffic through
+  // L2 of 128 rows, which bounds a long sum; a short sum gains more from two workgroups per CU
+  // (8192 rows of 8 groups, N 4096: K 256 46 -> 29 us with 128 rows, K 1024 94 -> 85, K 4096
+  // 280 against 389 with 256; TN, 32764 rows of 64 groups, 2048 x 1408: 330 against 340).
+  if (!tn && (a.R <= 32 * (int64_t)a.E || tiles_of(a, 128, 128) < 128)) p.bm = 32;
+  else if (a.bf16_in && (tn || (a.K > 1024 && a.R >= 192 * (int64_t)a.E)) && tiles_of(a, 256, 256) >= 256)
+    p.bm = 256;
+  if (p.bm == 256) return p;
+  // few tiles and a long sum: parts of at least 16 stages, about one workgroup per CU
+  const int64_t tiles = tiles_of(a, p.bm, 128), len = tn ? a.R / a.E : a.K;
+  const int64_t stages = len / (p.bm == 32 ? (a.bf16_in ? 64 : 32) : (a.bf16_in ? 32 : 16));
+  if (tiles <= 64 && stages >= 32) {
+    int64_t n = kCus / tiles;
+    n = n < stages / 16 ? n : stages / 16;
+    p.splits = (int)(n < 16 ? n : 16);
+  }
+  return p;
+}
+
 template <class G, typename TO>
 hipError_t launch_tile(const MatmulArgs& a, hipStream_t s) {
   // at most as many workgroups as are resident together, a multiple of the XCDs
   constexpr int64_t resident = kCus * (G::BM == 256 ? 1 : 2);
-  const int64_t nt = (a.N + G::BN - 1) / G::BN;
-  const int64_t mt = G::TN ? a.E * ((a.K + G::BM - 1) / G::BM) : a.R / G::BM + a.E;
-  const int64_t blocks = (mt * nt + kXcds - 1) / kXcds * kXcds;
+  const int64_t blocks = (tiles_of(a, G::BM, G::BN) * a.splits + kXcds - 1) / kXcds * kXcds;
   grouped_matmul_kernel<G, TO><<<(unsigned)(blocks < resident ? blocks : resident), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, int FORM, typename TO>
-hipError_t pick(const MatmulArgs& a, hipStream_t s) {
-  constexpr bool TN = FORM == MOE_MATMUL_TN;
+hipError_t launch_form(const MatmulArgs& a, int bm, hipStream_t s) {
   constexpr int BK = 64 / sizeof(T);  // 64 bytes
-  if constexpr (!TN) {
-    if (a.R <= 32 * (int64_t)a.E) return launch_tile<Geo<T, FORM, 32, 128, 2 * BK, 1>, TO>(a, s);
+  if constexpr (FORM != MOE_MATMUL_TN) {
+    if (bm == 32) return launch_tile<Geo<T, FORM, 32, 128, 2 * BK, 1>, TO>(a, s);
   }
   if constexpr (sizeof(T) == 2) {
-    const int64_t mt = TN ? a.E * ((a.K + 255) / 256) : a.R / 256 + a.E;
-    if ((TN || a.K > 1024) && mt * ((a.N + 255) / 256) >= 256)
-      return launch_tile<Geo<T, FORM, 256, 256, BK, 2>, TO>(a, s);
+    if (bm == 256) return launch_tile<Geo<T, FORM, 256, 256, BK, 2>, TO>(a, s);
   }
   return launch_tile<Geo<T, FORM, 128, 128, BK, 2>, TO>(a, s);
 }
 
 template <typename T, typename TO>
-hipError_t launch_forms(const MatmulArgs& a, hipStream_t s) {
-  if (a.form == MOE_MATMUL_NN) return pick<T, MOE_MATMUL_NN, TO>(a, s);
-  if (a.form == MOE_MATMUL_NT) return pick<T, MOE_MATMUL_NT, TO>(a, s);
-  return pick<T, MOE_MATMUL_TN, TO>(a, s);
+hipError_t launch_forms(const MatmulArgs& a, int bm, hipStream_t s) {
+  if (a.form == MOE_MATMUL_NN) return launch_form<T, MOE_MATMUL_NN, TO>(a, bm, s);
+  if (a.form == MOE_MATMUL_NT) return launch_form<T, MOE_MATMUL_NT, TO>(a, bm, s);
+  return launch_form<T, MOE_MATMUL_TN, TO>(a, bm, s);
+}
+
+hipError_t launch_types(const MatmulArgs& a, int bm, hipStream_t s) {
+  if (!a.bf16_in) return launch_forms<float, float>(a, bm, s);
+  return a.bf16_out ? launch_forms<bf16, bf16>(a, bm, s) : launch_forms<bf16, float>(a, bm, s);
+}
+
+int64_t out_values(const MatmulArgs& a) {
+  return a.form == MOE_MATMUL_TN ? (int64_t)a.E * a.K * a.N : a.R * a.N;
 }
 
 }  // namespace
 
-hipError_t launch_grouped_matmul(const MatmulArgs& a, hipStream_t s) {
-  if (!a.bf16_in) return launch_forms<float, float>(a, s);
-  return a.bf16_out ? launch_forms<bf16, bf16>(a, s) : launch_forms<bf16, float>(a, s);
+size_t grouped_matmul_workspace(const MatmulArgs& a) {
+  const Plan p = plan_of(a);
+  return p.splits > 1 ? (size_t)p.splits * out_values(a) * sizeof(float) : 0;
+}
+
+hipError_t launch_grouped_matmul(const MatmulArgs& args, float* ws, hipStream_t s) {
+  MatmulArgs a = args;
+  const Plan p = plan_of(a);
+  a.splits = p.splits;
+  a.split_stride = out_values(a);
+  if (p.splits == 1) return launch_types(a, p.bm, s);
+  MatmulArgs part = a;
+  part.out = ws;
+  part.bf16_out = part.accumulate = 0;
+  const hipError_t e = launch_types(part, p.bm, s);
+  if (e != hipSuccess) return e;
+  const unsigned grid = capped_grid((a.split_stride / 4 + 255) / 256);
+  if (a.bf16_out) join_parts_kernel<bf16><<<grid, 256, 0, s>>>(a, ws);
+  else join_parts_kernel<float><<<grid, 256, 0, s>>>(a, ws);
+  return hipGetLastError();
 }

@@ -46,6 +46,21 @@ moe_status check_matmul(const moe_matmul_shape* s) {
   return MOE_OK;
 }
 
+MatmulArgs matmul_args(const moe_matmul_shape& s) {
+  MatmulArgs m{};
+  m.R = s.R;
+  m.rows_a = s.rows_a;
+  m.rows_b = s.rows_b;
+  m.K = s.K;
+  m.N = s.N;
+  m.E = s.E;
+  m.form = s.form;
+  m.bf16_in = s.dtype == MOE_BF16;
+  m.bf16_out = s.out_dtype == MOE_BF16;
+  m.accumulate = s.accumulate;
+  return m;
+}
+
 moe_status check_route(const moe_shape* s) {
   if (!s) return MOE_ERR_NULL_ARG;
   if (bad_dtype(s->dtype)) return MOE_ERR_BAD_SHAPE;
@@ -74,9 +89,18 @@ moe_status check_norm(const moe_norm_shape* s) {
 
 extern "C" {
 
+moe_status moe_grouped_matmul_workspace_size(const moe_matmul_shape* shape, size_t* bytes) {
+  if (!bytes) return MOE_ERR_NULL_ARG;
+  const moe_status st = check_matmul(shape);
+  if (st != MOE_OK) return st;
+  *bytes = shape->R > 0 ? grouped_matmul_workspace(matmul_args(*shape)) : 0;
+  return MOE_OK;
+}
+
 moe_status moe_grouped_matmul(const moe_matmul_shape* shape, const void* a, const void* b,
                               const int32_t* offsets, const int32_t* gather_a,
-                              const int32_t* gather_b, void* out, hipStream_t stream) {
+                              const int32_t* gather_b, void* out, void* ws, size_t ws_bytes,
+                              hipStream_t stream) {
   moe_status st = check_matmul(shape);
   if (st != MOE_OK) return st;
   const moe_matmul_shape& s = *shape;
@@ -86,7 +110,7 @@ moe_status moe_grouped_matmul(const moe_matmul_shape* shape, const void* a, cons
   if (tn && !gather_b && s.rows_b != s.R) return MOE_ERR_BAD_SHAPE;
   // a gathered row has to exist
   if (s.R > 0 && (s.rows_a < 1 || (tn && s.rows_b < 1))) return MOE_ERR_BAD_SHAPE;
-  if (!all_aligned16(a, b, out)) return MOE_ERR_MISALIGNED;
+  if (!all_aligned16(a, b, out, ws)) return MOE_ERR_MISALIGNED;
   if (s.R > 0 && (!a || !b || !offsets || !out)) return MOE_ERR_NULL_ARG;
   if (s.R == 0) {
     if (!tn || s.accumulate) return MOE_OK;
@@ -94,24 +118,17 @@ moe_status moe_grouped_matmul(const moe_matmul_shape* shape, const void* a, cons
     return launched(launch_fill_zero(out, (size_t)s.E * s.K * s.N * (s.out_dtype == MOE_BF16 ? 2 : 4),
                                      stream));
   }
-  MatmulArgs m{};
+  MatmulArgs m = matmul_args(s);
+  const size_t need = grouped_matmul_workspace(m);
+  if (need && !ws) return MOE_ERR_NULL_ARG;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   m.a = a;
   m.b = b;
   m.offsets = offsets;
   m.gather_a = gather_a;
   m.gather_b = gather_b;
   m.out = out;
-  m.R = s.R;
-  m.rows_a = s.rows_a;
-  m.rows_b = s.rows_b;
-  m.K = s.K;
-  m.N = s.N;
-  m.E = s.E;
-  m.form = s.form;
-  m.bf16_in = s.dtype == MOE_BF16;
-  m.bf16_out = s.out_dtype == MOE_BF16;
-  m.accumulate = s.accumulate;
-  return launched(launch_grouped_matmul(m, stream));
+  return launched(launch_grouped_matmul(m, static_cast<float*>(ws), stream));
 }
 
 moe_status moe_swiglu_backward(const moe_swiglu_shape* shape, const void* g, const void* u,

@@ -16,8 +16,12 @@ struct MatmulArgs {
   void* out;
   int64_t R, rows_a, rows_b, K, N;
   int E, form, bf16_in, bf16_out, accumulate;
+  int splits;               // parts of the summed axis, split_stride values apart in out
+  int64_t split_stride;     // (both set by the launch)
 };
-hipError_t launch_grouped_matmul(const MatmulArgs& a, hipStream_t s);
+// Bytes of workspace: the parts' sums, where few tiles share a long sum; else 0.
+size_t grouped_matmul_workspace(const MatmulArgs& a);
+hipError_t launch_grouped_matmul(const MatmulArgs& a, float* ws, hipStream_t s);
 
 struct SwigluGradArgs {
   const void *g, *u, *dh;   // [R, f]

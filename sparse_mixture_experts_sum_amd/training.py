@@ -40,14 +40,15 @@ def declare(lib, shape_p):
     """Argument types of the training entry points (called once by load_library). The shape
     structs are passed as bytes."""
     P, SZ = ctypes.c_void_p, ctypes.c_size_t
-    lib.moe_grouped_matmul.argtypes = [P] * 8
+    lib.moe_grouped_matmul.argtypes = [P] * 8 + [SZ, P]
+    lib.moe_grouped_matmul_workspace_size.argtypes = [P, ctypes.POINTER(SZ)]
     lib.moe_swiglu_backward.argtypes = [P] * 13
     lib.moe_route_backward_workspace_size.argtypes = [P, ctypes.POINTER(SZ)]
     lib.moe_route_backward.argtypes = [P] * 13 + [SZ, P]
     lib.moe_block_norm.argtypes = [P] * 11
     lib.moe_block_norm_backward_workspace_size.argtypes = [P, ctypes.POINTER(SZ)]
     lib.moe_block_norm_backward.argtypes = [P] * 16 + [SZ, P]
-    for name in ("moe_grouped_matmul", "moe_swiglu_backward", "moe_route_backward_workspace_size",
+    for name in ("moe_grouped_matmul", "moe_grouped_matmul_workspace_size", "moe_swiglu_backward", "moe_route_backward_workspace_size",
                  "moe_route_backward", "moe_block_norm", "moe_block_norm_backward_workspace_size",
                  "moe_block_norm_backward"):
         getattr(lib, name).restype = ctypes.c_int32
@@ -128,7 +129,7 @@ def _scratch(fn: str, shape: bytes, dev, workspace):
 
 
 def moe_grouped_matmul(a, b, offsets, *, form="nn", gather_a=None, gather_b=None, out_dtype=None,
-                       accumulate=False, out=None) -> torch.Tensor:
+                       accumulate=False, out=None, workspace=None) -> torch.Tensor:
     """Products of rows grouped by expert: group e is rows [offsets[e], offsets[e+1]).
 
     form "nn": out[r] = a[r] @ b[e], b [E,K,N]; "nt": out[r] = a[r] @ b[e].T, b [E,N,K];
@@ -180,7 +181,12 @@ def moe_grouped_matmul(a, b, offsets, *, form="nn", gather_a=None, gather_b=None
         pout = out.data_ptr()
     s = _MATMUL_SHAPE(R, rows_a, rows_b, K, N, E, MATMUL_FORMS[form], dt, _TYPES[out_dtype],
                       1 if accumulate else 0)
-    _call("moe_grouped_matmul", dev, s, pa, pb, po, pga, pgb, pout)
+    ws = pws = None
+    ws_bytes = _workspace_bytes("moe_grouped_matmul_workspace_size", s)
+    if ws_bytes:
+        ws, ws_bytes = _scratch("moe_grouped_matmul_workspace_size", s, dev, workspace)
+        pws = ws.data_ptr()
+    _call("moe_grouped_matmul", dev, s, pa, pb, po, pga, pgb, pout, pws, ws_bytes)
     return out
 
 

@@ -259,6 +259,30 @@ def test_matmul_larger(moe, form, R, E, K, N):
         close(got, ref, mag, (max(c) if form == "tn" else K) + 2)
 
 
+@pytest.mark.parametrize("form,c,K,N", [("tn", [5000], 72, 136), ("tn", [2100, 0, 1900], 64, 64),
+                                        ("tn", [1, 4000, 33], 264, 8), ("nn", [3], 4104, 136),
+                                        ("nt", [1, 0, 2], 8200, 72), ("nn", [0, 40, 0], 4096, 64)])
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_matmul_in_parts(moe, form, c, K, N, dt):
+    # few output tiles and a long sum: the sum is taken in parts
+    say("parts", form, c, K, N, dt)
+    R, E, g = sum(c), len(c), gen(K)
+    a = draw(g, R + 5, K, dtype=dt)
+    b = draw(g, *{"nn": (E, K, N), "nt": (E, N, K), "tn": (R + 5, N)}[form], dtype=dt)
+    a[R:] = float("nan")
+    ref, mag = matmul_ref(form, a[:R], b[:R] if form == "tn" else b, c)
+    da, db, do = cuda(a, b, offsets_of(c))
+    for out in {dt, FP32}:
+        o = torch.full((E, K, N) if form == "tn" else (R + 5, N), 2.5, dtype=out, device="cuda")
+        moe.moe_grouped_matmul(da, db, do, form=form, out=o)
+        close(o if form == "tn" else o[:R], ref, mag, (max(c) if form == "tn" else K) + 18)
+        if form != "tn":
+            assert bool((o[R:] == 2.5).all())
+    acc = torch.full((E, K, N) if form == "tn" else (R + 5, N), 2.5, device="cuda")
+    moe.moe_grouped_matmul(da, db, do, form=form, out=acc, accumulate=True)
+    close(acc if form == "tn" else acc[:R], ref + 2.5, mag + 2.5, (max(c) if form == "tn" else K) + 18)
+
+
 def test_matmul_rows_past_2_31_elements(moe):
     # a and out of more than 2^31 elements: the last rows against the first ones' copies
     say("far rows")
