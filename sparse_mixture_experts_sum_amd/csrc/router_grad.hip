@@ -23,10 +23,15 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
+// The z-loss's dot products read W_g transposed: in LDS, where a workgroup of the ds kernel
+// puts it itself, up to this size; from HBM, by a kernel of its own, beyond (mid-size layer,
+// 16 KB: picking each expert's column out of W_g's rows instead took 14 us, this 9).
+constexpr size_t kLdsWg = 65536;
 constexpr int kTok = 16;     // tokens per workgroup of the ds kernel
 constexpr int kTile = 64;    // tokens that the dW_g workgroups take at a time
 constexpr int kSlab = 128;   // columns of x per dW_g workgroup: 32 per wave
-constexpr int kDxCols = 256; // columns of dx per workgroup: 64 per wave, 32 tokens
+constexpr int kDxCols = 256; // columns of dx per workgroup: 64 per wave
+constexpr int kRun = 4;      // tiles of 32 tokens per dx workgroup
 // Partial sums of dW_g and db: at most kChunks chunks of whole tiles of tokens, so that
 // d / kSlab times that many workgroups cover the chip and the partial sums stay small.
 constexpr int kChunks = 32;
@@ -38,7 +43,7 @@ int64_t chunks_of(int64_t T) { return T > 0 ? (T + chunk_len(T) - 1) / chunk_len
 int padded_experts(int E) { return E <= 32 ? 32 : 64; }
 
 // Workspace: operand rows of ds (bf16: hi rows, then lo rows; fp32: the values), W_g
-// transposed, the partial sums [chunk][d + 1][E]. Whole 256-byte pieces.
+// transposed, the partial sums, [E][d] of dW_g and [E] of db per chunk. Whole 256-byte pieces.
 struct Layout {
   size_t ds, wt, partial, total;
 };
@@ -65,7 +70,7 @@ __global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* __restri
 // ds of 16 tokens, 16 lanes per token, lane `sub` owning experts sub + 16 i: into dlogits
 // and the operand rows.
 template <typename TI, int EP>
-__device__ __forceinline__ void token_ds(const RouteGradArgs& a, const void* wt, int64_t t0) {
+__device__ __forceinline__ void token_ds(const RouteGradArgs& a, const TI* wt, int64_t t0) {
   const int tok = threadIdx.x >> 4, sub = threadIdx.x & 15;
   const int64_t t = t0 + tok < a.T ? t0 + tok : a.T - 1;  // (past the end: a copy, not stored)
   const int E = a.E, k = a.k;
@@ -78,26 +83,32 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const void* wt,
     dp[i] = (a.loss_grad != 0.f && e < E) ? a.loss_grad * ((float)E / (float)k) * inv_T * a.f[e] : 0.f;
   }
   if (a.dw) {
-    float S = 0.f, dot = 0.f;
-    float g[8];
-    int ex[8];
+    // every slot's loads first (a slot past k, and one without a row, reads another's)
+    float w[8], g[8], pj[8];
+    int ex[8], at[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+      const int64_t slot = t * k + (j < k ? j : 0);
+      w[j] = a.w[slot];
+      ex[j] = min(max(a.idx[slot], 0), E - 1);
+      at[j] = a.dw_by_row ? a.pos[slot] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool row = at[j] >= 0 && at[j] < a.R;
       g[j] = 0.f;
-      ex[j] = -1;
-      if (j >= k) continue;
-      const float w = a.w[t * k + j];
-      if (w == 0.f) continue;  // dropped (or a probability of 0, whose gradient is 0 too)
-      if (a.dw_by_row) {
-        const int r = a.pos[t * k + j];
-        if (r < 0 || r >= a.R) continue;
-        g[j] = a.dw[r];
-      } else {
-        g[j] = a.dw[t * k + j];
-      }
-      ex[j] = min(max(a.idx[t * k + j], 0), E - 1);
-      S += a.probs[t * E + ex[j]];
-      dot += g[j] * w;
+      if (!a.dw_by_row) g[j] = a.dw[t * k + (j < k ? j : 0)];
+      else if (a.R > 0) g[j] = a.dw[row ? at[j] : 0];
+      pj[j] = a.probs[t * E + ex[j]];
+      // w = 0: dropped (or a probability of 0, whose gradient is 0 too)
+      if (j >= k || w[j] == 0.f || (a.dw_by_row && !row)) ex[j] = -1;
+    }
+    float S = 0.f, dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (ex[j] < 0) continue;
+      S += pj[j];
+      dot += g[j] * w[j];
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -137,7 +148,7 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const void* wt,
     constexpr int N = Chunk<TI>::N;
     typedef typename Chunk<TI>::vec vec;
     const TI* x = static_cast<const TI*>(a.x) + t * a.d;
-    const TI* W = static_cast<const TI*>(wt) + (size_t)be * a.d;
+    const TI* W = wt + (size_t)be * a.d;
     float s = 0.f;
 #pragma unroll 8
     for (int c = sub * N; c < a.d; c += 16 * N) {
@@ -166,10 +177,33 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const void* wt,
   }
 }
 
-template <typename TI, int EP>
+// LDS_WG: W_g transposed into (dynamic) LDS first.
+template <typename TI, int EP, bool LDS_WG>
 __global__ __launch_bounds__(256) void ds_kernel(RouteGradArgs a) {
-  for (int64_t t0 = (int64_t)blockIdx.x * kTok; t0 < a.T; t0 += (int64_t)gridDim.x * kTok)
-    token_ds<TI, EP>(a, a.wt, t0);
+  extern __shared__ __attribute__((aligned(16))) char wg_lds[];
+  if constexpr (LDS_WG) {
+    constexpr int N = Chunk<TI>::N;
+    TI* W = reinterpret_cast<TI*>(wg_lds);
+    const int chunks = a.d * a.E / N;  // (d is a multiple of 64)
+    for (int p = threadIdx.x; p < chunks; p += 256) {
+      const auto v = *reinterpret_cast<const typename Chunk<TI>::vec*>(static_cast<const TI*>(a.Wg) + p * N);
+      int c = p * N / a.E, e = p * N - c * a.E;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        W[e * a.d + c] = v[i];
+        if (++e == a.E) {
+          e = 0;
+          ++c;
+        }
+      }
+    }
+    __syncthreads();
+    for (int64_t t0 = (int64_t)blockIdx.x * kTok; t0 < a.T; t0 += (int64_t)gridDim.x * kTok)
+      token_ds<TI, EP>(a, W, t0);
+  } else {
+    for (int64_t t0 = (int64_t)blockIdx.x * kTok; t0 < a.T; t0 += (int64_t)gridDim.x * kTok)
+      token_ds<TI, EP>(a, static_cast<const TI*>(a.wt), t0);
+  }
 }
 
 // Operands of the two products. A fragment covers 32 indices (lane % 32) and a piece of the
@@ -218,13 +252,97 @@ struct RowTile {
   }
 };
 
+// The columns' rows of W_g as first operands, 64 columns from c0: kept over a wave's tiles.
+template <typename TI, int EP>
+struct WgFrags;
+template <int EP>
+struct WgFrags<bf16, EP> {
+  s16x8 f[2][EP / 16];
+  __device__ __forceinline__ void load(const RouteGradArgs& a, int c0, int x, int h) {
+    const int E = a.E;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const short* w = static_cast<const short*>(a.Wg) + (size_t)min(c0 + 32 * b + x, a.d - 1) * E;
+#pragma unroll
+      for (int s = 0; s < EP / 16; ++s) {
+        const int e0 = 16 * s + 8 * h;
+        f[b][s] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+        if (E % 8 == 0) {
+          if (e0 < E) f[b][s] = *reinterpret_cast<const s16x8*>(w + e0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (e0 + i < E) f[b][s][i] = w[e0 + i];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void product(const RouteGradArgs& a, int64_t t, int h, f32x16 (&acc)[2]) const {
+    const bf16* hi = static_cast<const bf16*>(a.ds) + t * EP + 8 * h;
+    const bf16* lo = hi + a.T * EP;
+#pragma unroll
+    for (int s = 0; s < EP / 16; ++s) {
+      const s16x8 dh = *reinterpret_cast<const s16x8*>(hi + 16 * s);
+      const s16x8 dl = *reinterpret_cast<const s16x8*>(lo + 16 * s);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        acc[b] = mma(f[b][s], dh, acc[b]);
+        acc[b] = mma(f[b][s], dl, acc[b]);
+      }
+    }
+  }
+};
+// fp32: summed in the order e, EP / 2 + e, so that each lane's values are consecutive
+template <int EP>
+struct WgFrags<float, EP> {
+  float f[2][EP / 2];
+  __device__ __forceinline__ void load(const RouteGradArgs& a, int c0, int x, int h) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const float* w = static_cast<const float*>(a.Wg) + (size_t)min(c0 + 32 * b + x, a.d - 1) * a.E;
+#pragma unroll
+      for (int i = 0; i < EP / 2; ++i) {
+        const int e = h * (EP / 2) + i;
+        f[b][i] = e < a.E ? w[e] : 0.f;
+      }
+    }
+  }
+  __device__ __forceinline__ void product(const RouteGradArgs& a, int64_t t, int h, f32x16 (&acc)[2]) const {
+    const float* row = static_cast<const float*>(a.ds) + t * EP + h * (EP / 2);
+#pragma unroll
+    for (int i = 0; i < EP / 2; ++i) {
+      const float v = row[i];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) acc[b] = mma(f[b][i], v, acc[b]);
+    }
+  }
+};
+
+// The rows of a tile's slots, KM per token: entry ln + 64 i of the tile, -1 for none.
+template <int KM>
+struct TilePos {
+  int v[KM ? (32 * KM + 63) / 64 : 1];
+  __device__ __forceinline__ void fetch(const RouteGradArgs& a, int64_t t0, int ln) {
+    if constexpr (KM > 0) {
+#pragma unroll
+      for (int i = 0; i < (32 * KM + 63) / 64; ++i) {
+        const int at = ln + 64 * i, j = at % KM;
+        const int64_t tt = t0 + at / KM;
+        const int r = at < 32 * KM && tt < a.T && j < a.k ? a.pos[tt * a.k + j] : -1;
+        v[i] = r < a.R ? r : -1;
+      }
+    }
+  }
+};
+
 // dx of 32 tokens (t0 ..) and 64 columns (c0 ..), one wave: ds W_g^T with the columns as the
 // first operand, then through the wave's piece of LDS, so that rows and dx move in 16-byte
-// pieces, 128 or 256 contiguous bytes per row. The rows' loads go out first.
+// pieces, 128 or 256 contiguous bytes per row. The rows' loads go out first; `next` fetches the
+// following tile's slots behind them.
 template <typename TI, int EP, int KM>
-__device__ __forceinline__ void dx_tile(const RouteGradArgs& a, int64_t t0, int c0, float* buf, int* pos) {
-  const int ln = threadIdx.x & 63, x = ln & 31, h = ln >> 5, E = a.E;
-  const TI* W = static_cast<const TI*>(a.Wg);
+__device__ __forceinline__ void dx_tile(const RouteGradArgs& a, int64_t t0, int64_t t_next, int c0,
+                                        const WgFrags<TI, EP>& wg, TilePos<KM>& slots, float* buf, int* pos) {
+  const int ln = threadIdx.x & 63, x = ln & 31, h = ln >> 5;
   const int64_t t = min(t0 + x, a.T - 1);
   typedef RowTile<TI, KM> Rows;
   constexpr int N = Rows::N, PIECES = Rows::PIECES, RPI = Rows::RPI;
@@ -232,52 +350,13 @@ __device__ __forceinline__ void dx_tile(const RouteGradArgs& a, int64_t t0, int 
   Rows rows;
   if constexpr (KM > 0) {
 #pragma unroll
-    for (int i = 0; i < (32 * KM + 63) / 64; ++i) {
-      const int at = ln + 64 * i, j = at % KM;  // token at / KM, slot j
-      const int64_t tt = t0 + at / KM;
-      const int r = at < 32 * KM && tt < a.T && j < a.k ? a.pos[tt * a.k + j] : -1;
-      if (at < 32 * KM) pos[at] = r < a.R ? r : -1;
-    }
+    for (int i = 0; i < (32 * KM + 63) / 64; ++i)
+      if (ln + 64 * i < 32 * KM) pos[ln + 64 * i] = slots.v[i];
     rows.load(a, 0, pos, c_in, ln);
+    slots.fetch(a, t_next, ln);
   }
   f32x16 acc[2] = {zero16(), zero16()};
-  if constexpr (sizeof(TI) == 2) {
-    const bf16* hi = static_cast<const bf16*>(a.ds) + t * EP + 8 * h;
-    const bf16* lo = hi + a.T * EP;
-#pragma unroll
-    for (int s = 0; s < EP / 16; ++s) {
-      const s16x8 dh = *reinterpret_cast<const s16x8*>(hi + 16 * s);
-      const s16x8 dl = *reinterpret_cast<const s16x8*>(lo + 16 * s);
-      const int e0 = 16 * s + 8 * h;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const TI* w = W + (size_t)min(c0 + 32 * b + x, a.d - 1) * E;
-        s16x8 f = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (E % 8 == 0) {
-          if (e0 < E) f = *reinterpret_cast<const s16x8*>(w + e0);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (e0 + i < E) f[i] = reinterpret_cast<const short*>(w)[e0 + i];
-        }
-        acc[b] = mma(f, dh, acc[b]);
-        acc[b] = mma(f, dl, acc[b]);
-      }
-    }
-  } else {
-    // summed in the order e, EP / 2 + e: each lane's values are then consecutive
-    const float* row = static_cast<const float*>(a.ds) + t * EP + h * (EP / 2);
-#pragma unroll 8
-    for (int i = 0; i < EP / 2; ++i) {
-      const int e = h * (EP / 2) + i;
-      const float v = row[i];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const float f = e < E ? W[(size_t)min(c0 + 32 * b + x, a.d - 1) * E + e] : 0.f;
-        acc[b] = mma(f, v, acc[b]);
-      }
-    }
-  }
+  wg.product(a, t, h, acc);
   // [32 tokens][64 columns], 16-byte piece p of token row r at p ^ (r % 16)
 #pragma unroll
   for (int b = 0; b < 2; ++b)
@@ -345,9 +424,8 @@ __device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, 
       const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * width * 2));
       return s16x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
     };
-    for (int64_t t = t0; t < t1; t += kTile) {
-      // tokens past the chunk's end are zeros in both operands
-      u32x4 xv[4], dv[2 * EP / 32];
+    u32x4 xv[4], dv[2 * EP / 32];
+    auto load = [&](int64_t t) {  // tokens past the chunk's end are zeros in both operands
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int p = tid + 256 * i, r = p / 16, c = c0 + (p % 16) * 8;
@@ -359,6 +437,9 @@ __device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, 
         dv[i] = t + r < t1 ? ld16(D + ((lo ? a.T : 0) + t + r) * EP + (p % (EP / 8)) * 8)
                            : u32x4{0, 0, 0, 0};
       }
+    };
+    load(t0);
+    for (int64_t t = t0; t < t1; t += kTile) {
       __syncthreads();  // the last tile is no longer read
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -371,6 +452,7 @@ __device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, 
         st16((lo ? dl : dh) + r * EP * 2 + ((p % (EP / 8)) ^ sw(r, EP / 8)) * 16, dv[i]);
       }
       __syncthreads();
+      if (t + kTile < t1) load(t + kTile);  // in flight over this tile's products
 #pragma unroll
       for (int s = 0; s < kTile / 16; ++s) {
         const s16x8 f = frag(xs, kSlab, 16 * s, wave * 32);
@@ -408,7 +490,7 @@ __device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, 
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int e = 32 * n + 8 * (i / 4) + 4 * h + i % 4;
-        if (e < a.E) out[(size_t)c * a.E + e] = acc[n][i];
+        if (e < a.E) out[(size_t)e * a.d + c] = acc[n][i];
       }
   }
   // db's partial sum, in the first slab's workgroup: a wave takes every fourth token
@@ -438,11 +520,21 @@ __global__ __launch_bounds__(256) void route_products_kernel(RouteGradArgs a, in
     dw_chunk<TI, EP>(a, blockIdx.x / slabs, blockIdx.x % slabs, lds);
     return;
   }
-  const int wave = threadIdx.x >> 6;
-  const int64_t cols = (a.d + kDxCols - 1) / kDxCols, tiles = (a.T + 31) / 32 * cols;
-  for (int64_t i = blockIdx.x - dw_blocks; i < tiles; i += gridDim.x - dw_blocks) {
+  // kRun consecutive token tiles of a column block per workgroup, while W_g's rows are kept
+  const int wave = threadIdx.x >> 6, ln = threadIdx.x & 63;
+  const int64_t cols = (a.d + kDxCols - 1) / kDxCols, tiles = (a.T + 31) / 32;
+  const int64_t runs = (tiles + kRun - 1) / kRun * cols;
+  for (int64_t i = blockIdx.x - dw_blocks; i < runs; i += gridDim.x - dw_blocks) {
     const int c0 = (int)(i % cols) * kDxCols + wave * 64;
-    if (c0 < a.d) dx_tile<TI, EP, KM>(a, i / cols * 32, c0, reinterpret_cast<float*>(lds) + wave * 2048, pos[wave]);
+    if (c0 >= a.d) continue;
+    WgFrags<TI, EP> wg;
+    wg.load(a, c0, ln & 31, ln >> 5);
+    const int64_t first = i / cols * kRun, last = min(first + kRun, tiles);
+    TilePos<KM> slots;
+    slots.fetch(a, first * 32, ln);
+    for (int64_t n = first; n < last; ++n)
+      dx_tile<TI, EP, KM>(a, n * 32, (n + 1) * 32, c0, wg, slots, reinterpret_cast<float*>(lds) + wave * 2048,
+                          pos[wave]);
   }
 }
 
@@ -456,7 +548,8 @@ __global__ __launch_bounds__(256) void route_sum_kernel(RouteGradArgs a, int chu
   for (int c = 0; c < chunks; ++c) v += a.partial[c * n + i];
   const size_t nw = (size_t)a.d * a.E;
   if (i < nw) {
-    if (a.dWg) static_cast<TI*>(a.dWg)[i] = (TI)v;
+    const size_t e = i / a.d, c = i - e * a.d;
+    if (a.dWg) static_cast<TI*>(a.dWg)[c * a.E + e] = (TI)v;
   } else if (a.db) {
     a.db[i - nw] = v;
   }
@@ -472,17 +565,24 @@ hipError_t launch(RouteGradArgs a, hipStream_t s) {
   const int chunks = (int)chunks_of(a.T);
   hipError_t e = hipSuccess;
   if (a.T > 0) {
-    if (a.z_loss_grad != 0.f) {
+    const size_t wg_bytes = (size_t)a.d * a.E * sizeof(TI);
+    const unsigned grid = capped_grid((a.T + kTok - 1) / kTok);
+    if (a.z_loss_grad == 0.f) {
+      ds_kernel<TI, EP, false><<<grid, 256, 0, s>>>(a);
+    } else if (wg_bytes <= kLdsWg) {
+      // (as many workgroups as two per CU: each brings W_g into its LDS once)
+      ds_kernel<TI, EP, true><<<grid < 512 ? grid : 512, 256, wg_bytes, s>>>(a);
+    } else {
       const bool b16 = sizeof(TI) == 2;
       transpose_kernel<<<(a.d * a.E + 255) / 256, 256, 0, s>>>(
           b16 ? static_cast<const uint16_t*>(a.Wg) : nullptr,
           b16 ? nullptr : static_cast<const uint32_t*>(a.Wg), a.d, a.E, a.wt);
       if ((e = hipGetLastError()) != hipSuccess) return e;
+      ds_kernel<TI, EP, false><<<grid, 256, 0, s>>>(a);
     }
-    ds_kernel<TI, EP><<<capped_grid((a.T + kTok - 1) / kTok), 256, 0, s>>>(a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int dw_blocks = dw ? chunks * ((a.d + kSlab - 1) / kSlab) : 0;
-    const int64_t dx_blocks = a.dx ? (a.T + 31) / 32 * ((a.d + kDxCols - 1) / kDxCols) : 0;
+    const int64_t dx_blocks = a.dx ? (a.T + 32 * kRun - 1) / (32 * kRun) * ((a.d + kDxCols - 1) / kDxCols) : 0;
     if (dw_blocks || dx_blocks) {
       const unsigned grid = dw_blocks + (dx_blocks ? capped_grid(dx_blocks) : 0);
       const int km = a.rows && a.R > 0 ? a.k : 0;
