@@ -419,21 +419,117 @@ class SparseMoE:
     dimensions, [..., d_model] (the [batch, seq, d_model] input of the pages' layer
     modules): the tokens are those dimensions flattened (a view of the contiguous x), and
     y comes back with x's leading shape. The workspace is kept and reused while it is
-    large enough; ``last`` holds the full result of the latest call (routing, f, p, loss)."""
+    large enough; ``last`` holds the full result of the latest call (routing, f, p, loss).
+
+    As a block with its norms (``moe_block_norm``): with ``pre_gamma`` the layer reads
+    u = x / rms(x) * pre_gamma; with ``post_gamma`` the call returns
+    residual_scale * x + gate * (y / rms(y) * post_gamma) in x's type (``gate`` fp32 [d_model]
+    or None).
+
+    ``backward(d_out)`` gives the gradients of the latest call (token choice, with or without
+    a capacity, no training noise). It reads that call's x, u, y and workspace: x must not
+    have been changed since."""
 
     def __init__(self, W_g, W_gate, W_up, W_down, b_g=None, *, k=2, mode="tc",
-                 capacity_factor=1.0, renormalize=True):
+                 capacity_factor=1.0, renormalize=True, pre_gamma=None, post_gamma=None, gate=None,
+                 residual_scale=1.0, norm_eps=1e-6):
+        if gate is not None and post_gamma is None:
+            raise ValueError("gate needs post_gamma")
         self.W_g, self.W_gate, self.W_up, self.W_down, self.b_g = W_g, W_gate, W_up, W_down, b_g
         self.k, self.mode, self.cf, self.renormalize = k, mode, capacity_factor, renormalize
+        self.pre_gamma, self.post_gamma, self.gate = pre_gamma, post_gamma, gate
+        self.residual_scale, self.norm_eps = residual_scale, norm_eps
         self._ws = None
         self.last = None
 
     def __call__(self, x, **kw):
         _need(x, "x")
         lead, d = x.shape[:-1], x.shape[-1]
-        out = moe_forward(x.view(-1, d), self.W_g, self.b_g, self.W_gate, self.W_up,
+        x2 = x.view(-1, d)
+        pre = None
+        if self.pre_gamma is not None:
+            pre = moe_block_norm(x2, gamma=self.pre_gamma, eps=self.norm_eps)
+        u = x2 if pre is None else pre["u"]
+        out = moe_forward(u, self.W_g, self.b_g, self.W_gate, self.W_up,
                           self.W_down, k=self.k, mode=self.mode, capacity_factor=self.cf,
                           renormalize=self.renormalize, workspace=self._ws, **kw)
         self._ws = out["workspace"]
+        out["x"], out["u"], out["noise"] = x2, u, kw.get("eps") is not None
+        out["rstd"] = None if pre is None else pre["rstd"]
         self.last = out
-        return out["y"].view(*lead, d)
+        if self.post_gamma is None:
+            return out["y"].view(*lead, d)
+        post = moe_block_norm(x2, y=out["y"], gamma_post=self.post_gamma, gate=self.gate,
+                              residual_scale=self.residual_scale, eps=self.norm_eps)
+        out["out"], out["rstd_post"] = post["out"], post["rstd_post"]
+        return post["out"].view(*lead, d)
+
+    def backward(self, d_out, *, loss_grad=0.0, z_loss_grad=0.0) -> dict:
+        """Gradients of the latest call, given d_out, the gradient of what it returned, and
+        the gradients of the load-balancing loss and the z-loss: dx, dW_g, dW_gate, dW_up,
+        dW_down (their tensors' types) and, where present, db_g, d_pre_gamma, d_post_gamma,
+        d_gate (fp32).
+
+        The gate and up products are formed again from the call's routing. bf16: those
+        products, dy, the hidden gradients and the routed rows' gradients are rounded to bf16
+        between the kernels; every sum is fp32."""
+        last = self.last
+        if last is None:
+            raise ValueError("backward needs a call of the layer")
+        if self.mode not in ("tc", "tc_capacity"):
+            raise ValueError("backward is for token choice")
+        if last["noise"]:
+            raise ValueError("backward is for calls without training noise")
+        if last["probs"] is None or last["idx"] is None or (loss_grad != 0 and last["f"] is None):
+            raise ValueError("backward needs the call's routing (want_routing, want_probs, want_stats)")
+        x, u, dt = last["x"], last["u"], last["x"].dtype
+        T, d = x.shape
+        d_out = d_out.reshape(T, d)
+        residual, post = None, None
+        if self.post_gamma is not None:
+            post = moe_block_norm_backward(last["out"], d_out=d_out.to(dt).contiguous(), y=last["y"],
+                                           rstd_post=last["rstd_post"], gamma_post=self.post_gamma,
+                                           gate=self.gate, residual_scale=self.residual_scale)
+            dy, residual = post["dy"], post["dx"]
+        else:
+            dy = d_out.to(dt).contiguous()
+
+        E, k, R = self.W_g.shape[1], self.k, T * self.k
+        ws, shape = last["workspace"].view(torch.uint8).view(-1), last["shape"]
+
+        def routing(which, n):
+            at = workspace_offset(shape, which)
+            return ws[at:at + 4 * n].view(torch.int32)
+
+        offsets, src, pos = routing(WS_OFFSETS, E + 1), routing(WS_SRC, R), routing(WS_POS, R).view(T, k)
+        if T == 0:
+            offsets = torch.zeros_like(offsets)  # (a call without tokens leaves the workspace alone)
+        g = moe_grouped_matmul(u, self.W_gate, offsets, gather_a=src)
+        up = moe_grouped_matmul(u, self.W_up, offsets, gather_a=src)
+        dh = moe_grouped_matmul(dy, self.W_down, offsets, form="nt", gather_a=src)
+        act = moe_swiglu_backward(g, up, dh, last["w"], src=src, pos=pos, offsets=offsets, inplace=True)
+        dg, du, h = act["dg"], act["du"], act["h"]
+        grads = {
+            "dW_gate": moe_grouped_matmul(u, dg, offsets, form="tn", gather_a=src),
+            "dW_up": moe_grouped_matmul(u, du, offsets, form="tn", gather_a=src),
+            "dW_down": moe_grouped_matmul(h, dy, offsets, form="tn", gather_b=src),
+        }
+        rows = moe_grouped_matmul(dg, self.W_gate, offsets, form="nt", out_dtype=torch.float32)
+        moe_grouped_matmul(du, self.W_up, offsets, form="nt", out=rows, accumulate=True)
+        r = moe_route_backward(u, self.W_g, last["probs"], last["idx"], last["w"], act["dw"], b_g=self.b_g,
+                               f=last["f"], loss_grad=loss_grad, z_loss_grad=z_loss_grad,
+                               renormalize=self.renormalize, rows=rows.to(dt), pos=pos)
+        grads["dW_g"] = r["dW_g"]
+        if self.b_g is not None:
+            grads["db_g"] = r["db_g"]
+        if self.pre_gamma is not None:
+            pre = moe_block_norm_backward(x, d_out=residual, d_u=r["dx"], rstd=last["rstd"],
+                                          gamma=self.pre_gamma)
+            grads["dx"], grads["d_pre_gamma"] = pre["dx"], pre["dgamma"]
+        else:
+            grads["dx"] = r["dx"] if residual is None else residual + r["dx"]
+        if post is not None:
+            grads["d_post_gamma"] = post["dgamma_post"]
+            if self.gate is not None:
+                grads["d_gate"] = post["dgate"]
+        return grads

@@ -633,3 +633,180 @@ def test_norm_many_rows(moe):
     got = moe.moe_block_norm_backward(dx_, d_u=ddu, rstd=f["rstd"], gamma=dgm)
     z = x.double() * f["rstd"].double().cpu()[:, None]
     close(got["dgamma"], (du.double() * z).sum(0), (du.double() * z).abs().sum(0), T + 8)
+
+
+# ---- together: one layer's training step -----------------------------------------------
+def layer_inputs(T, d, f, E, dt, seed):
+    r = gen(seed)
+    return dict(x=draw(r, T, d, dtype=dt), W_g=draw(r, d, E, std=0.1, dtype=dt), b_g=draw(r, E, std=0.5),
+                W_gate=draw(r, E, d, f, std=d ** -0.5, dtype=dt), W_up=draw(r, E, d, f, std=d ** -0.5, dtype=dt),
+                W_down=draw(r, E, f, d, std=f ** -0.5, dtype=dt), pre_gamma=1 + draw(r, d, std=0.1),
+                post_gamma=1 + draw(r, d, std=0.1), gate=draw(r, d), d_out=draw(r, T, d, dtype=dt))
+
+
+def layer_ref(t, idx, kept, k, renorm, norms, lg, zg, eps):
+    """Gradients by automatic differentiation of the layer's definition in 64 bits, with the
+    forward's choice of experts and of kept slots."""
+    p = {n: v.double().requires_grad_() for n, v in t.items() if n != "d_out"}
+    x = p["x"]
+    T, E = x.shape[0], p["W_g"].shape[1]
+    rms = lambda v: (v.square().mean(1, keepdim=True) + eps).sqrt()  # noqa: E731
+    u = x / rms(x) * p["pre_gamma"] if norms else x
+    logits = u @ p["W_g"] + p["b_g"]
+    prob = torch.softmax(logits, 1)
+    sel = prob.gather(1, idx) * kept
+    w = sel / sel.sum(1, keepdim=True).clamp_min(1e-300) if renorm else sel
+    y = torch.zeros_like(x)
+    for e in range(E):
+        tok, slot = torch.nonzero((idx == e) & kept, as_tuple=True)
+        g = u[tok] @ p["W_gate"][e]
+        h = g / (1 + torch.exp(-g)) * (u[tok] @ p["W_up"][e])
+        y = y.index_add(0, tok, (h @ p["W_down"][e]) * w[tok, slot][:, None])
+    out = 0.5 * x + p["gate"] * (y / rms(y) * p["post_gamma"]) if norms else y
+    f = torch.bincount(idx.reshape(-1), minlength=E).double() / T
+    total = (out * t["d_out"].double()).sum() + lg * E * (f / k * prob.mean(0)).sum() \
+        + zg * torch.logsumexp(logits, 1).square().mean()
+    total.backward()
+    return {"d" + n if not n.endswith(("gamma", "gate")) or n == "W_gate" else "d_" + n: v.grad
+            for n, v in p.items() if v.grad is not None}
+
+
+@pytest.mark.parametrize("mode", ["tc", "tc_capacity"])
+@pytest.mark.parametrize("dt", [BF16, FP32])
+@pytest.mark.parametrize("norms,renorm", [(False, True), (True, True), (True, False)])
+def test_layer_backward(moe, mode, dt, norms, renorm):
+    say("layer", mode, dt, norms, renorm)
+    T, d, f, E, k, eps = 173, 128, 192, 8, 2, 1e-5
+    t = layer_inputs(T, d, f, E, dt, 21)
+    dev = {n: v.cuda() for n, v in t.items()}
+    kw = dict(pre_gamma=dev["pre_gamma"], post_gamma=dev["post_gamma"], gate=dev["gate"],
+              residual_scale=0.5, norm_eps=eps) if norms else {}
+    layer = moe.SparseMoE(dev["W_g"], dev["W_gate"], dev["W_up"], dev["W_down"], dev["b_g"], k=k, mode=mode,
+                          capacity_factor=0.9, renormalize=renorm, **kw)
+    lg, zg = 0.02 * T, 0.01 * T
+    out = layer(dev["x"].view(1, T, d))
+    assert out.shape == (1, T, d)
+    got = layer.backward(dev["d_out"].view(1, T, d), loss_grad=lg, z_loss_grad=zg)
+    kept = layer.last["w"].cpu() != 0
+    assert mode == "tc" or not bool(kept.all())
+    ref = layer_ref(t, layer.last["idx"].cpu().long(), kept, k, renorm, norms, lg, zg, eps)
+    assert set(got) == set(ref), (sorted(got), sorted(ref))
+    # Of each gradient's size, in the 2-norm. bf16: at most eight values on the way are
+    # rounded (u, the two products, dy, dh, the hidden gradient, the rows, the result), half a
+    # step of 2^-8 each. fp32: the longest chain of sums has d + f + d terms and T more.
+    tol = 8 * 2.0 ** -8 if dt == BF16 else (2 * d + f + T) * U * 8
+    for n in ref:
+        assert got[n].shape == ref[n].shape, n
+        err = float((got[n].double().cpu() - ref[n]).norm() / ref[n].norm())
+        assert err <= tol, (n, err)
+    # the same call again gives the same bits
+    layer(dev["x"])
+    again = layer.backward(dev["d_out"], loss_grad=lg, z_loss_grad=zg)
+    for n in got:
+        assert torch.equal(got[n], again[n]), n
+
+
+def test_layer_backward_without_tokens_and_refusals(moe):
+    say("layer none")
+    t = {n: v.cuda() for n, v in layer_inputs(0, 64, 64, 4, BF16, 3).items()}
+    layer = moe.SparseMoE(t["W_g"], t["W_gate"], t["W_up"], t["W_down"], t["b_g"])
+    with pytest.raises(ValueError):
+        layer.backward(t["d_out"])
+    layer(t["x"])
+    got = layer.backward(t["d_out"])
+    assert got["dx"].shape == (0, 64) and not any(bool(got[n].any()) for n in got if n != "dx")
+    x = torch.randn(32, 64, device="cuda").to(BF16)
+    layer(x, eps=torch.randn(32, 4, device="cuda"))
+    with pytest.raises(ValueError):
+        layer.backward(x)
+    layer(x, want_probs=False)
+    with pytest.raises(ValueError):
+        layer.backward(x)
+    ec = moe.SparseMoE(t["W_g"], t["W_gate"], t["W_up"], t["W_down"], mode="ec")
+    ec(x, want_stats=False)
+    with pytest.raises(ValueError):
+        ec.backward(x)
+
+
+def test_layer_step_captured_in_a_graph(moe):
+    # forward and backward of a block as one graph, replayed on new values with eager work of
+    # the same operators, on the same shapes, between the replays
+    say("graph")
+    T, d, f, E = 300, 128, 128, 8
+    t = {n: v.cuda() for n, v in layer_inputs(T, d, f, E, BF16, 5).items()}
+
+    def make():
+        return moe.SparseMoE(t["W_g"], t["W_gate"], t["W_up"], t["W_down"], t["b_g"], pre_gamma=t["pre_gamma"],
+                             post_gamma=t["post_gamma"], gate=t["gate"])
+
+    def step(layer, x, d_out):
+        out = layer(x)
+        return dict(layer.backward(d_out, loss_grad=1.0, z_loss_grad=0.5), out=out)
+
+    layer, x, d_out = make(), t["x"].clone(), t["d_out"].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(layer, x, d_out)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap = step(layer, x, d_out)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    for rep in range(4):
+        x.copy_(torch.randn(T, d, device="cuda", generator=g))
+        d_out.copy_(torch.randn(T, d, device="cuda", generator=g))
+        eager = step(make(), x, d_out)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in eager:
+            assert torch.equal(cap[n], eager[n]), (rep, n)
+
+
+def test_operators_run_on_the_current_stream(moe):
+    # two streams at once, each with inputs made on it: nothing runs on another stream
+    say("streams")
+    R, E, K, N = 700, 8, 256, 512
+    g = gen(31)
+    a, b = draw(g, R, K, dtype=BF16), draw(g, E, K, N, dtype=BF16)
+    off = offsets_of([R // E] * (E - 1) + [R - R // E * (E - 1)])
+    want = moe.moe_grouped_matmul(*cuda(a, b, off))
+    gm = torch.ones(K, device="cuda")
+    wn = moe.moe_block_norm(a.cuda(), gamma=gm)["u"]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    ha, hb, ho = a.pin_memory(), b.pin_memory(), off.pin_memory()
+    for s in streams:
+        with torch.cuda.stream(s):
+            da, db, do = (h.to("cuda", non_blocking=True) for h in (ha, hb, ho))
+            for _ in range(20):
+                y = moe.moe_grouped_matmul(da, db, do)
+                u = moe.moe_block_norm(da, gamma=gm)["u"]
+            got.append((y, u, da, db, do))
+    torch.cuda.synchronize()
+    for y, u, *_ in got:
+        assert torch.equal(y, want) and torch.equal(u, wn)
+
+
+def test_workspace_of_another_call_changes_nothing(moe):
+    # a caller's workspace, larger than needed and full of other values
+    say("workspace")
+    s = route_inputs(130, 128, 8, 2, BF16, True, 4)
+    x, W, p, idx, w, dw = cuda(*(s[n] for n in ("x", "W", "probs", "idx", "w", "dw")))
+    want = moe.moe_route_backward(x, W, p, idx, w, dw, z_loss_grad=1.0)
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    got = moe.moe_route_backward(x, W, p, idx, w, dw, z_loss_grad=1.0, workspace=ws)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    gm = torch.ones(128, device="cuda")
+    f = moe.moe_block_norm(x, gamma=gm)
+    a = moe.moe_block_norm_backward(x, d_u=x, rstd=f["rstd"], gamma=gm)
+    b = moe.moe_block_norm_backward(x, d_u=x, rstd=f["rstd"], gamma=gm, workspace=ws)
+    assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dgamma"], b["dgamma"])
+    rows, cols = draw(gen(5), 4000, 64, dtype=BF16).cuda(), draw(gen(6), 4000, 72, dtype=BF16).cuda()
+    off = torch.tensor([0, 4000], dtype=torch.int32, device="cuda")
+    a = moe.moe_grouped_matmul(rows, cols, off, form="tn")
+    b = moe.moe_grouped_matmul(rows, cols, off, form="tn", workspace=ws)
+    assert torch.equal(a, b)
