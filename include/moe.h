@@ -309,7 +309,8 @@ typedef enum moe_matmul_form {
 } moe_matmul_form;
 
 typedef struct moe_matmul_shape {
-  int64_t R;          /* rows of the grouped problem; groups end at or before R */
+  int64_t R;          /* rows of the grouped problem (at most 2^31 - 2^16); groups end at or
+                         before R */
   int64_t rows_a;     /* rows of a: R without gather_a */
   int64_t rows_b;     /* TN: rows of b, R without gather_b; ignored otherwise */
   int64_t K;          /* width of a */

@@ -11,6 +11,8 @@ namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 31, kMaxWidth = 1 << 20;
 constexpr int64_t kMaxNormWidth = 16384;
+// The grouped products count rows past a group's end, by up to a tile or a ring turn, in int32.
+constexpr int64_t kMaxMatmulRows = kMaxRows - (1 << 16);
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 template <typename... P>
@@ -33,7 +35,7 @@ moe_status check_matmul(const moe_matmul_shape* s) {
     return MOE_ERR_BAD_SHAPE;
   if (bad_dtype(s->dtype) || bad_dtype(s->out_dtype) || bad_flag(s->accumulate))
     return MOE_ERR_BAD_SHAPE;
-  if (s->R < 0 || s->R >= kMaxRows || s->rows_a < 0 || s->rows_a >= kMaxRows || s->E < 1)
+  if (s->R < 0 || s->R > kMaxMatmulRows || s->rows_a < 0 || s->rows_a >= kMaxRows || s->E < 1)
     return MOE_ERR_BAD_SHAPE;
   if (s->form == MOE_MATMUL_TN && (s->rows_b < 0 || s->rows_b >= kMaxRows))
     return MOE_ERR_BAD_SHAPE;
@@ -286,7 +288,8 @@ moe_status moe_block_norm_backward(const moe_norm_shape* shape, const void* d_ou
   const moe_norm_shape& s = *shape;
   if (!y && (gamma_post || gate || rstd_post || dy || dgamma_post || dgate || s.gate != MOE_GATE_NONE))
     return MOE_ERR_BAD_SHAPE;
-  if ((s.gate != MOE_GATE_NONE) != (gate != nullptr) || (dgate && !gate)) return MOE_ERR_BAD_SHAPE;
+  if ((s.gate != MOE_GATE_NONE) != (gate != nullptr) || (dgate && !gate) || (dgamma && !d_u))
+    return MOE_ERR_BAD_SHAPE;
   if (!all_aligned16(d_out, d_u, out, gamma, y, gamma_post, dx, dy, ws) ||
       (s.gate == MOE_GATE_CHANNEL && !aligned16(gate)))
     return MOE_ERR_MISALIGNED;
