@@ -374,7 +374,8 @@ __device__ __forceinline__ Item locate(const MatmulArgs& a, const Groups& g, int
 
 // TN: row indices of a ring turn (four stages) of a group: a wave loads RW of each stage's BK
 // rows, so lane l < 4 RW holds a's row of stage l / RW, place l % RW, and lane 32 + l b's.
-// Rows past the group's end give its last one again.
+// Rows past the group's end give its last one again. Fetched a turn ahead and used (clamped)
+// in the next: a use here would wait for the load, and with it for everything in flight.
 template <class G>
 __device__ __forceinline__ int fetch_turn(const MatmulArgs& a, const Item& t, int turn, int wave, int lane) {
   if constexpr (G::TN) {
@@ -382,13 +383,18 @@ __device__ __forceinline__ int fetch_turn(const MatmulArgs& a, const Item& t, in
     const int l = (lane & 31) % (kStages * G::RW);
     const int64_t at = (int64_t)t.r0 + (int64_t)turn * (kStages * G::BK) + l / G::RW * G::BK +
                        wave * G::RW + l % G::RW;
-    const int64_t r = max(min(at, (int64_t)t.r1 - 1), (int64_t)0);
-    const bool is_a = lane < 32;
-    const int32_t* g = is_a ? a.gather_a : a.gather_b;
-    const int64_t rows = is_a ? a.rows_a : a.rows_b;
-    return (int)(g ? min(max((int64_t)g[r], (int64_t)0), rows - 1) : r);
+    const int r = (int)max(min(at, (int64_t)t.r1 - 1), (int64_t)0);
+    const int32_t* g = lane < 32 ? a.gather_a : a.gather_b;
+    int v = r;
+    if (g) v = g[r];
+    return v;
   }
   return 0;
+}
+template <class G>
+__device__ __forceinline__ int use_turn(const MatmulArgs& a, int turn, int lane) {
+  const int64_t rows = lane < 32 ? a.rows_a : a.rows_b;
+  return G::TN ? (int)min(max((int64_t)turn, (int64_t)0), rows - 1) : 0;
 }
 
 // NN, NT: the rows of a that this lane's loads of a tile read (fetched long before their use).
@@ -557,7 +563,7 @@ __global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
   make_loader<G>(a, t, wave, ln, rows, ld);
   Frags<G> F0, F1;
   // TN: row indices of the turn whose loads come next, and of the next tile's first turn
-  int turn = fetch_turn<G>(a, t, 0, wave, ln), turn_first = 0;
+  int turn = use_turn<G>(a, fetch_turn<G>(a, t, 0, wave, ln), ln), turn_first = 0;
 #pragma unroll
   for (int q = 0; q < kStages; ++q)
 #pragma unroll
@@ -590,7 +596,7 @@ __global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
   Wait<G>::run();              \
   Step<G, J, CLAMP, true>::run(RS, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1)
     for (; kt + 2 * kStages <= whole && kt + kStages < end; kt += kStages) {
-      const int now = turn;
+      const int now = use_turn<G>(a, turn, ln);
       turn = fetch_turn<G>(a, cur, kt / kStages + 2, wave, ln);
       MOE_STEP(0, false, kt + 4);
       MOE_STEP(1, false, kt + 5);
@@ -598,7 +604,7 @@ __global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
       MOE_STEP(3, false, kt + 7);
     }
     if (kt + kStages < end) {  // the refills end past len
-      const int now = turn;
+      const int now = use_turn<G>(a, turn, ln);
       MOE_STEP(0, true, kt + 4);
       MOE_STEP(1, true, kt + 5);
       MOE_STEP(2, true, kt + 6);
@@ -608,7 +614,7 @@ __global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
     }
     // the last turn: the next item's first stages (without one, this item's, never used)
     if (more) make_loader<G>(a, t, wave, ln, rows, ld);
-    const int now = turn_first;
+    const int now = use_turn<G>(a, turn_first, ln);
     turn = fetch_turn<G>(a, t, 1, wave, ln);
 #define MOE_LAST(J)                                                                             \
   Wait<G>::run();                                                                               \
