@@ -12,6 +12,8 @@
 // What is out of range is never loaded: addresses are clamped to the last row, column or
 // chunk, and the values of the summed axis past its end are zeroed in both operands'
 // fragments (the last stage only), so that a non-finite value there reaches no sum.
+#include <type_traits>
+
 #include "train_common.h"
 #include "train_kernels.h"
 
@@ -244,8 +246,9 @@ __device__ __forceinline__ void mask_frags(Frags<G>& F, int left, int ln) {
 // stage's buffer is free. Then the stage's MFMAs, with the reads of the next stage into Fn and
 // the refill of this buffer (stage `rs` of ld) spread between them.
 // Every step loads and reads the same amounts, so that the loads in flight are known at
-// every wait: past an item's last stage the refills are the next item's first stages, and an
-// item is a whole number of ring turns, whose spare stages (CALC false) skip the MFMAs.
+// every wait (where paths join inside a turn, the compiler loses count and waits for all of
+// them): past an item's last stage the refills are the next item's first stages, and an item
+// is a whole number of ring turns, whose spare stages run on zeros.
 template <class G>
 struct Wait {
   static __device__ __forceinline__ void run() {
@@ -255,7 +258,7 @@ struct Wait {
     sync_point();
   }
 };
-template <class G, int J, bool CLAMP, bool CALC>
+template <class G, int J, bool CLAMP>
 struct Step {
   static __device__ __forceinline__ void run(int rs, int turn, char* const (&ring)[kStages],
                                              const Loader<G>& ld, Wave<G>& w, Frags<G>& Fc,
@@ -265,10 +268,8 @@ struct Step {
     char* const dst = ring[J];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      if constexpr (CALC) {
 #pragma unroll
-        for (int m = NM * g / NG; m < NM * (g + 1) / NG; ++m) w.mfma(m, Fc);
-      }
+      for (int m = NM * g / NG; m < NM * (g + 1) / NG; ++m) w.mfma(m, Fc);
 #pragma unroll
       for (int r = NR * g / NG; r < NR * (g + 1) / NG; ++r) w.read(r, src, Fn);
       Issue<G, CLAMP>::run(ld, g, rs, turn, J, dst);
@@ -372,49 +373,62 @@ __device__ __forceinline__ Item locate(const MatmulArgs& a, const Groups& g, int
   return t;
 }
 
-// TN: row indices of a ring turn (four stages) of a group: a wave loads RW of each stage's BK
-// rows, so lane l < 4 RW holds a's row of stage l / RW, place l % RW, and lane 32 + l b's.
-// Rows past the group's end give its last one again. Fetched a turn ahead and used (clamped)
-// in the next: a use here would wait for the load, and with it for everything in flight.
+// TN: rows of the problem that a wave loads in a ring turn (four stages) of a group: RW of each
+// stage's BK rows, so lane l < 4 RW stands for a's row of stage l / RW, place l % RW, and lane
+// 32 + l for b's. Rows past the group's end give its last one again.
+template <class G>
+__device__ __forceinline__ int turn_row(const Item& t, int turn, int wave, int lane) {
+  static_assert(!G::TN || kStages * G::RW <= 32, "a turn's rows in half a wave");
+  const int l = (lane & 31) % (kStages * G::RW);
+  const int64_t at = (int64_t)t.r0 + (int64_t)turn * (kStages * G::BK) + l / G::RW * G::BK +
+                     wave * G::RW + l % G::RW;
+  return (int)max(min(at, (int64_t)t.r1 - 1), (int64_t)0);
+}
+// Their gathered indices, fetched ahead and taken (clamped) a turn later. The load is always
+// issued (without a gather, of any word): under a test the compiler would copy its value, and
+// so wait for it, and for everything in flight, right away.
 template <class G>
 __device__ __forceinline__ int fetch_turn(const MatmulArgs& a, const Item& t, int turn, int wave, int lane) {
-  if constexpr (G::TN) {
-    static_assert(kStages * G::RW <= 32, "a turn's rows in half a wave");
-    const int l = (lane & 31) % (kStages * G::RW);
-    const int64_t at = (int64_t)t.r0 + (int64_t)turn * (kStages * G::BK) + l / G::RW * G::BK +
-                       wave * G::RW + l % G::RW;
-    const int r = (int)max(min(at, (int64_t)t.r1 - 1), (int64_t)0);
-    const int32_t* g = lane < 32 ? a.gather_a : a.gather_b;
-    int v = r;
-    if (g) v = g[r];
-    return v;
-  }
-  return 0;
+  if constexpr (!G::TN) return 0;
+  const int32_t* g = lane < 32 ? a.gather_a : a.gather_b;
+  const int32_t* p = g ? g + turn_row<G>(t, turn, wave, lane) : a.offsets;
+  return *p;
 }
 template <class G>
-__device__ __forceinline__ int use_turn(const MatmulArgs& a, int turn, int lane) {
+__device__ __forceinline__ int take_turn(const MatmulArgs& a, const Item& t, int turn, int fetched, int wave,
+                                         int lane) {
+  if constexpr (!G::TN) return 0;
   const int64_t rows = lane < 32 ? a.rows_a : a.rows_b;
-  return G::TN ? (int)min(max((int64_t)turn, (int64_t)0), rows - 1) : 0;
+  const bool gathers = (lane < 32 ? a.gather_a : a.gather_b) != nullptr;
+  const int g = (int)min(max((int64_t)fetched, (int64_t)0), rows - 1);
+  return here(gathers ? g : turn_row<G>(t, turn, wave, lane));
 }
 
-// NN, NT: the rows of a that this lane's loads of a tile read (fetched long before their use).
+// What a tile's loads take from memory, raw: NN, NT the gathered rows of a of this lane's
+// loads, TN the row indices of the first turn.
 template <class G>
-__device__ __forceinline__ void fetch_rows(const MatmulArgs& a, const Item& t, int wave, int lane,
-                                           int (&rows)[G::A::PW]) {
-  if constexpr (!G::TN) {
-    const int ln = here(lane), m0 = t.r0 + t.mt * G::BM;
+struct Ahead {
+  int rows[G::TN ? 1 : G::A::PW], turn;
+  static __device__ __forceinline__ int row(const Item& t, int j, int wave, int ln) {
+    return min(t.r0 + t.mt * G::BM + G::A::row(j, wave, ln), t.r1 - 1);
+  }
+  __device__ __forceinline__ void fetch(const MatmulArgs& a, const Item& t, int wave, int lane) {
+    turn = fetch_turn<G>(a, t, 0, wave, lane);
+    if constexpr (!G::TN) {
+      const int ln = here(lane);
 #pragma unroll
-    for (int j = 0; j < G::A::PW; ++j) {
-      const int r = min(m0 + G::A::row(j, wave, ln), t.r1 - 1);
-      rows[j] = a.gather_a ? a.gather_a[r] : r;
+      for (int j = 0; j < G::A::PW; ++j) {
+        const int32_t* p = a.gather_a ? a.gather_a + row(t, j, wave, ln) : a.offsets;
+        rows[j] = *p;
+      }
     }
   }
-}
+};
 
 // The item's sources, in `ld`.
 template <class G>
 __device__ __forceinline__ void make_loader(const MatmulArgs& a, const Item& t, int wave, int lane,
-                                            const int (&rows)[G::A::PW], Loader<G>& ld) {
+                                            const Ahead<G>& ahead, Loader<G>& ld) {
   const int K = (int)a.K, N = (int)a.N, n0 = t.nt * G::BN;
   typedef typename G::type T;
   constexpr int C = G::EPC;
@@ -437,8 +451,11 @@ __device__ __forceinline__ void make_loader(const MatmulArgs& a, const Item& t, 
     ld.len = t.len;
     ld.step_a = G::BK;
 #pragma unroll
-    for (int j = 0; j < G::A::PW; ++j)
-      ld.pa[j] = A + (size_t)min(max((int64_t)rows[j], (int64_t)0), a.rows_a - 1) * K + t.k0 + G::A::chunk(j, wave, ln) * C;
+    for (int j = 0; j < G::A::PW; ++j) {
+      const int64_t g = min(max((int64_t)ahead.rows[j], (int64_t)0), a.rows_a - 1);
+      const int64_t r = a.gather_a ? g : Ahead<G>::row(t, j, wave, ln);
+      ld.pa[j] = A + (size_t)r * K + t.k0 + G::A::chunk(j, wave, ln) * C;
+    }
     if constexpr (G::FORM == MOE_MATMUL_NT) {
       ld.step_b = G::BK;
 #pragma unroll
@@ -492,9 +509,14 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const Item& t, i
         }
     }
   } else {
-    constexpr int SEG = G::OUT_BYTES / 32, CHUNKS = SEG / 16;       // of a row, per pass
-    constexpr int COLS = SEG / (int)sizeof(TO), BLOCKS = COLS / 32; // columns, 32-column blocks
-    constexpr int RPS = 64 / CHUNKS;                                // rows per store instruction
+    // The values are put there in fp32 by the 256-row tiles, whose accumulators go into LDS
+    // as they are (converting them first takes registers those tiles do not have: the
+    // spills' reloads wait for every load and store in flight), in TO by the 128-row ones.
+    typedef typename std::conditional<G::BM == 256, float, TO>::type TL;
+    constexpr int SEG = G::OUT_BYTES / 32, CHUNKS = SEG / 16;        // of a row, per pass
+    constexpr int COLS = SEG / (int)sizeof(TL), BLOCKS = COLS / 32;  // columns, 32-column blocks
+    constexpr int N16 = 16 / (int)sizeof(TO), PER = COLS / N16;      // a lane's columns; lanes per row
+    constexpr int RPS = 64 / PER;                                    // rows per store instruction
 #pragma unroll
     for (int mb = 0; mb < G::MB; ++mb)
 #pragma unroll
@@ -505,17 +527,27 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const Item& t, i
         for (int nb = 0; nb < BLOCKS; ++nb)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int at = (nb * 32 + 8 * q + 4 * (ln >> 5)) * (int)sizeof(TO);
+            const int at = (nb * 32 + 8 * q + 4 * (ln >> 5)) * (int)sizeof(TL);
             char* p = buf + r * SEG + (((at >> 4) ^ (r % CHUNKS)) << 4) + (at & 15);
             const f32x4 v = vec(mb, nb0 + nb, q);
-            if constexpr (sizeof(TO) == 2) *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(v, bf16x4);
+            if constexpr (sizeof(TL) == 2) *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(v, bf16x4);
             else *reinterpret_cast<f32x4*>(p) = v;
           }
 #pragma unroll
         for (int i = 0; i < 32 / RPS; ++i) {
-          const int row = i * RPS + ln / CHUNKS, c = ln % CHUNKS;
-          const int m = m0 + mb * 32 + row, n = n0 + nb0 * 32 + c * (16 / (int)sizeof(TO));
-          u32x4 v = *reinterpret_cast<const u32x4*>(buf + row * SEG + ((c ^ (row % CHUNKS)) << 4));
+          const int row = i * RPS + ln / PER, c = ln % PER;
+          const int m = m0 + mb * 32 + row, n = n0 + nb0 * 32 + c * N16;
+          auto chunk = [&](int k) {
+            return *reinterpret_cast<const u32x4*>(buf + row * SEG + ((k ^ (row % CHUNKS)) << 4));
+          };
+          u32x4 v;
+          if constexpr (sizeof(TL) == sizeof(TO)) {
+            v = chunk(c);
+          } else {
+            const bf16x4 lo = __builtin_convertvector(__builtin_bit_cast(f32x4, chunk(2 * c)), bf16x4);
+            const bf16x4 hi = __builtin_convertvector(__builtin_bit_cast(f32x4, chunk(2 * c + 1)), bf16x4);
+            v = __builtin_bit_cast(u32x4, bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+          }
           if (m >= mend || n >= N) continue;  // (N is a multiple of a chunk)
           TO* p = out + (size_t)m * N + n;
           if constexpr (sizeof(TO) == 4) {
@@ -548,7 +580,7 @@ __global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
   const int slot = blockIdx.x / kXcds;
   int round = 0;
   auto place = [&](int r) { return lo + r * slots + (G::TN && r % 2 ? slots - 1 - slot : slot); };
-  int i = place(0);
+  const int i = place(0);
   if (i >= hi) return;
 
   Wave<G> w;
@@ -556,23 +588,29 @@ __global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
   for (int j = 0; j < G::MB; ++j) w.a_at[j] = G::A::frag(wm * G::WM + j * 32, ln);
 #pragma unroll
   for (int j = 0; j < G::NB; ++j) w.b_at[j] = G::B::frag(wn * G::WN + j * 32, ln);
+  // What the loads of a tile need to be told by memory (NN, NT: the rows of a; TN: the row
+  // indices of its first turn) is fetched two tiles ahead: a whole turn, with its waits, then
+  // lies between the fetch and the use, whatever the tiles' lengths.
   Loader<G> ld;
-  int rows[G::A::PW];  // NN, NT: rows of a of the next tile's loads
+  Ahead<G> one, two;
   Item t = locate<G>(a, groups, i);
-  fetch_rows<G>(a, t, wave, ln, rows);
-  make_loader<G>(a, t, wave, ln, rows, ld);
+  one.fetch(a, t, wave, ln);
+  make_loader<G>(a, t, wave, ln, one, ld);
   Frags<G> F0, F1;
-  // TN: row indices of the turn whose loads come next, and of the next tile's first turn
-  int turn = use_turn<G>(a, fetch_turn<G>(a, t, 0, wave, ln), ln), turn_first = 0;
+  // TN: row indices of the turn whose loads come next
+  int turn = fetch_turn<G>(a, t, 1, wave, ln);
+  {
+    const int now = take_turn<G>(a, t, 0, one.turn, wave, ln);
+    one.fetch(a, place(1) < hi ? locate<G>(a, groups, place(1)) : t, wave, ln);
 #pragma unroll
-  for (int q = 0; q < kStages; ++q)
+    for (int q = 0; q < kStages; ++q)
 #pragma unroll
-    for (int j = 0; j < G::LPS; ++j) Issue<G, true>::run(ld, j, q, turn, q, ring[q]);
+      for (int j = 0; j < G::LPS; ++j) Issue<G, true>::run(ld, j, q, now, q, ring[q]);
+  }
   wait_vmcnt<(kStages - 1) * G::LPS>();
   sync_point();
 #pragma unroll
   for (int r = 0; r < G::SUB * (G::MB + G::NB); ++r) w.read(r, ring[0], F0);
-  turn = fetch_turn<G>(a, t, 1, wave, ln);
 
   for (;;) {
 #pragma unroll
@@ -584,19 +622,17 @@ __global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
     const Item cur = t;
     const int len = ld.len, nk = (len + G::BK - 1) / G::BK, whole = len / G::BK;
     const int end = max((nk + kStages - 1) / kStages, 1) * kStages;  // whole ring turns
-    i = place(++round);
-    const bool more = i < hi;
-    if (more) t = locate<G>(a, groups, i);
-    fetch_rows<G>(a, t, wave, ln, rows);
-    turn_first = fetch_turn<G>(a, t, 0, wave, ln);
+    const bool more = place(++round) < hi;
+    if (more) t = locate<G>(a, groups, place(round));
+    two.fetch(a, place(round + 1) < hi ? locate<G>(a, groups, place(round + 1)) : t, wave, ln);
 
     mask_first<G>(F0, len, ln);
     int kt = 0;
 #define MOE_STEP(J, CLAMP, RS) \
   Wait<G>::run();              \
-  Step<G, J, CLAMP, true>::run(RS, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1)
+  Step<G, J, CLAMP>::run(RS, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1)
     for (; kt + 2 * kStages <= whole && kt + kStages < end; kt += kStages) {
-      const int now = use_turn<G>(a, turn, ln);
+      const int now = take_turn<G>(a, cur, kt / kStages + 1, turn, wave, ln);
       turn = fetch_turn<G>(a, cur, kt / kStages + 2, wave, ln);
       MOE_STEP(0, false, kt + 4);
       MOE_STEP(1, false, kt + 5);
@@ -604,7 +640,7 @@ __global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
       MOE_STEP(3, false, kt + 7);
     }
     if (kt + kStages < end) {  // the refills end past len
-      const int now = use_turn<G>(a, turn, ln);
+      const int now = take_turn<G>(a, cur, kt / kStages + 1, turn, wave, ln);
       MOE_STEP(0, true, kt + 4);
       MOE_STEP(1, true, kt + 5);
       MOE_STEP(2, true, kt + 6);
@@ -613,25 +649,21 @@ __global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
       if ((kt + 1) * G::BK > len) mask_frags<G>(F0, len - kt * G::BK, ln);
     }
     // the last turn: the next item's first stages (without one, this item's, never used)
-    if (more) make_loader<G>(a, t, wave, ln, rows, ld);
-    const int now = use_turn<G>(a, turn_first, ln);
+    const int now = take_turn<G>(a, t, 0, one.turn, wave, ln);
+    if (more) make_loader<G>(a, t, wave, ln, one, ld);
     turn = fetch_turn<G>(a, t, 1, wave, ln);
-#define MOE_LAST(J)                                                                             \
-  Wait<G>::run();                                                                               \
-  if (kt + J < nk)                                                                              \
-    Step<G, J, true, true>::run(J, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1);     \
-  else                                                                                          \
-    Step<G, J, true, false>::run(J, now, ring, ld, w, (J) % 2 ? F1 : F0, (J) % 2 ? F0 : F1);    \
-  if (J < 3 && kt + J + 1 < nk && (kt + J + 2) * G::BK > len)                                   \
-    mask_frags<G>((J) % 2 ? F0 : F1, len - (kt + J + 1) * G::BK, ln);
-    MOE_LAST(0)
-    MOE_LAST(1)
-    MOE_LAST(2)
-    MOE_LAST(3)
+    const int left = len - kt * G::BK;
+    MOE_STEP(0, true, 0);
+    if (left < 2 * G::BK) mask_frags<G>(F1, left - G::BK, ln);
+    MOE_STEP(1, true, 1);
+    if (left < 3 * G::BK) mask_frags<G>(F0, left - 2 * G::BK, ln);
+    MOE_STEP(2, true, 2);
+    if (left < 4 * G::BK) mask_frags<G>(F1, left - 3 * G::BK, ln);
+    MOE_STEP(3, true, 3);
 #undef MOE_STEP
-#undef MOE_LAST
     store_tile<G, TO>(a, cur, wm, wn, ln, outs + wave * G::OUT_BYTES, w);
     if (!more) break;
+    one = two;
   }
   wait_vmcnt<0>();  // the loads that nobody reads have landed before the LDS is given back
 }
