@@ -703,23 +703,35 @@ int64_t tiles_of(const MatmulArgs& a, int bm, int bn) {
 Plan plan_of(const MatmulArgs& a) {
   const bool tn = a.form == MOE_MATMUL_TN;
   Plan p{128, 1};
-  // 32 rows: a row tile's other rows are work for nothing, or there are too few 128-row
-  // tiles to fill the chip (fp32, 512 rows of 8 groups, K 128: 12.7 -> 7.2 us; bf16, 300 rows
-  // of 4 groups, K 512, N 1024: 8.7 -> 7.8 us). 256 rows: half the operand traffic through
-  // L2 of 128 rows, which bounds a long sum; a short sum gains more from two workgroups per CU
-  // (8192 rows of 8 groups, N 4096: K 256 46 -> 29 us with 128 rows, K 1024 94 -> 85, K 4096
-  // 280 against 389 with 256; TN, 32764 rows of 64 groups, 2048 x 1408: 330 against 340).
+  // 32 rows: a row tile's other rows are work for nothing, or there are too few 128-row tiles
+  // to fill the chip (us with 128 rows -> 32: fp32, 512 rows of 8 groups, K 128, 12.9 -> 7.3;
+  // bf16, 300 rows of 4 groups, K 512, N 1024, 8.3 -> 6.7; 8 rows a group, 64 groups, K 2048,
+  // N 1408, 67.9 -> 63.4; 64 rows a group, 20.5 with 32 against 15.8).
+  const int64_t groups = a.R < a.E ? a.R : a.E;
   if (!tn && (a.R <= 32 * (int64_t)a.E || tiles_of(a, 128, 128) < 128)) p.bm = 32;
-  else if (a.bf16_in && (tn || (a.K > 1024 && a.R >= 192 * (int64_t)a.E)) && tiles_of(a, 256, 256) >= 256)
+  // 256 rows: half the traffic through L2 of 128 rows, but one workgroup per CU. They pay once
+  // the 128-row tiles (half of one lost per group) are more than are resident at once (us with
+  // 128 -> 256 rows, 8192 rows of 8 groups, K 4096: N 4096 381 -> 292, N 1024 109 -> 79, N 512
+  // 66 against 75; TN 1024 x 2048 53.5 -> 45.9, 1024 x 1024 29.5 against 37.9); in NN and NT
+  // if the sum is long too (N 4096: K 1024 82 against 90, K 2048 159 -> 151) and a group has
+  // rows enough (64 groups, K 2048, N 4096: 128 rows each 372 -> 251, 64 rows 223 against 242).
+  const int64_t rows128 = a.R / 128 + groups / 2;
+  const int64_t tiles128 = tn ? tiles_of(a, 128, 128) : rows128 * ((a.N + 127) / 128);
+  if (p.bm == 128 && a.bf16_in && tiles128 > 2 * kCus && (tn || (a.K > 1024 && a.R >= 128 * (int64_t)a.E)))
     p.bm = 256;
   if (p.bm == 256) return p;
-  // few tiles and a long sum: parts of at least 16 stages, about one workgroup per CU
+  // Few tiles and a long sum: parts of at least 16 stages, about one workgroup per CU. 65 to
+  // 128 tiles are few where the matrix units are the bound (fp32, 16 rows, K 1024, N 2048: 21.7
+  // -> 17.0 us) or the sum is very long (NT, 4 rows, N 4096: K 14336 103 -> 82, K 10240 75 ->
+  // 57; K 4096 22.0 against 24.9). TN 16384 x 104 x 200: 164 us whole, 26 in 16 parts; 65536
+  // rows, 128 x 128: 56 in 16 parts, 44 in 32.
   const int64_t tiles = tiles_of(a, p.bm, 128), len = tn ? a.R / a.E : a.K;
   const int64_t stages = len / (p.bm == 32 ? (a.bf16_in ? 64 : 32) : (a.bf16_in ? 32 : 16));
-  if (tiles <= 64 && stages >= 32) {
+  if (tiles <= (a.bf16_in && stages < 160 ? 64 : 128) && stages >= 32) {
+    const int64_t most = stages >= 1024 ? 32 : 16;
     int64_t n = kCus / tiles;
     n = n < stages / 16 ? n : stages / 16;
-    p.splits = (int)(n < 16 ? n : 16);
+    p.splits = (int)(n < most ? n : most);
   }
   return p;
 }

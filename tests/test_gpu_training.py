@@ -283,6 +283,37 @@ def test_matmul_in_parts(moe, form, c, K, N, dt):
     close(acc if form == "tn" else acc[:R], ref + 2.5, mag + 2.5, (max(c) if form == "tn" else K) + 18)
 
 
+@pytest.mark.parametrize("form,c,K,N", [("nn", [1, 700, 0, 799], 1032, 5640), ("nt", [257, 1, 1242], 1160, 5512),
+                                        ("tn", [33, 0, 300], 1000, 2832), ("tn", [1, 97, 64], 1288, 2056)])
+@pytest.mark.parametrize("gathered", [False, True])
+def test_matmul_many_tiles(moe, form, c, K, N, gathered):
+    # more tiles than are resident at once: the largest tiles, several of them per workgroup
+    say("many tiles", form, c, K, N, gathered)
+    R, E, g = sum(c), len(c), gen(N)
+    rows = 501 if gathered else R + 5
+    a = draw(g, rows, K, dtype=BF16)
+    ga = torch.randint(0, rows, (R,), generator=g).int() if gathered else None
+    gb = None
+    if form == "tn":
+        b = draw(g, rows, N, dtype=BF16)
+        gb = torch.randint(0, rows, (R,), generator=g).int() if gathered else None
+    else:
+        b = draw(g, E, *((K, N) if form == "nn" else (N, K)), dtype=BF16)
+    if not gathered:
+        a[R:] = float("nan")
+    ref, mag = matmul_ref(form, a if gathered else a[:R], b if gathered or form != "tn" else b[:R], c, ga, gb)
+    da, db, do, dga, dgb = cuda(a, b, offsets_of(c), ga, gb)
+    terms = max(c) if form == "tn" else K
+    for out in (BF16, FP32):
+        o = torch.full((E, K, N) if form == "tn" else (R if gathered else R + 5, N), 2.5, dtype=out, device="cuda")
+        moe.moe_grouped_matmul(da, db, do, form=form, gather_a=dga, gather_b=dgb, out=o)
+        close(o if form == "tn" else o[:R], ref, mag, terms + 2)
+        if form != "tn":
+            assert bool((o[R:] == 2.5).all())
+    moe.moe_grouped_matmul(da, db, do, form=form, gather_a=dga, gather_b=dgb, out=o, accumulate=True)
+    close(o if form == "tn" else o[:R], 2 * ref, 2 * mag, terms + 4)
+
+
 def test_matmul_rows_past_2_31_elements(moe):
     # a and out of more than 2^31 elements: the last rows against the first ones' copies
     say("far rows")
