@@ -332,8 +332,8 @@ typedef struct moe_matmul_shape {
  * leave the rows of out at and past offsets[E] as they are; a TN group without rows
  * gives zeros (accumulate: leaves its matrix as it is). K and N at most 2^20 and multiples of 8
  * (bf16) or 4 (fp32): rows are read in 16-byte pieces (otherwise MOE_ERR_UNSUPPORTED). a, b
- * and out must be 16-byte aligned. gather_b in NN or NT, and accumulate or a bf16 dtype's
- * opposite that out_dtype does not allow, return MOE_ERR_UNSUPPORTED. */
+ * and out must be 16-byte aligned, the workspace too. gather_b in NN or NT, a bf16 out of fp32
+ * inputs and accumulate into a bf16 out return MOE_ERR_UNSUPPORTED. */
 moe_status moe_grouped_matmul(const moe_matmul_shape* shape, const void* a, const void* b,
                               const int32_t* offsets, const int32_t* gather_a,
                               const int32_t* gather_b, void* out, void* ws, size_t ws_bytes,

@@ -427,8 +427,10 @@ class SparseMoE:
     or None).
 
     ``backward(d_out)`` gives the gradients of the latest call (token choice, with or without
-    a capacity, no training noise). It reads that call's x, u, y and workspace: x must not
-    have been changed since."""
+    a capacity, no training noise). It reads that call's x, u, y and workspace, and the
+    weights: none of them must have been changed since. Calls of one layer share its
+    workspace, captured ones too: they run one after another, each with its backward before
+    the next call."""
 
     def __init__(self, W_g, W_gate, W_up, W_down, b_g=None, *, k=2, mode="tc",
                  capacity_factor=1.0, renormalize=True, pre_gamma=None, post_gamma=None, gate=None,

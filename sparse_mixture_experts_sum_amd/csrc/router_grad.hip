@@ -4,6 +4,9 @@
 // Per token, over its kept slots (w != 0) with S = sum of their probabilities,
 //   dp_e = (dw_j - sum_i dw_i w_i) / S at e = idx_j (or dw_j), + loss_grad E f_e / (k T),
 //   ds_e = p_e (dp_e - sum_c p_c dp_c) + z_loss_grad 2 lse p_e / T;
+// the slots' part of it from w itself: as w = p / S (or p), p_e dp_e = w_j (dw_j - sum_i dw_i
+// w_i), whose sum over e is 0 (or w_j dw_j, and sum_i dw_i w_i). No division by an S that may
+// be as small as the smallest kept probability, and no load of p_e behind idx's.
 //   dx = ds W_g^T (+ the token's expert rows), dW_g = x^T ds, db = sum_t ds.
 // x, dx and the rows are read or written once each (x twice with the z-loss, whose lse takes
 // a dot product first): bound by HBM, and by the launches at small sizes. Four kernels: W_g
@@ -75,7 +78,8 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const TI* wt, i
   const int64_t t = t0 + tok < a.T ? t0 + tok : a.T - 1;  // (past the end: a copy, not stored)
   const int E = a.E, k = a.k;
   const float inv_T = 1.0f / (float)a.T;
-  float p[4], dp[4];
+  float p[4], dp[4], sel[4] = {0.f, 0.f, 0.f, 0.f};  // sel: the slots' part of ds
+  float dot = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = sub + 16 * i;
@@ -84,7 +88,7 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const TI* wt, i
   }
   if (a.dw) {
     // every slot's loads first (a slot past k, and one without a row, reads another's)
-    float w[8], g[8], pj[8];
+    float w[8], g[8];
     int ex[8], at[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -99,31 +103,28 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const TI* wt, i
       g[j] = 0.f;
       if (!a.dw_by_row) g[j] = a.dw[t * k + (j < k ? j : 0)];
       else if (a.R > 0) g[j] = a.dw[row ? at[j] : 0];
-      pj[j] = a.probs[t * E + ex[j]];
       // w = 0: dropped (or a probability of 0, whose gradient is 0 too)
       if (j >= k || w[j] == 0.f || (a.dw_by_row && !row)) ex[j] = -1;
     }
-    float S = 0.f, dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (ex[j] >= 0) dot += g[j] * w[j];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (ex[j] < 0) continue;
-      S += pj[j];
-      dot += g[j] * w[j];
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (ex[j] < 0) continue;
-      const float v = a.renorm ? (g[j] - dot) / S : g[j];
+      const float v = w[j] * (a.renorm ? g[j] - dot : g[j]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (ex[j] == sub + 16 * i) dp[i] += v;
+        if (ex[j] == sub + 16 * i) sel[i] += v;
     }
+    if (a.renorm) dot = 0.f;  // (of sel's sum)
   }
   float mean = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) mean += p[i] * dp[i];
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) mean += __shfl_xor(mean, o);
+  mean += dot;
   float zc = 0.f;
   if (a.z_loss_grad != 0.f) {
     // lse = s - log p at the most probable expert (p >= 1 / E there, so log p is exact to
@@ -165,7 +166,7 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const TI* wt, i
 #pragma unroll
   for (int i = 0; i < EP / 16; ++i) {
     const int e = sub + 16 * i;
-    const float v = p[i] * (dp[i] - mean + zc);  // (0 past E: p is)
+    const float v = sel[i] + p[i] * (dp[i] - mean + zc);  // (0 past E: both are)
     if (e < E) a.dlogits[t * E + e] = v;
     if constexpr (sizeof(TI) == 2) {
       const bf16 hi = (bf16)v, lo = (bf16)(v - (float)hi);

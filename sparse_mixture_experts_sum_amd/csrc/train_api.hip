@@ -239,11 +239,12 @@ moe_status moe_block_norm(const moe_norm_shape* shape, const void* x, const floa
   const moe_status st = check_norm(shape);
   if (st != MOE_OK) return st;
   const moe_norm_shape& s = *shape;
-  // what belongs to a part that does not run is not given: a forgotten y or gamma shows
-  if (!y && (gamma_post || gate || out || rstd_post || s.gate != MOE_GATE_NONE))
+  // what belongs to a part that does not run is not given: a forgotten y or gamma shows (with
+  // rows: a tensor without elements may have no address)
+  if (s.T > 0 && !y && (gamma_post || gate || out || rstd_post || s.gate != MOE_GATE_NONE))
     return MOE_ERR_BAD_SHAPE;
   if (!gamma && (u || rstd)) return MOE_ERR_BAD_SHAPE;
-  if ((s.gate != MOE_GATE_NONE) != (gate != nullptr)) return MOE_ERR_BAD_SHAPE;
+  if (s.T > 0 && (s.gate != MOE_GATE_NONE) != (gate != nullptr)) return MOE_ERR_BAD_SHAPE;
   if (!all_aligned16(x, y, gamma_post, gamma, out, u) ||
       (s.gate == MOE_GATE_CHANNEL && !aligned16(gate)))
     return MOE_ERR_MISALIGNED;
@@ -286,9 +287,9 @@ moe_status moe_block_norm_backward(const moe_norm_shape* shape, const void* d_ou
   const moe_status st = moe_block_norm_backward_workspace_size(shape, &need);
   if (st != MOE_OK) return st;
   const moe_norm_shape& s = *shape;
-  if (!y && (gamma_post || gate || rstd_post || dy || dgamma_post || dgate || s.gate != MOE_GATE_NONE))
+  if (s.T > 0 && !y && (gamma_post || gate || rstd_post || dy || dgamma_post || dgate || s.gate != MOE_GATE_NONE))
     return MOE_ERR_BAD_SHAPE;
-  if ((s.gate != MOE_GATE_NONE) != (gate != nullptr) || (dgate && !gate) || (dgamma && !d_u))
+  if (s.T > 0 && ((s.gate != MOE_GATE_NONE) != (gate != nullptr) || (dgate && !gate) || (dgamma && !d_u)))
     return MOE_ERR_BAD_SHAPE;
   if (!all_aligned16(d_out, d_u, out, gamma, y, gamma_post, dx, dy, ws) ||
       (s.gate == MOE_GATE_CHANNEL && !aligned16(gate)))

@@ -212,6 +212,8 @@ def moe_swiglu_backward(g, u, dh, w=None, *, src=None, pos=None, offsets=None, i
         ((g, "g", rows, dtype), (u, "u", rows, dtype), (dh, "dh", rows, dtype), (w, "w", w_shape, _F32),
          (src, "src", (R,), _I32), (pos, "pos", w_shape, _I32), (offsets, "offsets", (E + 1,), _I32)), dev)
     if inplace:
+        if R and len({pg, pu, pdh}) < 3:
+            raise ValueError("inplace needs g, u and dh to be three tensors")
         dg, du, h = g, u, dh
     else:
         dg, du, h = torch.empty_like(g), torch.empty_like(u), torch.empty_like(dh)

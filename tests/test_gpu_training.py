@@ -397,6 +397,13 @@ def test_swiglu_weights_by_slot_and_rows_behind(moe):
     assert torch.equal(dg[last:], keep[last:])
 
 
+def test_swiglu_in_place_of_one_tensor_is_refused(moe):
+    g, dh = torch.ones(3, 8, device="cuda"), torch.ones(3, 8, device="cuda")
+    with pytest.raises(ValueError, match="three tensors"):
+        moe.moe_swiglu_backward(g, g, dh, inplace=True)
+    assert bool((g == 1).all())
+
+
 def test_swiglu_without_rows_or_weights(moe):
     say("swiglu none")
     e = torch.empty(0, 64, device="cuda")
@@ -499,6 +506,28 @@ def test_route_adds_rows_and_takes_dw_by_row(moe, dt):
     # rows alone: every gradient of the router's is zero
     out = moe.moe_route_backward(x, W, p, idx, w, None, rows=drows, pos=dpos)
     assert not bool(out["dlogits"].any()) and not bool(out["dW_g"].any())
+
+
+def test_route_with_kept_slots_of_the_smallest_probabilities(moe):
+    # the likely experts' slots were dropped by the capacity: S of the kept ones is a
+    # denormal number, their weights are not. ds is w_j (dw_j - sum_i dw_i w_i) there, and
+    # at most 1e-38 elsewhere
+    say("route small S")
+    T, d, E, k = 5, 64, 8, 3
+    p = torch.zeros(T, E)
+    p[:, 0] = 1.0
+    p[:, 3], p[:, 5] = 1e-40, 3e-40
+    idx = torch.tensor([[0, 5, 3]] * T, dtype=torch.int32)
+    w = torch.tensor([[0.0, 0.75, 0.25]] * T)
+    dw = draw(gen(3), T, k)
+    x, W = draw(gen(4), T, d), draw(gen(5), d, E)
+    out = moe.moe_route_backward(*cuda(x, W, p, idx, w, dw))
+    g, wd = dw.double(), w.double()
+    mean = (g * wd).sum(1, keepdim=True)
+    ref, mag = torch.zeros(T, E, dtype=torch.float64), torch.zeros(T, E, dtype=torch.float64)
+    ref.scatter_(1, idx.long(), wd * (g - mean))
+    mag.scatter_(1, idx.long(), wd * (g.abs() + (g.abs() * wd).sum(1, keepdim=True)))
+    close(out["dlogits"], ref, mag, 4, "dlogits")  # (two products, their sum, a difference)
 
 
 def test_route_without_tokens(moe):
@@ -651,6 +680,33 @@ def test_norm_zero_row_and_no_rows(moe):
     assert got["u"].shape == (0, d)
     res = moe.moe_block_norm_backward(e, d_u=e, rstd=got["rstd"], gamma=gm)
     assert res["dx"].shape == (0, d) and not bool(res["dgamma"].any())
+
+
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+def test_norms_after_a_block_without_rows(moe, gate):
+    say("norm no rows", gate)
+    d = 128
+    x, y = torch.empty(0, d, dtype=BF16, device="cuda"), torch.empty(0, d, device="cuda")
+    gm = torch.ones(d, device="cuda")
+    gt = {"none": None, "channel": gm, "token": torch.empty(0, 1, device="cuda")}[gate]
+    got = moe.moe_block_norm(x, gamma=gm, y=y, gamma_post=gm, gate=gt)
+    assert got["out"].shape == got["u"].shape == (0, d)
+    res = moe.moe_block_norm_backward(got["out"], d_out=x, d_u=x, rstd=got["rstd"], gamma=gm, y=y,
+                                      rstd_post=got["rstd_post"], gamma_post=gm, gate=gt)
+    assert res["dx"].shape == res["dy"].shape == (0, d)
+    assert not bool(res["dgamma"].any()) and not bool(res["dgamma_post"].any())
+    if gate == "channel":
+        assert not bool(res["dgate"].any())
+
+
+def test_layer_block_without_tokens(moe):
+    say("layer block none")
+    t = {n: v.cuda() for n, v in layer_inputs(0, 64, 64, 4, BF16, 3).items()}
+    ones = torch.ones(64, device="cuda")
+    layer = moe.SparseMoE(t["W_g"], t["W_gate"], t["W_up"], t["W_down"], pre_gamma=ones, post_gamma=ones, gate=ones)
+    assert layer(t["x"]).shape == (0, 64)
+    got = layer.backward(t["d_out"].to(BF16))
+    assert got["dx"].shape == (0, 64) and not any(bool(got[n].any()) for n in got if n != "dx")
 
 
 def test_norm_many_rows(moe):
