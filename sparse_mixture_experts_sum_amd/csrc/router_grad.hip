@@ -11,7 +11,10 @@
 // x, dx and the rows are read or written once each (x twice with the z-loss, whose lse takes
 // a dot product first): bound by HBM, and by the launches at small sizes. Four kernels: W_g
 // transposed (z-loss only), ds, then dx and partial sums of dW_g and db side by side in one
-// launch, and the partial sums' sum in chunk order: no atomics, one fixed order.
+// launch, and the partial sums' sum in chunk order: no atomics, one fixed order. bf16, both
+// losses: 4096 tokens of 1024, 8 experts, 21 us (ds 8.8, products 7.6, sum 3.6: latencies, a
+// copy of those bytes takes 3.4); 8191 tokens of 2048, 64 experts, top-4 with the rows'
+// gradients added, 73-85 us (transpose 4.5, ds 16, products 50 at 4 TB/s, sum 5; a copy 40).
 //
 // Both products run on the matrix cores. fp32: v_mfma_f32_32x32x2_f32 on the values. bf16:
 // v_mfma_f32_32x32x16_bf16 with ds split into two bf16 terms (ds ~ hi + lo, off by 2^-17 of
