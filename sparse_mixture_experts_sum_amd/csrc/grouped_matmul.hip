@@ -296,8 +296,8 @@ __device__ __forceinline__ void mask_first(Frags<G>& F, int len, int ln) {
 }
 
 // A workgroup's work: output tile (mt, nt) of group e, whose rows are [r0, r1), over a part of
-// the summed axis: NN, NT [k0, k0 + len); TN rows [r0, r1) are that part, and `split` says
-// which.
+// the summed axis: NN, NT [k0, k0 + len); TN rows [r0, r1) are that part. `split`: which of
+// the part sums it is (TN: -1 for a whole sum, which goes to out).
 struct Item {
   int e, r0, r1, mt, nt, k0, len, split;
 };
@@ -315,7 +315,26 @@ constexpr int kColBlock = 4;  // columns of tiles walked together
 // inner, so that the tiles an XCD runs together share rows of a and columns of b in its L2.
 struct Groups {  // lane i: the i-th group of the list
   int e, start, end, first, incl;  // first: the share's first tile in the group; incl: tiles so far
+  int parts, slot;  // TN: parts of the group's sum, and the first one's place among all part sums
 };
+
+// TN: in how many parts a group's sum is taken, so that none of them is much longer than a CU's
+// share of the work, and the place of the group's first part sum (lane e: group e).
+constexpr int kMaxParts = 32;
+__device__ __forceinline__ void group_parts(const MatmulArgs& a, int len, int& parts, int& slot) {
+  const int lane = threadIdx.x & 63;
+  parts = 1;
+  if (a.part_rows && len > a.part_rows)
+    parts = (int)min(((int64_t)len + a.part_rows - 1) / a.part_rows, (int64_t)kMaxParts);
+  const int mine = parts > 1 ? parts : 0;
+  slot = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(slot, o);
+    if (lane >= o) slot += v;
+  }
+  slot -= mine;
+}
 
 template <class G>
 __device__ __forceinline__ void make_groups(const MatmulArgs& a, int xcd, Groups& g, int& lo, int& hi) {
@@ -323,10 +342,12 @@ __device__ __forceinline__ void make_groups(const MatmulArgs& a, int xcd, Groups
   const int NT = (int)((a.N + G::BN - 1) / G::BN);
   int start, end;
   group_bounds(a.offsets, a.E, (int)a.R, start, end);
-  g = Groups{lane, start, end, 0, 0};
+  g = Groups{lane, start, end, 0, 0, 1, 0};
   int tiles;  // (with splits: each part is a tile of its own)
   if constexpr (G::TN) {
-    const int len = lane < a.E ? end - start : -1;
+    int parts, slot;
+    group_parts(a, end - start, parts, slot);
+    const int len = lane < a.E ? (end - start) / parts : -1;
     int rank = 0;
     for (int j = 0; j < 64; ++j) {
       const int other = __builtin_amdgcn_readlane(len, j);
@@ -335,7 +356,9 @@ __device__ __forceinline__ void make_groups(const MatmulArgs& a, int xcd, Groups
     g.e = __builtin_amdgcn_ds_permute(4 * rank, lane);
     g.start = __builtin_amdgcn_ds_permute(4 * rank, start);
     g.end = __builtin_amdgcn_ds_permute(4 * rank, end);
-    const int64_t n = lane < a.E ? (a.K + G::BM - 1) / G::BM * NT * a.splits : 0;
+    g.parts = __builtin_amdgcn_ds_permute(4 * rank, parts);
+    g.slot = __builtin_amdgcn_ds_permute(4 * rank, slot);
+    const int64_t n = lane < a.E ? (a.K + G::BM - 1) / G::BM * NT * g.parts : 0;
     const int x = (xcd + lane) % kXcds;  // (a group of few tiles: another XCD's for each)
     g.first = (int)(n * x / kXcds);
     tiles = (int)(n * (x + 1) / kXcds) - g.first;
@@ -364,23 +387,29 @@ __device__ __forceinline__ Item locate(const MatmulArgs& a, const Groups& g, int
   const int m = G::TN ? (int)((a.K + G::BM - 1) / G::BM) : (t.r1 - t.r0 + G::BM - 1) / G::BM;
   const int before = at_group ? __builtin_amdgcn_readlane(g.incl, at_group - 1) : 0;
   const int part = i - before + __builtin_amdgcn_readlane(g.first, at_group);
-  const int in = part / a.splits;
-  t.split = part - in * a.splits;
+  // TN: a part's tiles one after another (they share its rows), else a tile's parts
+  const int parts = G::TN ? __builtin_amdgcn_readlane(g.parts, at_group) : a.splits;
+  const int in = G::TN ? part % (m * NT) : part / parts;
+  int split = G::TN ? part / (m * NT) : part - in * parts;
   const int blk = in / (m * kColBlock), cols = min(kColBlock, NT - blk * kColBlock);
   const int at = in - blk * m * kColBlock;
   t.mt = at / cols;
   t.nt = blk * kColBlock + at % cols;
   t.k0 = 0;
   t.len = G::TN ? t.r1 - t.r0 : (int)a.K;
-  if (a.splits > 1) {  // whole stages per part; a part may be empty (TN)
-    const int per = ((t.len + G::BK - 1) / G::BK + a.splits - 1) / a.splits * G::BK;
-    t.k0 = min(t.split * per, t.len);
+  if (parts > 1) {  // whole stages per part; the last ones may be empty
+    const int per = ((t.len + G::BK - 1) / G::BK + parts - 1) / parts * G::BK;
+    t.k0 = min(split * per, t.len);
     t.len = min(per, t.len - t.k0);
     if constexpr (G::TN) {
       t.r0 += t.k0;
       t.r1 = t.r0 + t.len;
+      split += __builtin_amdgcn_readlane(g.slot, at_group);
     }
+  } else if (G::TN) {
+    split = -1;
   }
+  t.split = split;
   return t;
 }
 
@@ -493,7 +522,12 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const Item& t, i
   const int K = (int)a.K, N = (int)a.N;
   const int m0 = t.mt * G::BM + (G::TN ? 0 : t.r0) + wm * G::WM, mend = G::TN ? K : t.r1;
   const int n0 = t.nt * G::BN + wn * G::WN;
-  TO* out = static_cast<TO*>(a.out) + (size_t)t.split * a.split_stride + (G::TN ? (size_t)t.e * K * N : 0);
+  const bool whole = G::TN && t.split < 0;  // (TN)
+  const bool add = a.accumulate && (!G::TN || whole);
+  TO* out = static_cast<TO*>(a.out) + (G::TN ? (size_t)t.e * K * N : (size_t)t.split * a.split_stride);
+  if constexpr (G::TN && sizeof(TO) == 4) {
+    if (!whole) out = a.parts + (size_t)t.split * K * N;
+  }
   auto vec = [&](int mb, int nb, int q) {
     return f32x4{w.acc[nb][mb][4 * q], w.acc[nb][mb][4 * q + 1], w.acc[nb][mb][4 * q + 2],
                  w.acc[nb][mb][4 * q + 3]};
@@ -514,7 +548,7 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const Item& t, i
           if constexpr (sizeof(TO) == 2) {
             *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(v, bf16x4);
           } else {
-            if (a.accumulate) v += *reinterpret_cast<const f32x4*>(p);
+            if (add) v += *reinterpret_cast<const f32x4*>(p);
             *reinterpret_cast<f32x4*>(p) = v;
           }
         }
@@ -562,7 +596,7 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, const Item& t, i
           if (m >= mend || n >= N) continue;  // (N is a multiple of a chunk)
           TO* p = out + (size_t)m * N + n;
           if constexpr (sizeof(TO) == 4) {
-            if (a.accumulate)
+            if (add)
               v = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, v) + *reinterpret_cast<const f32x4*>(p));
           }
           __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
@@ -672,25 +706,38 @@ __global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
     if (left < 4 * G::BK) mask_frags<G>(F1, left - 3 * G::BK, ln);
     MOE_STEP(3, true, 3);
 #undef MOE_STEP
-    store_tile<G, TO>(a, cur, wm, wn, ln, outs + wave * G::OUT_BYTES, w);
+    if (G::TN && sizeof(TO) == 2 && cur.split >= 0)
+      store_tile<G, float>(a, cur, wm, wn, ln, outs + wave * G::OUT_BYTES, w);
+    else
+      store_tile<G, TO>(a, cur, wm, wn, ln, outs + wave * G::OUT_BYTES, w);
     if (!more) break;
     one = two;
   }
   wait_vmcnt<0>();  // the loads that nobody reads have landed before the LDS is given back
 }
 
-// Parts' sums, in order, into out: n values, NN and NT up to the last group's end.
+// Parts' sums, in order, into out. NN, NT: up to the last group's end; TN: of the groups that
+// have parts, a group per grid row.
 template <typename TO>
-__global__ __launch_bounds__(256) void join_parts_kernel(MatmulArgs a, const float* __restrict__ parts) {
-  int64_t n = a.split_stride;
-  if (a.form != MOE_MATMUL_TN) {
-    int b0, b1;
-    n = (int64_t)group_bounds(a.offsets, a.E, (int)a.R, b0, b1) * a.N;
-  }
+__global__ __launch_bounds__(256) void join_parts_kernel(MatmulArgs a, const float* __restrict__ sums) {
   TO* out = static_cast<TO*>(a.out);
+  int parts = a.splits, start, end;
+  int64_t n = a.split_stride;
+  const int last = group_bounds(a.offsets, a.E, (int)a.R, start, end);
+  if (a.form == MOE_MATMUL_TN) {
+    int all, slot;
+    group_parts(a, end - start, all, slot);
+    parts = __builtin_amdgcn_readlane(all, blockIdx.y);
+    if (parts < 2) return;
+    sums += (size_t)__builtin_amdgcn_readlane(slot, blockIdx.y) * a.split_stride;
+    out += (size_t)blockIdx.y * a.split_stride;
+  } else {
+    n = (int64_t)last * a.N;
+  }
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
-    f32x4 v = *reinterpret_cast<const f32x4*>(parts + i);
-    for (int p = 1; p < a.splits; ++p) v += *reinterpret_cast<const f32x4*>(parts + p * a.split_stride + i);
+    f32x4 v = *reinterpret_cast<const f32x4*>(sums + i);
+#pragma unroll 4
+    for (int p = 1; p < parts; ++p) v += *reinterpret_cast<const f32x4*>(sums + p * a.split_stride + i);
     if constexpr (sizeof(TO) == 2) {
       *reinterpret_cast<bf16x4*>(out + i) = __builtin_convertvector(v, bf16x4);
     } else {
@@ -704,7 +751,10 @@ __global__ __launch_bounds__(256) void join_parts_kernel(MatmulArgs a, const flo
 // bounded from the sizes alone (the groups' sizes are on the device): one part tile per group
 // that can have rows.
 struct Plan {
-  int bm, splits;
+  int bm;
+  int splits;           // NN, NT: parts of every sum
+  int64_t part_rows;    // TN: rows of a part, 0: no parts
+  int64_t part_sums;    // TN: the most part sums there can be
 };
 int64_t tiles_of(const MatmulArgs& a, int bm, int bn) {
   const int64_t nt = (a.N + bn - 1) / bn;
@@ -713,7 +763,7 @@ int64_t tiles_of(const MatmulArgs& a, int bm, int bn) {
 }
 Plan plan_of(const MatmulArgs& a) {
   const bool tn = a.form == MOE_MATMUL_TN;
-  Plan p{128, 1};
+  Plan p{128, 1, 0, 0};
   // 32 rows: a row tile's other rows are work for nothing, or there are too few 128-row tiles
   // to fill the chip (us with 128 rows -> 32: fp32, 512 rows of 8 groups, K 128, 12.9 -> 7.3;
   // bf16, 300 rows of 4 groups, K 512, N 1024, 8.3 -> 6.7; 8 rows a group, 64 groups, K 2048,
@@ -731,18 +781,40 @@ Plan plan_of(const MatmulArgs& a) {
   if (p.bm == 128 && a.bf16_in && tiles128 > 2 * kCus && (tn || (a.K > 1024 && a.R >= 128 * (int64_t)a.E)))
     p.bm = 256;
   if (p.bm == 256) return p;
-  // Few tiles and a long sum: parts of at least 16 stages, about one workgroup per CU. 65 to
-  // 128 tiles are few where the matrix units are the bound (fp32, 16 rows, K 1024, N 2048: 21.7
-  // -> 17.0 us) or the sum is very long (NT, 4 rows, N 4096: K 14336 103 -> 82, K 10240 75 ->
-  // 57; K 4096 22.0 against 24.9). TN 16384 x 104 x 200: 164 us whole, 26 in 16 parts; 65536
-  // rows, 128 x 128: 56 in 16 parts, 44 in 32.
-  const int64_t tiles = tiles_of(a, p.bm, 128), len = tn ? a.R / a.E : a.K;
-  const int64_t stages = len / (p.bm == 32 ? (a.bf16_in ? 64 : 32) : (a.bf16_in ? 32 : 16));
+  if (tn) {
+    // A group's tiles have its rows' work, and a group that has most of the rows keeps a few
+    // CUs busy long after the others: its sums are taken in parts of little more than a CU's
+    // share of the rows, where a part stays long enough to be worth its 64 KB of partial sums
+    // and the second launch. The device counts the parts, the host knows only the sizes: it
+    // leaves parts out where three times the mean group would have none, and where the tiles
+    // are many. 128-row tiles, us without parts -> with, for even groups and one with 3.7 times
+    // the mean's rows: 32768 rows of 8, 512 x 512 51 -> 42 and 155 -> 42; 512 x 1024 63 -> 64
+    // and 156 -> 64; 1024 x 1024 88 -> 94 and 156 -> 106; 8192 rows of 8, 512 x 1024 21 -> 25 and
+    // 47 -> 30; fp32, 512 x 512 54 -> 55 and 142 -> 62, 1024 x 1024 151 -> 150 and 277 -> 192.
+    // 16384 rows of one group, 104 x 200: 164 -> 21. Left whole: bf16, 8192 rows, 1024 x 1024
+    // (28 against 31 even, 36 against 41 with 2.6 times the mean's, 45 against 39 with 3.7).
+    const int64_t tiles = tiles_of(a, 128, 128), share = a.R * (tiles / a.E) / kCus;
+    const int bk = a.bf16_in ? 32 : 16;
+    const int64_t least = (a.bf16_in ? 24 : 8) * bk, few = (a.bf16_in ? 80 : 40) * bk;
+    int64_t rows = share + share / 4 < few ? share + share / 4 : few;
+    if (rows < share * 4 / 5) rows = share * 4 / 5;
+    if (rows < least) rows = least;
+    const int64_t longest = 3 * a.R / a.E < a.R ? 3 * a.R / a.E : a.R;
+    if (longest <= rows || tiles > 4 * kCus || (a.bf16_in && tiles > kCus && share < 128 * bk)) return p;
+    p.part_rows = rows;
+    p.part_sums = a.R / rows + (groups < a.R / rows ? groups : a.R / rows);
+    return p;
+  }
+  // NN, NT, few tiles and a long sum: parts of at least 16 stages, about one workgroup per CU.
+  // 65 to 128 tiles are few where the matrix units are the bound (fp32, 16 rows, K 1024, N 2048:
+  // 21.7 -> 17.0 us) or the sum is very long (NT, 4 rows, N 4096: K 14336 103 -> 82, K 10240 75
+  // -> 57; K 4096 22.0 against 24.9). One row of 8 groups, K 14336, N 4096: 46 -> 38.
+  const int64_t tiles = tiles_of(a, p.bm, 128);
+  const int64_t stages = a.K / (p.bm == 32 ? (a.bf16_in ? 64 : 32) : (a.bf16_in ? 32 : 16));
   if (tiles <= (a.bf16_in && stages < 160 ? 64 : 128) && stages >= 32) {
-    const int64_t most = stages >= 1024 ? 32 : 16;
     int64_t n = kCus / tiles;
     n = n < stages / 16 ? n : stages / 16;
-    p.splits = (int)(n < most ? n : most);
+    p.splits = (int)(n < 16 ? n : 16);
   }
   return p;
 }
@@ -751,7 +823,9 @@ template <class G, typename TO>
 hipError_t launch_tile(const MatmulArgs& a, hipStream_t s) {
   // at most as many workgroups as are resident together, a multiple of the XCDs
   constexpr int64_t resident = kCus * (G::BM == 256 ? 1 : 2);
-  const int64_t blocks = (tiles_of(a, G::BM, G::BN) * a.splits + kXcds - 1) / kXcds * kXcds;
+  const int64_t tiles = tiles_of(a, G::BM, G::BN);
+  const int64_t items = G::TN ? tiles + tiles / a.E * a.part_sums : tiles * a.splits;
+  const int64_t blocks = (items + kXcds - 1) / kXcds * kXcds;
   grouped_matmul_kernel<G, TO><<<(unsigned)(blocks < resident ? blocks : resident), 256, 0, s>>>(a);
   return hipGetLastError();
 }
@@ -780,29 +854,37 @@ hipError_t launch_types(const MatmulArgs& a, int bm, hipStream_t s) {
   return a.bf16_out ? launch_forms<bf16, bf16>(a, bm, s) : launch_forms<bf16, float>(a, bm, s);
 }
 
-int64_t out_values(const MatmulArgs& a) {
-  return a.form == MOE_MATMUL_TN ? (int64_t)a.E * a.K * a.N : a.R * a.N;
-}
+// Values of one part sum.
+int64_t part_values(const MatmulArgs& a) { return (a.form == MOE_MATMUL_TN ? a.K : a.R) * a.N; }
 
 }  // namespace
 
 size_t grouped_matmul_workspace(const MatmulArgs& a) {
   const Plan p = plan_of(a);
-  return p.splits > 1 ? (size_t)p.splits * out_values(a) * sizeof(float) : 0;
+  const int64_t sums = a.form == MOE_MATMUL_TN ? p.part_sums : p.splits > 1 ? p.splits : 0;
+  return (size_t)sums * part_values(a) * sizeof(float);
 }
 
 hipError_t launch_grouped_matmul(const MatmulArgs& args, float* ws, hipStream_t s) {
   MatmulArgs a = args;
   const Plan p = plan_of(a);
+  const bool tn = a.form == MOE_MATMUL_TN;
   a.splits = p.splits;
-  a.split_stride = out_values(a);
-  if (p.splits == 1) return launch_types(a, p.bm, s);
+  a.split_stride = part_values(a);
+  a.part_rows = p.part_rows;
+  a.part_sums = p.part_sums;
+  a.parts = ws;
+  if (p.splits == 1 && !p.part_rows) return launch_types(a, p.bm, s);
   MatmulArgs part = a;
-  part.out = ws;
-  part.bf16_out = part.accumulate = 0;
+  if (!tn) {  // every sum is in parts
+    part.out = ws;
+    part.bf16_out = part.accumulate = 0;
+  }
   const hipError_t e = launch_types(part, p.bm, s);
   if (e != hipSuccess) return e;
-  const unsigned grid = capped_grid((a.split_stride / 4 + 255) / 256);
+  // (TN: few workgroups per group, of which most leave at once where most groups are whole)
+  const int64_t blocks = (a.split_stride / 4 + 255) / 256, most = 2048 / a.E;
+  const dim3 grid(capped_grid(tn && blocks > most ? most : blocks), tn ? a.E : 1);
   if (a.bf16_out) join_parts_kernel<bf16><<<grid, 256, 0, s>>>(a, ws);
   else join_parts_kernel<float><<<grid, 256, 0, s>>>(a, ws);
   return hipGetLastError();

@@ -16,8 +16,12 @@ struct MatmulArgs {
   void* out;
   int64_t R, rows_a, rows_b, K, N;
   int E, form, bf16_in, bf16_out, accumulate;
-  int splits;               // parts of the summed axis, split_stride values apart in out
-  int64_t split_stride;     // (both set by the launch)
+  // set by the launch
+  int splits;               // NN, NT: parts of the summed axis, split_stride values apart in out
+  int64_t split_stride;     // values of a part's sum
+  int64_t part_rows;        // TN: groups of more rows have their sum in parts, 0: none has
+  int64_t part_sums;        // TN: the most part sums there can be
+  float* parts;             // TN: the part sums
 };
 // Bytes of workspace: the parts' sums, where few tiles share a long sum; else 0.
 size_t grouped_matmul_workspace(const MatmulArgs& a);

@@ -283,6 +283,41 @@ def test_matmul_in_parts(moe, form, c, K, N, dt):
     close(acc if form == "tn" else acc[:R], ref + 2.5, mag + 2.5, (max(c) if form == "tn" else K) + 18)
 
 
+@pytest.mark.parametrize("c,K,N", [([3, 2500, 0, 70, 1], 136, 264), ([30000], 64, 64), ([800, 0, 5100, 769, 768], 72, 128),
+                                   ([20, 60, 4000, 0, 33, 5, 1, 1500], 520, 1032)])
+@pytest.mark.parametrize("dt,out", [(BF16, BF16), (BF16, FP32), (FP32, FP32)])
+def test_matmul_tn_groups_in_parts_beside_whole_ones(moe, c, K, N, dt, out):
+    # a long group's sum is taken in parts (32 at most), its neighbours' are not
+    say("tn parts", c, K, N, dt, out)
+    R, E, g = sum(c), len(c), gen(K)
+    a, b = draw(g, 501, K, dtype=dt), draw(g, R + 5, N, dtype=dt)
+    b[R:] = float("nan")
+    ga = torch.randint(0, 501, (R + 5,), generator=g).int()
+    gb = torch.arange(R + 5).int()
+    ref, mag = matmul_ref("tn", a, b[:R], c, ga[:R], None)
+    da, db, do, dga, dgb = cuda(a, b, offsets_of(c), ga, gb)
+    terms = max(c) + 34
+    got = moe.moe_grouped_matmul(da, db, do, form="tn", gather_a=dga, gather_b=dgb, out_dtype=out)
+    close(got, ref, mag, terms)
+    ws = torch.full((1 << 26,), float("nan"), device="cuda")
+    again = moe.moe_grouped_matmul(da, db, do, form="tn", gather_a=dga, out_dtype=out, workspace=ws)
+    assert torch.equal(got, again)
+    if out is FP32:
+        acc = torch.full((E, K, N), 2.5, device="cuda")
+        moe.moe_grouped_matmul(da, db, do, form="tn", gather_a=dga, out=acc, accumulate=True)
+        close(acc, ref + 2.5, mag + 2.5, terms + 2)
+    # a table that is no table: bounds are taken as the running maximum, at most R
+    bad = do.clone()
+    bad[0], bad[-1] = -5, 2 ** 31 - 1
+    if E > 3:
+        bad[2] = 0
+    good = torch.cummax(bad.cpu().clamp(0, R + 5), 0).values.cuda()
+    x = moe.moe_grouped_matmul(da, db, bad, form="tn", gather_a=dga, out_dtype=out)
+    y = moe.moe_grouped_matmul(da, db, good, form="tn", gather_a=dga, out_dtype=out)
+    assert torch.equal(x.view(torch.int16 if out is BF16 else torch.int32),
+                       y.view(torch.int16 if out is BF16 else torch.int32))
+
+
 @pytest.mark.parametrize("form,c,K,N", [("nn", [1, 700, 0, 799], 1032, 5640), ("nt", [257, 1, 1242], 1160, 5512),
                                         ("tn", [33, 0, 300], 1000, 2832), ("tn", [1, 97, 64], 1288, 2056)])
 @pytest.mark.parametrize("gathered", [False, True])
