@@ -160,10 +160,11 @@ struct Source {
   static __device__ __forceinline__ const T* at(const Loader<G>& ld, const T* p, size_t step, int j, int kt) {
     const T* q = p + (size_t)kt * step;
     if constexpr (CLAMP) {
-      const int l = here(ld.ln);
+      const int l = G::BM == 256 ? here(ld.ln) : ld.ln;
       const int k = kt * G::BK + (Op::KS ? Op::row(j, ld.wave, l) : Op::chunk(j, ld.wave, l) * G::EPC);
       const int back = min(0, ld.len - (Op::KS ? 1 : G::EPC) - k);
-      q += Op::KS ? (int64_t)back * (int64_t)(step / G::BK) : (int64_t)back;
+      // (at most two ring turns back, of rows of at most 2^20 values)
+      q += Op::KS ? back * (int)(step / G::BK) : back;
     }
     return q;
   }
@@ -349,10 +350,13 @@ __device__ __forceinline__ void make_groups(const MatmulArgs& a, int xcd, Groups
     group_parts(a, end - start, parts, slot);
     const int len = lane < a.E ? (end - start) / parts : -1;
     int rank = 0;
-    for (int j = 0; j < 64; ++j) {
-      const int other = __builtin_amdgcn_readlane(len, j);
-      rank += other > len || (other == len && j < lane);
-    }
+    for (int j0 = 0; j0 < a.E; j0 += 8)
+#pragma unroll
+      for (int j = j0; j < j0 + 8; ++j) {
+        const int other = __builtin_amdgcn_readlane(len, j);
+        rank += other > len || (other == len && j < lane);
+      }
+    if (lane >= a.E) rank = lane;
     g.e = __builtin_amdgcn_ds_permute(4 * rank, lane);
     g.start = __builtin_amdgcn_ds_permute(4 * rank, start);
     g.end = __builtin_amdgcn_ds_permute(4 * rank, end);
