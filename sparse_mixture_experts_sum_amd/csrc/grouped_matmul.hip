@@ -23,6 +23,8 @@
 // us (629 TFLOP/s and 2.9 TB/s at once; 168 us for the slower of the two alone); 16 rows of 8,
 // K 4096, N 14336: NN 160-167 us (5.6-5.9 TB/s). fp32, 8192 rows of 8, K 1024, N 4096: NN 562 us
 // (122 TFLOP/s, a large square product 134).
+#include <math.h>
+
 #include <type_traits>
 
 #include "train_common.h"
@@ -798,24 +800,30 @@ Plan plan_of(const MatmulArgs& a) {
   // N 1408, 67.9 -> 63.4; 64 rows a group, 20.5 with 32 against 15.8).
   const int64_t groups = a.R < a.E ? a.R : a.E;
   if (!tn && (a.R <= 32 * (int64_t)a.E || tiles_of(a, 128, 128) < 128)) p.bm = 32;
+  // The rows of the longest group, as the host has to guess them: a skewed router gives it
+  // about sqrt(E) times the mean (2.6 to 3.7 times of 8 groups, 5.6 to 10 of 64).
+  const int64_t longest = (int64_t)((double)a.R / sqrt((double)a.E));
   // 256 rows: half the traffic through L2 of 128 rows, but one workgroup per CU. They pay once
   // the 128-row tiles (half of one lost per group) are more than are resident at once (us with
   // 128 -> 256 rows, 8192 rows of 8 groups, K 4096: N 4096 381 -> 292, N 1024 109 -> 79, N 512
-  // 66 against 75; TN 1024 x 2048 53.5 -> 45.9, 1024 x 1024 29.5 against 37.9); in NN and NT
-  // if the sum is long too (N 4096: K 1024 82 against 90, K 2048 159 -> 151) and a group has
-  // rows enough (64 groups, K 2048, N 4096: 128 rows each 372 -> 251, 64 rows 223 against 242).
+  // 66 against 75); in NN and NT if the sum is long too (N 4096: K 1024 82 against 90, K 2048
+  // 159 -> 151) and a group has rows enough (64 groups, K 2048, N 4096: 128 rows each 372 ->
+  // 251, 64 rows 223 against 242); in TN, whose tiles have their group's rows' work, if a CU has
+  // tiles enough to even out a long group (8192 rows of 8, even groups / one with 2.6 / with
+  // 3.7 times the mean's rows: 1024 x 4096 97 -> 84, 97 -> 90, 95 against 105; 1024 x 2048 53
+  // -> 51, 50 against 70, 58 against 90; 32764 rows of 64, 2048 x 1408 317 -> 294).
   const int64_t rows128 = a.R / 128 + groups / 2;
   const int64_t tiles128 = tn ? tiles_of(a, 128, 128) : rows128 * ((a.N + 127) / 128);
-  if (p.bm == 128 && a.bf16_in && tiles128 > 2 * kCus && (tn || (a.K > 1024 && a.R >= 128 * (int64_t)a.E)))
-    p.bm = 256;
+  const bool enough = tn ? a.R * (tiles_of(a, 256, 256) / a.E) / kCus * 3 / 2 >= longest
+                         : a.K > 1024 && a.R >= 128 * (int64_t)a.E;
+  if (p.bm == 128 && a.bf16_in && tiles128 > 2 * kCus && enough) p.bm = 256;
   if (p.bm == 256) return p;
   if (tn) {
-    // A group's tiles have its rows' work, and a group that has most of the rows keeps a few
-    // CUs busy long after the others: its sums are taken in parts of little more than a CU's
-    // share of the rows, where a part stays long enough to be worth its 64 KB of partial sums
-    // and the second launch. The device counts the parts, the host knows only the sizes: it
-    // leaves parts out where three times the mean group would have none, and where the tiles
-    // are many. 128-row tiles, us without parts -> with, for even groups and one with 3.7 times
+    // So a group that has most of the rows keeps a few CUs busy long after the others: its sums
+    // are taken in parts of little more than a CU's share of the rows, where a part stays long
+    // enough to be worth its 64 KB of partial sums and the second launch. The device counts the
+    // parts; the host leaves them out where the longest group should have none. 128-row tiles,
+    // us without parts -> with, for even groups and one with 3.7 times
     // the mean's rows: 32768 rows of 8, 512 x 512 51 -> 42 and 155 -> 42; 512 x 1024 63 -> 64
     // and 156 -> 64; 1024 x 1024 88 -> 94 and 156 -> 106; 8192 rows of 8, 512 x 1024 21 -> 25 and
     // 47 -> 30; fp32, 512 x 512 54 -> 55 and 142 -> 62, 1024 x 1024 151 -> 150 and 277 -> 192.
@@ -827,8 +835,7 @@ Plan plan_of(const MatmulArgs& a) {
     int64_t rows = share + share / 4 < few ? share + share / 4 : few;
     if (rows < share * 4 / 5) rows = share * 4 / 5;
     if (rows < least) rows = least;
-    const int64_t longest = 3 * a.R / a.E < a.R ? 3 * a.R / a.E : a.R;
-    if (longest <= rows || tiles > 4 * kCus || (a.bf16_in && tiles > kCus && share < 128 * bk)) return p;
+    if (longest <= rows || (a.bf16_in && tiles > kCus && share < 128 * bk)) return p;
     p.part_rows = rows;
     p.part_sums = a.R / rows + (groups < a.R / rows ? groups : a.R / rows);
     return p;

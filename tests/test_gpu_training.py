@@ -319,7 +319,8 @@ def test_matmul_tn_groups_in_parts_beside_whole_ones(moe, c, K, N, dt, out):
 
 
 @pytest.mark.parametrize("form,c,K,N", [("nn", [1, 700, 0, 799], 1032, 5640), ("nt", [257, 1, 1242], 1160, 5512),
-                                        ("tn", [33, 0, 300], 1000, 2832), ("tn", [1, 97, 64], 1288, 2056)])
+                                        ("tn", [33, 0, 300], 1000, 2832), ("tn", [1, 97, 64], 1288, 2056),
+                                        ("tn", [0, 70, 130], 2312, 2568), ("tn", [150], 2568, 4360)])
 @pytest.mark.parametrize("gathered", [False, True])
 def test_matmul_many_tiles(moe, form, c, K, N, gathered):
     # more tiles than are resident at once: the largest tiles, several of them per workgroup
