@@ -14,7 +14,7 @@
 // launch, and the partial sums' sum in chunk order: no atomics, one fixed order. bf16, both
 // losses: 4096 tokens of 1024, 8 experts, 21 us (ds 8.8, products 7.6, sum 3.6: latencies, a
 // copy of those bytes takes 3.4); 8191 tokens of 2048, 64 experts, top-4 with the rows'
-// gradients added, 73-85 us (transpose 4.5, ds 16, products 50 at 4 TB/s, sum 5; a copy 40).
+// gradients added, 71-83 us (transpose 4.5, ds 14, products 50 at 4 TB/s, sum 5; a copy 40).
 //
 // Both products run on the matrix cores. fp32: v_mfma_f32_32x32x2_f32 on the values. bf16:
 // v_mfma_f32_32x32x16_bf16 with ds split into two bf16 terms (ds ~ hi + lo, off by 2^-17 of
@@ -33,7 +33,6 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // puts it itself, up to this size; from HBM, by a kernel of its own, beyond (mid-size layer,
 // 16 KB: picking each expert's column out of W_g's rows instead took 14 us, this 9).
 constexpr size_t kLdsWg = 65536;
-constexpr int kTok = 16;     // tokens per workgroup of the ds kernel
 constexpr int kTile = 64;    // tokens that the dW_g workgroups take at a time
 constexpr int kSlab = 128;   // columns of x per dW_g workgroup: 32 per wave
 constexpr int kDxCols = 256; // columns of dx per workgroup: 64 per wave
@@ -73,19 +72,20 @@ __global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* __restri
   else static_cast<uint32_t*>(out)[i] = w32[(size_t)c * E + e];
 }
 
-// ds of 16 tokens, 16 lanes per token, lane `sub` owning experts sub + 16 i: into dlogits
-// and the operand rows.
-template <typename TI, int EP>
+// ds of 256 / LANES tokens, LANES lanes per token, lane `sub` owning experts sub + LANES i: into
+// dlogits and the operand rows.
+template <typename TI, int EP, int LANES>
 __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const TI* wt, int64_t t0) {
-  const int tok = threadIdx.x >> 4, sub = threadIdx.x & 15;
+  const int tok = threadIdx.x / LANES, sub = threadIdx.x % LANES;
   const int64_t t = t0 + tok < a.T ? t0 + tok : a.T - 1;  // (past the end: a copy, not stored)
   const int E = a.E, k = a.k;
   const float inv_T = 1.0f / (float)a.T;
-  float p[4], dp[4], sel[4] = {0.f, 0.f, 0.f, 0.f};  // sel: the slots' part of ds
+  constexpr int PE = 64 / LANES;  // experts per lane
+  float p[PE], dp[PE], sel[PE] = {};  // sel: the slots' part of ds
   float dot = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = sub + 16 * i;
+  for (int i = 0; i < PE; ++i) {
+    const int e = sub + LANES * i;
     p[i] = e < E ? a.probs[t * E + e] : 0.f;
     dp[i] = (a.loss_grad != 0.f && e < E) ? a.loss_grad * ((float)E / (float)k) * inv_T * a.f[e] : 0.f;
   }
@@ -117,31 +117,31 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const TI* wt, i
       if (ex[j] < 0) continue;
       const float v = w[j] * (a.renorm ? g[j] - dot : g[j]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (ex[j] == sub + 16 * i) sel[i] += v;
+      for (int i = 0; i < PE; ++i)
+        if (ex[j] == sub + LANES * i) sel[i] += v;
     }
     if (a.renorm) dot = 0.f;  // (of sel's sum)
   }
   float mean = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) mean += p[i] * dp[i];
+  for (int i = 0; i < PE; ++i) mean += p[i] * dp[i];
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) mean += __shfl_xor(mean, o);
+  for (int o = LANES / 2; o > 0; o >>= 1) mean += __shfl_xor(mean, o);
   mean += dot;
   float zc = 0.f;
   if (a.z_loss_grad != 0.f) {
     // lse = s - log p at the most probable expert (p >= 1 / E there, so log p is exact to
-    // about an ulp); the 16 lanes split the dot product
+    // about an ulp); the lanes split the dot product
     float best = -1.f;
     int be = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (sub + 16 * i < E && p[i] > best) {
+    for (int i = 0; i < PE; ++i)
+      if (sub + LANES * i < E && p[i] > best) {
         best = p[i];
-        be = sub + 16 * i;
+        be = sub + LANES * i;
       }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
+    for (int o = LANES / 2; o > 0; o >>= 1) {
       const float ob = __shfl_xor(best, o);
       const int oe = __shfl_xor(be, o);
       if (ob > best || (ob == best && oe < be)) {
@@ -155,20 +155,20 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const TI* wt, i
     const TI* W = wt + (size_t)be * a.d;
     float s = 0.f;
 #pragma unroll 8
-    for (int c = sub * N; c < a.d; c += 16 * N) {
+    for (int c = sub * N; c < a.d; c += LANES * N) {
       const vec v = *reinterpret_cast<const vec*>(x + c), u = *reinterpret_cast<const vec*>(W + c);
 #pragma unroll
       for (int i = 0; i < N; ++i) s += (float)v[i] * (float)u[i];
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor(s, o);
     if (a.bias) s += a.bias[be];
     zc = a.z_loss_grad * 2.0f * inv_T * (s - logf(best));
   }
   if (t0 + tok >= a.T) return;
 #pragma unroll
-  for (int i = 0; i < EP / 16; ++i) {
-    const int e = sub + 16 * i;
+  for (int i = 0; i < EP / LANES; ++i) {
+    const int e = sub + LANES * i;
     const float v = sel[i] + p[i] * (dp[i] - mean + zc);  // (0 past E: both are)
     if (e < E) a.dlogits[t * E + e] = v;
     if constexpr (sizeof(TI) == 2) {
@@ -182,9 +182,10 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const TI* wt, i
 }
 
 // LDS_WG: W_g transposed into (dynamic) LDS first.
-template <typename TI, int EP, bool LDS_WG>
+template <typename TI, int EP, bool LDS_WG, int LANES>
 __global__ __launch_bounds__(256) void ds_kernel(RouteGradArgs a) {
   extern __shared__ __attribute__((aligned(16))) char wg_lds[];
+  constexpr int TOK = 256 / LANES;
   if constexpr (LDS_WG) {
     constexpr int N = Chunk<TI>::N;
     TI* W = reinterpret_cast<TI*>(wg_lds);
@@ -202,11 +203,11 @@ __global__ __launch_bounds__(256) void ds_kernel(RouteGradArgs a) {
       }
     }
     __syncthreads();
-    for (int64_t t0 = (int64_t)blockIdx.x * kTok; t0 < a.T; t0 += (int64_t)gridDim.x * kTok)
-      token_ds<TI, EP>(a, W, t0);
+    for (int64_t t0 = (int64_t)blockIdx.x * TOK; t0 < a.T; t0 += (int64_t)gridDim.x * TOK)
+      token_ds<TI, EP, LANES>(a, W, t0);
   } else {
-    for (int64_t t0 = (int64_t)blockIdx.x * kTok; t0 < a.T; t0 += (int64_t)gridDim.x * kTok)
-      token_ds<TI, EP>(a, static_cast<const TI*>(a.wt), t0);
+    for (int64_t t0 = (int64_t)blockIdx.x * TOK; t0 < a.T; t0 += (int64_t)gridDim.x * TOK)
+      token_ds<TI, EP, LANES>(a, static_cast<const TI*>(a.wt), t0);
   }
 }
 
@@ -570,19 +571,26 @@ hipError_t launch(RouteGradArgs a, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (a.T > 0) {
     const size_t wg_bytes = (size_t)a.d * a.E * sizeof(TI);
-    const unsigned grid = capped_grid((a.T + kTok - 1) / kTok);
+    // Lanes per token: 32 where the z-loss's dot product is a chain of loads that more waves
+    // hide (us of the whole gradient with 16 -> 32: 8191 tokens of 2048, 64 experts, 48.6 -> 46.3;
+    // 200 of 1024, 8 experts, 14.7 -> 14.0), 16 without it, and where the workgroups come back
+    // for more tokens (16384 of 4096, 8 experts, 97.7 against 103.6).
+    constexpr int64_t kLdsGroups = 512;  // two per CU: each brings W_g into its LDS once
+    const auto groups = [&](int lanes) { return capped_grid((a.T + 256 / lanes - 1) / (256 / lanes)); };
     if (a.z_loss_grad == 0.f) {
-      ds_kernel<TI, EP, false><<<grid, 256, 0, s>>>(a);
+      ds_kernel<TI, EP, false, 16><<<groups(16), 256, 0, s>>>(a);
     } else if (wg_bytes <= kLdsWg) {
-      // (as many workgroups as two per CU: each brings W_g into its LDS once)
-      ds_kernel<TI, EP, true><<<grid < 512 ? grid : 512, 256, wg_bytes, s>>>(a);
+      if (a.T <= kLdsGroups * 8)
+        ds_kernel<TI, EP, true, 32><<<groups(32), 256, wg_bytes, s>>>(a);
+      else
+        ds_kernel<TI, EP, true, 16><<<kLdsGroups < groups(16) ? kLdsGroups : groups(16), 256, wg_bytes, s>>>(a);
     } else {
       const bool b16 = sizeof(TI) == 2;
       transpose_kernel<<<(a.d * a.E + 255) / 256, 256, 0, s>>>(
           b16 ? static_cast<const uint16_t*>(a.Wg) : nullptr,
           b16 ? nullptr : static_cast<const uint32_t*>(a.Wg), a.d, a.E, a.wt);
       if ((e = hipGetLastError()) != hipSuccess) return e;
-      ds_kernel<TI, EP, false><<<grid, 256, 0, s>>>(a);
+      ds_kernel<TI, EP, false, 32><<<groups(32), 256, 0, s>>>(a);
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int dw_blocks = dw ? chunks * ((a.d + kSlab - 1) / kSlab) : 0;
