@@ -350,6 +350,39 @@ def test_matmul_many_tiles(moe, form, c, K, N, gathered):
     close(o if form == "tn" else o[:R], 2 * ref, 2 * mag, terms + 4)
 
 
+@pytest.mark.parametrize("form", ["nn", "nt", "tn"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_matmul_captured_with_other_groups_at_each_replay(moe, form, accumulate):
+    # the bounds are read when the graph runs: long and empty groups, whole sums and parts
+    say("captured", form, accumulate)
+    R, E, K, N = 3000, 4, 264, 136
+    g = gen(21)
+    a, b = draw(g, R, K, dtype=BF16), draw(g, *{"nn": (E, K, N), "nt": (E, N, K), "tn": (R, N)}[form], dtype=BF16)
+    tables = [[0, 0, 3000, 0], [700, 800, 750, 750], [2990, 1, 0, 9], [0, 0, 0, 0], [1, 2, 3, 2000]]
+    da, db, do = cuda(a, b, offsets_of(tables[1]))
+    shape = (E, K, N) if form == "tn" else (R, N)
+    out = torch.zeros(shape, device="cuda")
+    moe.moe_grouped_matmul(da, db, do, form=form, out=out, accumulate=accumulate)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        moe.moe_grouped_matmul(da, db, do, form=form, out=out, accumulate=accumulate)
+    for c in tables:
+        do.copy_(offsets_of(c))
+        out.fill_(1.5)
+        want = out.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        moe.moe_grouped_matmul(da, db, do, form=form, out=want, accumulate=accumulate)
+        assert torch.equal(out, want), c
+        last = sum(c)
+        rows = slice(None) if form == "tn" else slice(0, last)
+        ref, mag = matmul_ref(form, a[:last], b[:last] if form == "tn" else b, c)
+        close(out[rows], ref + 1.5 * accumulate, mag + 1.5 * accumulate, (max(c) if form == "tn" else K) + 34, c)
+        if form != "tn":
+            assert bool((out[last:] == 1.5).all())
+
+
 def test_matmul_rows_past_2_31_elements(moe):
     # a and out of more than 2^31 elements: the last rows against the first ones' copies
     say("far rows")
