@@ -138,8 +138,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_kernel(NormA
 }
 
 // Gradient. As above; acc[0..2]: this thread's column sums of dgamma, dgamma_post and the
-// per-channel dgate over its workgroup's rows, written to partial[group][3][d] (group: the
-// workgroup, or the wave where a row is a wave's).
+// per-channel dgate over its rows, which the workgroup writes to partial[workgroup][3][d],
+// those that are asked for.
 template <typename TI, int TPR, int CH>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_grad_kernel(NormGradArgs a) {
   constexpr int ROWS = TPR > 256 ? 1 : 256 / TPR;
@@ -240,12 +240,29 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void block_norm_grad_kernel(
     }
   }
 #pragma unroll
-  for (int s = 0; s < 3; ++s)
+  for (int s = 0; s < 3; ++s) {
+    if (s == 0 ? !a.dgamma : s == 1 ? !a.dgamma_post : !a.dgate || a.gate_kind != MOE_GATE_CHANNEL) continue;
+    float* out = a.partial + ((size_t)blockIdx.x * 3 + s) * a.d;
+    if constexpr (ROWS == 1) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = tid + c * TPR;
-      if (i < nch) store8(a.partial + ((size_t)group * 3 + s) * a.d + i * 8, acc[s][c]);
+      for (int c = 0; c < CH; ++c) {
+        const int i = tid + c * TPR;
+        if (i < nch) store8(out + i * 8, acc[s][c]);
+      }
+    } else {  // the waves' sums first, in order
+      __shared__ __attribute__((aligned(16))) float cols[ROWS][CH * TPR * 8];
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < CH; ++c) store8(cols[threadIdx.x / TPR] + (tid + c * TPR) * 8, acc[s][c]);
+      __syncthreads();
+      for (int i = threadIdx.x; i < a.d; i += ROWS * TPR) {
+        float v = cols[0][i];
+#pragma unroll
+        for (int r = 1; r < ROWS; ++r) v += cols[r][i];
+        out[i] = v;
+      }
     }
+  }
 }
 
 // Column sums of the partials: 64 columns per workgroup, sixteen threads per column on a
@@ -275,13 +292,27 @@ __global__ __launch_bounds__(64 * kSumParts) void norm_grad_sum_kernel(const flo
   out[c] = v;
 }
 
-// Workgroups of the gradient: enough rows in flight for HBM, few enough partial sums.
-int64_t grad_groups(int64_t T) { return T < 1024 ? (T > 0 ? T : 1) : 1024; }
+// Rows of up to 1024 values are a wave's, four to a workgroup.
+constexpr int kWaveRow = 1024;
+// Workgroups of the gradient: enough rows in flight for HBM, and few enough partial sums: 2^21
+// column sums of each kind, two rounds of rows (us, by workgroups: 8192 rows of 2048: 54 with
+// 1024, 67 with 512; 2048 of 4096: 50 with 1024, 39 with 512, 54 with 256; 8192 of 8192: 245 with
+// 1024, 214 with 256).
+int64_t grad_groups(int64_t T, int d) {
+  const int64_t rounds = d <= kWaveRow ? (T + 3) / 4 : T;
+  int64_t most = (int64_t(1) << 21) / d;
+  most = most > 1024 ? 1024 : most < 256 ? 256 : most;
+  const int64_t few = rounds < 256 ? rounds : 256;
+  int64_t n = rounds / 2 > few ? rounds / 2 : few;
+  n = n < most ? n : most;
+  return n > 0 ? n : 1;
+}
 
 template <typename TI>
 hipError_t launch_fwd(const NormArgs& a, hipStream_t s) {
   const int64_t T = a.T;
   if (a.d <= 512) block_norm_kernel<TI, 64, 1><<<capped_grid((T + 3) / 4), 256, 0, s>>>(a);
+  else if (a.d <= kWaveRow) block_norm_kernel<TI, 64, 2><<<capped_grid((T + 3) / 4), 256, 0, s>>>(a);
   else if (a.d <= 2048) block_norm_kernel<TI, 256, 1><<<capped_grid(T), 256, 0, s>>>(a);
   else if (a.d <= 4096) block_norm_kernel<TI, 256, 2><<<capped_grid(T), 256, 0, s>>>(a);
   else if (a.d <= 8192) block_norm_kernel<TI, 1024, 1><<<capped_grid(T), 1024, 0, s>>>(a);
@@ -291,20 +322,14 @@ hipError_t launch_fwd(const NormArgs& a, hipStream_t s) {
 
 template <typename TI>
 hipError_t launch_bwd(const NormGradArgs& a, hipStream_t s) {
-  const int64_t G = grad_groups(a.T);
-  int64_t groups = G;
-  if (a.d <= 512) {
-    groups = (G + 3) / 4 * 4;
-    block_norm_grad_kernel<TI, 64, 1><<<(unsigned)(groups / 4), 256, 0, s>>>(a);
-  } else if (a.d <= 2048) {
-    block_norm_grad_kernel<TI, 256, 1><<<(unsigned)G, 256, 0, s>>>(a);
-  } else if (a.d <= 4096) {
-    block_norm_grad_kernel<TI, 256, 2><<<(unsigned)G, 256, 0, s>>>(a);
-  } else if (a.d <= 8192) {
-    block_norm_grad_kernel<TI, 1024, 1><<<(unsigned)G, 1024, 0, s>>>(a);
-  } else {
-    block_norm_grad_kernel<TI, 1024, 2><<<(unsigned)G, 1024, 0, s>>>(a);
-  }
+  const int64_t groups = grad_groups(a.T, a.d);
+  const unsigned grid = (unsigned)groups;
+  if (a.d <= 512) block_norm_grad_kernel<TI, 64, 1><<<grid, 256, 0, s>>>(a);
+  else if (a.d <= kWaveRow) block_norm_grad_kernel<TI, 64, 2><<<grid, 256, 0, s>>>(a);
+  else if (a.d <= 2048) block_norm_grad_kernel<TI, 256, 1><<<grid, 256, 0, s>>>(a);
+  else if (a.d <= 4096) block_norm_grad_kernel<TI, 256, 2><<<grid, 256, 0, s>>>(a);
+  else if (a.d <= 8192) block_norm_grad_kernel<TI, 1024, 1><<<grid, 1024, 0, s>>>(a);
+  else block_norm_grad_kernel<TI, 1024, 2><<<grid, 1024, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   float* chan = a.gate_kind == MOE_GATE_CHANNEL ? a.dgate : nullptr;
@@ -317,7 +342,7 @@ hipError_t launch_bwd(const NormGradArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t norm_grad_workspace(int64_t T, int d) {
-  return (size_t)((grad_groups(T) + 3) / 4 * 4) * 3 * (size_t)d;
+  return (size_t)grad_groups(T, d) * 3 * (size_t)d;
 }
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
