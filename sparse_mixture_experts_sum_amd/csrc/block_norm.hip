@@ -294,14 +294,15 @@ __global__ __launch_bounds__(64 * kSumParts) void norm_grad_sum_kernel(const flo
 
 // Rows of up to 1024 values are a wave's, four to a workgroup.
 constexpr int kWaveRow = 1024;
-// Workgroups of the gradient: enough rows in flight for HBM, and few enough partial sums: 2^21
-// column sums of each kind, two rounds of rows (us, by workgroups: 8192 rows of 2048: 54 with
-// 1024, 67 with 512; 2048 of 4096: 50 with 1024, 39 with 512, 54 with 256; 8192 of 8192: 245 with
-// 1024, 214 with 256).
+// Workgroups of the gradient: as many as are resident together (their registers say how many),
+// and half as many as there are rounds of rows, so that the partial sums stay few (us, by
+// workgroups: 2048 rows of 4096: 43 with 1024, 36 with 512; 8192 of 3584: 130 with 585, 98
+// with 512; 8192 of 8192: 245 with 1024, 214 with 256; 8192 of 2048: 54 with 1024, 67 with 512).
+// 512 threads per row of 2049 to 4096 values, a chunk each: 16384 rows of 4096 262 -> 213 us
+// against 256 threads with two chunks, whose registers left two waves per SIMD.
 int64_t grad_groups(int64_t T, int d) {
   const int64_t rounds = d <= kWaveRow ? (T + 3) / 4 : T;
-  int64_t most = (int64_t(1) << 21) / d;
-  most = most > 1024 ? 1024 : most < 256 ? 256 : most;
+  const int64_t most = d <= 512 ? 1024 : d <= kWaveRow ? 512 : d <= 2048 ? 1024 : d <= 4096 ? 512 : 256;
   const int64_t few = rounds < 256 ? rounds : 256;
   int64_t n = rounds / 2 > few ? rounds / 2 : few;
   n = n < most ? n : most;
@@ -327,7 +328,7 @@ hipError_t launch_bwd(const NormGradArgs& a, hipStream_t s) {
   if (a.d <= 512) block_norm_grad_kernel<TI, 64, 1><<<grid, 256, 0, s>>>(a);
   else if (a.d <= kWaveRow) block_norm_grad_kernel<TI, 64, 2><<<grid, 256, 0, s>>>(a);
   else if (a.d <= 2048) block_norm_grad_kernel<TI, 256, 1><<<grid, 256, 0, s>>>(a);
-  else if (a.d <= 4096) block_norm_grad_kernel<TI, 256, 2><<<grid, 256, 0, s>>>(a);
+  else if (a.d <= 4096) block_norm_grad_kernel<TI, 512, 1><<<grid, 512, 0, s>>>(a);
   else if (a.d <= 8192) block_norm_grad_kernel<TI, 1024, 1><<<grid, 1024, 0, s>>>(a);
   else block_norm_grad_kernel<TI, 1024, 2><<<grid, 1024, 0, s>>>(a);
   hipError_t e = hipGetLastError();
