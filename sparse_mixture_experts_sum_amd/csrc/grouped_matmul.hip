@@ -21,7 +21,7 @@
 // TFLOP/s), NN 3.03 ms (1268), TN 3.3 ms (1163); 8192 rows of 8, K 1024, N 4096: NN 83 us
 // (822 TFLOP/s, 57 us at those rates); 32764 rows of 64, 2048 x 1408: TN with fp32 results 300
 // us (629 TFLOP/s and 2.9 TB/s at once; 168 us for the slower of the two alone); 16 rows of 8,
-// K 4096, N 14336: NN 160-167 us (5.6-5.9 TB/s). fp32, 8192 rows of 8, K 1024, N 4096: NN 562 us
+// K 4096, N 14336: NN 152-159 us (5.9-6.2 TB/s). fp32, 8192 rows of 8, K 1024, N 4096: NN 562 us
 // (122 TFLOP/s, a large square product 134).
 #include <math.h>
 
@@ -122,10 +122,11 @@ struct Operand {
   }
 };
 
-// BM x BN tile, WGM x (4 / WGM) waves.
-template <typename T, int FORM_, int BM_, int BN_, int BK_, int WGM>
+// BM x BN tile, WGM x (4 / WGM) waves. STREAM: b's loads are non-temporal.
+template <typename T, int FORM_, int BM_, int BN_, int BK_, int WGM, bool STREAM_ = false>
 struct Geo {
   typedef T type;
+  static constexpr bool STREAM = STREAM_;
   static constexpr int FORM = FORM_, BM = BM_, BN = BN_, BK = BK_;
   static constexpr bool TN = FORM == MOE_MATMUL_TN;
   static constexpr int EPC = 16 / sizeof(T);
@@ -199,7 +200,8 @@ struct Issue {
     }
     char* to = is_a ? st + (ld.wave * G::A::PW + i) * 1024
                     : st + G::A::BYTES + (ld.wave * G::B::PW + i) * 1024;
-    __builtin_amdgcn_global_load_lds(p, (lds_void*)to, 16, 0, 0);
+    if (G::STREAM && !is_a) __builtin_amdgcn_global_load_lds(p, (lds_void*)to, 16, 0, 2);
+    else __builtin_amdgcn_global_load_lds(p, (lds_void*)to, 16, 0, 0);
   }
 };
 
@@ -872,10 +874,22 @@ hipError_t launch_tile(const MatmulArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Weights that are read once and do not fit the last-level cache: 32-row tiles, of the groups
+// that R rows spread over E evenly leave with a row or more (us: NT, 16 rows of 8 groups, K 14336,
+// N 4096, 147 -> 136; NN, 128 rows, K 4096, N 14336, 183 -> 164; what fits is better kept: NN, 2
+// rows, 36 against 40).
+template <typename T>
+bool streams(const MatmulArgs& a) {
+  constexpr double kLastLevel = 256e6;
+  const double active = a.E * (1.0 - exp(-(double)a.R / a.E));
+  return a.R <= 32 * (int64_t)a.E && active * (double)a.K * (double)a.N * sizeof(T) > kLastLevel;
+}
+
 template <typename T, int FORM, typename TO>
 hipError_t launch_form(const MatmulArgs& a, int bm, hipStream_t s) {
   constexpr int BK = 64 / sizeof(T);  // 64 bytes
   if constexpr (FORM != MOE_MATMUL_TN) {
+    if (bm == 32 && streams<T>(a)) return launch_tile<Geo<T, FORM, 32, 128, 2 * BK, 1, true>, TO>(a, s);
     if (bm == 32) return launch_tile<Geo<T, FORM, 32, 128, 2 * BK, 1>, TO>(a, s);
   }
   if constexpr (sizeof(T) == 2) {

@@ -350,6 +350,27 @@ def test_matmul_many_tiles(moe, form, c, K, N, gathered):
     close(o if form == "tn" else o[:R], 2 * ref, 2 * mag, terms + 4)
 
 
+@pytest.mark.parametrize("form", ["nn", "nt"])
+def test_matmul_weights_past_the_last_level_cache(moe, form):
+    # few rows a group, weights of more than 256 MB
+    c, K, N = [(7 * i * i + i) % 9 for i in range(40)], 1032, 3400
+    c[3], c[39] = 45, 0
+    R, E, g = sum(c), len(c), gen(5)
+    say("far weights", form, R)
+    a = draw(g, 77, K, dtype=BF16)
+    b = torch.randn(E, *((K, N) if form == "nn" else (N, K)), dtype=BF16, generator=g)
+    ga = torch.randint(0, 77, (R + 3,), generator=g).int()
+    ref, mag = matmul_ref(form, a, b, c, ga[:R])
+    da, db, do, dga = cuda(a, b, offsets_of(c), ga)
+    for out in (BF16, FP32):
+        o = torch.full((R + 3, N), 2.5, dtype=out, device="cuda")
+        moe.moe_grouped_matmul(da, db, do, form=form, gather_a=dga, out=o)
+        close(o[:R], ref, mag, K + 2)
+        assert bool((o[R:] == 2.5).all())
+    moe.moe_grouped_matmul(da, db, do, form=form, gather_a=dga, out=o, accumulate=True)
+    close(o[:R], 2 * ref, 2 * mag, K + 4)
+
+
 @pytest.mark.parametrize("form", ["nn", "nt", "tn"])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_matmul_captured_with_other_groups_at_each_replay(moe, form, accumulate):
