@@ -14,7 +14,7 @@
 // launch, and the partial sums' sum in chunk order: no atomics, one fixed order. bf16, both
 // losses: 4096 tokens of 1024, 8 experts, 21 us (ds 8.8, products 7.6, sum 3.6: latencies, a
 // copy of those bytes takes 3.4); 8191 tokens of 2048, 64 experts, top-4 with the rows'
-// gradients added, 71-83 us (transpose 4.5, ds 14, products 50 at 4 TB/s, sum 5; a copy 40).
+// gradients added, 76 us (transpose 4.5, ds 14, products 46 at 5 TB/s, sum 5; a copy 40).
 //
 // Both products run on the matrix cores. fp32: v_mfma_f32_32x32x2_f32 on the values. bf16:
 // v_mfma_f32_32x32x16_bf16 with ds split into two bf16 terms (ds ~ hi + lo, off by 2^-17 of
@@ -230,8 +230,8 @@ __device__ __forceinline__ f32x16 zero16() {
 }
 
 // The routed rows of a dx tile: 32 tokens of up to KM slots, 64 columns, in passes of 32 /
-// PASSES tokens whose loads are all in flight together.
-template <typename TI, int KM>
+// PASSES tokens whose loads are all in flight together. STREAM: non-temporal loads.
+template <typename TI, int KM, bool STREAM>
 struct RowTile {
   static constexpr int N = Chunk<TI>::N, PIECES = 64 / N, RPI = 64 / PIECES;  // tokens per load
   static constexpr int ITS = 32 / RPI, PASSES = KM > 4 ? ITS : ITS > 4 ? ITS / 4 : 1;
@@ -251,7 +251,8 @@ struct RowTile {
         const int at = pos[r * KM + j];
         in[i] |= (at >= 0 ? 1u : 0u) << j;
         // (a slot without a row reads row 0 and drops it: no branch between the loads)
-        v[i][j] = *reinterpret_cast<const vec*>(static_cast<const TI*>(a.rows) + (size_t)max(at, 0) * a.d + c);
+        const vec* p = reinterpret_cast<const vec*>(static_cast<const TI*>(a.rows) + (size_t)max(at, 0) * a.d + c);
+        v[i][j] = STREAM ? __builtin_nontemporal_load(p) : *p;
       }
     }
   }
@@ -344,12 +345,12 @@ struct TilePos {
 // first operand, then through the wave's piece of LDS, so that rows and dx move in 16-byte
 // pieces, 128 or 256 contiguous bytes per row. The rows' loads go out first; `next` fetches the
 // following tile's slots behind them.
-template <typename TI, int EP, int KM>
+template <typename TI, int EP, int KM, bool STREAM>
 __device__ __forceinline__ void dx_tile(const RouteGradArgs& a, int64_t t0, int64_t t_next, int c0,
                                         const WgFrags<TI, EP>& wg, TilePos<KM>& slots, float* buf, int* pos) {
   const int ln = threadIdx.x & 63, x = ln & 31, h = ln >> 5;
   const int64_t t = min(t0 + x, a.T - 1);
-  typedef RowTile<TI, KM> Rows;
+  typedef RowTile<TI, KM, STREAM> Rows;
   constexpr int N = Rows::N, PIECES = Rows::PIECES, RPI = Rows::RPI;
   const int c = c0 + (ln % PIECES) * N, c_in = min(c, a.d - N);
   Rows rows;
@@ -514,7 +515,7 @@ __device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, 
 
 // Workgroups [0, dw_blocks): partial sums of dW_g and db, column slabs within a chunk; the
 // others: dx tiles, columns within 32 tokens.
-template <typename TI, int EP, int KM>
+template <typename TI, int EP, int KM, bool STREAM>
 __global__ __launch_bounds__(256) void route_products_kernel(RouteGradArgs a, int dw_blocks) {
   // dx: 8 KB per wave; dW_g (bf16): x and ds tiles
   __shared__ __attribute__((aligned(16))) char lds[32768];
@@ -538,7 +539,7 @@ __global__ __launch_bounds__(256) void route_products_kernel(RouteGradArgs a, in
     TilePos<KM> slots;
     slots.fetch(a, first * 32, ln);
     for (int64_t n = first; n < last; ++n)
-      dx_tile<TI, EP, KM>(a, n * 32, (n + 1) * 32, c0, wg, slots, reinterpret_cast<float*>(lds) + wave * 2048,
+      dx_tile<TI, EP, KM, STREAM>(a, n * 32, (n + 1) * 32, c0, wg, slots, reinterpret_cast<float*>(lds) + wave * 2048,
                           pos[wave]);
   }
 }
@@ -558,6 +559,13 @@ __global__ __launch_bounds__(256) void route_sum_kernel(RouteGradArgs a, int chu
   } else if (a.db) {
     a.db[i - nw] = v;
   }
+}
+
+template <typename TI, int EP, bool STREAM>
+void launch_products(const RouteGradArgs& a, int km, unsigned grid, int dw_blocks, hipStream_t s) {
+  if (km <= 2) route_products_kernel<TI, EP, 2, STREAM><<<grid, 256, 0, s>>>(a, dw_blocks);
+  else if (km <= 4) route_products_kernel<TI, EP, 4, STREAM><<<grid, 256, 0, s>>>(a, dw_blocks);
+  else route_products_kernel<TI, EP, 8, STREAM><<<grid, 256, 0, s>>>(a, dw_blocks);
 }
 
 template <typename TI, int EP>
@@ -598,10 +606,13 @@ hipError_t launch(RouteGradArgs a, hipStream_t s) {
     if (dw_blocks || dx_blocks) {
       const unsigned grid = dw_blocks + (dx_blocks ? capped_grid(dx_blocks) : 0);
       const int km = a.rows && a.R > 0 ? a.k : 0;
-      if (km == 0) route_products_kernel<TI, EP, 0><<<grid, 256, 0, s>>>(a, dw_blocks);
-      else if (km <= 2) route_products_kernel<TI, EP, 2><<<grid, 256, 0, s>>>(a, dw_blocks);
-      else if (km <= 4) route_products_kernel<TI, EP, 4><<<grid, 256, 0, s>>>(a, dw_blocks);
-      else route_products_kernel<TI, EP, 8><<<grid, 256, 0, s>>>(a, dw_blocks);
+      // Rows that fill half of the last-level cache or more push out what is read again (8191
+      // tokens of 2048, top-4, 134 MB: the whole gradient 80.2 -> 76.5 us); fewer stay there
+      // from the kernel that wrote them.
+      const bool stream = (double)a.R * a.d * sizeof(TI) > 128e6;
+      if (km == 0) route_products_kernel<TI, EP, 0, false><<<grid, 256, 0, s>>>(a, dw_blocks);
+      else if (stream) launch_products<TI, EP, true>(a, km, grid, dw_blocks, s);
+      else launch_products<TI, EP, false>(a, km, grid, dw_blocks, s);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }

@@ -598,6 +598,27 @@ def test_route_adds_rows_and_takes_dw_by_row(moe, dt):
     assert not bool(out["dlogits"].any()) and not bool(out["dW_g"].any())
 
 
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_route_adds_rows_past_half_the_last_level_cache(moe, dt):
+    # (only dx's sums of rows: dw is None, so every other gradient is zero)
+    T, d, E, k = 9001, 2048, 8, 4
+    say("route many rows", dt)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows = torch.randn(T * k, d, device="cuda", generator=g).to(dt)
+    pos = torch.randperm(T * k, device="cuda", generator=g).int().view(T, k)
+    pos[5] = -1
+    pos[6, 1] = T * k
+    x, W = torch.zeros(T, d, dtype=dt, device="cuda"), torch.zeros(d, E, dtype=dt, device="cuda")
+    p = torch.full((T, E), 1 / E, device="cuda")
+    idx = torch.arange(k, dtype=torch.int32, device="cuda").repeat(T, 1)
+    out = moe.moe_route_backward(x, W, p, idx, torch.full((T, k), 1 / k, device="cuda"), None, rows=rows, pos=pos)
+    some = torch.cat([torch.arange(0, 200), torch.arange(T - 300, T)])
+    at = pos.cpu()[some].long()
+    ok = ((at >= 0) & (at < T * k))[..., None]
+    v = torch.where(ok, rows.cpu().double()[at.clamp(0, T * k - 1)], 0.0)
+    close(out["dx"][some.cuda()], v.sum(1), v.abs().sum(1), k)
+
+
 def test_route_with_kept_slots_of_the_smallest_probabilities(moe):
     # the likely experts' slots were dropped by the capacity: S of the kept ones is a
     # denormal number, their weights are not. ds is w_j (dw_j - sum_i dw_i w_i) there, and
