@@ -340,7 +340,7 @@ moe_status moe_grouped_matmul(const moe_matmul_shape* shape, const void* a, cons
                               hipStream_t stream);
 
 /* Bytes of workspace moe_grouped_matmul needs for `shape`: partial sums where few output tiles
- * share a long sum, or a TN group may have most of the rows; some 40 MiB at most. 0 (and a NULL
+ * share a long sum, or a TN group may have most of the rows; some 64 MiB at most. 0 (and a NULL
  * workspace) elsewhere. Host only. */
 moe_status moe_grouped_matmul_workspace_size(const moe_matmul_shape* shape, size_t* bytes);
 

@@ -835,7 +835,11 @@ Plan plan_of(const MatmulArgs& a) {
     const int bk = a.bf16_in ? 32 : 16;
     const int64_t least = (a.bf16_in ? 24 : 8) * bk, few = (a.bf16_in ? 80 : 40) * bk;
     int64_t rows = share + share / 4 < few ? share + share / 4 : few;
-    if (rows < share * 4 / 5) rows = share * 4 / 5;
+    // fp32, bound by the matrix units: all items (half a part more per group) are one round of
+    // two workgroups per CU (us: 32768 rows of 8 groups, 512 x 512, against the bf16 rule: 218 -> 168;
+    // 20000 rows of one, 1024 x 512: 277 -> 183; bf16, 32768 rows of 4, 512 x 1408: 73 against 92).
+    const int64_t round = a.bf16_in ? share * 4 / 5 : tiles < 2 * kCus ? share * 2 * kCus / (4 * kCus - tiles) : share;
+    if (rows < round) rows = round;
     if (rows < least) rows = least;
     if (longest <= rows || (a.bf16_in && tiles > kCus && share < 128 * bk)) return p;
     p.part_rows = rows;
