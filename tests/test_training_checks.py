@@ -161,7 +161,8 @@ def test_workspace_sizes(lib):
     s = M.make_shape(1000, 256, 64, 8, 2)
     assert lib.moe_route_backward_workspace_size(bytes(s), ctypes.byref(n)) == 0 and n.value > 0
     assert lib.moe_block_norm_backward_workspace_size(TR._NORM_SHAPE(100, 64, 1, 0, 1.0, 1.0), ctypes.byref(n)) == 0
-    assert n.value >= 100 * 3 * 64 * 4
+    # partial sums of three kinds per workgroup, at least one workgroup
+    assert n.value >= 3 * 64 * 4 and n.value % (3 * 64 * 4) == 0
 
 
 def test_swiglu_statuses(lib):
