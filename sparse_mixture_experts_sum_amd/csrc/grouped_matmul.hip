@@ -824,21 +824,23 @@ Plan plan_of(const MatmulArgs& a) {
     // So a group that has most of the rows keeps a few CUs busy long after the others: its sums
     // are taken in parts of little more than a CU's share of the rows, where a part stays long
     // enough to be worth its 64 KB of partial sums and the second launch. The device counts the
-    // parts; the host leaves them out where the longest group should have none. 128-row tiles,
-    // us without parts -> with, for even groups and one with 3.7 times
-    // the mean's rows: 32768 rows of 8, 512 x 512 51 -> 42 and 155 -> 42; 512 x 1024 63 -> 64
-    // and 156 -> 64; 1024 x 1024 88 -> 94 and 156 -> 106; 8192 rows of 8, 512 x 1024 21 -> 25 and
-    // 47 -> 30; fp32, 512 x 512 54 -> 55 and 142 -> 62, 1024 x 1024 151 -> 150 and 277 -> 192.
-    // 16384 rows of one group, 104 x 200: 164 -> 21. Left whole: bf16, 8192 rows, 1024 x 1024
-    // (28 against 31 even, 36 against 41 with 2.6 times the mean's, 45 against 39 with 3.7).
+    // parts; the host leaves them out where the longest group should have none. 128-row tiles, us
+    // without parts -> with, for even groups and one with 3.7 times the mean's rows: 32768 rows of
+    // 8, 512 x 512 51 -> 42 and 155 -> 42; 512 x 1024 63 -> 54 and 156 -> 57; 1024 x 1024 88 -> 82
+    // and 156 -> 97; 8192 rows of 8, 512 x 1024 21 -> 22 and 47 -> 26; fp32, 512 x 512 54 -> 53 and
+    // 142 -> 60, 1024 x 1024 151 -> 147 and 277 -> 166. 16384 rows of one group, 104 x 200: 164 ->
+    // 21. Left whole: bf16, 8192 rows, 1024 x 1024 (28 against 31 even, 36 against 41 with 2.6
+    // times the mean's, 45 against 39 with 3.7).
     const int64_t tiles = tiles_of(a, 128, 128), share = a.R * (tiles / a.E) / kCus;
     const int bk = a.bf16_in ? 32 : 16;
     const int64_t least = (a.bf16_in ? 24 : 8) * bk, few = (a.bf16_in ? 80 : 40) * bk;
     int64_t rows = share + share / 4 < few ? share + share / 4 : few;
     // fp32, bound by the matrix units: all items (half a part more per group) are one round of
-    // two workgroups per CU (us: 32768 rows of 8 groups, 512 x 512, against the bf16 rule: 218 -> 168;
-    // 20000 rows of one, 1024 x 512: 277 -> 183; bf16, 32768 rows of 4, 512 x 1408: 73 against 92).
-    const int64_t round = a.bf16_in ? share * 4 / 5 : tiles < 2 * kCus ? share * 2 * kCus / (4 * kCus - tiles) : share;
+    // two workgroups per CU (us, against the bf16 rule: 32768 rows of 8 groups, 512 x 512 218 ->
+    // 168; 20000 rows of one, 1024 x 512 277 -> 183; bf16, 32768 rows of 4, 512 x 1408 73 against 92).
+    const int64_t round = a.bf16_in          ? share * 4 / 5
+                          : tiles < 2 * kCus ? share * 2 * kCus / (4 * kCus - tiles)
+                                             : share;
     if (rows < round) rows = round;
     if (rows < least) rows = least;
     if (longest <= rows || (a.bf16_in && tiles > kCus && share < 128 * bk)) return p;
