@@ -17,9 +17,11 @@
 // gradients added, 76 us (transpose 4.5, ds 14, products 46 at 5 TB/s, sum 5; a copy 40).
 //
 // Both products run on the matrix cores. fp32: v_mfma_f32_32x32x2_f32 on the values. bf16:
-// v_mfma_f32_32x32x16_bf16 with ds split into two bf16 terms (ds ~ hi + lo, off by 2^-17 of
-// its size, against the 2^-8 that the bf16 results are rounded to); x and W_g are bf16
-// already. The ds kernel leaves the operands in rows of EP = 32 or 64 experts, zeros past E.
+// v_mfma_f32_32x32x16_bf16 with ds as a sum of three bf16 terms, which is ds to its last bit: ds
+// sums to zero over a token's experts, and a weight's gradient over tokens nearly so, so dx and
+// dW_g may be far smaller than their terms (two terms, off by 2^-17, take 167 against 174 us for
+// 16384 tokens of 4096, 8 experts, rows added, and the same time within 2% at the sizes above).
+// x and W_g are bf16 already. The ds kernel leaves ds in fp32 rows of EP = 32 or 64 experts, zeros past E.
 #include "train_common.h"
 #include "train_kernels.h"
 
@@ -47,8 +49,7 @@ __host__ __device__ inline int64_t chunk_len(int64_t T) {
 int64_t chunks_of(int64_t T) { return T > 0 ? (T + chunk_len(T) - 1) / chunk_len(T) : 0; }
 int padded_experts(int E) { return E <= 32 ? 32 : 64; }
 
-// Workspace: operand rows of ds (bf16: hi rows, then lo rows; fp32: the values), W_g
-// transposed, the partial sums, [E][d] of dW_g and [E] of db per chunk. Whole 256-byte pieces.
+// Workspace: padded rows of ds, W_g transposed, the partial sums, [E][d] of dW_g and [E] of db per chunk. Whole 256-byte pieces.
 struct Layout {
   size_t ds, wt, partial, total;
 };
@@ -73,7 +74,7 @@ __global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* __restri
 }
 
 // ds of 256 / LANES tokens, LANES lanes per token, lane `sub` owning experts sub + LANES i: into
-// dlogits and the operand rows.
+// dlogits and the padded rows.
 template <typename TI, int EP, int LANES>
 __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const TI* wt, int64_t t0) {
   const int tok = threadIdx.x / LANES, sub = threadIdx.x % LANES;
@@ -171,13 +172,7 @@ __device__ __forceinline__ void token_ds(const RouteGradArgs& a, const TI* wt, i
     const int e = sub + LANES * i;
     const float v = sel[i] + p[i] * (dp[i] - mean + zc);  // (0 past E: both are)
     if (e < E) a.dlogits[t * E + e] = v;
-    if constexpr (sizeof(TI) == 2) {
-      const bf16 hi = (bf16)v, lo = (bf16)(v - (float)hi);
-      static_cast<bf16*>(a.ds)[t * EP + e] = hi;
-      static_cast<bf16*>(a.ds)[(a.T + t) * EP + e] = lo;
-    } else {
-      static_cast<float*>(a.ds)[t * EP + e] = v;
-    }
+    a.ds[t * EP + e] = v;
   }
 }
 
@@ -221,6 +216,26 @@ __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
 }
 __device__ __forceinline__ f32x16 mma(float a, float b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
+}
+// Eight values as bf16 terms hi + mid + lo, each cut off instead of rounded: eight of the 24 bits
+// a term, so that the sum is the value (to 2^-133, the smallest bf16) and hi is finite where it
+// is. A non-finite value is hi alone.
+struct Terms {
+  s16x8 t[3];
+};
+__device__ __forceinline__ Terms split(f32x4 a, f32x4 b) {
+  Terms t;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = i < 4 ? a[i % 4] : b[i % 4];
+    const uint32_t hi = __builtin_bit_cast(uint32_t, v) & 0xffff0000u;
+    const float r = (hi & 0x7f800000u) == 0x7f800000u ? 0.f : v - __builtin_bit_cast(float, hi);
+    const uint32_t mid = __builtin_bit_cast(uint32_t, r) & 0xffff0000u;
+    t.t[0][i] = (short)(hi >> 16);
+    t.t[1][i] = (short)(mid >> 16);
+    t.t[2][i] = (short)(__builtin_bit_cast(uint32_t, r - __builtin_bit_cast(float, mid)) >> 16);
+  }
+  return t;
 }
 __device__ __forceinline__ f32x16 zero16() {
   f32x16 v;
@@ -284,17 +299,14 @@ struct WgFrags<bf16, EP> {
     }
   }
   __device__ __forceinline__ void product(const RouteGradArgs& a, int64_t t, int h, f32x16 (&acc)[2]) const {
-    const bf16* hi = static_cast<const bf16*>(a.ds) + t * EP + 8 * h;
-    const bf16* lo = hi + a.T * EP;
+    const f32x4* row = reinterpret_cast<const f32x4*>(a.ds + t * EP + 8 * h);
 #pragma unroll
     for (int s = 0; s < EP / 16; ++s) {
-      const s16x8 dh = *reinterpret_cast<const s16x8*>(hi + 16 * s);
-      const s16x8 dl = *reinterpret_cast<const s16x8*>(lo + 16 * s);
+      const Terms d = split(row[4 * s], row[4 * s + 1]);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        acc[b] = mma(f[b][s], dh, acc[b]);
-        acc[b] = mma(f[b][s], dl, acc[b]);
-      }
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int n = 0; n < 3; ++n) acc[b] = mma(f[b][s], d.t[n], acc[b]);
     }
   }
 };
@@ -314,7 +326,7 @@ struct WgFrags<float, EP> {
     }
   }
   __device__ __forceinline__ void product(const RouteGradArgs& a, int64_t t, int h, f32x16 (&acc)[2]) const {
-    const float* row = static_cast<const float*>(a.ds) + t * EP + h * (EP / 2);
+    const float* row = a.ds + t * EP + h * (EP / 2);
 #pragma unroll
     for (int i = 0; i < EP / 2; ++i) {
       const float v = row[i];
@@ -414,13 +426,11 @@ __device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, 
 #pragma unroll
   for (int n = 0; n < NE; ++n) acc[n] = zero16();
   if constexpr (sizeof(TI) == 2) {
-    // x [64][128], ds hi and lo [64][EP], bf16, read back transposed (a 16-lane group's four
-    // rows give each lane four tokens of one column); 16-byte pieces swizzled by the row
+    // x [64][128] and the terms of ds, [64][EP] each, bf16, read back transposed (a 16-lane
+    // group's four rows give each lane four tokens of one column); 16-byte pieces swizzled by the row
     char* xs = lds;
-    char* dh = lds + kTile * kSlab * 2;
-    char* dl = dh + kTile * EP * 2;
+    char* ds = lds + kTile * kSlab * 2;
     const bf16* X = static_cast<const bf16*>(a.x);
-    const bf16* D = static_cast<const bf16*>(a.ds);
     auto sw = [](int row, int pieces) { return ((0xCA60 >> (4 * (row & 3))) & 15) % pieces; };
     auto frag = [&](const char* base, int width, int k0, int col0) {  // rows k0 .. + 15, 32 columns
       const int g = ln >> 4, r = (ln & 15) >> 2, cc = ln & 3;
@@ -430,7 +440,9 @@ __device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, 
       const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * width * 2));
       return s16x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
     };
-    u32x4 xv[4], dv[2 * EP / 32];
+    constexpr int ND = EP / 32;  // eight experts of a token per thread, ND times
+    u32x4 xv[4];
+    f32x4 dv[ND][2];
     auto load = [&](int64_t t) {  // tokens past the chunk's end are zeros in both operands
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -438,10 +450,11 @@ __device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, 
         xv[i] = t + r < t1 && c < a.d ? ld16(X + (t + r) * a.d + c) : u32x4{0, 0, 0, 0};
       }
 #pragma unroll
-      for (int i = 0; i < 2 * EP / 32; ++i) {
-        const int p = (tid + 256 * i) % (kTile * EP / 8), r = p / (EP / 8), lo = i >= EP / 32;
-        dv[i] = t + r < t1 ? ld16(D + ((lo ? a.T : 0) + t + r) * EP + (p % (EP / 8)) * 8)
-                           : u32x4{0, 0, 0, 0};
+      for (int i = 0; i < ND; ++i) {
+        const int p = tid + 256 * i, r = p / (EP / 8);
+        const f32x4* d = reinterpret_cast<const f32x4*>(a.ds + (t + r) * EP + (p % (EP / 8)) * 8);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) dv[i][n] = t + r < t1 ? d[n] : f32x4{0, 0, 0, 0};
       }
     };
     load(t0);
@@ -453,9 +466,12 @@ __device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, 
         st16(xs + r * kSlab * 2 + ((p % 16) ^ sw(r, 16)) * 16, xv[i]);
       }
 #pragma unroll
-      for (int i = 0; i < 2 * EP / 32; ++i) {
-        const int p = (tid + 256 * i) % (kTile * EP / 8), r = p / (EP / 8), lo = i >= EP / 32;
-        st16((lo ? dl : dh) + r * EP * 2 + ((p % (EP / 8)) ^ sw(r, EP / 8)) * 16, dv[i]);
+      for (int i = 0; i < ND; ++i) {
+        const int p = tid + 256 * i, r = p / (EP / 8);
+        const Terms d = split(dv[i][0], dv[i][1]);
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+          st16(ds + (n * kTile + r) * EP * 2 + ((p % (EP / 8)) ^ sw(r, EP / 8)) * 16, __builtin_bit_cast(u32x4, d.t[n]));
       }
       __syncthreads();
       if (t + kTile < t1) load(t + kTile);  // in flight over this tile's products
@@ -463,15 +479,15 @@ __device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, 
       for (int s = 0; s < kTile / 16; ++s) {
         const s16x8 f = frag(xs, kSlab, 16 * s, wave * 32);
 #pragma unroll
-        for (int n = 0; n < NE; ++n) {
-          acc[n] = mma(frag(dh, EP, 16 * s, 32 * n), f, acc[n]);
-          acc[n] = mma(frag(dl, EP, 16 * s, 32 * n), f, acc[n]);
-        }
+        for (int n = 0; n < NE; ++n)
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            acc[n] = mma(frag(ds + i * kTile * EP * 2, EP, 16 * s, 32 * n), f, acc[n]);
       }
     }
   } else {
     const float* X = static_cast<const float*>(a.x) + min(c0 + wave * 32 + x, a.d - 1);
-    const float* D = static_cast<const float*>(a.ds) + x;
+    const float* D = a.ds + x;
     for (int64_t t = t0; t < t1; t += 16) {
       float xv[8], dv[8][NE];
 #pragma unroll
@@ -518,8 +534,8 @@ __device__ __forceinline__ void dw_chunk(const RouteGradArgs& a, int64_t chunk, 
 template <typename TI, int EP, int KM, bool STREAM>
 __global__ __launch_bounds__(256) void route_products_kernel(RouteGradArgs a, int dw_blocks) {
   // dx: 8 KB per wave; dW_g (bf16): x and ds tiles
-  __shared__ __attribute__((aligned(16))) char lds[32768];
-  static_assert(kTile * kSlab * 2 + 2 * kTile * EP * 2 <= 32768, "tiles");
+  constexpr int kTiles = sizeof(TI) == 2 ? kTile * kSlab * 2 + 3 * kTile * EP * 2 : 0;
+  __shared__ __attribute__((aligned(16))) char lds[kTiles > 32768 ? kTiles : 32768];
   __shared__ int pos[4][KM ? 32 * KM : 1];
   if ((int)blockIdx.x < dw_blocks) {
     const int slabs = (a.d + kSlab - 1) / kSlab;
@@ -571,7 +587,7 @@ void launch_products(const RouteGradArgs& a, int km, unsigned grid, int dw_block
 template <typename TI, int EP>
 hipError_t launch(RouteGradArgs a, hipStream_t s) {
   const Layout l = layout(a.T, a.d, a.E);
-  a.ds = a.ws + l.ds;
+  a.ds = reinterpret_cast<float*>(a.ws + l.ds);
   a.wt = a.ws + l.wt;
   a.partial = reinterpret_cast<float*>(a.ws + l.partial);
   const bool dw = a.dWg || a.db;

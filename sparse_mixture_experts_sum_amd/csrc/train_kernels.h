@@ -53,8 +53,8 @@ struct RouteGradArgs {
   void *dx, *dWg;
   float *db, *dlogits;
   char* ws;                 // workspace: route_grad_workspace bytes
-  void *ds, *wt;            // pieces of it (set by the launch)
-  float* partial;
+  void* wt;                 // pieces of it (set by the launch)
+  float *ds, *partial;
 };
 // Bytes of workspace.
 size_t route_grad_workspace(int64_t T, int64_t d, int E);

@@ -1,0 +1,85 @@
+"""The training operators where their sums cancel, where groups start behind row 0, and in the
+variants that only larger or other sizes reach, against their definitions in 64 bits.
+
+Tolerances as in test_gpu_training.py: half a step of the output's type plus, for fp32 sums,
+2^-24 of the terms' magnitudes for each rounding on the way.
+"""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from tests.test_gpu_training import (BF16, FP32, close, cuda, draw, gen, layer_inputs, layer_ref,  # noqa: F401
+                                     matmul_ref, moe, norm_ref, offsets_of, route_inputs, route_ref, say,
+                                     swiglu_ref)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- router gradient -------------------------------------------------------------------
+def _route_alone(moe, T, E, k, dt, d=64, seed=0, **given):
+    """dx and dW_g of given weights, probabilities and dw (no losses), and the ds they are of."""
+    r = gen(seed)
+    t = dict(x=draw(r, T, d, dtype=dt), W=draw(r, d, E, dtype=dt), probs=torch.zeros(T, E),
+             idx=torch.arange(k).repeat(T, 1).int(), w=torch.ones(T, k), dw=draw(r, T, k))
+    t.update(given)
+    out = moe.moe_route_backward(*cuda(*(t[n] for n in ("x", "W", "probs", "idx", "w", "dw"))), renormalize=False)
+    return t, out, out["dlogits"].double().cpu()
+
+
+@pytest.mark.parametrize("dt", [BF16, FP32])
+@pytest.mark.parametrize("E", [4, 64])
+def test_route_dx_where_ds_cancels(moe, dt, E):
+    # ds sums to zero over a token's experts, so that dx keeps 1e-5 of its terms here: the
+    # terms have to be ds in 32 bits. One rounding per added expert, and one of each product
+    # (ds as a sum of narrower terms: those of the smaller ones are some 2^-8 of it more).
+    say("route dx cancels", dt, E)
+    T, k = 64, 2
+    logits = draw(gen(1), T, E)
+    logits[:, -1] = -10.0
+    probs = torch.softmax(logits, 1)
+    idx = torch.topk(probs[:, :-1], k).indices
+    W = torch.ones(64, E, dtype=dt)
+    W[:, -1] = 0.0
+    t, out, ds = _route_alone(moe, T, E, k, dt, W=W, probs=probs, idx=idx.int(), w=probs.gather(1, idx))
+    ref, mag = ds @ W.double().t(), ds.abs() @ W.double().abs().t()
+    assert float((ref.abs() / mag).max()) < 1e-3
+    close(out["dx"], ref, mag, E + 2, "dx")
+
+
+@pytest.mark.parametrize("dt", [BF16, FP32])
+@pytest.mark.parametrize("E", [8, 40])
+def test_route_weight_gradient_where_tokens_cancel(moe, dt, E):
+    # two tokens x and -x whose ds differ by 2^-12 of themselves: one addition
+    say("route dW cancels", dt, E)
+    k, r = 8, gen(2)
+    x = draw(r, 1, 64, dtype=dt)
+    for e0 in range(0, E, k):
+        dw = draw(r, 1, k)
+        t, out, ds = _route_alone(moe, 2, E, k, dt, x=torch.cat([x, -x]), dw=torch.cat([dw, dw * (1 + 2.0 ** -12)]),
+                                  idx=torch.arange(e0, e0 + k).repeat(2, 1).int())
+        X = t["x"].double()
+        ref, mag = X.t() @ ds, X.abs().t() @ ds.abs()
+        close(out["dW_g"], ref, mag, 4, "dW_g")
+
+
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_route_products_of_the_largest_and_non_finite_ds(moe, dt):
+    # a ds past the largest bf16 value, one that overflowed and NaN: dx is what one product in
+    # fp32 gives, and no other token's changes
+    say("route non-finite", dt)
+    E, inf, nan = 4, float("inf"), float("nan")
+    w = torch.tensor([[0.5, 0.5], [1.0, 1.0], [0.1, 0.9], [0.1, 0.9], [0.5, 0.5], [0.5, 0.5]])
+    dw = torch.tensor([[1.0, 2.0], [0.0, -3.4e38], [3.4e38, -3.4e38], [-3.4e38, 3.4e38], [nan, 1.0], [3.0, 1.0]])
+    T, W = w.shape[0], torch.full((64, E), 0.25, dtype=dt)
+    idx = torch.tensor([[0, 1]] * T, dtype=torch.int32)
+    out = moe.moe_route_backward(*cuda(draw(gen(3), T, 64, dtype=dt), W, torch.zeros(T, E), idx, w, dw))
+    ds = out["dlogits"].double().cpu()
+    assert ds[1, 0] > 3.39e38 and ds[2, 0] == inf and ds[3, 0] == -inf
+    assert bool(torch.isnan(ds[4, :2]).all())
+    want = 0.25 * ds.sum(1, keepdim=True).expand(T, 64)
+    got = out["dx"].double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    over = torch.isinf(want)
+    assert torch.equal(got[over], want[over])
+    close(out["dx"], want, 0.25 * ds.abs().sum(1, keepdim=True).expand(T, 64), E + 2, "dx")
