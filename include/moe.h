@@ -322,18 +322,20 @@ typedef struct moe_matmul_shape {
   int32_t accumulate; /* 1: the product is added to out's values (fp32 out only); 0: stored */
 } moe_matmul_shape;
 
-/*   offsets   [E+1] int32 on the device, ascending from 0 (offsets of moe_forward's
- *             workspace, MOE_WS_OFFSETS, as they are). A bound is taken for the largest of
- *             itself, the bounds before it and 0, and at most R.
+/*   offsets   [E+1] int32 on the device, ascending (offsets of moe_forward's workspace,
+ *             MOE_WS_OFFSETS, as they are; a slice of them, with those experts' matrices, is a
+ *             table of their groups alone). A bound is taken for the largest of itself, the
+ *             bounds before it and 0, and at most R.
  *   gather_a  [R] int32 or NULL: row r of the problem is row gather_a[r] of a (the same row
  *             any number of times); values are clamped into [0, rows_a)
  *   gather_b  TN only: the same for b
  * Sums are fp32 (bf16 products are exact in it); bf16 outputs are rounded once. NN and NT
- * leave the rows of out at and past offsets[E] as they are; a TN group without rows
- * gives zeros (accumulate: leaves its matrix as it is). K and N at most 2^20 and multiples of 8
- * (bf16) or 4 (fp32): rows are read in 16-byte pieces (otherwise MOE_ERR_UNSUPPORTED). a, b
- * and out must be 16-byte aligned, the workspace too. gather_b in NN or NT, a bf16 out of fp32
- * inputs and accumulate into a bf16 out return MOE_ERR_UNSUPPORTED. */
+ * leave the rows of out in no group, before offsets[0] and at and past offsets[E], as they
+ * are; a TN group without rows gives zeros (accumulate: leaves its matrix as it is). K and N
+ * at most 2^20 and multiples of 8 (bf16) or 4 (fp32): rows are read in 16-byte pieces
+ * (otherwise MOE_ERR_UNSUPPORTED). a, b and out must be 16-byte aligned, the workspace too.
+ * gather_b in NN or NT, a bf16 out of fp32 inputs and accumulate into a bf16 out return
+ * MOE_ERR_UNSUPPORTED. */
 moe_status moe_grouped_matmul(const moe_matmul_shape* shape, const void* a, const void* b,
                               const int32_t* offsets, const int32_t* gather_a,
                               const int32_t* gather_b, void* out, void* ws, size_t ws_bytes,

@@ -748,13 +748,13 @@ __global__ __launch_bounds__(256, 1) void grouped_matmul_kernel(MatmulArgs a) {
   wait_vmcnt<0>();  // the loads that nobody reads have landed before the LDS is given back
 }
 
-// Parts' sums, in order, into out. NN, NT: up to the last group's end; TN: of the groups that
-// have parts, a group per grid row.
+// Parts' sums, in order, into out. NN, NT: from the first group's start to the last one's end (only
+// these rows have sums); TN: of the groups that have parts, a group per grid row.
 template <typename TO>
 __global__ __launch_bounds__(256) void join_parts_kernel(MatmulArgs a, const float* __restrict__ sums) {
   TO* out = static_cast<TO*>(a.out);
   int parts = a.splits, start, end;
-  int64_t n = a.split_stride;
+  int64_t from = 0, n = a.split_stride;
   const int last = group_bounds(a.offsets, a.E, (int)a.R, start, end);
   if (a.form == MOE_MATMUL_TN) {
     int all, slot;
@@ -764,9 +764,10 @@ __global__ __launch_bounds__(256) void join_parts_kernel(MatmulArgs a, const flo
     sums += (size_t)__builtin_amdgcn_readlane(slot, blockIdx.y) * a.split_stride;
     out += (size_t)blockIdx.y * a.split_stride;
   } else {
+    from = (int64_t)__builtin_amdgcn_readlane(start, 0) * a.N;
     n = (int64_t)last * a.N;
   }
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
+  for (int64_t i = from + ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
     f32x4 v = *reinterpret_cast<const f32x4*>(sums + i);
 #pragma unroll 4
     for (int p = 1; p < parts; ++p) v += *reinterpret_cast<const f32x4*>(sums + p * a.split_stride + i);

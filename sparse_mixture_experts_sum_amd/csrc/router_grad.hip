@@ -21,7 +21,8 @@
 // sums to zero over a token's experts, and a weight's gradient over tokens nearly so, so dx and
 // dW_g may be far smaller than their terms (two terms, off by 2^-17, take 167 against 174 us for
 // 16384 tokens of 4096, 8 experts, rows added, and the same time within 2% at the sizes above).
-// x and W_g are bf16 already. The ds kernel leaves ds in fp32 rows of EP = 32 or 64 experts, zeros past E.
+// x and W_g are bf16 already. The ds kernel leaves ds in fp32 rows of EP = 32 or 64 experts,
+// zeros past E.
 #include "train_common.h"
 #include "train_kernels.h"
 
@@ -49,7 +50,8 @@ __host__ __device__ inline int64_t chunk_len(int64_t T) {
 int64_t chunks_of(int64_t T) { return T > 0 ? (T + chunk_len(T) - 1) / chunk_len(T) : 0; }
 int padded_experts(int E) { return E <= 32 ? 32 : 64; }
 
-// Workspace: padded rows of ds, W_g transposed, the partial sums, [E][d] of dW_g and [E] of db per chunk. Whole 256-byte pieces.
+// Workspace: padded rows of ds, W_g transposed, the partial sums, [E][d] of dW_g and [E] of db per
+// chunk. Whole 256-byte pieces.
 struct Layout {
   size_t ds, wt, partial, total;
 };

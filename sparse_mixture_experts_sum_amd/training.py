@@ -136,8 +136,8 @@ def moe_grouped_matmul(a, b, offsets, *, form="nn", gather_a=None, gather_b=None
     "tn": out[e] = a[group].T @ b[group], b [R,N], out [E,K,N]. a is [R,K], or any rows with
     gather_a [R] int32 (row r of the problem is a[gather_a[r]]); gather_b likewise for b in
     "tn". Sums are fp32; out_dtype (a's by default) is fp32 or, for bf16 inputs, bf16.
-    accumulate adds to the given fp32 out. "nn" and "nt" leave rows at and past offsets[E] as
-    they are (in a new `out`: unset)."""
+    accumulate adds to the given fp32 out. "nn" and "nt" leave rows in no group, before offsets[0]
+    and at and past offsets[E], as they are (in a new `out`: unset)."""
     if form not in MATMUL_FORMS:
         raise ValueError(f"form must be one of {sorted(MATMUL_FORMS)}, got {form!r}")
     rows_a, K = _matrix(a, "a")

@@ -83,3 +83,39 @@ def test_route_products_of_the_largest_and_non_finite_ds(moe, dt):
     over = torch.isinf(want)
     assert torch.equal(got[over], want[over])
     close(out["dx"], want, 0.25 * ds.abs().sum(1, keepdim=True).expand(T, 64), E + 2, "dx")
+
+
+# ---- rows in front of the first group --------------------------------------------------
+@pytest.mark.parametrize("form,c,K,N", [("nn", [3], 4104, 136), ("nt", [1, 0, 2], 8200, 72), ("nn", [0, 40, 0], 4096, 64),
+                                        ("nt", [300], 2056, 136), ("nn", [70, 9], 64, 136), ("nt", [0, 130], 72, 200)])
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_matmul_leaves_rows_before_the_first_group(moe, form, c, K, N, dt):
+    # a slice of a table of bounds with its experts' weights, into the whole table's out: rows of
+    # the other groups stay, whether the sum is in parts (the long ones here) or not
+    say("before", form, c, K, N, dt)
+    first, last, E, g = 7, 7 + sum(c), len(c), gen(K)
+    R = last + 5
+    a = draw(g, R, K, dtype=dt)
+    a[:first] = a[last:] = float("nan")
+    b = draw(g, E, *((K, N) if form == "nn" else (N, K)), dtype=dt)
+    ref, mag = matmul_ref(form, a[first:last], b, c)
+    da, db, do = cuda(a, b, first + offsets_of(c))
+    ws = torch.full((1 << 23,), float("nan"), device="cuda")
+    for out in {dt, FP32}:
+        for accumulate in (False, True) if out is FP32 else (False,):
+            o = torch.full((R, N), 2.5, dtype=out, device="cuda")
+            moe.moe_grouped_matmul(da, db, do, form=form, out=o, accumulate=accumulate, workspace=ws)
+            close(o[first:last], ref + 2.5 * accumulate, mag + 2.5 * accumulate, K + 18)
+            assert bool((o[:first] == 2.5).all()) and bool((o[last:] == 2.5).all())
+
+
+def test_matmul_tn_takes_no_rows_before_the_first_group(moe):
+    say("tn before")
+    for c, K, N in (([40, 0, 30], 72, 136), ([5000], 72, 136)):
+        first, g = 9, gen(K)
+        R = first + sum(c) + 3
+        a, b = draw(g, R, K, dtype=BF16), draw(g, R, N, dtype=BF16)
+        ref, mag = matmul_ref("tn", a[first:], b[first:], c)
+        a[:first] = float("nan")
+        got = moe.moe_grouped_matmul(*cuda(a, b, first + offsets_of(c)), form="tn", out_dtype=FP32)
+        close(got, ref, mag, max(c) + 18)
