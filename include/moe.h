@@ -358,8 +358,8 @@ moe_status moe_grouped_matmul_workspace_size(const moe_matmul_shape* shape, size
  *                with pos[src[r], j] = r (MOE_WS_SRC, MOE_WS_POS), and a row that no slot of
  *                its token names has weight 0
  *   dw           [R] fp32 by row, NULL to skip
- *   offsets      NULL, or the [E+1] bounds: rows at and past offsets[E] are neither read
- *                nor written
+ *   offsets      NULL, or the [E+1] bounds, taken as in moe_grouped_matmul: rows in no group,
+ *                before offsets[0] and at and past offsets[E], are neither read nor written
  * f at most 2^20 and a multiple of 8 (bf16) or 4 (fp32), else MOE_ERR_UNSUPPORTED. Tensors
  * of R rows must be 16-byte aligned. */
 typedef struct moe_swiglu_shape {

@@ -29,14 +29,15 @@ __global__ __launch_bounds__(256) void swiglu_grad_kernel(SwigluGradArgs a) {
   typedef typename Chunk<TI>::vec vec;
   __shared__ float part[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t last = a.R;
+  int64_t first = 0, last = a.R;
   if (a.offsets) {
-    int b0, b1;
-    last = group_bounds(a.offsets, a.E, (int)a.R, b0, b1);
+    int start, end;
+    last = group_bounds(a.offsets, a.E, (int)a.R, start, end);
+    first = __builtin_amdgcn_readlane(start, 0);
   }
   const int nch = (int)(a.f / N), step = WAVE_ROW ? 64 : 256;
   const int64_t rows = WAVE_ROW ? 4 : 1;
-  for (int64_t r = blockIdx.x * rows + (WAVE_ROW ? wave : 0); r < last; r += gridDim.x * rows) {
+  for (int64_t r = first + blockIdx.x * rows + (WAVE_ROW ? wave : 0); r < last; r += gridDim.x * rows) {
     float w = 1.f;
     if (a.w) {
       if (!a.pos) {

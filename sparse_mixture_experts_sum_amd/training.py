@@ -194,8 +194,8 @@ def moe_swiglu_backward(g, u, dh, w=None, *, src=None, pos=None, offsets=None, i
     """Gradient of h = silu(g) * u, with the rows' gate weights: dg, du, h (times w) and dw
     [R] fp32 = sum over the row of dh * silu(g) * u. dh is the unweighted dy W_down^T. w is
     [R] by row, or [T,k] by slot with src [R] and pos [T,k] (the routing of the forward's
-    workspace). Rows at and past offsets[E] are left alone. inplace writes dg, du and h over
-    g, u and dh."""
+    workspace). Rows before offsets[0] and at and past offsets[E] are left alone. inplace writes
+    dg, du and h over g, u and dh."""
     R, f = rows = _matrix(g, "g")
     T = k = E = 0
     if (src is None) != (pos is None):

@@ -119,3 +119,22 @@ def test_matmul_tn_takes_no_rows_before_the_first_group(moe):
         a[:first] = float("nan")
         got = moe.moe_grouped_matmul(*cuda(a, b, first + offsets_of(c)), form="tn", out_dtype=FP32)
         close(got, ref, mag, max(c) + 18)
+
+
+@pytest.mark.parametrize("dt", [BF16, FP32])
+@pytest.mark.parametrize("f", [72, 4104])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_swiglu_leaves_rows_before_the_first_group(moe, dt, f, inplace):
+    # two slices of one table of bounds, in place: every row's gradient is taken once
+    say("swiglu before", dt, f, inplace)
+    R, r = 40, gen(f)
+    g, u, dh = (draw(r, R, f, dtype=dt) for _ in range(3))
+    w, off = torch.rand(R, generator=r), torch.tensor([0, 5, 17, 17, 33], dtype=torch.int32)
+    ref, mag = swiglu_ref(g, u, dh, w)
+    dg, du, ddh, dw, doff = cuda(g, u, dh, w, off)
+    parts = [moe.moe_swiglu_backward(dg, du, ddh, dw, offsets=doff[e:e + 3].contiguous(), inplace=inplace) for e in (2, 0)]
+    for (lo, hi), got in zip(((17, 33), (0, 17)), parts):
+        for n in ref:
+            close(got[n][lo:hi], ref[n][lo:hi], mag[n][lo:hi], 16 + (f if n == "dw" else 0), n)
+    if inplace:
+        assert torch.equal(dg[33:].cpu(), g[33:]) and torch.equal(ddh[33:].cpu(), dh[33:])
