@@ -12,15 +12,10 @@
 
 namespace {
 
-// s = 1 / (1 + e^-g). bf16: the hardware base-2 exponential and reciprocal (about 1 ulp
-// each, the results are rounded to 8 bits); fp32: expf and IEEE division.
-template <typename TI>
-__device__ __forceinline__ float sigmoid(float g) {
-  if constexpr (sizeof(TI) == 2)
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
-  else
-    return 1.0f / (1.0f + expf(-g));
-}
+// s = 1 / (1 + e^-g), for both types by expf and IEEE division: dw is fp32 for bf16 rows too, and
+// the hardware's base-2 exponential of a rounded -g log2(e) is off by |g| 2^-24 of itself (bf16,
+// 8192 x 4096: 78.1 against 78.5 us; 2048 x 4096, in the last-level cache, 16.3 against 17.5).
+__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
 
 // (no __restrict__: dg, du and hw may be g, u and dh)
 template <typename TI, bool WAVE_ROW>
@@ -60,7 +55,7 @@ __global__ __launch_bounds__(256) void swiglu_grad_kernel(SwigluGradArgs a) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float gf = (float)g[i], uf = (float)u[i], df = (float)dh[i];
-        const float s = sigmoid<TI>(gf), act = gf * s, wd = w * df;
+        const float s = sigmoid(gf), act = gf * s, wd = w * df;
         sum += df * act * uf;
         og[i] = (TI)(wd * uf * s * (1.0f + gf * (1.0f - s)));
         ou[i] = (TI)(wd * act);

@@ -138,3 +138,19 @@ def test_swiglu_leaves_rows_before_the_first_group(moe, dt, f, inplace):
             close(got[n][lo:hi], ref[n][lo:hi], mag[n][lo:hi], 16 + (f if n == "dw" else 0), n)
     if inplace:
         assert torch.equal(dg[33:].cpu(), g[33:]) and torch.equal(ddh[33:].cpu(), dh[33:])
+
+
+# ---- SwiGLU gradient -------------------------------------------------------------------
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_swiglu_gate_weight_gradient_of_far_gates(moe, dt):
+    # dw is fp32 for bf16 rows too. Far below 0, s is e^g: an exponent of |g| rounded in 32 bits
+    # would move it by |g| 2^-24. Of each term: exp (one step: 2), the sum and the division
+    # (1 each), three products, and seven additions to the row's sum
+    say("swiglu far gates", dt)
+    R, f, r = 512, 8, gen(1)
+    g = (-20 - 64 * torch.rand(R, 1, generator=r)).expand(R, f).to(dt)
+    u, dh = draw(r, R, f, dtype=dt), draw(r, R, f, dtype=dt)
+    s = 1 / (1 + torch.exp(-g.double()))
+    v = dh.double() * g.double() * s * u.double()
+    got = moe.moe_swiglu_backward(*cuda(g.contiguous(), u, dh))
+    close(got["dw"], v.sum(1), v.abs().sum(1), 2 + 1 + 1 + 3 + 7, "dw")
