@@ -33,8 +33,6 @@ _ROUTE_UPSTREAM = struct.Struct("@PiffPPPq0q").pack
 _NORM_SHAPE = struct.Struct("@qqiiff0q").pack
 _LAYER_SHAPE = struct.Struct("@qqqiiiii0dd").pack
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # (torch.cuda.current_stream builds an object)
-
 
 def declare(lib, shape_p):
     """Argument types of the training entry points (called once by load_library). The shape
@@ -102,11 +100,12 @@ def _call(fn: str, dev: torch.device, *args):
     """One library call on dev's current stream, with dev the current device."""
     f = getattr(load_library(), fn)
     index = dev.index
+    stream = torch._C._cuda_getCurrentRawStream  # (torch.cuda.current_stream builds an object)
     if torch.cuda.current_device() == index:
-        st = f(*args, _raw_stream(index))
+        st = f(*args, stream(index))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, _raw_stream(index))
+            st = f(*args, stream(index))
     if st:
         _check(fn, st)
 
