@@ -117,7 +117,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "moe_forward", "moe_forward_noalloc", "moe_aux_loss", "moe_profile_enable",
                  "moe_profile_read"):
         getattr(lib, name).restype = I32
-    training.declare(lib, S)
+    training.declare(lib)
     _lib = lib
     return lib
 

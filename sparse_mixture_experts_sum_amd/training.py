@@ -34,7 +34,7 @@ _NORM_SHAPE = struct.Struct("@qqiiff0q").pack
 _LAYER_SHAPE = struct.Struct("@qqqiiiii0dd").pack
 
 
-def declare(lib, shape_p):
+def declare(lib):
     """Argument types of the training entry points (called once by load_library). The shape
     structs are passed as bytes."""
     P, SZ = ctypes.c_void_p, ctypes.c_size_t
