@@ -9,9 +9,10 @@ from __future__ import annotations
 import pytest
 import torch
 
-from tests.test_gpu_training import (BF16, FP32, close, cuda, draw, gen, layer_inputs, layer_ref,  # noqa: F401
-                                     matmul_ref, moe, norm_ref, offsets_of, route_inputs, route_ref, say,
-                                     swiglu_ref)
+import sparse_mixture_experts_sum_amd as M
+from sparse_mixture_experts_sum_amd import training as TR
+from tests.test_gpu_training import (BF16, FP32, close, cuda, draw, gen, layer_inputs, matmul_ref,  # noqa: F401
+                                     moe, offsets_of, route_inputs, route_ref, say, swiglu_ref)
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +155,82 @@ def test_swiglu_gate_weight_gradient_of_far_gates(moe, dt):
     v = dh.double() * g.double() * s * u.double()
     got = moe.moe_swiglu_backward(*cuda(g.contiguous(), u, dh))
     close(got["dw"], v.sum(1), v.abs().sum(1), 2 + 1 + 1 + 3 + 7, "dw")
+
+
+# ---- grouped products: tiles and addresses that larger sizes take --------------------------
+@pytest.mark.parametrize("form,K,N", [("nn", 1024, 1032), ("nt", 1032, 1024)])
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_matmul_128_row_tiles(moe, form, K, N, dt):
+    # groups of many rows with too few tiles for the 256-row ones, stored and accumulated
+    say("128-row tiles", form, K, N, dt)
+    c, g = [1399, 1, 700], gen(K)
+    a = draw(g, sum(c), K, dtype=dt)
+    b = draw(g, 3, *((K, N) if form == "nn" else (N, K)), dtype=dt)
+    ref, mag = matmul_ref(form, a, b, c)
+    da, db, do = cuda(a, b, offsets_of(c))
+    out = moe.moe_grouped_matmul(da, db, do, form=form, out_dtype=FP32)
+    close(out, ref, mag, K + 2)
+    moe.moe_grouped_matmul(da, db, do, form=form, out=out, accumulate=True)
+    close(out, 2 * ref, 2 * mag, K + 4)
+
+
+@pytest.mark.parametrize("form", ["nn", "nt"])
+def test_matmul_fp32_weights_past_the_last_level_cache(moe, form):
+    say("far weights fp32", form)
+    c, K, N = [(7 * i * i + i) % 9 for i in range(40)], 520, 3400
+    c[39] = 0
+    R, E, g = sum(c), len(c), gen(6)
+    a = draw(g, R + 3, K)
+    b = draw(g, E, *((K, N) if form == "nn" else (N, K)))
+    ref, mag = matmul_ref(form, a[:R], b, c)
+    da, db, do = cuda(a, b, offsets_of(c))
+    o = torch.full((R + 3, N), 2.5, device="cuda")
+    moe.moe_grouped_matmul(da, db, do, form=form, out=o)
+    close(o[:R], ref, mag, K + 2)
+    assert bool((o[R:] == 2.5).all())
+    moe.moe_grouped_matmul(da, db, do, form=form, out=o, accumulate=True)
+    close(o[:R], 2 * ref, 2 * mag, K + 4)
+
+
+def test_matmul_inputs_past_2_31_elements(moe):
+    # a of more than 2^31 elements without a gather, and gathered rows that lie there (TN)
+    say("far a")
+    K, N, few = 4096, 72, 512
+    R = 2 ** 31 // K + 1000
+    g = gen(14)
+    rows = draw(g, few, K, dtype=BF16)
+    a = torch.zeros(R, K, dtype=BF16, device="cuda")
+    a[R - few:] = rows.cuda()
+    b = draw(g, 2, K, N, dtype=BF16)
+    ref, mag = matmul_ref("nn", rows, b[1:], [few])
+    out = moe.moe_grouped_matmul(a, b.cuda(), torch.tensor([0, R - few, R], dtype=torch.int32, device="cuda"))
+    close(out[R - few:], ref, mag, K + 2)
+    assert not bool(out[:R - few].any())
+    src = torch.arange(R - few, R).int()
+    cols = draw(g, few, N, dtype=BF16)
+    ref, mag = matmul_ref("tn", rows, cols, [200, few - 200])
+    got = moe.moe_grouped_matmul(a, cols.cuda(), offsets_of([200, few - 200]).cuda(), form="tn", gather_a=src.cuda())
+    close(got, ref, mag, few + 2)
+
+
+@pytest.mark.parametrize("form", ["nn", "nt", "tn"])
+def test_matmul_weights_past_2_31_elements(moe, form):
+    # b (TN: out) of more than 2^31 elements: the last experts' matrices
+    say("far b", form)
+    E, K, N, g = 33, 8192, 8200, gen(15)
+    c = [0] * 30 + [3, 0, 40]
+    R = sum(c)
+    a = draw(g, R, K, dtype=BF16)
+    if form == "tn":
+        b = draw(g, R, N, dtype=BF16)
+        out = moe.moe_grouped_matmul(*cuda(a, b, offsets_of(c)), form=form)
+        ref, mag = matmul_ref(form, a[:, -256:], b, c[30:])
+        close(out[30:, -256:], ref, mag, R + 2)
+        assert not bool(out[:30].any())
+        return
+    b = torch.zeros(E, *((K, N) if form == "nn" else (N, K)), dtype=BF16, device="cuda")
+    last = draw(g, *b.shape[1:], std=0.1, dtype=BF16)
+    b[30], b[32] = last.cuda(), last.cuda()
+    out = moe.moe_grouped_matmul(a.cuda(), b, offsets_of(c).cuda(), form=form)
+    ref, mag = matmul_ref(form, a, last[None], [R])
+    close(out, ref, mag, K + 18)
