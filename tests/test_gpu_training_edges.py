@@ -234,3 +234,66 @@ def test_matmul_weights_past_2_31_elements(moe, form):
     out = moe.moe_grouped_matmul(a.cuda(), b, offsets_of(c).cuda(), form=form)
     ref, mag = matmul_ref(form, a, last[None], [R])
     close(out, ref, mag, K + 18)
+
+
+# ---- router gradient: several tiles a chunk, W_g in memory, more slots ------------------
+@pytest.mark.parametrize("T,d,E,k,dt", [(2100, 128, 8, 2, BF16), (2100, 192, 40, 5, BF16), (2100, 128, 33, 3, FP32),
+                                        (8300, 64, 8, 2, BF16), (8300, 64, 5, 1, FP32), (4200, 64, 64, 8, BF16),
+                                        (300, 1024, 64, 4, BF16), (300, 512, 64, 8, FP32), (9, 2048, 17, 2, FP32)])
+def test_route_of_many_tokens_and_wide_rows(moe, T, d, E, k, dt):
+    # tokens past 2048: chunks of several tiles; past 8192: groups that come back for more;
+    # W_g past 64 KB: transposed in memory for the z-loss
+    say("route sizes", T, d, E, k, dt)
+    for renorm, drop in ((True, 0.3), (False, 0.0)):
+        lg, zg = 0.1 * T, 0.05 * T
+        s = route_inputs(T, d, E, k, dt, renorm, T + E, drop)
+        ref, mag = route_ref(s, k, renorm, lg, zg)
+        x, W, p, idx, w, dw, b, f = cuda(*(s[n] for n in ("x", "W", "probs", "idx", "w", "dw", "b", "f")))
+        out = moe.moe_route_backward(x, W, p, idx, w, dw, b_g=b, f=f, loss_grad=lg, z_loss_grad=zg,
+                                     renormalize=renorm)
+        for n in ref:
+            close(out[n], ref[n], mag[n], {"dx": E, "dW_g": T, "db_g": T, "dlogits": 0}[n] + 16, (n, drop))
+        for want in (dict(want_dx=False), dict(want_dW=False), dict(want_dx=False, want_dW=False)):
+            some = moe.moe_route_backward(x, W, p, idx, w, dw, b_g=b, f=f, loss_grad=lg, z_loss_grad=zg,
+                                          renormalize=renorm, **want)
+            for n in ref:
+                skipped = (n == "dx" and "want_dx" in want) or (n in ("dW_g", "db_g") and "want_dW" in want)
+                assert some[n] is None if skipped else torch.equal(some[n], out[n]), (n, want)
+
+
+@pytest.mark.parametrize("T,d,E,k", [(300, 192, 8, 3), (100, 320, 64, 4), (70, 64, 33, 5), (257, 128, 64, 8), (33, 64, 1, 1)])
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_route_adds_rows_of_any_number_of_slots(moe, T, d, E, k, dt):
+    say("route slots", T, d, E, k, dt)
+    s = route_inputs(T, d, E, k, dt, True, 5, drop=0.2)
+    r = gen(6)
+    order = torch.randperm(T * k, generator=r).int().view(T, k)
+    pos = torch.where(s["kept"], order, torch.full_like(order, -1))
+    rows = draw(r, T * k, d, dtype=dt)
+    ref, mag = route_ref(s, k, True, 0.0, 0.0, rows, pos)
+    s["dw"][~s["kept"]] = float("nan")
+    x, W, p, idx, w, dw, dpos, drows = cuda(*(s[n] for n in ("x", "W", "probs", "idx", "w", "dw")), pos, rows)
+    out = moe.moe_route_backward(x, W, p, idx, w, dw, rows=drows, pos=dpos)
+    for n in ref:
+        close(out[n], ref[n], mag[n], {"dx": E + k, "dW_g": T, "db_g": T, "dlogits": 0}[n] + 16, n)
+
+
+@pytest.mark.parametrize("k,T", [(2, 17001), (8, 4601)])
+@pytest.mark.parametrize("E", [8, 40])
+def test_route_adds_rows_past_half_the_last_level_cache_of_any_number_of_slots(moe, k, T, E):
+    # (dw is None: dx is the rows' sums)
+    say("route many rows", k, T, E)
+    d, g = 2048, torch.Generator(device="cuda").manual_seed(2)
+    rows = torch.randn(T * k, d, device="cuda", generator=g).to(BF16)
+    pos = torch.randperm(T * k, device="cuda", generator=g).int().view(T, k)
+    pos[5] = -1
+    pos[6, 1] = T * k
+    x, W = torch.zeros(T, d, dtype=BF16, device="cuda"), torch.zeros(d, E, dtype=BF16, device="cuda")
+    idx = torch.arange(k, dtype=torch.int32, device="cuda").repeat(T, 1)
+    out = moe.moe_route_backward(x, W, torch.full((T, E), 1 / E, device="cuda"), idx,
+                                 torch.full((T, k), 1 / k, device="cuda"), None, rows=rows, pos=pos)
+    some = torch.cat([torch.arange(0, 200), torch.arange(T - 300, T)])
+    at = pos.cpu()[some].long()
+    ok = ((at >= 0) & (at < T * k))[..., None]
+    v = torch.where(ok, rows.cpu().double()[at.clamp(0, T * k - 1)], 0.0)
+    close(out["dx"][some.cuda()], v.sum(1), v.abs().sum(1), k)
