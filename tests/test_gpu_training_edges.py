@@ -297,3 +297,38 @@ def test_route_adds_rows_past_half_the_last_level_cache_of_any_number_of_slots(m
     ok = ((at >= 0) & (at < T * k))[..., None]
     v = torch.where(ok, rows.cpu().double()[at.clamp(0, T * k - 1)], 0.0)
     close(out["dx"][some.cuda()], v.sum(1), v.abs().sum(1), k)
+
+
+# ---- norms: several rows per workgroup at every width --------------------------------------
+@pytest.mark.parametrize("d,T", [(256, 8209), (1024, 4099), (1032, 2051), (2048, 2051), (4096, 1027), (8192, 515), (16384, 515)])
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_norm_gradient_of_many_rows(moe, d, T, gate, dt):
+    # more rows than workgroups, an uneven last round: column sums carried over rows
+    say("norm rows", d, T, gate, dt)
+    r, eps, scale = torch.Generator(device="cuda").manual_seed(d), 1e-5, 0.7
+    rn = lambda *s, std=1.0, t=FP32: (torch.randn(*s, device="cuda", generator=r) * std).to(t)  # noqa: E731
+    x, y, d_out, d_u = rn(T, d, t=dt), rn(T, d, std=2.0), rn(T, d, t=dt), rn(T, d, t=dt)
+    gp, gm = 1 + rn(d, std=0.2), 1 + rn(d, std=0.2)
+    gt = {"none": None, "channel": rn(d), "token": rn(T, 1)}[gate]
+    f = moe.moe_block_norm(x, gamma=gm, y=y, gamma_post=gp, gate=gt, residual_scale=scale, eps=eps)
+    res = moe.moe_block_norm_backward(f["out"], d_out=d_out, d_u=d_u, rstd=f["rstd"], gamma=gm, y=y,
+                                      rstd_post=f["rstd_post"], gamma_post=gp, gate=gt, residual_scale=scale)
+    q, rstd = f["rstd_post"].double()[:, None], f["rstd"].double()[:, None]
+    z, dz = f["out"].double() * rstd, d_u.double() * gm.double()
+    D = d_out.double() + rstd * (dz - z * (dz * z).mean(1, keepdim=True))
+    Dm = d_out.double().abs() + rstd * (dz.abs() + z.abs() * (dz * z).abs().mean(1, keepdim=True))
+    n = y.double() * q
+    g = torch.ones(1, dtype=torch.float64, device="cuda") if gt is None else gt.double()
+    dn, dnm = g * D * gp.double(), (g * gp.double()).abs() * Dm
+    v, vm = D * n * gp.double(), Dm * (n * gp.double()).abs()
+    want = {"dx": (scale * D, Dm, d + 12),
+            "dy": (q * (dn - n * (dn * n).mean(1, keepdim=True)),
+                   q * (dnm + n.abs() * (dnm * n.abs()).mean(1, keepdim=True)), 2 * d + 24),
+            "dgamma": ((d_u.double() * z).sum(0), (d_u.double() * z).abs().sum(0), T + 8),
+            "dgamma_post": ((g * D * n).sum(0), (g.abs() * Dm * n.abs()).sum(0), T + d + 24)}
+    if gt is not None:
+        dim = 0 if gate == "channel" else 1
+        want["dgate"] = v.sum(dim).view(gt.shape), vm.sum(dim).view(gt.shape), T + 2 * d + 24
+    for name, (ref, mag, terms) in want.items():
+        close(res[name], ref.cpu(), mag.cpu(), terms, name)
