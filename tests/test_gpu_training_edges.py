@@ -332,3 +332,93 @@ def test_norm_gradient_of_many_rows(moe, d, T, gate, dt):
         want["dgate"] = v.sum(dim).view(gt.shape), vm.sum(dim).view(gt.shape), T + 2 * d + 24
     for name, (ref, mag, terms) in want.items():
         close(res[name], ref.cpu(), mag.cpu(), terms, name)
+
+
+# ---- outputs that the C entry points skip ----------------------------------------------
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _each_output_alone(call, shapes):
+    """call(outputs) with all outputs, then with each one alone and with each one left out: the
+    same bits. shapes: name -> (shape, type)."""
+    def fresh(names):
+        return {n: torch.full(shapes[n][0], 7.0, dtype=shapes[n][1], device="cuda") if n in names else None for n in shapes}
+    full = fresh(shapes)
+    call(full)
+    for n in shapes:
+        for names in ({n}, set(shapes) - {n}):
+            got = fresh(names)
+            call(got)
+            for m in names:
+                assert torch.equal(got[m], full[m]), (m, sorted(names))
+
+
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_swiglu_skips_outputs(moe, dt):
+    say("swiglu skips", dt)
+    R, f, r = 37, 264, gen(1)
+    g, u, dh, w = cuda(draw(r, R, f, dtype=dt), draw(r, R, f, dtype=dt), draw(r, R, f, dtype=dt), torch.rand(R, generator=r))
+    shape = TR._SWIGLU_SHAPE(R, f, 0, 0, 0, TR._TYPES[dt])
+
+    def call(o):
+        TR._call("moe_swiglu_backward", g.device, shape, _p(g), _p(u), _p(dh), _p(w), None, None, None, _p(o["dg"]),
+                 _p(o["du"]), _p(o["hw"]), _p(o["dw"]))
+    _each_output_alone(call, dict(dg=((R, f), dt), du=((R, f), dt), hw=((R, f), dt), dw=((R,), FP32)))
+
+
+@pytest.mark.parametrize("T,d", [(70, 512), (70, 2048), (5, 4096), (9, 8200)])
+@pytest.mark.parametrize("kind", [TR.GATE_NONE, TR.GATE_CHANNEL, TR.GATE_TOKEN])
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_norms_skip_outputs(moe, T, d, kind, dt):
+    say("norm skips", T, d, kind, dt)
+    r = gen(d)
+    x, d_out, d_u, y = cuda(*(draw(r, T, d, dtype=t) for t in (dt, dt, dt, FP32)))
+    gp, gm = cuda(draw(r, d), draw(r, d))
+    gate = {TR.GATE_NONE: None, TR.GATE_CHANNEL: draw(r, d).cuda(), TR.GATE_TOKEN: draw(r, T).cuda()}[kind]
+    shape = TR._NORM_SHAPE(T, d, TR._TYPES[dt], kind, 1e-5, 0.7)
+    rows, cols, tok = ((T, d), dt), ((d,), FP32), ((T,), FP32)
+    keep = {}
+
+    def forward(o):
+        out, u = torch.empty_like(x), torch.empty_like(x)
+        TR._call("moe_block_norm", x.device, shape, _p(x), _p(y), _p(gp), _p(gate), _p(gm), _p(out), _p(u),
+                 _p(o["rstd_post"]), _p(o["rstd"]))
+        for n, v in (("out", out), ("u", u)):
+            assert torch.equal(keep.setdefault(n, v), v), n
+    _each_output_alone(forward, dict(rstd_post=tok, rstd=tok))
+    rstd, rstd_post = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    forward(dict(rstd=rstd, rstd_post=rstd_post))
+    n = TR._workspace_bytes("moe_block_norm_backward_workspace_size", shape)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+
+    def backward(o):
+        ws.fill_(255)
+        TR._call("moe_block_norm_backward", x.device, shape, _p(d_out), _p(d_u), _p(keep["out"]), _p(rstd), _p(gm), _p(y),
+                 _p(rstd_post), _p(gp), _p(gate), _p(o["dx"]), _p(o["dy"]), _p(o["dgamma"]), _p(o["dgamma_post"]),
+                 _p(o.get("dgate")), _p(ws), n)
+    shapes = dict(dx=rows, dy=rows, dgamma=cols, dgamma_post=cols)
+    if gate is not None:
+        shapes["dgate"] = cols if kind == TR.GATE_CHANNEL else tok
+    _each_output_alone(backward, shapes)
+
+
+@pytest.mark.parametrize("E,d", [(8, 128), (64, 1024)])
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_route_skips_outputs(moe, E, d, dt):
+    say("route skips", E, d, dt)
+    T, k = 2100, 2
+    s = route_inputs(T, d, E, k, dt, True, 3)
+    x, W, b, p, idx, w, dw, f = cuda(*(s[n] for n in ("x", "W", "b", "probs", "idx", "w", "dw", "f")))
+    shape = TR._LAYER_SHAPE(T, d, 64, E, k, M.MOE_TOKEN_CHOICE, TR._TYPES[dt], 1, 1.0)
+    up = TR._ROUTE_UPSTREAM(_p(dw), 0, 2.0, 3.0, _p(f), 0, 0, 0)
+    n = TR._workspace_bytes("moe_route_backward_workspace_size", shape)
+    ws, keep = torch.full((n,), 255, dtype=torch.uint8, device="cuda"), {}
+
+    def call(o):
+        ws.fill_(255)
+        ds = torch.empty(T, E, device="cuda")
+        TR._call("moe_route_backward", x.device, shape, _p(x), _p(W), _p(b), _p(p), _p(idx), _p(w), up, _p(o["dx"]),
+                 _p(o["dW_g"]), _p(o["db_g"]), _p(ds), _p(ws), n)
+        assert torch.equal(keep.setdefault("ds", ds), ds)
+    _each_output_alone(call, dict(dx=((T, d), dt), dW_g=((d, E), dt), db_g=((E,), FP32)))
