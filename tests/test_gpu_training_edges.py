@@ -422,3 +422,60 @@ def test_route_skips_outputs(moe, E, d, dt):
                  _p(o["dW_g"]), _p(o["db_g"]), _p(ds), _p(ws), n)
         assert torch.equal(keep.setdefault("ds", ds), ds)
     _each_output_alone(call, dict(dx=((T, d), dt), dW_g=((d, E), dt), db_g=((E,), FP32)))
+
+
+# ---- together: a layer's training step with either norm, and of the largest tiles --------
+def _layer_ref(t, idx, kept, pre, post, gate, scale, lg, zg, eps):
+    """As layer_ref, with each norm and the gate on its own; renormalised weights."""
+    p = {n: v.double().requires_grad_() for n, v in t.items() if n != "d_out"}
+    x, E = p["x"], p["W_g"].shape[1]
+    T, k = idx.shape
+    rms = lambda v: (v.square().mean(1, keepdim=True) + eps).sqrt()  # noqa: E731
+    u = x / rms(x) * p["pre_gamma"] if pre else x
+    logits = u @ p["W_g"] + p["b_g"]
+    prob = torch.softmax(logits, 1)
+    sel = prob.gather(1, idx) * kept
+    w = sel / sel.sum(1, keepdim=True).clamp_min(1e-300)
+    y = torch.zeros_like(x)
+    for e in range(E):
+        tok, slot = torch.nonzero((idx == e) & kept, as_tuple=True)
+        g = u[tok] @ p["W_gate"][e]
+        h = g / (1 + torch.exp(-g)) * (u[tok] @ p["W_up"][e])
+        y = y.index_add(0, tok, (h @ p["W_down"][e]) * w[tok, slot][:, None])
+    out = y
+    if post:
+        out = scale * x + y / rms(y) * p["post_gamma"] * (p["gate"] if gate else 1.0)
+    f = torch.bincount(idx.reshape(-1), minlength=E).double() / T
+    total = (out * t["d_out"].double()).sum() + lg * E * (f / k * prob.mean(0)).sum() \
+        + zg * torch.logsumexp(logits, 1).square().mean()
+    total.backward()
+    names = {"pre_gamma": "d_pre_gamma", "post_gamma": "d_post_gamma", "gate": "d_gate"}
+    return {names.get(n, "d" + n): v.grad for n, v in p.items() if v.grad is not None}
+
+
+@pytest.mark.parametrize("pre,post,gate", [(True, False, False), (False, True, True), (False, True, False),
+                                           (True, True, False)])
+@pytest.mark.parametrize("T,d,f,E,dt", [(173, 128, 192, 8, BF16), (173, 128, 192, 8, FP32), (4200, 1088, 1152, 4, BF16),
+                                        (8209, 128, 192, 8, BF16)])
+def test_layer_backward_with_either_norm(moe, pre, post, gate, T, d, f, E, dt):
+    say("layer norms", pre, post, gate, T, d, f, E, dt)
+    k, eps, scale = 2, 1e-5, 0.7
+    t = {n: v.cuda() for n, v in layer_inputs(T, d, f, E, dt, 22).items()}
+    layer = moe.SparseMoE(t["W_g"], t["W_gate"], t["W_up"], t["W_down"], t["b_g"], k=k, mode="tc_capacity",
+                          capacity_factor=0.9, pre_gamma=t["pre_gamma"] if pre else None,
+                          post_gamma=t["post_gamma"] if post else None, gate=t["gate"] if gate else None,
+                          residual_scale=scale, norm_eps=eps)
+    lg, zg = 0.02 * T, 0.01 * T
+    layer(t["x"])
+    got = layer.backward(t["d_out"], loss_grad=lg, z_loss_grad=zg)
+    last = layer.last
+    ref = _layer_ref(t, last["idx"].long(), last["w"] != 0, pre, post, gate, scale, lg, zg, eps)
+    assert set(got) == set(ref), (sorted(got), sorted(ref))
+    # Of each gradient's size, in the 2-norm. bf16: at most nine values on the way are rounded (u,
+    # the two products, dy, dh, the hidden gradient, the rows, the residual's gradient or u's, the
+    # result), half a step of 2^-8 each. fp32: the longest chain of sums has d + f + d terms and T more.
+    tol = 9 * 2.0 ** -8 if dt == BF16 else (2 * d + f + T) * 2.0 ** -24 * 8
+    for n in ref:
+        assert got[n].shape == ref[n].shape, n
+        err = float((got[n].double() - ref[n]).norm() / ref[n].norm())
+        assert err <= tol, (n, err)
