@@ -624,9 +624,12 @@ hipError_t launch(RouteGradArgs a, hipStream_t s) {
     if (dw_blocks || dx_blocks) {
       const unsigned grid = dw_blocks + (dx_blocks ? capped_grid(dx_blocks) : 0);
       const int km = a.rows && a.R > 0 ? a.k : 0;
-      // Rows that fill half of the last-level cache or more push out what is read again (8191
-      // tokens of 2048, top-4, 134 MB: the whole gradient 80.2 -> 76.5 us); fewer stay there
-      // from the kernel that wrote them.
+      // Rows that fill half of the last-level cache or more push out what is read again; fewer
+      // stay there from the kernel that wrote them. us of the gradient without the hint -> with,
+      // rows long written / with the cast that writes them right before: 8192 rows of 2048, 33 MB,
+      // 42.1 -> 44.0 / 61.3 -> 60.9; 24576, 100 MB, 71.3 -> 67.7 / 117.4 -> 119.2; 32764, 134 MB,
+      // 81.4 -> 77.9 / 146.2 -> 144.4; 49152, 201 MB, 116 -> 110 / 217 -> 208; 16384 of 4096, 134
+      // MB, 100.8 -> 98.2 / 170.1 -> 166.1; 65536 of 1024, 134 MB, 55.9 -> 53.8 / 114.0 -> 114.9.
       const bool stream = (double)a.R * a.d * sizeof(TI) > 128e6;
       if (km == 0) route_products_kernel<TI, EP, 0, false><<<grid, 256, 0, s>>>(a, dw_blocks);
       else if (stream) launch_products<TI, EP, true>(a, km, grid, dw_blocks, s);
