@@ -472,9 +472,12 @@ class SparseMoE:
         dW_down (their tensors' types) and, where present, db_g, d_pre_gamma, d_post_gamma,
         d_gate (fp32).
 
-        The gate and up products are formed again from the call's routing. bf16: those
-        products, dy, the hidden gradients and the routed rows' gradients are rounded to bf16
-        between the kernels; every sum is fp32."""
+        The gate and up products are formed again from the call's routing. Sums within a kernel
+        are fp32. What passes from one kernel to the next is of the layer's type; bf16 rounds
+        there d_out (where it is fp32), dy, the two products, the hidden gradient and what is
+        formed of them (dg, du, the weighted h), each routed row's gradient before a token's rows
+        are added, u's gradient, and with post_gamma the residual's: dx without pre_gamma is
+        the sum of these last two, rounded again."""
         last = self.last
         if last is None:
             raise ValueError("backward needs a call of the layer")
