@@ -12,9 +12,10 @@
 // a dot product first): bound by HBM, and by the launches at small sizes. Four kernels: W_g
 // transposed (z-loss only), ds, then dx and partial sums of dW_g and db side by side in one
 // launch, and the partial sums' sum in chunk order: no atomics, one fixed order. bf16, both
-// losses: 4096 tokens of 1024, 8 experts, 21 us (ds 8.8, products 7.6, sum 3.6: latencies, a
+// losses: 4096 tokens of 1024, 8 experts, 21 us (ds 8.0, products 9.1, sum 3.5: latencies, a
 // copy of those bytes takes 3.4); 8191 tokens of 2048, 64 experts, top-4 with the rows'
-// gradients added, 76 us (transpose 4.5, ds 14, products 46 at 5 TB/s, sum 5; a copy 40).
+// gradients added, 77 us (traced: transpose 4.8, ds 11, products 60 at 4.2 TB/s, sum 5; a copy
+// 40). fp32: 32 and 168 us.
 //
 // Both products run on the matrix cores. fp32: v_mfma_f32_32x32x2_f32 on the values. bf16:
 // v_mfma_f32_32x32x16_bf16 with ds as a sum of three bf16 terms, which is ds to its last bit: ds

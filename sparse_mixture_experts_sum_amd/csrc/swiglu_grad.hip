@@ -3,7 +3,7 @@
 // With s = 1 / (1 + e^-g) the row's four results are
 //   dg = w dh u s (1 + g (1 - s)),  du = w dh g s,  hw = w g s u,  dw = sum_f dh g s u,
 // one pass over three inputs and three outputs: bound by HBM (6 f elements per row). bf16,
-// 8192 x 4096: 76 us, 5.3 TB/s (a copy reaches 5.1); 37 x 1408 fp32: 4.5 us, one row's latency.
+// 8192 x 4096: 78 us, 5.1 TB/s (a copy's rate); fp32 155 us, 5.2; 37 x 1408 fp32: 4.3 us, one row's latency.
 // A row is read in 16-byte chunks, by one wave where it has at most 256 chunks (the row sum
 // is then a shuffle tree, and the workgroup's four rows need no barrier) and by the whole
 // workgroup beyond, so that a long row's loads are spread over four waves.
