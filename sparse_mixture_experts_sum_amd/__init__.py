@@ -519,6 +519,8 @@ class SparseMoE:
             "dW_up": moe_grouped_matmul(u, du, offsets, form="tn", gather_a=src),
             "dW_down": moe_grouped_matmul(h, dy, offsets, form="tn", gather_b=src),
         }
+        # the two products' sum is fp32, and rounded once to rows that the router's gradient reads
+        # in half the bytes: each is off by as much as the dx that they add up to is rounded by
         rows = moe_grouped_matmul(dg, self.W_gate, offsets, form="nt", out_dtype=torch.float32)
         moe_grouped_matmul(du, self.W_up, offsets, form="nt", out=rows, accumulate=True)
         r = moe_route_backward(u, self.W_g, last["probs"], last["idx"], last["w"], act["dw"], b_g=self.b_g,

@@ -221,7 +221,7 @@ __device__ __forceinline__ f32x16 mma(float a, float b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
 }
 // Eight values as bf16 terms hi + mid + lo, each cut off instead of rounded: eight of the 24 bits
-// a term, so that the sum is the value (to 2^-133, the smallest bf16) and hi is finite where it
+// a term, so that the sum is the value (to 2^-126, the smallest normal) and hi is finite where it
 // is. A non-finite value is hi alone.
 struct Terms {
   s16x8 t[3];
