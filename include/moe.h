@@ -460,6 +460,98 @@ moe_status moe_block_norm_backward(const moe_norm_shape* shape, const void* d_ou
                                    float* dgamma, float* dgamma_post, float* dgate, void* ws,
                                    size_t ws_bytes, hipStream_t stream);
 
+/* ---- A training step's other ends: layer norms, the experts' update -------------------
+ * Conventions of the training section: device memory, the caller's buffers and stream, host
+ * checks before any HIP call, deterministic results, no allocation, no synchronisation. */
+
+/* Layer norm of the residual sum, in one pass, row by row:
+ *   out = residual_scale * x + y          (y given; out = x without y)
+ *   u   = (out - mean) * rstd * gamma + beta,
+ *   mean = mean(out), rstd = 1 / sqrt(mean((out - mean)^2) + eps)
+ * `out` is rounded to dtype and u, mean and rstd are computed from the rounded values, so that
+ * a call with y and one without it on `out` give the same bits. The variance is the mean square
+ * of the differences from the mean, not a difference of squares. */
+typedef struct moe_layer_norm_shape {
+  int64_t T;             /* rows */
+  int64_t d;             /* width: at most 16384 (a row is held in registers) and a multiple of 8 */
+  int32_t dtype;         /* moe_dtype of x, out, u and their gradients */
+  float eps;             /* > 0, finite */
+  float residual_scale;  /* finite; only with y */
+} moe_layer_norm_shape;
+
+/*   x [T, d] dtype, y [T, d] fp32 (moe_forward's output) or NULL, gamma [d] fp32, beta [d] fp32
+ *   or NULL for none
+ *   out [T, d] dtype (with y, else NULL; may be x), u [T, d] dtype
+ *   mean, rstd [T] fp32: for the gradient, NULL to skip
+ * All tensors but the [T] ones 16-byte aligned. */
+moe_status moe_layer_norm(const moe_layer_norm_shape* shape, const void* x, const float* y,
+                          const float* gamma, const float* beta, void* out, void* u, float* mean,
+                          float* rstd, hipStream_t stream);
+
+/* Bytes of workspace moe_layer_norm_backward needs. Host only. */
+moe_status moe_layer_norm_backward_workspace_size(const moe_layer_norm_shape* shape, size_t* bytes);
+
+/* Its gradient, with z = (out - mean) rstd and dz = d_u gamma:
+ *   D  = d_out + rstd (dz - mean(dz) - z mean(dz z))      (d_out NULL: without it)
+ *   dx = residual_scale D,  dy = D,  dgamma = sum_t d_u z,  dbeta = sum_t d_u
+ *   out [T, d] dtype (the forward's rounded sum; x where it had no y, with residual_scale 1),
+ *   d_u, d_out [T, d] dtype, mean, rstd [T], gamma [d] fp32
+ *   dx, dy [T, d] dtype, dgamma, dbeta [d] fp32: NULL to skip. dx may be d_out or d_u.
+ * With T = 0 dgamma and dbeta are zero. eps is not looked at. */
+moe_status moe_layer_norm_backward(const moe_layer_norm_shape* shape, const void* out,
+                                   const void* d_u, const void* d_out, const float* mean,
+                                   const float* rstd, const float* gamma, void* dx, void* dy,
+                                   float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                                   hipStream_t stream);
+
+/* Newton-Schulz orthogonalisation of E matrices G_e [m, n], each by itself:
+ *   X = G / (|G|_F + eps), then `steps` times
+ *   X <- a X + (b A + c A^2) X,  A = X X^T     (m <= n; m > n: the same of the transpose)
+ * which moves the singular values s of X to p(s) = a s + b s^3 + c s^5 at every step and keeps
+ * its singular vectors.
+ * Products are taken on the matrix cores in fp16 with fp32 sums, the matrices scaled so that
+ * their values lie in fp16's range. What passes from one product to the next is, for
+ *   bf16 matrices whose sides are both over 512, rounded to fp16 (2^-11 of a value at most). A
+ *     step multiplies small singular values by up to a, and with them what was rounded before
+ *     it: matrices of full rank come out within about 2e-3 of their norm (and half a bf16 step),
+ *     those of a rank r far below their sides within 0.15 / sqrt(r);
+ *   others, kept as two fp16 terms (22 bits), three products for one: as in fp32.
+ * The coefficients are expected to keep the singular values below about 8 (beyond that a value may
+ * leave fp16's range and come out infinite), and a not to be small beside b and c: a X carries the
+ * small singular values, for which A is not kept to a relative precision. A matrix of zeros gives zeros; one that holds a value
+ * that is not finite gives no finite ones; the others are not affected. Each matrix's scale is
+ * found first, in fp64, so that every finite fp32 matrix has one. */
+typedef struct moe_orthogonalize_shape {
+  int64_t m, n;      /* sides: 1 .. 2^18, the shorter one at most 16384 */
+  int32_t E;         /* matrices, 1 .. 64 */
+  int32_t dtype;     /* moe_dtype of G and the result (moe_muon_update: of G and W) */
+  int32_t steps;     /* 1 .. 64 */
+  float a, b, c;     /* finite */
+  float eps;         /* >= 0, finite */
+} moe_orthogonalize_shape;
+
+/* Bytes of workspace moe_orthogonalize and moe_muon_update need. Host only. */
+moe_status moe_orthogonalize_workspace_size(const moe_orthogonalize_shape* shape, size_t* bytes);
+
+/*   g, out [E, m, n] dtype, row-major; out may be g. ws 256-byte aligned; g and out need no
+ *   alignment beyond their type's (rows of whole 16 bytes, 16-byte aligned, are faster). */
+moe_status moe_orthogonalize(const moe_orthogonalize_shape* shape, const void* g, void* out,
+                             void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* One update step of E weight matrices with momentum, in place:
+ *   m <- momentum m + g,  u = g + momentum m (nesterov) or m
+ *   w <- (1 - lr weight_decay) w - lr scale orthogonalize(u)
+ * The orthogonalised update is not rounded before it is applied. */
+typedef struct moe_muon_params {
+  float lr, momentum, weight_decay, scale;  /* finite */
+  int32_t nesterov;                         /* 0 or 1 */
+} moe_muon_params;
+
+/*   w, g [E, m, n] dtype, m [E, m, n] fp32. */
+moe_status moe_muon_update(const moe_orthogonalize_shape* shape, const moe_muon_params* params,
+                           void* w, const void* g, float* m, void* ws, size_t ws_bytes,
+                           hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,6 +22,7 @@ __all__ = [
     "MoEError", "load_library", "LIB_PATH",
     "moe_grouped_matmul", "moe_swiglu_backward", "moe_route_backward", "moe_block_norm",
     "moe_block_norm_backward",
+    "moe_layer_norm", "moe_layer_norm_backward", "moe_orthogonalize", "moe_muon_update",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_hip.so")
@@ -42,6 +43,8 @@ EXPORTS = (
     "moe_route_backward_workspace_size",
     "moe_route_backward", "moe_block_norm", "moe_block_norm_backward_workspace_size",
     "moe_block_norm_backward",
+    "moe_layer_norm", "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward",
+    "moe_orthogonalize_workspace_size", "moe_orthogonalize", "moe_muon_update",
 )
 
 
@@ -118,6 +121,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                  "moe_profile_read"):
         getattr(lib, name).restype = I32
     training.declare(lib)
+    step.declare(lib)
     _lib = lib
     return lib
 
@@ -410,6 +414,9 @@ def profile_read() -> dict:
 from . import training  # noqa: E402  (its bindings use the helpers above)
 from .training import (moe_block_norm, moe_block_norm_backward,  # noqa: E402
                        moe_grouped_matmul, moe_route_backward, moe_swiglu_backward)
+from . import step  # noqa: E402
+from .step import (moe_layer_norm, moe_layer_norm_backward, moe_muon_update,  # noqa: E402
+                   moe_orthogonalize)
 
 
 class SparseMoE:
@@ -426,22 +433,38 @@ class SparseMoE:
     residual_scale * x + gate * (y / rms(y) * post_gamma) in x's type (``gate`` fp32 [d_model]
     or None).
 
+    With ``norm="layer"`` they are layer norms (``moe_layer_norm``), ``pre_beta`` and ``post_beta``
+    their shifts or None: with ``pre_gamma`` the layer reads u = norm(x), with ``post_gamma`` the
+    call returns norm(residual_scale * x + y), the norm after the sum (no gate).
+
     ``backward(d_out)`` gives the gradients of the latest call (token choice, with or without
     a capacity, no training noise). It reads that call's x, u, y and workspace, and the
     weights: none of them must have been changed since. Calls of one layer share its
     workspace, captured ones too: they run one after another, each with its backward before
-    the next call."""
+    the next call.
+
+    ``muon_update(grads, lr=...)`` takes an optimiser's step on the experts' weights."""
 
     def __init__(self, W_g, W_gate, W_up, W_down, b_g=None, *, k=2, mode="tc",
                  capacity_factor=1.0, renormalize=True, pre_gamma=None, post_gamma=None, gate=None,
-                 residual_scale=1.0, norm_eps=1e-6):
+                 residual_scale=1.0, norm_eps=1e-6, norm="rms", pre_beta=None, post_beta=None):
         if gate is not None and post_gamma is None:
             raise ValueError("gate needs post_gamma")
+        if norm not in ("rms", "layer"):
+            raise ValueError(f"norm must be 'rms' or 'layer', got {norm!r}")
+        if norm == "layer" and gate is not None:
+            raise ValueError("gate belongs to the RMS norms")
+        if norm == "rms" and (pre_beta is not None or post_beta is not None):
+            raise ValueError("pre_beta and post_beta belong to norm='layer'")
+        if (pre_beta is not None and pre_gamma is None) or (post_beta is not None and post_gamma is None):
+            raise ValueError("a norm's beta needs its gamma")
         self.W_g, self.W_gate, self.W_up, self.W_down, self.b_g = W_g, W_gate, W_up, W_down, b_g
         self.k, self.mode, self.cf, self.renormalize = k, mode, capacity_factor, renormalize
         self.pre_gamma, self.post_gamma, self.gate = pre_gamma, post_gamma, gate
         self.residual_scale, self.norm_eps = residual_scale, norm_eps
-        self._ws = None
+        self.norm, self.pre_beta, self.post_beta = norm, pre_beta, post_beta
+        self.momentum = {}  # muon_update's, by weight
+        self._ws = self._update_ws = None
         self.last = None
 
     def __call__(self, x, **kw):
@@ -449,7 +472,10 @@ class SparseMoE:
         lead, d = x.shape[:-1], x.shape[-1]
         x2 = x.view(-1, d)
         pre = None
-        if self.pre_gamma is not None:
+        layer_norm = self.norm == "layer"
+        if self.pre_gamma is not None and layer_norm:
+            pre = moe_layer_norm(x2, self.pre_gamma, self.pre_beta, eps=self.norm_eps)
+        elif self.pre_gamma is not None:
             pre = moe_block_norm(x2, gamma=self.pre_gamma, eps=self.norm_eps)
         u = x2 if pre is None else pre["u"]
         out = moe_forward(u, self.W_g, self.b_g, self.W_gate, self.W_up,
@@ -458,9 +484,15 @@ class SparseMoE:
         self._ws = out["workspace"]
         out["x"], out["u"], out["noise"] = x2, u, kw.get("eps") is not None
         out["rstd"] = None if pre is None else pre["rstd"]
+        out["mean"] = pre["mean"] if pre is not None and layer_norm else None
         self.last = out
         if self.post_gamma is None:
             return out["y"].view(*lead, d)
+        if layer_norm:
+            post = moe_layer_norm(x2, self.post_gamma, self.post_beta, y=out["y"],
+                                  residual_scale=self.residual_scale, eps=self.norm_eps)
+            out["out"], out["mean_post"], out["rstd_post"] = post["out"], post["mean"], post["rstd"]
+            return post["u"].view(*lead, d)
         post = moe_block_norm(x2, y=out["y"], gamma_post=self.post_gamma, gate=self.gate,
                               residual_scale=self.residual_scale, eps=self.norm_eps)
         out["out"], out["rstd_post"] = post["out"], post["rstd_post"]
@@ -470,7 +502,7 @@ class SparseMoE:
         """Gradients of the latest call, given d_out, the gradient of what it returned, and
         the gradients of the load-balancing loss and the z-loss: dx, dW_g, dW_gate, dW_up,
         dW_down (their tensors' types) and, where present, db_g, d_pre_gamma, d_post_gamma,
-        d_gate (fp32).
+        d_gate, d_pre_beta, d_post_beta (fp32).
 
         The gate and up products are formed again from the call's routing. Sums within a kernel
         are fp32. What passes from one kernel to the next is of the layer's type; bf16 rounds
@@ -491,7 +523,12 @@ class SparseMoE:
         T, d = x.shape
         d_out = d_out.reshape(T, d)
         residual, post = None, None
-        if self.post_gamma is not None:
+        if self.post_gamma is not None and self.norm == "layer":
+            post = moe_layer_norm_backward(last["out"], d_out.to(dt).contiguous(), last["mean_post"],
+                                           last["rstd_post"], self.post_gamma,
+                                           residual_scale=self.residual_scale, want_dy=True)
+            dy, residual = post["dy"], post["dx"]
+        elif self.post_gamma is not None:
             post = moe_block_norm_backward(last["out"], d_out=d_out.to(dt).contiguous(), y=last["y"],
                                            rstd_post=last["rstd_post"], gamma_post=self.post_gamma,
                                            gate=self.gate, residual_scale=self.residual_scale)
@@ -529,14 +566,37 @@ class SparseMoE:
         grads["dW_g"] = r["dW_g"]
         if self.b_g is not None:
             grads["db_g"] = r["db_g"]
-        if self.pre_gamma is not None:
+        if self.pre_gamma is not None and self.norm == "layer":
+            pre = moe_layer_norm_backward(x, r["dx"], last["mean"], last["rstd"], self.pre_gamma, d_out=residual)
+            grads["dx"], grads["d_pre_gamma"] = pre["dx"], pre["dgamma"]
+            if self.pre_beta is not None:
+                grads["d_pre_beta"] = pre["dbeta"]
+        elif self.pre_gamma is not None:
             pre = moe_block_norm_backward(x, d_out=residual, d_u=r["dx"], rstd=last["rstd"],
                                           gamma=self.pre_gamma)
             grads["dx"], grads["d_pre_gamma"] = pre["dx"], pre["dgamma"]
         else:
             grads["dx"] = r["dx"] if residual is None else residual + r["dx"]
         if post is not None:
-            grads["d_post_gamma"] = post["dgamma_post"]
+            grads["d_post_gamma"] = post["dgamma" if self.norm == "layer" else "dgamma_post"]
             if self.gate is not None:
                 grads["d_gate"] = post["dgate"]
+            if self.post_beta is not None:
+                grads["d_post_beta"] = post["dbeta"]
         return grads
+
+    def muon_update(self, grads, *, lr, momentum=0.95, nesterov=True, weight_decay=0.0, **kw):
+        """One step of orthogonalised updates with momentum (``moe_muon_update``) on W_gate, W_up
+        and W_down, in place, from ``backward``'s dW_gate, dW_up and dW_down. Each expert's update
+        is scaled by sqrt(max(1, its columns / its rows)), the ratio of its output's width to its
+        input's. The momentum (fp32, zeros before the first step) is kept in ``self.momentum``; so is a
+        workspace, which the steps of one layer share: they run one after another."""
+        for name in ("W_gate", "W_up", "W_down"):
+            w = getattr(self, name)
+            m = self.momentum.get(name)
+            if m is None:
+                m = self.momentum[name] = torch.zeros_like(w, dtype=torch.float32)
+            rows, cols = w.shape[-2:]
+            self._update_ws = moe_muon_update(
+                w, grads["d" + name], m, lr=lr, momentum=momentum, nesterov=nesterov, weight_decay=weight_decay,
+                scale=max(1.0, cols / rows) ** 0.5, workspace=self._update_ws, **kw)

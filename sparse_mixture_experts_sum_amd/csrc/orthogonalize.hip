@@ -1,0 +1,751 @@
+// Newton-Schulz orthogonalisation of E matrices, and the update step around it.
+//
+// X = G / (|G| + eps); a step is X <- P X with A = X X^T and P = a I + b A + c A^2 (X^T X, of the short
+// side, and X P where G is tall). All polynomials of A commute, so two steps share the long products:
+// with A' = (P X) (P X)^T = P^2 A and P' of it, X <- P' P X.
+// Per pair of steps, with s and l the short and the long side, 3 s^2 l + 5 s^3 operations in place of
+// 6 s^2 l + 2 s^3; every product but the last is symmetric, and only the tiles on and below its
+// diagonal are computed, each stored a second time as its own transpose.
+// P and P' P are kept with their diagonals, as they are multiplied: a I apart and b A + c A^2 rounded
+// by itself would cancel where P is small, at the large singular values.
+//
+// Products: one workgroup of four waves per 128 x 128 or 256 x 256 tile, v_mfma_f32_32x32x16_f16,
+// stages of 32 of the summed axis through a ring of four LDS buffers, tile after tile as one
+// stream (matmul_tile.h says how operands lie in LDS). All matrices of the iteration are padded with
+// zeros to multiples of 128, so that a sum is a whole number of ring turns and no value of an
+// operand has to be masked.
+//
+// What is kept between products: fp16, of values scaled to lie in its range (X times a power of
+// two near the square root of its long side; A and P as they are, of order 1). G itself enters
+// as G 2^p, exact for bf16, and the rest of its norm as a factor of the first products' sums.
+// bf16 matrices: one fp16 term (2^-11 of a value at most; with bf16 terms a full-rank matrix would be
+// off by 1%, not by 0.2%). fp32 matrices, and bf16 ones of short sides (few large singular values,
+// whose roundings do not average out: 64 x 128 is 0.7% off with one term, 700 x 700 0.2%; the products
+// are too small there to be what counts): two terms, hi + lo / 2048 (22 bits; lo is scaled so that
+// it stays normal where hi is), and three products: lo hi and hi lo first, their sum divided by
+// 2048, then hi hi.
+#include <math.h>
+
+#include "matmul_tile.h"
+#include "step_kernels.h"
+#include "train_common.h"
+
+namespace {
+
+typedef _Float16 f16;
+typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kPad = 128;           // sides of the iteration's matrices
+constexpr int kXcds = 8;
+constexpr int kCus = 256;
+constexpr int kColBlock = 4;        // columns of tiles walked together
+constexpr float kLo = 1.0f / 2048;  // scale of the second term
+constexpr int kNormBlocks = 256;    // most partial sums of a matrix's squares
+constexpr int kOneTerm = 512;       // bf16 matrices with short sides past it are kept in one term
+
+// ---- the matrix in, and its norm -------------------------------------------------------
+// u, what is orthogonalised: g, or its momentum step, from g and the momentum before
+// (`fresh`) or after it.
+__device__ __forceinline__ float momentum_of(const OrthArgs& a, float m, float g) { return a.mu * m + g; }
+__device__ __forceinline__ float update_of(const OrthArgs& a, float m, float g) {
+  return a.nesterov ? a.mu * m + g : m;
+}
+template <typename TI>
+__device__ __forceinline__ void load_row(const TI* p, int n, bool vec, float (&v)[8]) {
+  if (vec && n >= 8) {
+    if constexpr (sizeof(TI) == 2) {
+      const bf16x8 t = *reinterpret_cast<const bf16x8*>(p);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = (float)t[i];
+    } else {
+      const f32x4 t0 = *reinterpret_cast<const f32x4*>(p), t1 = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = t0[i];
+        v[4 + i] = t1[i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? (float)p[i] : 0.f;
+  }
+}
+template <typename TI>
+__device__ __forceinline__ void store_row(TI* p, int n, bool vec, const float (&v)[8]) {
+  if (vec && n >= 8) {
+    if constexpr (sizeof(TI) == 2) {
+      bf16x8 t;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = (bf16)v[i];
+      *reinterpret_cast<bf16x8*>(p) = t;
+    } else {
+      *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (TI)v[i];
+  }
+}
+
+__device__ __forceinline__ double block_sum(double v, double* sh) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = ((sh[0] + sh[1]) + sh[2]) + sh[3];
+  __syncthreads();
+  return v;
+}
+
+// The momentum's step, and sums of u^2 (fp64: no finite fp32 matrix overflows or vanishes).
+// Workgroup x of matrix y. vec: whole chunks of 8 values, 16-byte aligned.
+template <typename TI>
+__global__ __launch_bounds__(256) void square_kernel(OrthArgs a, bool vec, double* partial) {
+  __shared__ double sh[4];
+  const int64_t size = a.m * a.n, at = (int64_t)blockIdx.y * size;
+  const TI* g = static_cast<const TI*>(a.g) + at;
+  float* mom = a.momentum ? a.momentum + at : nullptr;
+  double sum = 0;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < size; i += (int64_t)gridDim.x * 2048) {
+    const int n = (int)min((int64_t)8, size - i);
+    float u[8];
+    load_row(g + i, n, vec, u);
+    if (mom) {
+      float m[8];
+      load_row(mom + i, n, vec, m);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        m[e] = momentum_of(a, m[e], u[e]);
+        u[e] = update_of(a, m[e], u[e]);
+      }
+      store_row(mom + i, n, vec, m);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += (double)u[e] * (double)u[e];
+  }
+  sum = block_sum(sum, sh);
+  if (threadIdx.x == 0) partial[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = sum;
+}
+
+// v in two terms. (v is hidden from the compiler: where it is a product's sum, the compiler may
+// take hi a second time, from that sum and in one rounding, and store another hi than the one that
+// lo was taken against; the value was then off by 2^-11, once in some thousands.)
+__device__ __forceinline__ void split(float v, f16& hi, f16& lo) {
+  asm("" : "+v"(v));
+  hi = (f16)v;
+  lo = (f16)((v - (float)hi) * 2048.f);
+}
+
+// u 2^p in fp16 terms, padded with zeros to rows x cols, and first[e] = 2^-p / (|u| + eps).
+// scale: about what X's values are to be multiplied by.
+template <typename TI, int TERMS>
+__global__ __launch_bounds__(256) void scale_kernel(OrthArgs a, bool vec, const double* partial, int blocks,
+                                                    double scale, f16* x, int64_t rows, int64_t cols,
+                                                    int64_t plane, float* first) {
+  __shared__ double sh[4];
+  const int e = blockIdx.y;
+  const double sq = block_sum((int)threadIdx.x < blocks ? partial[(int64_t)e * blocks + threadIdx.x] : 0.0, sh);
+  const double norm = sqrt(sq) + (double)a.eps;
+  int p = 0;
+  float t0 = __builtin_nanf("");  // a value that is not finite: no value of the result is
+  if (norm == 0.0) {
+    t0 = 0.f;
+  } else if (norm < __builtin_huge_val()) {
+    frexp(scale / norm, &p);
+    --p;
+    t0 = (float)(ldexp(1.0, -p) / norm);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) first[e] = t0;
+  const double by = ldexp(1.0, p);
+  const int64_t at = (int64_t)e * a.m * a.n, row_chunks = cols / 8, chunks = rows * row_chunks;
+  const TI* g = static_cast<const TI*>(a.g) + at;
+  const float* mom = a.momentum ? a.momentum + at : nullptr;
+  f16* out = x + (int64_t)e * rows * cols;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / row_chunks, c = (i - r * row_chunks) * 8;
+    const int n = r < a.m ? (int)max(min((int64_t)8, a.n - c), (int64_t)0) : 0;
+    float u[8] = {};
+    if (n > 0) {
+      load_row(g + r * a.n + c, n, vec, u);
+      if (mom) {
+        float m[8];
+        load_row(mom + r * a.n + c, n, vec, m);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = update_of(a, m[k], u[k]);
+      }
+    }
+    f16x8 hi, lo;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      f16 h, l;
+      split((float)((double)u[k] * by), h, l);
+      hi[k] = h;
+      lo[k] = l;
+    }
+    *reinterpret_cast<f16x8*>(out + i * 8) = hi;
+    if constexpr (TERMS == 2) *reinterpret_cast<f16x8*>(out + plane + i * 8) = lo;
+  }
+}
+
+// ---- products --------------------------------------------------------------------------
+// d[i][j] = f sum_k A(i, k) B(j, k) (+ p c[i][j] + q I), f times first[e]^power, of E matrices. An operand is K-contiguous ([i][k]) or K-strided ([k][i]). A matrix's fp16 terms are
+// `plane` values apart, its neighbours `mat` values.
+struct Operands {
+  const f16* at;
+  int64_t plane, mat;
+  int ld;
+};
+struct ProductArgs {
+  Operands a, b, c;
+  int64_t K, rows, cols;  // padded
+  f16* d;                 // [rows][cols] in fp16 terms, or
+  int64_t d_plane;
+  void* out;              // the result of the iteration, [m][n]
+  int64_t m, n;
+  int E, power, vec, update;
+  float f, p, q, keep, rate;
+  const float* first;
+};
+
+template <int BM_, bool AKS, bool BKS>
+struct Tile {
+  static constexpr int BM = BM_, BK = 32;
+  typedef Operand<f16, AKS, BM, BK, 4> A;
+  typedef Operand<f16, BKS, BM, BK, 4> B;
+  static constexpr int WM = BM / 2, MB = WM / 32, SUB = BK / 16;  // 2 x 2 waves
+  static constexpr int STAGE = A::BYTES + B::BYTES, LPS = A::PW + B::PW;
+  static constexpr int OUT_BYTES = 32 * WM * 2;  // LDS of each wave for its output
+};
+
+template <class G>
+struct Frags {
+  u32x4 a[G::SUB][G::MB], b[G::SUB][G::MB];
+};
+
+template <class G>
+struct Wave {
+  int a_at[G::MB], b_at[G::MB];
+  f32x16 acc[G::MB][G::MB];  // [columns][rows]
+
+  // LDS read r of a stage's fragments (r constant at every call)
+  __device__ __forceinline__ void read(int r, const char* st, Frags<G>& F) const {
+    const int s = r / (2 * G::MB), i = r % (2 * G::MB);
+    if (i < G::MB) F.a[s][i] = G::A::read(st, a_at[i], s);
+    else F.b[s][i - G::MB] = G::B::read(st + G::A::BYTES, b_at[i - G::MB], s);
+  }
+  __device__ __forceinline__ void mfma(int i, const Frags<G>& F) {
+    const int s = i / (G::MB * G::MB), nb = i / G::MB % G::MB, mb = i % G::MB;
+    acc[nb][mb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+        __builtin_bit_cast(f16x8, F.b[s][nb]), __builtin_bit_cast(f16x8, F.a[s][mb]), acc[nb][mb], 0, 0, 0);
+  }
+};
+
+// A tile's sources: where its operands begin (uniform), each lane's offsets of its loads from
+// there, in bytes, and the bytes per stage.
+template <class G>
+struct Loader {
+  const char *a, *b;
+  uint32_t va[G::A::PW], vb[G::B::PW];
+  int64_t sa, sb;
+  int wave;
+};
+
+// One tile of a matrix.
+struct Item {
+  int e, i, j;
+};
+
+// Stage J of a turn: wait for this wave's loads of the next stage and its own LDS reads of this
+// one, then the barrier: after it the next stage is whole in LDS and this stage's buffer is
+// free. Then the stage's MFMAs, with the reads of the next stage into Fn and the refill of this
+// buffer (stage J of the turn that begins at ra, rb) spread between them.
+template <class G, int J>
+struct Step {
+  static __device__ __forceinline__ void load(const Loader<G>& ld, int g, const char* ra, const char* rb, char* st) {
+    const bool is_a = g < G::A::PW;
+    const int i = is_a ? g : g - G::A::PW;
+    const char* p = is_a ? ra + J * ld.sa + ld.va[i] : rb + J * ld.sb + ld.vb[i];
+    char* to = is_a ? st + (ld.wave * G::A::PW + i) * 1024 : st + G::A::BYTES + (ld.wave * G::B::PW + i) * 1024;
+    __builtin_amdgcn_global_load_lds(p, (lds_void*)to, 16, 0, 0);
+  }
+  static __device__ __forceinline__ void run(char* const (&ring)[kStages], const Loader<G>& ld, const char* ra,
+                                             const char* rb, Wave<G>& w, Frags<G>& Fc, Frags<G>& Fn) {
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<(kStages - 2) * G::LPS>();
+    wait_lgkmcnt0();
+    sync_point();
+    constexpr int NM = G::SUB * G::MB * G::MB, NR = G::SUB * 2 * G::MB, NG = G::LPS;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+#pragma unroll
+      for (int m = NM * g / NG; m < NM * (g + 1) / NG; ++m) w.mfma(m, Fc);
+#pragma unroll
+      for (int r = NR * g / NG; r < NR * (g + 1) / NG; ++r) w.read(r, ring[(J + 1) % kStages], Fn);
+      load(ld, g, ra, rb, ring[J]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+};
+
+// Tiles of a matrix: all, column block after column block, rows outer and the block's columns
+// inner; or, SYM, those on and below the diagonal in the same order.
+template <bool SYM>
+__device__ __forceinline__ Item locate(int at, int Mt, int Nt) {
+  Item t;
+  if constexpr (SYM) {
+    const int per = Mt * (Mt + 1) / 2;
+    t.e = at / per;
+    int r = at - t.e * per, c0 = 0;
+    for (;; c0 += kColBlock) {
+      const int left = Mt - c0, w = min(left, kColBlock), n = w * (w + 1) / 2 + (left - w) * w;
+      if (r < n) {
+        int row = 0;
+        while (row < w && r > row) r -= ++row;  // the block's corner: rows of 1, 2, .. tiles
+        if (row < w) {
+          t.i = c0 + row;
+          t.j = c0 + r;
+        } else {
+          t.i = c0 + w + r / w;
+          t.j = c0 + r % w;
+        }
+        return t;
+      }
+      r -= n;
+    }
+  } else {
+    const int per = Mt * Nt;
+    t.e = at / per;
+    const int r = at - t.e * per, blk = r / (Mt * kColBlock), cols = min(kColBlock, Nt - blk * kColBlock);
+    const int in = r - blk * Mt * kColBlock;
+    t.i = in / cols;
+    t.j = blk * kColBlock + in % cols;
+    return t;
+  }
+}
+
+template <class G>
+__device__ __forceinline__ void make_loader(const ProductArgs& a, const Item& t, int lane, Loader<G>& ld) {
+  const int ln = here(lane);
+  auto side = [&](auto op, const Operands& o, int x0, int64_t size, const char*& base, uint32_t* v, int64_t& step) {
+    typedef decltype(op) Op;
+    const int last = (int)size - 1 - x0;  // (256-row tiles: the last row or chunk again past the end)
+    base = reinterpret_cast<const char*>(o.at + t.e * o.mat + (Op::KS ? (int64_t)x0 : (int64_t)x0 * o.ld));
+    step = (Op::KS ? (int64_t)o.ld : 1) * (G::BK * 2);
+#pragma unroll
+    for (int j = 0; j < Op::PW; ++j) {
+      const int row = Op::row(j, ld.wave, ln), chunk = Op::chunk(j, ld.wave, ln) * 8;
+      v[j] = Op::KS ? (uint32_t)(row * o.ld + min(chunk, last - 7)) * 2 : (uint32_t)(min(row, last) * o.ld + chunk) * 2;
+    }
+  };
+  side(typename G::A{}, a.a, t.i * G::BM, a.rows, ld.a, ld.va, ld.sa);
+  side(typename G::B{}, a.b, t.j * G::BM, a.cols, ld.b, ld.vb, ld.sb);
+}
+
+// The values of a chunk of 8 in fp16 terms.
+template <int TERMS>
+struct Terms {
+  u32x4 hi, lo;
+  __device__ __forceinline__ void load(const Operands& o, int e, int64_t row, int64_t col) {
+    const f16* p = o.at + e * o.mat + row * o.ld + col;
+    hi = ld16(p);
+    if constexpr (TERMS == 2) lo = ld16(p + o.plane);
+  }
+  __device__ __forceinline__ float value(int k) const {
+    const float h = (float)__builtin_bit_cast(f16x8, hi)[k];
+    if constexpr (TERMS == 2) return h + (float)__builtin_bit_cast(f16x8, lo)[k] * kLo;
+    return h;
+  }
+};
+
+// What a product does with its sums.
+enum { kProduct, kPolynomial, kLast };  // f S; f S + p c + q I; the result
+
+// acc[nb][mb][4 q + i] is row lane % 32 of block mb, column 8 q + 4 (lane / 32) + i of block nb.
+// 32 rows at a time go through a piece of LDS of the wave's own (16-byte chunk c of a row at
+// c ^ (row % chunks)) and leave as whole row segments; c's values are loaded a pass ahead. The transposed tile leaves by the same piece of LDS, column by column.
+template <class G, bool SYM, int TERMS, int KIND, typename TO>
+__device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, int wm, int wn, int lane, char* buf,
+                                           const Wave<G>& w) {
+  constexpr int SEG = G::OUT_BYTES / 32, CHUNKS = SEG / 16, COLS = SEG / 4, BLOCKS = COLS / 32;
+  constexpr int PER = COLS / 8, RPS = 64 / PER, N = 32 / RPS, PASSES = G::MB * (G::MB / BLOCKS);
+  const int ln = here(lane);
+  const int64_t m0 = (int64_t)t.i * G::BM + wm * G::WM, n0 = (int64_t)t.j * G::BM + wn * G::WM;
+  float f = a.f;
+  for (int i = 0; i < a.power; ++i) f *= a.first[t.e];
+  const int r0 = ln / PER, c0 = ln % PER;
+  Terms<TERMS> old[KIND == kPolynomial ? 2 : 1][N];
+  auto row_of = [&](int pass, int i) { return m0 + pass / (G::MB / BLOCKS) * 32 + i * RPS + r0; };
+  auto col_of = [&](int pass) { return n0 + pass % (G::MB / BLOCKS) * COLS + c0 * 8; };
+  auto fetch = [&](int pass) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      // (256-row tiles: past the end the last row or chunk again)
+      const int64_t row = min(row_of(pass, i), a.rows - 1), col = min(col_of(pass), a.cols - 8);
+      old[KIND == kPolynomial ? pass % 2 : 0][i].load(a.c, t.e, row, col);
+    }
+  };
+  if constexpr (KIND == kPolynomial) fetch(0);
+#pragma unroll
+  for (int pass = 0; pass < PASSES; ++pass) {
+    __builtin_amdgcn_sched_barrier(0);  // (one pass's registers at a time)
+    const int mb = pass / (G::MB / BLOCKS), nb0 = pass % (G::MB / BLOCKS) * BLOCKS, r = ln & 31;
+    if constexpr (KIND == kPolynomial) {
+      if (pass + 1 < PASSES) fetch(pass + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int nb = 0; nb < BLOCKS; ++nb)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = nb * 8 + 2 * q + (ln >> 5);
+        const f32x16& v = w.acc[nb0 + nb][mb];
+        *reinterpret_cast<f32x4*>(buf + r * SEG + ((c ^ (r % CHUNKS)) << 4)) =
+            f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      }
+    f16x8 hi[N], lo[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int row = i * RPS + r0;
+      f32x4 s[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        s[h] = *reinterpret_cast<const f32x4*>(buf + row * SEG + (((2 * c0 + h) ^ (row % CHUNKS)) << 4));
+      const int64_t gr = row_of(pass, i), gc = col_of(pass);
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = f * s[k / 4][k % 4];
+        if constexpr (KIND == kPolynomial)
+          v[k] += a.p * old[pass % 2][i].value(k) + (gr == gc + k ? a.q : 0.f);
+      }
+      if constexpr (KIND == kLast) {
+        if (gr >= a.m || gc >= a.n) continue;
+        const int n = (int)min((int64_t)8, a.n - gc);
+        TO* o = static_cast<TO*>(a.out) + ((int64_t)t.e * a.m + gr) * a.n + gc;
+        if (a.update) {
+          float old[8];
+          load_row(o, n, a.vec, old);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = a.keep * old[k] - a.rate * v[k];
+        }
+        store_row(o, n, a.vec, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          f16 h, l;
+          split(v[k], h, l);
+          hi[i][k] = h;
+          lo[i][k] = l;
+        }
+        if (G::BM > kPad && (gr >= a.rows || gc >= a.cols)) continue;
+        f16* d = a.d + (t.e * a.rows + gr) * a.cols + gc;
+        *reinterpret_cast<f16x8*>(d) = hi[i];
+        if constexpr (TERMS == 2) *reinterpret_cast<f16x8*>(d + a.d_plane) = lo[i];
+      }
+    }
+    if constexpr (SYM && KIND != kLast) {
+      if (t.i != t.j) {
+        // [column][32 rows] of fp16, chunk c of a column's rows at c ^ (column / 8 % 4)
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int row = i * RPS + r0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<f16*>(buf + (c0 * 8 + k) * 64 + (((row >> 3) ^ (c0 & 3)) << 4) + (row & 7) * 2) =
+                  term ? lo[i][k] : hi[i][k];
+          }
+#pragma unroll
+          for (int i = 0; i < COLS / 16; ++i) {
+            const int col = i * 16 + ln / 4, c = ln % 4;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(buf + col * 64 + ((c ^ (col / 8 % 4)) << 4));
+            const int64_t gr = n0 + pass % (G::MB / BLOCKS) * COLS + col, gc = m0 + mb * 32 + c * 8;
+            if (G::BM > kPad && (gr >= a.rows || gc >= a.cols)) continue;
+            st16(a.d + (t.e * a.rows + gr) * a.cols + gc + term * a.d_plane, v);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Workgroups take their XCD's tiles in strides of the XCD's workgroups, as one stream of
+// stages: the last ring turn of a tile loads the first one of the next.
+template <class G, bool SYM, int TERMS, int KIND, typename TO>
+__global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs a) {
+  // (an array of its own for each stage: the compiler then sees that the reads of one stage
+  // do not wait for the loads into another)
+  __shared__ __attribute__((aligned(1024))) char s0[G::STAGE], s1[G::STAGE], s2[G::STAGE], s3[G::STAGE];
+  __shared__ __attribute__((aligned(1024))) char outs[4 * G::OUT_BYTES];
+  char* const ring[kStages] = {s0, s1, s2, s3};
+  const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / 2, wn = wave % 2;
+  const int Mt = (int)((a.rows + G::BM - 1) / G::BM), Nt = (int)((a.cols + G::BM - 1) / G::BM);
+  const int64_t all = (int64_t)a.E * (SYM ? Mt * (Mt + 1) / 2 : Mt * Nt);
+  const int xcd = blockIdx.x % kXcds, slots = gridDim.x / kXcds;
+  const int hi = (int)(all * (xcd + 1) / kXcds);
+  int at = (int)(all * xcd / kXcds) + blockIdx.x / kXcds;
+  if (at >= hi) return;
+
+  Wave<G> w;
+#pragma unroll
+  for (int j = 0; j < G::MB; ++j) {
+    w.a_at[j] = G::A::frag(wm * G::WM + j * 32, ln);
+    w.b_at[j] = G::B::frag(wn * G::WM + j * 32, ln);
+  }
+  // A sum's turns: of one term K / 128, of two that many of lo hi, of hi lo and of hi hi.
+  const int per = (int)(a.K / (kStages * G::BK)), turns = TERMS == 2 ? 3 * per : per;
+  const int64_t a_plane = a.a.plane * 2, b_plane = a.b.plane * 2;
+  Loader<G> ld;
+  ld.wave = wave;
+  auto turn_a = [&](int u) {
+    if (TERMS == 1) return ld.a + u * kStages * ld.sa;
+    const int term = u < per ? 0 : u < 2 * per ? 1 : 2;
+    return ld.a + (term == 0 ? a_plane : 0) + (u - term * per) * kStages * ld.sa;
+  };
+  auto turn_b = [&](int u) {
+    if (TERMS == 1) return ld.b + u * kStages * ld.sb;
+    const int term = u < per ? 0 : u < 2 * per ? 1 : 2;
+    return ld.b + (term == 1 ? b_plane : 0) + (u - term * per) * kStages * ld.sb;
+  };
+  Item t = locate<SYM>(at, Mt, Nt);
+  make_loader<G>(a, t, ln, ld);
+  Frags<G> F0, F1;
+  {
+    const char *ra = turn_a(0), *rb = turn_b(0);
+#pragma unroll
+    for (int g = 0; g < G::LPS; ++g) Step<G, 0>::load(ld, g, ra, rb, s0);
+#pragma unroll
+    for (int g = 0; g < G::LPS; ++g) Step<G, 1>::load(ld, g, ra, rb, s1);
+#pragma unroll
+    for (int g = 0; g < G::LPS; ++g) Step<G, 2>::load(ld, g, ra, rb, s2);
+#pragma unroll
+    for (int g = 0; g < G::LPS; ++g) Step<G, 3>::load(ld, g, ra, rb, s3);
+  }
+  wait_vmcnt<(kStages - 1) * G::LPS>();
+  sync_point();
+#pragma unroll
+  for (int r = 0; r < G::SUB * 2 * G::MB; ++r) w.read(r, s0, F0);
+
+  for (;;) {
+#pragma unroll
+    for (int nb = 0; nb < G::MB; ++nb)
+#pragma unroll
+      for (int mb = 0; mb < G::MB; ++mb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) w.acc[nb][mb][r] = 0.f;
+    const Item cur = t;
+    at += slots;
+    const bool more = at < hi;
+    if (more) t = locate<SYM>(at, Mt, Nt);
+#define MOE_TURN(RA, RB)                                      \
+  {                                                           \
+    const char *const ra = (RA), *const rb = (RB);            \
+    Step<G, 0>::run(ring, ld, ra, rb, w, F0, F1);             \
+    Step<G, 1>::run(ring, ld, ra, rb, w, F1, F0);             \
+    Step<G, 2>::run(ring, ld, ra, rb, w, F0, F1);             \
+    Step<G, 3>::run(ring, ld, ra, rb, w, F1, F0);             \
+  }
+    int u = 0;
+    f32x16 sum[TERMS == 2 ? G::MB : 1][TERMS == 2 ? G::MB : 1];
+    auto flush = [&](float scale, bool begin) {
+#pragma unroll
+      for (int nb = 0; nb < G::MB; ++nb)
+#pragma unroll
+        for (int mb = 0; mb < G::MB; ++mb)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            sum[nb][mb][r] = begin ? w.acc[nb][mb][r] * scale : sum[nb][mb][r] + w.acc[nb][mb][r] * scale;
+            w.acc[nb][mb][r] = 0.f;
+          }
+    };
+    if constexpr (TERMS == 2) {
+      for (; u < 2 * per; ++u) MOE_TURN(turn_a(u + 1), turn_b(u + 1));
+      flush(kLo, true);
+    }
+    for (; u < turns - 1; ++u) {
+      MOE_TURN(turn_a(u + 1), turn_b(u + 1));
+      if constexpr (TERMS == 2) flush(1.f, false);
+    }
+    // the last turn loads the next tile's first (without one, this tile's, never used)
+    if (more) make_loader<G>(a, t, ln, ld);
+    MOE_TURN(turn_a(0), turn_b(0));
+#undef MOE_TURN
+    if constexpr (TERMS == 2) {
+#pragma unroll
+      for (int nb = 0; nb < G::MB; ++nb)
+#pragma unroll
+        for (int mb = 0; mb < G::MB; ++mb) w.acc[nb][mb] += sum[nb][mb];
+    }
+    store_tile<G, SYM, TERMS, KIND, TO>(a, cur, wm, wn, ln, outs + wave * G::OUT_BYTES, w);
+    if (!more) break;
+  }
+  wait_vmcnt<0>();  // the loads that nobody reads have landed before the LDS is given back
+}
+
+// ---- host ------------------------------------------------------------------------------
+int64_t padded(int64_t n) { return (n + kPad - 1) / kPad * kPad; }
+size_t aligned(size_t n) { return (n + 255) / 256 * 256; }
+
+int64_t tiles_of(const ProductArgs& a, int bm, bool sym) {
+  const int64_t mt = (a.rows + bm - 1) / bm, nt = (a.cols + bm - 1) / bm;
+  return a.E * (sym ? mt * (mt + 1) / 2 : mt * nt);
+}
+
+template <class G, bool SYM, int TERMS, int KIND, typename TO>
+hipError_t launch_tile(const ProductArgs& a, hipStream_t s) {
+  constexpr int64_t resident = kCus * (G::BM == 256 ? 1 : 2);
+  const int64_t tiles = tiles_of(a, G::BM, SYM), blocks = (tiles + kXcds - 1) / kXcds * kXcds;
+  product_kernel<G, SYM, TERMS, KIND, TO><<<(unsigned)(blocks < resident ? blocks : resident), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <bool AKS, bool BKS, bool SYM, int TERMS, int KIND, typename TO>
+hipError_t product(const ProductArgs& a, hipStream_t s) {
+  if constexpr (TERMS == 1) {
+    if (tiles_of(a, 256, SYM) >= kCus) return launch_tile<Tile<256, AKS, BKS>, SYM, TERMS, KIND, TO>(a, s);
+  }
+  return launch_tile<Tile<128, AKS, BKS>, SYM, TERMS, KIND, TO>(a, s);
+}
+
+int terms_of(const OrthArgs& a) { return a.bf16 && (a.m < a.n ? a.m : a.n) > kOneTerm ? 1 : 2; }
+
+// Pieces of the workspace.
+struct Layout {
+  int64_t rows, cols, side;  // padded
+  int blocks;                // partial sums per matrix
+  size_t partial, first, x[2], sq[3], bytes;
+};
+Layout layout_of(const OrthArgs& a) {
+  Layout l;
+  const int terms = terms_of(a);
+  l.rows = padded(a.m);
+  l.cols = padded(a.n);
+  l.side = l.rows < l.cols ? l.rows : l.cols;
+  const int64_t blocks = (a.m * a.n + 4095) / 4096;
+  l.blocks = (int)(blocks < kNormBlocks ? blocks : kNormBlocks);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t p = at;
+    at += aligned(n);
+    return p;
+  };
+  l.partial = take((size_t)a.E * l.blocks * sizeof(double));
+  l.first = take((size_t)a.E * sizeof(float));
+  const size_t x = (size_t)a.E * l.rows * l.cols * terms * 2, sq = (size_t)a.E * l.side * l.side * terms * 2;
+  for (int i = 0; i < 2; ++i) l.x[i] = i == 0 || a.steps > 2 ? take(x) : 0;
+  for (int i = 0; i < 3; ++i) l.sq[i] = i < 2 || a.steps > 1 ? take(sq) : 0;
+  l.bytes = at;
+  return l;
+}
+
+template <typename TI, int TERMS>
+hipError_t run(const OrthArgs& a, hipStream_t s) {
+  const Layout l = layout_of(a);
+  double* partial = reinterpret_cast<double*>(a.ws + l.partial);
+  float* first = reinterpret_cast<float*>(a.ws + l.first);
+  const bool tall = a.m > a.n;
+  auto aligned16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  const bool aligned_in = aligned16(a.g) && aligned16(a.momentum);
+  const int64_t x_plane = a.E * l.rows * l.cols, sq_plane = a.E * l.side * l.side;
+  f16* x[2] = {reinterpret_cast<f16*>(a.ws + l.x[0]), reinterpret_cast<f16*>(a.ws + l.x[1])};
+  f16* sq[3] = {reinterpret_cast<f16*>(a.ws + l.sq[0]), reinterpret_cast<f16*>(a.ws + l.sq[1]),
+                reinterpret_cast<f16*>(a.ws + l.sq[2])};
+  // 2^k near the square root of the long side: X's values are of order 1 / sqrt(long side) at the end
+  double scale = 1;
+  while (scale * scale < (double)(a.m > a.n ? a.m : a.n)) scale *= 2;
+
+  square_kernel<TI><<<dim3(l.blocks, a.E), 256, 0, s>>>(a, aligned_in && a.m * a.n % 8 == 0, partial);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t chunks = (l.rows * l.cols / 8 + 255) / 256, most = (4096 + a.E - 1) / a.E;
+  scale_kernel<TI, TERMS><<<dim3((unsigned)(chunks < most ? chunks : most), a.E), 256, 0, s>>>(
+      a, aligned_in && a.n % 8 == 0, partial, l.blocks, scale, x[0], l.rows, l.cols, x_plane, first);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+
+  auto big = [&](const f16* p) { return Operands{p, x_plane, l.rows * l.cols, (int)l.cols}; };
+  auto square = [&](const f16* p) { return Operands{p, sq_plane, l.side * l.side, (int)l.side}; };
+  // of symmetric matrices that commute: d = u v, or a I + b u + c u^2
+  auto symmetric = [&](const f16* u, const f16* v, f16* d) {
+    ProductArgs r{};
+    r.a = r.c = square(u);
+    r.b = square(v ? v : u);
+    r.K = r.rows = r.cols = l.side;
+    r.E = a.E;
+    r.d = d;
+    r.d_plane = sq_plane;
+    r.f = v ? 1.f : a.c;
+    r.p = a.b;
+    r.q = a.a;
+    return v ? product<false, false, true, TERMS, kProduct, f16>(r, s)
+             : product<false, false, true, TERMS, kPolynomial, f16>(r, s);
+  };
+  f16 *A = sq[0], *P = sq[1], *Y = sq[2];
+  for (int done = 0, at = 0; done < a.steps; at ^= 1) {
+    const bool begin = done == 0, two = a.steps - done >= 2;
+    const float unit = (float)(1.0 / scale);  // X = unit X^ (the first X^: first[e] X^)
+    ProductArgs r{};
+    r.a = r.b = big(x[at]);
+    r.K = tall ? l.rows : l.cols;
+    r.rows = r.cols = l.side;
+    r.E = a.E;
+    r.d = A;
+    r.d_plane = sq_plane;
+    r.first = first;
+    r.power = begin ? 2 : 0;
+    r.f = begin ? 1.f : unit * unit;
+    e = tall ? product<true, true, true, TERMS, kProduct, f16>(r, s) : product<false, false, true, TERMS, kProduct, f16>(r, s);
+    if (e == hipSuccess) e = symmetric(A, nullptr, P);
+    const f16* Q = P;
+    if (two) {
+      if (e == hipSuccess) e = symmetric(P, A, Y);
+      if (e == hipSuccess) e = symmetric(P, Y, A);        // A'
+      if (e == hipSuccess) e = symmetric(A, nullptr, Y);  // P'
+      if (e == hipSuccess) e = symmetric(Y, P, A);
+      Q = A;
+    }
+    if (e != hipSuccess) return e;
+    done += two ? 2 : 1;
+    const bool last = done == a.steps;
+    ProductArgs g{};
+    g.a = tall ? big(x[at]) : square(Q);
+    g.b = tall ? square(Q) : big(x[at]);
+    g.K = l.side;
+    g.rows = l.rows;
+    g.cols = l.cols;
+    g.E = a.E;
+    g.first = first;
+    g.power = begin ? 1 : 0;
+    if (last) {
+      g.f = begin ? 1.f : unit;
+      g.out = a.out;
+      g.m = a.m;
+      g.n = a.n;
+      g.vec = aligned16(a.out) && a.n % 8 == 0;
+      g.update = a.momentum != nullptr;
+      g.keep = a.keep;
+      g.rate = a.rate;
+      e = tall ? product<false, false, false, TERMS, kLast, TI>(g, s) : product<false, true, false, TERMS, kLast, TI>(g, s);
+    } else {
+      g.f = begin ? (float)scale : 1.f;
+      g.d = x[at ^ 1];
+      g.d_plane = x_plane;
+      e = tall ? product<false, false, false, TERMS, kProduct, f16>(g, s) : product<false, true, false, TERMS, kProduct, f16>(g, s);
+    }
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t orthogonalize_workspace(const OrthArgs& a) { return layout_of(a).bytes; }
+
+hipError_t launch_orthogonalize(const OrthArgs& a, hipStream_t s) {
+  if (terms_of(a) == 1) return run<bf16, 1>(a, s);
+  return a.bf16 ? run<bf16, 2>(a, s) : run<float, 2>(a, s);
+}
