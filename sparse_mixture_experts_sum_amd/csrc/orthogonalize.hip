@@ -9,11 +9,12 @@
 // P and P' P are kept with their diagonals, as they are multiplied: a I apart and b A + c A^2 rounded
 // by itself would cancel where P is small, at the large singular values.
 //
-// Products: one workgroup of four waves per 128 x 128 or 256 x 256 tile, v_mfma_f32_32x32x16_f16,
-// stages of 32 of the summed axis through a ring of four LDS buffers, tile after tile as one
-// stream (matmul_tile.h says how operands lie in LDS). All matrices of the iteration are padded with
-// zeros to multiples of 128, so that a sum is a whole number of ring turns and no value of an
-// operand has to be masked.
+// Products: one workgroup of four waves per square tile, v_mfma_f32_32x32x16_f16, stages of 32 of the
+// summed axis through a ring of four LDS buffers, tile after tile as one stream (matmul_tile.h says
+// how operands lie in LDS). All matrices of the iteration are padded with zeros to multiples of
+// 128, so that a sum is a whole number of ring turns and no value of an operand has to be masked.
+// Tiles that would leave most CUs without one in the last round have their sums in parts,
+// which a second kernel joins in order.
 //
 // What is kept between products: fp16, of values scaled to lie in its range (X times a power of
 // two near the square root of its long side; A and P as they are, of order 1). G itself enters
@@ -42,6 +43,7 @@ constexpr int kCus = 256;
 constexpr int kColBlock = 4;        // columns of tiles walked together
 constexpr float kLo = 1.0f / 2048;  // scale of the second term
 constexpr int kNormBlocks = 256;    // most partial sums of a matrix's squares
+constexpr int kMaxParts = 16;       // of a product's sum
 constexpr int kOneTerm = 512;       // bf16 matrices with short sides past it are kept in one term
 
 // ---- the matrix in, and its norm -------------------------------------------------------
@@ -191,7 +193,8 @@ __global__ __launch_bounds__(256) void scale_kernel(OrthArgs a, bool vec, const 
 }
 
 // ---- products --------------------------------------------------------------------------
-// d[i][j] = f sum_k A(i, k) B(j, k) (+ p c[i][j] + q I), f times first[e]^power, of E matrices. An operand is K-contiguous ([i][k]) or K-strided ([k][i]). A matrix's fp16 terms are
+// d[i][j] = f sum_k A(i, k) B(j, k) (+ p c[i][j] + q I), f times first[e]^power, of E matrices. An
+// operand is K-contiguous ([i][k]) or K-strided ([k][i]). A matrix's fp16 terms are
 // `plane` values apart, its neighbours `mat` values.
 struct Operands {
   const f16* at;
@@ -208,54 +211,97 @@ struct ProductArgs {
   int E, power, vec, update;
   float f, p, q, keep, rate;
   const float* first;
+  // set by the launch: of every XCD's tiles, how many are whole; the others' sums are in `parts`
+  // parts, of which there are at most `rest` tiles an XCD
+  int whole, parts, rest;
+  float* sums;
 };
 
-template <int BM_, bool AKS, bool BKS>
+template <int BM_, bool AKS, bool BKS, int TERMS_>
 struct Tile {
-  static constexpr int BM = BM_, BK = 32;
+  static constexpr int BM = BM_, BK = 32, TERMS = TERMS_;
   typedef Operand<f16, AKS, BM, BK, 4> A;
   typedef Operand<f16, BKS, BM, BK, 4> B;
   static constexpr int WM = BM / 2, MB = WM / 32, SUB = BK / 16;  // 2 x 2 waves
-  static constexpr int STAGE = A::BYTES + B::BYTES, LPS = A::PW + B::PW;
-  static constexpr int OUT_BYTES = 32 * WM * 2;  // LDS of each wave for its output
+  // a stage: A's terms, then B's
+  static constexpr int STAGE = TERMS * (A::BYTES + B::BYTES), LPS = TERMS * (A::PW + B::PW);
+  static constexpr int OUT_BYTES = BM == 64 ? 4096 : 32 * WM * 2;  // LDS of each wave for its output
+  static constexpr int LDS = kStages * STAGE + 4 * OUT_BYTES, PER_CU = 160 * 1024 / LDS;
+  static constexpr int SLOTS = PER_CU * kCus / kXcds;  // workgroups of an XCD that are resident
+  static constexpr int MFMAS = TERMS == 2 ? 3 : 1;     // per pair of fragments
 };
 
 template <class G>
 struct Frags {
-  u32x4 a[G::SUB][G::MB], b[G::SUB][G::MB];
+  u32x4 a[G::TERMS][G::SUB][G::MB], b[G::TERMS][G::SUB][G::MB];
 };
 
 template <class G>
 struct Wave {
   int a_at[G::MB], b_at[G::MB];
-  f32x16 acc[G::MB][G::MB];  // [columns][rows]
+  f32x16 acc[G::MB][G::MB];  // [columns][rows]; two terms: hi hi of one ring turn
+  f32x16 cross[G::TERMS == 2 ? G::MB : 1][G::TERMS == 2 ? G::MB : 1];
+  f32x16 sum[G::TERMS == 2 ? G::MB : 1][G::TERMS == 2 ? G::MB : 1];
 
   // LDS read r of a stage's fragments (r constant at every call)
   __device__ __forceinline__ void read(int r, const char* st, Frags<G>& F) const {
-    const int s = r / (2 * G::MB), i = r % (2 * G::MB);
-    if (i < G::MB) F.a[s][i] = G::A::read(st, a_at[i], s);
-    else F.b[s][i - G::MB] = G::B::read(st + G::A::BYTES, b_at[i - G::MB], s);
+    const int s = r / (2 * G::TERMS * G::MB), i = r % (2 * G::TERMS * G::MB), t = i / G::MB % G::TERMS, b = i % G::MB;
+    if (i < G::TERMS * G::MB) F.a[t][s][b] = G::A::read(st + t * G::A::BYTES, a_at[b], s);
+    else F.b[t][s][b] = G::B::read(st + G::TERMS * G::A::BYTES + t * G::B::BYTES, b_at[b], s);
   }
   __device__ __forceinline__ void mfma(int i, const Frags<G>& F) {
-    const int s = i / (G::MB * G::MB), nb = i / G::MB % G::MB, mb = i % G::MB;
-    acc[nb][mb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-        __builtin_bit_cast(f16x8, F.b[s][nb]), __builtin_bit_cast(f16x8, F.a[s][mb]), acc[nb][mb], 0, 0, 0);
+    const int s = i / (G::MB * G::MB * G::MFMAS), nb = i / (G::MB * G::MFMAS) % G::MB, mb = i / G::MFMAS % G::MB;
+    const int k = i % G::MFMAS;  // hi hi, lo hi, hi lo
+    const u32x4 b = F.b[k == 2 ? 1 : 0][s][nb], a = F.a[k == 1 ? 1 : 0][s][mb];
+    f32x16& to = k ? cross[nb][mb] : acc[nb][mb];
+    to = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), to, 0, 0, 0);
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int nb = 0; nb < G::MB; ++nb)
+#pragma unroll
+      for (int mb = 0; mb < G::MB; ++mb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          acc[nb][mb][r] = 0.f;
+          if constexpr (G::TERMS == 2) cross[nb][mb][r] = sum[nb][mb][r] = 0.f;
+        }
+  }
+  // two terms: a turn's sums go to the others (last: with the cross terms, back into acc)
+  __device__ __forceinline__ void flush(bool last) {
+    if constexpr (G::TERMS == 2) {
+#pragma unroll
+      for (int nb = 0; nb < G::MB; ++nb)
+#pragma unroll
+        for (int mb = 0; mb < G::MB; ++mb)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float v = sum[nb][mb][r] + acc[nb][mb][r];
+            if (last) {
+              acc[nb][mb][r] = v + kLo * cross[nb][mb][r];
+            } else {
+              sum[nb][mb][r] = v;
+              acc[nb][mb][r] = 0.f;
+            }
+          }
+    }
   }
 };
 
 // A tile's sources: where its operands begin (uniform), each lane's offsets of its loads from
-// there, in bytes, and the bytes per stage.
+// there, in bytes, and the bytes per stage and from term to term.
 template <class G>
 struct Loader {
   const char *a, *b;
   uint32_t va[G::A::PW], vb[G::B::PW];
-  int64_t sa, sb;
+  int64_t sa, sb, pa, pb;
   int wave;
 };
 
-// One tile of a matrix.
+// One tile of a matrix, ring turns [u0, u1) of its sum; part: where the sum of these goes, -1:
+// it is the whole one.
 struct Item {
-  int e, i, j;
+  int e, i, j, u0, u1, part;
 };
 
 // Stage J of a turn: wait for this wave's loads of the next stage and its own LDS reads of this
@@ -265,10 +311,12 @@ struct Item {
 template <class G, int J>
 struct Step {
   static __device__ __forceinline__ void load(const Loader<G>& ld, int g, const char* ra, const char* rb, char* st) {
-    const bool is_a = g < G::A::PW;
-    const int i = is_a ? g : g - G::A::PW;
-    const char* p = is_a ? ra + J * ld.sa + ld.va[i] : rb + J * ld.sb + ld.vb[i];
-    char* to = is_a ? st + (ld.wave * G::A::PW + i) * 1024 : st + G::A::BYTES + (ld.wave * G::B::PW + i) * 1024;
+    constexpr int NA = G::TERMS * G::A::PW;
+    const bool is_a = g < NA;
+    const int i = is_a ? g : g - NA, pw = is_a ? G::A::PW : G::B::PW, t = i / pw, l = i % pw;
+    const char* p = is_a ? ra + (J * ld.sa + t * ld.pa) + ld.va[l] : rb + (J * ld.sb + t * ld.pb) + ld.vb[l];
+    char* to = is_a ? st + t * G::A::BYTES + (ld.wave * G::A::PW + l) * 1024
+                    : st + G::TERMS * G::A::BYTES + t * G::B::BYTES + (ld.wave * G::B::PW + l) * 1024;
     __builtin_amdgcn_global_load_lds(p, (lds_void*)to, 16, 0, 0);
   }
   static __device__ __forceinline__ void run(char* const (&ring)[kStages], const Loader<G>& ld, const char* ra,
@@ -277,7 +325,7 @@ struct Step {
     wait_vmcnt<(kStages - 2) * G::LPS>();
     wait_lgkmcnt0();
     sync_point();
-    constexpr int NM = G::SUB * G::MB * G::MB, NR = G::SUB * 2 * G::MB, NG = G::LPS;
+    constexpr int NM = G::SUB * G::MB * G::MB * G::MFMAS, NR = G::SUB * 2 * G::TERMS * G::MB, NG = G::LPS;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
 #pragma unroll
@@ -293,8 +341,7 @@ struct Step {
 // Tiles of a matrix: all, column block after column block, rows outer and the block's columns
 // inner; or, SYM, those on and below the diagonal in the same order.
 template <bool SYM>
-__device__ __forceinline__ Item locate(int at, int Mt, int Nt) {
-  Item t;
+__device__ __forceinline__ void locate_tile(int at, int Mt, int Nt, Item& t) {
   if constexpr (SYM) {
     const int per = Mt * (Mt + 1) / 2;
     t.e = at / per;
@@ -311,7 +358,7 @@ __device__ __forceinline__ Item locate(int at, int Mt, int Nt) {
           t.i = c0 + w + r / w;
           t.j = c0 + r % w;
         }
-        return t;
+        return;
       }
       r -= n;
     }
@@ -322,9 +369,40 @@ __device__ __forceinline__ Item locate(int at, int Mt, int Nt) {
     const int in = r - blk * Mt * kColBlock;
     t.i = in / cols;
     t.j = blk * kColBlock + in % cols;
-    return t;
   }
 }
+// The grid of tiles, and the XCD's eighth of all of them.
+template <class G, bool SYM>
+struct Share {
+  int Mt, Nt, lo, n, turns;
+  __device__ __forceinline__ Share(const ProductArgs& a, int xcd) {
+    Mt = (int)((a.rows + G::BM - 1) / G::BM);
+    Nt = (int)((a.cols + G::BM - 1) / G::BM);
+    const int64_t all = (int64_t)a.E * (SYM ? Mt * (Mt + 1) / 2 : Mt * Nt);
+    lo = (int)(all * xcd / kXcds);
+    n = (int)(all * (xcd + 1) / kXcds) - lo;
+    turns = (int)(a.K / (kStages * G::BK));
+  }
+  // items: the whole tiles, then the others' parts
+  __device__ __forceinline__ int items(const ProductArgs& a) const {
+    return a.parts > 1 ? a.whole + (n - a.whole) * a.parts : n;
+  }
+  __device__ __forceinline__ Item locate(const ProductArgs& a, int xcd, int at) const {
+    Item t;
+    t.part = -1;
+    t.u0 = 0;
+    t.u1 = turns;
+    if (a.parts > 1 && at >= a.whole) {
+      const int in = at - a.whole, tile = in / a.parts, part = in - tile * a.parts;
+      t.u0 = turns * part / a.parts;
+      t.u1 = turns * (part + 1) / a.parts;
+      t.part = (xcd * a.rest + tile) * a.parts + part;
+      at = a.whole + tile;
+    }
+    locate_tile<SYM>(lo + at, Mt, Nt, t);
+    return t;
+  }
+};
 
 template <class G>
 __device__ __forceinline__ void make_loader(const ProductArgs& a, const Item& t, int lane, Loader<G>& ld) {
@@ -332,8 +410,9 @@ __device__ __forceinline__ void make_loader(const ProductArgs& a, const Item& t,
   auto side = [&](auto op, const Operands& o, int x0, int64_t size, const char*& base, uint32_t* v, int64_t& step) {
     typedef decltype(op) Op;
     const int last = (int)size - 1 - x0;  // (256-row tiles: the last row or chunk again past the end)
-    base = reinterpret_cast<const char*>(o.at + t.e * o.mat + (Op::KS ? (int64_t)x0 : (int64_t)x0 * o.ld));
     step = (Op::KS ? (int64_t)o.ld : 1) * (G::BK * 2);
+    base = reinterpret_cast<const char*>(o.at + t.e * o.mat + (Op::KS ? (int64_t)x0 : (int64_t)x0 * o.ld)) +
+           t.u0 * kStages * step;
 #pragma unroll
     for (int j = 0; j < Op::PW; ++j) {
       const int row = Op::row(j, ld.wave, ln), chunk = Op::chunk(j, ld.wave, ln) * 8;
@@ -365,10 +444,12 @@ enum { kProduct, kPolynomial, kLast };  // f S; f S + p c + q I; the result
 
 // acc[nb][mb][4 q + i] is row lane % 32 of block mb, column 8 q + 4 (lane / 32) + i of block nb.
 // 32 rows at a time go through a piece of LDS of the wave's own (16-byte chunk c of a row at
-// c ^ (row % chunks)) and leave as whole row segments; c's values are loaded a pass ahead. The transposed tile leaves by the same piece of LDS, column by column.
-template <class G, bool SYM, int TERMS, int KIND, typename TO>
+// c ^ (row % chunks)) and leave as whole row segments; c's values are loaded a pass ahead.
+// The transposed tile leaves by the same piece of LDS, column by column.
+template <class G, bool SYM, int KIND, typename TO>
 __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, int wm, int wn, int lane, char* buf,
                                            const Wave<G>& w) {
+  constexpr int TERMS = G::TERMS;
   constexpr int SEG = G::OUT_BYTES / 32, CHUNKS = SEG / 16, COLS = SEG / 4, BLOCKS = COLS / 32;
   constexpr int PER = COLS / 8, RPS = 64 / PER, N = 32 / RPS, PASSES = G::MB * (G::MB / BLOCKS);
   const int ln = here(lane);
@@ -448,24 +529,26 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
     }
     if constexpr (SYM && KIND != kLast) {
       if (t.i != t.j) {
-        // [column][32 rows] of fp16, chunk c of a column's rows at c ^ (column / 8 % 4)
+        // [32 rows][columns] of fp16, chunk c of a row at c ^ swz(row), and out of there in columns
+        // by transposing reads: 16 columns at a time, lane l with rows 8 (l / 16) .. + 7 of column l % 16
+        auto swz = [](int row) { return ((0xCA60 >> (4 * (row & 3))) & 15) % PER; };
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             const int row = i * RPS + r0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<f16*>(buf + (c0 * 8 + k) * 64 + (((row >> 3) ^ (c0 & 3)) << 4) + (row & 7) * 2) =
-                  term ? lo[i][k] : hi[i][k];
+            *reinterpret_cast<f16x8*>(buf + row * (COLS * 2) + ((c0 ^ swz(row)) << 4)) = term ? lo[i] : hi[i];
           }
 #pragma unroll
           for (int i = 0; i < COLS / 16; ++i) {
-            const int col = i * 16 + ln / 4, c = ln % 4;
-            const u32x4 v = *reinterpret_cast<const u32x4*>(buf + col * 64 + ((c ^ (col / 8 % 4)) << 4));
-            const int64_t gr = n0 + pass % (G::MB / BLOCKS) * COLS + col, gc = m0 + mb * 32 + c * 8;
+            const int row = 8 * (ln >> 4) + (ln & 15) / 4, col = 16 * i + 4 * (ln & 3);
+            const char* p = buf + row * (COLS * 2) + (((col >> 3) ^ swz(row)) << 4) + (col & 4) * 2;
+            const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+            const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * COLS * 2));
+            const s16x8 v{v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+            const int64_t gr = n0 + pass % (G::MB / BLOCKS) * COLS + 16 * i + (ln & 15), gc = m0 + mb * 32 + 8 * (ln >> 4);
             if (G::BM > kPad && (gr >= a.rows || gc >= a.cols)) continue;
-            st16(a.d + (t.e * a.rows + gr) * a.cols + gc + term * a.d_plane, v);
+            st16(a.d + (t.e * a.rows + gr) * a.cols + gc + term * a.d_plane, __builtin_bit_cast(u32x4, v));
           }
         }
       }
@@ -473,9 +556,29 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
   }
 }
 
-// Workgroups take their XCD's tiles in strides of the XCD's workgroups, as one stream of
-// stages: the last ring turn of a tile loads the first one of the next.
-template <class G, bool SYM, int TERMS, int KIND, typename TO>
+// A part's sums, as they lie in the registers: 16 bytes of every lane at a time.
+template <class G>
+__device__ __forceinline__ float* part_at(const ProductArgs& a, int64_t part, int wave, int lane) {
+  return a.sums + (part * G::BM * G::BM + wave * G::WM * G::WM) + lane * 4;
+}
+template <class G>
+__device__ __forceinline__ void put_part(const ProductArgs& a, int part, int wave, int lane, const Wave<G>& w) {
+  float* p = part_at<G>(a, part, wave, here(lane));
+#pragma unroll
+  for (int nb = 0; nb < G::MB; ++nb)
+#pragma unroll
+    for (int mb = 0; mb < G::MB; ++mb)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x16& v = w.acc[nb][mb];
+        *reinterpret_cast<f32x4*>(p + ((nb * G::MB + mb) * 4 + q) * 256) =
+            f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      }
+}
+
+// Workgroups take their XCD's items in strides of the XCD's workgroups, as one stream of
+// stages: the last ring turn of an item loads the first one of the next.
+template <class G, bool SYM, int KIND, typename TO>
 __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs a) {
   // (an array of its own for each stage: the compiler then sees that the reads of one stage
   // do not wait for the loads into another)
@@ -484,12 +587,11 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs a) {
   char* const ring[kStages] = {s0, s1, s2, s3};
   const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / 2, wn = wave % 2;
-  const int Mt = (int)((a.rows + G::BM - 1) / G::BM), Nt = (int)((a.cols + G::BM - 1) / G::BM);
-  const int64_t all = (int64_t)a.E * (SYM ? Mt * (Mt + 1) / 2 : Mt * Nt);
   const int xcd = blockIdx.x % kXcds, slots = gridDim.x / kXcds;
-  const int hi = (int)(all * (xcd + 1) / kXcds);
-  int at = (int)(all * xcd / kXcds) + blockIdx.x / kXcds;
-  if (at >= hi) return;
+  const Share<G, SYM> share(a, xcd);
+  const int items = share.items(a);
+  int at = blockIdx.x / kXcds;
+  if (at >= items) return;
 
   Wave<G> w;
 #pragma unroll
@@ -497,51 +599,32 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs a) {
     w.a_at[j] = G::A::frag(wm * G::WM + j * 32, ln);
     w.b_at[j] = G::B::frag(wn * G::WM + j * 32, ln);
   }
-  // A sum's turns: of one term K / 128, of two that many of lo hi, of hi lo and of hi hi.
-  const int per = (int)(a.K / (kStages * G::BK)), turns = TERMS == 2 ? 3 * per : per;
-  const int64_t a_plane = a.a.plane * 2, b_plane = a.b.plane * 2;
   Loader<G> ld;
   ld.wave = wave;
-  auto turn_a = [&](int u) {
-    if (TERMS == 1) return ld.a + u * kStages * ld.sa;
-    const int term = u < per ? 0 : u < 2 * per ? 1 : 2;
-    return ld.a + (term == 0 ? a_plane : 0) + (u - term * per) * kStages * ld.sa;
-  };
-  auto turn_b = [&](int u) {
-    if (TERMS == 1) return ld.b + u * kStages * ld.sb;
-    const int term = u < per ? 0 : u < 2 * per ? 1 : 2;
-    return ld.b + (term == 1 ? b_plane : 0) + (u - term * per) * kStages * ld.sb;
-  };
-  Item t = locate<SYM>(at, Mt, Nt);
+  ld.pa = a.a.plane * 2;
+  ld.pb = a.b.plane * 2;
+  Item t = share.locate(a, xcd, at);
   make_loader<G>(a, t, ln, ld);
   Frags<G> F0, F1;
-  {
-    const char *ra = turn_a(0), *rb = turn_b(0);
 #pragma unroll
-    for (int g = 0; g < G::LPS; ++g) Step<G, 0>::load(ld, g, ra, rb, s0);
+  for (int g = 0; g < G::LPS; ++g) Step<G, 0>::load(ld, g, ld.a, ld.b, s0);
 #pragma unroll
-    for (int g = 0; g < G::LPS; ++g) Step<G, 1>::load(ld, g, ra, rb, s1);
+  for (int g = 0; g < G::LPS; ++g) Step<G, 1>::load(ld, g, ld.a, ld.b, s1);
 #pragma unroll
-    for (int g = 0; g < G::LPS; ++g) Step<G, 2>::load(ld, g, ra, rb, s2);
+  for (int g = 0; g < G::LPS; ++g) Step<G, 2>::load(ld, g, ld.a, ld.b, s2);
 #pragma unroll
-    for (int g = 0; g < G::LPS; ++g) Step<G, 3>::load(ld, g, ra, rb, s3);
-  }
+  for (int g = 0; g < G::LPS; ++g) Step<G, 3>::load(ld, g, ld.a, ld.b, s3);
   wait_vmcnt<(kStages - 1) * G::LPS>();
   sync_point();
 #pragma unroll
-  for (int r = 0; r < G::SUB * 2 * G::MB; ++r) w.read(r, s0, F0);
+  for (int r = 0; r < G::SUB * 2 * G::TERMS * G::MB; ++r) w.read(r, s0, F0);
 
   for (;;) {
-#pragma unroll
-    for (int nb = 0; nb < G::MB; ++nb)
-#pragma unroll
-      for (int mb = 0; mb < G::MB; ++mb)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) w.acc[nb][mb][r] = 0.f;
+    w.clear();
     const Item cur = t;
     at += slots;
-    const bool more = at < hi;
-    if (more) t = locate<SYM>(at, Mt, Nt);
+    const bool more = at < items;
+    if (more) t = share.locate(a, xcd, at);
 #define MOE_TURN(RA, RB)                                      \
   {                                                           \
     const char *const ra = (RA), *const rb = (RB);            \
@@ -550,41 +633,47 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs a) {
     Step<G, 2>::run(ring, ld, ra, rb, w, F0, F1);             \
     Step<G, 3>::run(ring, ld, ra, rb, w, F1, F0);             \
   }
-    int u = 0;
-    f32x16 sum[TERMS == 2 ? G::MB : 1][TERMS == 2 ? G::MB : 1];
-    auto flush = [&](float scale, bool begin) {
-#pragma unroll
-      for (int nb = 0; nb < G::MB; ++nb)
-#pragma unroll
-        for (int mb = 0; mb < G::MB; ++mb)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            sum[nb][mb][r] = begin ? w.acc[nb][mb][r] * scale : sum[nb][mb][r] + w.acc[nb][mb][r] * scale;
-            w.acc[nb][mb][r] = 0.f;
-          }
-    };
-    if constexpr (TERMS == 2) {
-      for (; u < 2 * per; ++u) MOE_TURN(turn_a(u + 1), turn_b(u + 1));
-      flush(kLo, true);
+    for (int u = 1; u < cur.u1 - cur.u0; ++u) {
+      MOE_TURN(ld.a + u * kStages * ld.sa, ld.b + u * kStages * ld.sb);
+      w.flush(false);
     }
-    for (; u < turns - 1; ++u) {
-      MOE_TURN(turn_a(u + 1), turn_b(u + 1));
-      if constexpr (TERMS == 2) flush(1.f, false);
-    }
-    // the last turn loads the next tile's first (without one, this tile's, never used)
+    // the last turn loads the next item's first (without one, this item's, never used)
     if (more) make_loader<G>(a, t, ln, ld);
-    MOE_TURN(turn_a(0), turn_b(0));
+    MOE_TURN(ld.a, ld.b);
 #undef MOE_TURN
-    if constexpr (TERMS == 2) {
-#pragma unroll
-      for (int nb = 0; nb < G::MB; ++nb)
-#pragma unroll
-        for (int mb = 0; mb < G::MB; ++mb) w.acc[nb][mb] += sum[nb][mb];
-    }
-    store_tile<G, SYM, TERMS, KIND, TO>(a, cur, wm, wn, ln, outs + wave * G::OUT_BYTES, w);
+    w.flush(true);
+    if (cur.part >= 0) put_part<G>(a, cur.part, wave, ln, w);
+    else store_tile<G, SYM, KIND, TO>(a, cur, wm, wn, ln, outs + wave * G::OUT_BYTES, w);
     if (!more) break;
   }
   wait_vmcnt<0>();  // the loads that nobody reads have landed before the LDS is given back
+}
+
+// The sums of the tiles that are in parts, in order: a quarter of a tile (what one of the product's
+// waves holds) per workgroup.
+template <class G, bool SYM, int KIND, typename TO>
+__global__ __launch_bounds__(64, 1) void join_kernel(ProductArgs a) {
+  __shared__ __attribute__((aligned(1024))) char buf[G::OUT_BYTES];
+  const int wave = blockIdx.x % 4, tile = blockIdx.x / 4 / kXcds, xcd = blockIdx.x / 4 % kXcds, ln = threadIdx.x;
+  const Share<G, SYM> share(a, xcd);
+  if (a.whole + tile >= share.n) return;
+  const Item t = share.locate(a, xcd, a.whole + tile * a.parts);
+  Wave<G> w;
+  w.clear();
+  for (int i = 0; i < a.parts; ++i) {
+    const float* p = part_at<G>(a, t.part + i, wave, ln);
+#pragma unroll
+    for (int nb = 0; nb < G::MB; ++nb)
+#pragma unroll
+      for (int mb = 0; mb < G::MB; ++mb)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(p + ((nb * G::MB + mb) * 4 + q) * 256);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w.acc[nb][mb][4 * q + k] += v[k];
+        }
+  }
+  store_tile<G, SYM, KIND, TO>(a, t, wave / 2, wave % 2, ln, buf, w);
 }
 
 // ---- host ------------------------------------------------------------------------------
@@ -596,28 +685,64 @@ int64_t tiles_of(const ProductArgs& a, int bm, bool sym) {
   return a.E * (sym ? mt * (mt + 1) / 2 : mt * nt);
 }
 
-template <class G, bool SYM, int TERMS, int KIND, typename TO>
-hipError_t launch_tile(const ProductArgs& a, hipStream_t s) {
-  constexpr int64_t resident = kCus * (G::BM == 256 ? 1 : 2);
-  const int64_t tiles = tiles_of(a, G::BM, SYM), blocks = (tiles + kXcds - 1) / kXcds * kXcds;
-  product_kernel<G, SYM, TERMS, KIND, TO><<<(unsigned)(blocks < resident ? blocks : resident), 256, 0, s>>>(a);
+// The tiles of a product and its sums' parts.
+struct Plan {
+  int bm;
+  int whole, parts, rest;
+};
+// Parts for the last round's tiles, where it would leave half of the chip without one: as many as
+// fill it, of two ring turns at least.
+Plan plan_of(const ProductArgs& a, int bm, int slots, bool sym) {
+  const int64_t all = tiles_of(a, bm, sym), turns = a.K / (kStages * 32);
+  Plan p{bm, (int)((all / kXcds) / slots * slots), 1, 0};
+  p.rest = (int)((all + kXcds - 1) / kXcds) - p.whole;
+  if (p.rest > 0) p.parts = (int)(slots / p.rest < turns / 2 ? slots / p.rest : turns / 2);
+  if (p.parts > kMaxParts) p.parts = kMaxParts;
+  return p;
+}
+template <class G>
+Plan plan_for(const ProductArgs& a, bool sym) {
+  Plan p = plan_of(a, G::BM, G::SLOTS, sym);
+  if (a.K < 1024 || p.whole) p.parts = 1;
+  return p;
+}
+
+template <class G, bool SYM, int KIND, typename TO>
+hipError_t launch_tile(const ProductArgs& args, hipStream_t s) {
+  ProductArgs a = args;
+  const Plan p = plan_for<G>(a, SYM);
+  const int64_t each = (tiles_of(a, G::BM, SYM) + kXcds - 1) / kXcds;
+  a.parts = p.parts;
+  a.whole = p.whole;
+  a.rest = p.rest;
+  const int64_t items = a.parts > 1 ? a.whole + (int64_t)a.rest * a.parts : each;
+  product_kernel<G, SYM, KIND, TO><<<(unsigned)((items < G::SLOTS ? items : G::SLOTS) * kXcds), 256, 0, s>>>(a);
+  if (a.parts > 1) join_kernel<G, SYM, KIND, TO><<<(unsigned)(a.rest * kXcds * 4), 64, 0, s>>>(a);
   return hipGetLastError();
 }
+// 256-row tiles
+bool wide(const ProductArgs& a, bool sym) { return tiles_of(a, 256, sym) >= kCus; }
+bool small(const ProductArgs& a, bool sym) { return tiles_of(a, 128, sym) < kCus / 2; }
 template <bool AKS, bool BKS, bool SYM, int TERMS, int KIND, typename TO>
 hipError_t product(const ProductArgs& a, hipStream_t s) {
   if constexpr (TERMS == 1) {
-    if (tiles_of(a, 256, SYM) >= kCus) return launch_tile<Tile<256, AKS, BKS>, SYM, TERMS, KIND, TO>(a, s);
+    if (wide(a, SYM)) return launch_tile<Tile<256, AKS, BKS, 1>, SYM, KIND, TO>(a, s);
+  } else {
+    if (small(a, SYM)) return launch_tile<Tile<64, AKS, BKS, 2>, SYM, KIND, TO>(a, s);
   }
-  return launch_tile<Tile<128, AKS, BKS>, SYM, TERMS, KIND, TO>(a, s);
+  return launch_tile<Tile<128, AKS, BKS, TERMS>, SYM, KIND, TO>(a, s);
 }
 
 int terms_of(const OrthArgs& a) { return a.bf16 && (a.m < a.n ? a.m : a.n) > kOneTerm ? 1 : 2; }
+
+// Most bytes of part sums: a round's tiles, of 256 rows one per CU.
+constexpr size_t kSumBytes = (size_t)kCus * 256 * 256 * sizeof(float);
 
 // Pieces of the workspace.
 struct Layout {
   int64_t rows, cols, side;  // padded
   int blocks;                // partial sums per matrix
-  size_t partial, first, x[2], sq[3], bytes;
+  size_t partial, first, sums, x[2], sq[3], bytes;
 };
 Layout layout_of(const OrthArgs& a) {
   Layout l;
@@ -635,6 +760,7 @@ Layout layout_of(const OrthArgs& a) {
   };
   l.partial = take((size_t)a.E * l.blocks * sizeof(double));
   l.first = take((size_t)a.E * sizeof(float));
+  l.sums = take(kSumBytes);
   const size_t x = (size_t)a.E * l.rows * l.cols * terms * 2, sq = (size_t)a.E * l.side * l.side * terms * 2;
   for (int i = 0; i < 2; ++i) l.x[i] = i == 0 || a.steps > 2 ? take(x) : 0;
   for (int i = 0; i < 3; ++i) l.sq[i] = i < 2 || a.steps > 1 ? take(sq) : 0;
@@ -647,6 +773,7 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
   const Layout l = layout_of(a);
   double* partial = reinterpret_cast<double*>(a.ws + l.partial);
   float* first = reinterpret_cast<float*>(a.ws + l.first);
+  float* sums = reinterpret_cast<float*>(a.ws + l.sums);
   const bool tall = a.m > a.n;
   auto aligned16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   const bool aligned_in = aligned16(a.g) && aligned16(a.momentum);
@@ -676,6 +803,7 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
     r.b = square(v ? v : u);
     r.K = r.rows = r.cols = l.side;
     r.E = a.E;
+    r.sums = sums;
     r.d = d;
     r.d_plane = sq_plane;
     r.f = v ? 1.f : a.c;
@@ -693,6 +821,7 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
     r.K = tall ? l.rows : l.cols;
     r.rows = r.cols = l.side;
     r.E = a.E;
+    r.sums = sums;
     r.d = A;
     r.d_plane = sq_plane;
     r.first = first;
@@ -718,6 +847,7 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
     g.rows = l.rows;
     g.cols = l.cols;
     g.E = a.E;
+    g.sums = sums;
     g.first = first;
     g.power = begin ? 1 : 0;
     if (last) {
