@@ -141,8 +141,26 @@ __device__ __forceinline__ void split(float v, f16& hi, f16& lo) {
   lo = (f16)((v - (float)hi) * 2048.f);
 }
 
-// u 2^p in fp16 terms, padded with zeros to rows x cols, and first[e] = 2^-p / (|u| + eps).
-// scale: about what X's values are to be multiplied by.
+// How a matrix of norm `norm` (eps included) is brought to values of X times about `scale`: by 2^p,
+// and X = first times that. A norm that is not finite: no value of the result is.
+struct Scale {
+  double by;
+  float first;
+  __device__ __forceinline__ Scale(double norm, double scale) {
+    int p = 0;
+    first = __builtin_nanf("");
+    if (norm == 0.0) {
+      first = 0.f;
+    } else if (norm < __builtin_huge_val()) {
+      frexp(scale / norm, &p);
+      --p;
+      first = (float)(ldexp(1.0, -p) / norm);
+    }
+    by = ldexp(1.0, p);
+  }
+};
+
+// u 2^p in fp16 terms, padded with zeros to rows x cols, and each matrix's Scale::first.
 template <typename TI, int TERMS>
 __global__ __launch_bounds__(256) void scale_kernel(OrthArgs a, bool vec, const double* partial, int blocks,
                                                     double scale, f16* x, int64_t rows, int64_t cols,
@@ -150,18 +168,8 @@ __global__ __launch_bounds__(256) void scale_kernel(OrthArgs a, bool vec, const 
   __shared__ double sh[4];
   const int e = blockIdx.y;
   const double sq = block_sum((int)threadIdx.x < blocks ? partial[(int64_t)e * blocks + threadIdx.x] : 0.0, sh);
-  const double norm = sqrt(sq) + (double)a.eps;
-  int p = 0;
-  float t0 = __builtin_nanf("");  // a value that is not finite: no value of the result is
-  if (norm == 0.0) {
-    t0 = 0.f;
-  } else if (norm < __builtin_huge_val()) {
-    frexp(scale / norm, &p);
-    --p;
-    t0 = (float)(ldexp(1.0, -p) / norm);
-  }
-  if (blockIdx.x == 0 && threadIdx.x == 0) first[e] = t0;
-  const double by = ldexp(1.0, p);
+  const Scale sc(sqrt(sq) + (double)a.eps, scale);
+  if (blockIdx.x == 0 && threadIdx.x == 0) first[e] = sc.first;
   const int64_t at = (int64_t)e * a.m * a.n, row_chunks = cols / 8, chunks = rows * row_chunks;
   const TI* g = static_cast<const TI*>(a.g) + at;
   const float* mom = a.momentum ? a.momentum + at : nullptr;
@@ -183,7 +191,7 @@ __global__ __launch_bounds__(256) void scale_kernel(OrthArgs a, bool vec, const 
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       f16 h, l;
-      split((float)((double)u[k] * by), h, l);
+      split((float)((double)u[k] * sc.by), h, l);
       hi[k] = h;
       lo[k] = l;
     }
@@ -319,6 +327,8 @@ struct Step {
                     : st + G::TERMS * G::A::BYTES + t * G::B::BYTES + (ld.wave * G::B::PW + l) * 1024;
     __builtin_amdgcn_global_load_lds(p, (lds_void*)to, 16, 0, 0);
   }
+  // IDLE: a wave without values of the tile only loads (and reads the next item's first fragments).
+  template <bool IDLE>
   static __device__ __forceinline__ void run(char* const (&ring)[kStages], const Loader<G>& ld, const char* ra,
                                              const char* rb, Wave<G>& w, Frags<G>& Fc, Frags<G>& Fn) {
     __builtin_amdgcn_sched_barrier(0);
@@ -329,9 +339,13 @@ struct Step {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
 #pragma unroll
-      for (int m = NM * g / NG; m < NM * (g + 1) / NG; ++m) w.mfma(m, Fc);
+      for (int m = NM * g / NG; m < NM * (g + 1) / NG; ++m) {
+        if constexpr (!IDLE) w.mfma(m, Fc);
+      }
 #pragma unroll
-      for (int r = NR * g / NG; r < NR * (g + 1) / NG; ++r) w.read(r, ring[(J + 1) % kStages], Fn);
+      for (int r = NR * g / NG; r < NR * (g + 1) / NG; ++r) {
+        if constexpr (!IDLE || J == kStages - 1) w.read(r, ring[(J + 1) % kStages], Fn);
+      }
       load(ld, g, ra, rb, ring[J]);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -423,6 +437,14 @@ __device__ __forceinline__ void make_loader(const ProductArgs& a, const Item& t,
   side(typename G::B{}, a.b, t.j * G::BM, a.cols, ld.b, ld.vb, ld.sb);
 }
 
+// A wave whose quarter of the tile lies past the matrix (256-row tiles), or above the diagonal of
+// a symmetric one: that quarter is the transpose of another wave's.
+template <class G, bool SYM>
+__device__ __forceinline__ bool idle(const ProductArgs& a, const Item& t, int wm, int wn) {
+  const int m0 = t.i * G::BM + wm * G::WM, n0 = t.j * G::BM + wn * G::WM;
+  return m0 >= a.rows || n0 >= a.cols || (SYM && m0 < n0);
+}
+
 // The values of a chunk of 8 in fp16 terms.
 template <int TERMS>
 struct Terms {
@@ -463,9 +485,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
   auto fetch = [&](int pass) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      // (256-row tiles: past the end the last row or chunk again)
-      const int64_t row = min(row_of(pass, i), a.rows - 1), col = min(col_of(pass), a.cols - 8);
-      old[KIND == kPolynomial ? pass % 2 : 0][i].load(a.c, t.e, row, col);
+      old[KIND == kPolynomial ? pass % 2 : 0][i].load(a.c, t.e, row_of(pass, i), col_of(pass));
     }
   };
   if constexpr (KIND == kPolynomial) fetch(0);
@@ -521,14 +541,13 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
           hi[i][k] = h;
           lo[i][k] = l;
         }
-        if (G::BM > kPad && (gr >= a.rows || gc >= a.cols)) continue;
         f16* d = a.d + (t.e * a.rows + gr) * a.cols + gc;
         *reinterpret_cast<f16x8*>(d) = hi[i];
         if constexpr (TERMS == 2) *reinterpret_cast<f16x8*>(d + a.d_plane) = lo[i];
       }
     }
     if constexpr (SYM && KIND != kLast) {
-      if (t.i != t.j) {
+      if (m0 != n0) {
         // [32 rows][columns] of fp16, chunk c of a row at c ^ swz(row), and out of there in columns
         // by transposing reads: 16 columns at a time, lane l with rows 8 (l / 16) .. + 7 of column l % 16
         auto swz = [](int row) { return ((0xCA60 >> (4 * (row & 3))) & 15) % PER; };
@@ -547,7 +566,6 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
             const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * COLS * 2));
             const s16x8 v{v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
             const int64_t gr = n0 + pass % (G::MB / BLOCKS) * COLS + 16 * i + (ln & 15), gc = m0 + mb * 32 + 8 * (ln >> 4);
-            if (G::BM > kPad && (gr >= a.rows || gc >= a.cols)) continue;
             st16(a.d + (t.e * a.rows + gr) * a.cols + gc + term * a.d_plane, __builtin_bit_cast(u32x4, v));
           }
         }
@@ -625,25 +643,32 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs a) {
     at += slots;
     const bool more = at < items;
     if (more) t = share.locate(a, xcd, at);
-#define MOE_TURN(RA, RB)                                      \
-  {                                                           \
-    const char *const ra = (RA), *const rb = (RB);            \
-    Step<G, 0>::run(ring, ld, ra, rb, w, F0, F1);             \
-    Step<G, 1>::run(ring, ld, ra, rb, w, F1, F0);             \
-    Step<G, 2>::run(ring, ld, ra, rb, w, F0, F1);             \
-    Step<G, 3>::run(ring, ld, ra, rb, w, F1, F0);             \
+#define MOE_TURN(IDLE, RA, RB)                                         \
+  {                                                                    \
+    const char *const ra = (RA), *const rb = (RB);                     \
+    Step<G, 0>::template run<IDLE>(ring, ld, ra, rb, w, F0, F1);       \
+    Step<G, 1>::template run<IDLE>(ring, ld, ra, rb, w, F1, F0);       \
+    Step<G, 2>::template run<IDLE>(ring, ld, ra, rb, w, F0, F1);       \
+    Step<G, 3>::template run<IDLE>(ring, ld, ra, rb, w, F1, F0);       \
   }
-    for (int u = 1; u < cur.u1 - cur.u0; ++u) {
-      MOE_TURN(ld.a + u * kStages * ld.sa, ld.b + u * kStages * ld.sb);
-      w.flush(false);
-    }
     // the last turn loads the next item's first (without one, this item's, never used)
-    if (more) make_loader<G>(a, t, ln, ld);
-    MOE_TURN(ld.a, ld.b);
+    if (idle<G, SYM>(a, cur, wm, wn)) {
+      for (int u = 1; u < cur.u1 - cur.u0; ++u)
+        MOE_TURN(true, ld.a + u * kStages * ld.sa, ld.b + u * kStages * ld.sb);
+      if (more) make_loader<G>(a, t, ln, ld);
+      MOE_TURN(true, ld.a, ld.b);
+    } else {
+      for (int u = 1; u < cur.u1 - cur.u0; ++u) {
+        MOE_TURN(false, ld.a + u * kStages * ld.sa, ld.b + u * kStages * ld.sb);
+        w.flush(false);
+      }
+      if (more) make_loader<G>(a, t, ln, ld);
+      MOE_TURN(false, ld.a, ld.b);
+      w.flush(true);
+      if (cur.part >= 0) put_part<G>(a, cur.part, wave, ln, w);
+      else store_tile<G, SYM, KIND, TO>(a, cur, wm, wn, ln, outs + wave * G::OUT_BYTES, w);
+    }
 #undef MOE_TURN
-    w.flush(true);
-    if (cur.part >= 0) put_part<G>(a, cur.part, wave, ln, w);
-    else store_tile<G, SYM, KIND, TO>(a, cur, wm, wn, ln, outs + wave * G::OUT_BYTES, w);
     if (!more) break;
   }
   wait_vmcnt<0>();  // the loads that nobody reads have landed before the LDS is given back
@@ -658,6 +683,7 @@ __global__ __launch_bounds__(64, 1) void join_kernel(ProductArgs a) {
   const Share<G, SYM> share(a, xcd);
   if (a.whole + tile >= share.n) return;
   const Item t = share.locate(a, xcd, a.whole + tile * a.parts);
+  if (idle<G, SYM>(a, t, wave / 2, wave % 2)) return;
   Wave<G> w;
   w.clear();
   for (int i = 0; i < a.parts; ++i) {
@@ -674,6 +700,273 @@ __global__ __launch_bounds__(64, 1) void join_kernel(ProductArgs a) {
         }
   }
   store_tile<G, SYM, KIND, TO>(a, t, wave / 2, wave % 2, ln, buf, w);
+}
+
+// ---- small matrices --------------------------------------------------------------------
+// Products of matrices that stay in LDS, by one workgroup of eight waves per matrix: what a launch
+// of its own for every product costs (5 us where nothing else counts) would be most of their time.
+
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
+
+// A matrix in two fp16 terms in LDS, rows of `row` bytes (a multiple of 128). 16-byte chunk c of a
+// row lies at c ^ swz(row): free of bank conflicts for 32 rows' chunks as for transposing reads.
+struct InLds {
+  char* hi;
+  char* lo;
+  int row;
+  static __device__ __forceinline__ int swz(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+  __device__ __forceinline__ int at(int r, int c) const { return r * row + (((c >> 3) ^ swz(r)) << 4) + (c & 7) * 2; }
+  // fragment of 32 rows from x0, columns k0 .. k0 + 15 of the summed axis
+  static __device__ __forceinline__ f16x8 rows(const char* p, const InLds& m, int x0, int k0, int ln) {
+    return *reinterpret_cast<const f16x8*>(p + m.at(x0 + (ln & 31), k0 + 8 * (ln >> 5)));
+  }
+  // fragment of 32 columns from x0, rows k0 .. k0 + 15 of the summed axis
+  static __device__ __forceinline__ f16x8 columns(const char* p, const InLds& m, int x0, int k0, int ln) {
+    const int g = ln >> 4, k = k0 + 8 * (g >> 1) + ((ln & 15) >> 2), n = x0 + 16 * (g & 1) + 4 * (ln & 3);
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + m.at(k, n)));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + m.at(k + 4, n)));
+    return __builtin_bit_cast(f16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+  }
+  // four values of row r from column c (a multiple of 4)
+  __device__ __forceinline__ void put(int r, int c, const float (&v)[4]) const {
+    f16x4 h, l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f16 a, b;
+      split(v[i], a, b);
+      h[i] = a;
+      l[i] = b;
+    }
+    *reinterpret_cast<f16x4*>(hi + at(r, c)) = h;
+    *reinterpret_cast<f16x4*>(lo + at(r, c)) = l;
+  }
+  __device__ __forceinline__ void get(int r, int c, float (&v)[4]) const {
+    const f16x4 h = *reinterpret_cast<const f16x4*>(hi + at(r, c)), l = *reinterpret_cast<const f16x4*>(lo + at(r, c));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)h[i] + kLo * (float)l[i];
+  }
+};
+
+// Block of 32 rows of A from i0 and 32 columns from j0 of A B^T (or, COLUMNS, A B) over K: value
+// 4 q + t of lane l is row l % 32, column 8 q + 4 (l / 32) + t.
+template <bool COLUMNS>
+__device__ __forceinline__ f32x16 lds_block(const InLds& A, const InLds& B, int i0, int j0, int K, int lane) {
+  const int ln = here(lane);
+  f32x16 sum = {}, cross = {};
+  for (int k1 = 0; k1 < K; k1 += 64) {  // (sums of hi hi of 64 terms, as in the tiles above)
+    f32x16 acc = {};
+#pragma unroll
+    for (int k = 0; k < 64; k += 16) {
+      const f16x8 ah = InLds::rows(A.hi, A, i0, k1 + k, ln), al = InLds::rows(A.lo, A, i0, k1 + k, ln);
+      f16x8 bh, bl;
+      if constexpr (COLUMNS) {
+        bh = InLds::columns(B.hi, B, j0, k1 + k, ln);
+        bl = InLds::columns(B.lo, B, j0, k1 + k, ln);
+      } else {
+        bh = InLds::rows(B.hi, B, j0, k1 + k, ln);
+        bl = InLds::rows(B.lo, B, j0, k1 + k, ln);
+      }
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(bh, ah, acc, 0, 0, 0);
+      cross = __builtin_amdgcn_mfma_f32_32x32x16_f16(bh, al, cross, 0, 0, 0);
+      cross = __builtin_amdgcn_mfma_f32_32x32x16_f16(bl, ah, cross, 0, 0, 0);
+    }
+    sum += acc;
+  }
+  return sum + kLo * cross;
+}
+
+// d = u v, or a I + b u + c u^2 (POLY), of SIDE x SIDE symmetric matrices that commute; d may be u or v.
+// All waves call it; it ends with d whole.
+template <int SIDE, bool POLY>
+__device__ __forceinline__ void lds_square(const OrthArgs& a, const InLds& u, const InLds& v, const InLds& d, int wave,
+                                           int ln) {
+  constexpr int BLOCKS = SIDE * SIDE / 1024, EACH = BLOCKS >= kWaves ? BLOCKS / kWaves : 1;
+  f32x16 r[EACH];
+  float old[POLY ? EACH : 1][4][4];
+  const bool mine = wave * EACH < BLOCKS;
+  const int i0 = wave * EACH / (SIDE / 32) * 32;
+  auto j0 = [&](int n) { return (wave * EACH + n) % (SIDE / 32) * 32; };
+  const int row = i0 + (ln & 31), col = 4 * (ln >> 5);
+  if (mine) {
+#pragma unroll
+    for (int n = 0; n < EACH; ++n) {
+      r[n] = lds_block<false>(u, v, i0, j0(n), SIDE, ln);
+      if constexpr (POLY) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) u.get(row, j0(n) + 8 * q + col, old[n][q]);
+      }
+    }
+  }
+  __syncthreads();  // (everyone has read what d is written over)
+  if (mine) {
+#pragma unroll
+    for (int n = 0; n < EACH; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float w[4];
+        const int c = j0(n) + 8 * q + col;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          w[t] = r[n][4 * q + t];
+          if constexpr (POLY) w[t] = a.c * w[t] + a.b * old[n][q][t] + (row == c + t ? a.a : 0.f);
+        }
+        d.put(row, c, w);
+      }
+  }
+  __syncthreads();
+}
+
+// Everything between a Gram matrix A and what X is multiplied by: P, or with `two` P' P. A and the
+// result in global memory, [side][side] in two terms; SIDE: what of it is not zero.
+template <int SIDE>
+__global__ __launch_bounds__(kThreads) void polynomial_kernel(OrthArgs a, bool two, const f16* A, f16* out, int side,
+                                                              int64_t plane) {
+  __shared__ __attribute__((aligned(1024))) char lds[2][2][SIDE * SIDE * 2];
+  const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const InLds U{lds[0][0], lds[0][1], SIDE * 2}, P{lds[1][0], lds[1][1], SIDE * 2};
+  const int64_t at = (int64_t)blockIdx.x * side * side;
+  constexpr int CHUNKS = SIDE / 8;
+#pragma unroll
+  for (int i = threadIdx.x; i < SIDE * CHUNKS; i += kThreads) {
+    const int r = i / CHUNKS, c = i % CHUNKS * 8;
+    *reinterpret_cast<u32x4*>(U.hi + U.at(r, c)) = ld16(A + at + (int64_t)r * side + c);
+    *reinterpret_cast<u32x4*>(U.lo + U.at(r, c)) = ld16(A + plane + at + (int64_t)r * side + c);
+  }
+  __syncthreads();
+  lds_square<SIDE, true>(a, U, U, P, wave, ln);
+  if (two) {
+    lds_square<SIDE, false>(a, P, U, U, wave, ln);
+    lds_square<SIDE, false>(a, P, U, U, wave, ln);  // A'
+    lds_square<SIDE, true>(a, U, U, U, wave, ln);   // P'
+    lds_square<SIDE, false>(a, U, P, P, wave, ln);
+  }
+  for (int i = threadIdx.x; i < side * (side / 8); i += kThreads) {
+    const int r = i / (side / 8), c = i % (side / 8) * 8;
+    const bool in = r < SIDE && c < SIDE;
+    const u32x4 zero = {0, 0, 0, 0};
+    st16(out + at + (int64_t)r * side + c, in ? *reinterpret_cast<const u32x4*>(P.hi + P.at(r, c)) : zero);
+    st16(out + plane + at + (int64_t)r * side + c, in ? *reinterpret_cast<const u32x4*>(P.lo + P.at(r, c)) : zero);
+  }
+}
+
+// The whole of it for matrices of at most 64 x 384: X and the square matrices in LDS.
+constexpr int kSmallSide = 64, kSmallLong = 384;
+template <typename TI>
+__global__ __launch_bounds__(kThreads) void small_kernel(OrthArgs a, double scale) {
+  __shared__ __attribute__((aligned(1024))) char xs[2][kSmallSide * kSmallLong * 2];
+  __shared__ __attribute__((aligned(1024))) char sq[3][2][kSmallSide * kSmallSide * 2];
+  __shared__ double sums[kWaves];
+  const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = (int)a.m, n = (int)a.n, size = m * n, l = (max(m, n) + 63) / 64 * 64;
+  const bool tall = m > n;
+  const int64_t at = (int64_t)blockIdx.x * size;
+  const TI* g = static_cast<const TI*>(a.g) + at;
+  TI* out = static_cast<TI*>(a.out) + at;
+  float* mom = a.momentum ? a.momentum + at : nullptr;
+  const InLds X{xs[0], xs[1], l * 2};
+  const InLds A{sq[0][0], sq[0][1], kSmallSide * 2}, P{sq[1][0], sq[1][1], kSmallSide * 2},
+      Y{sq[2][0], sq[2][1], kSmallSide * 2};
+
+  double sum = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < size; i += kThreads) {
+    float u = (float)g[i];
+    if (mom) {
+      const float v = momentum_of(a, mom[i], u);
+      mom[i] = v;
+      u = update_of(a, v, u);
+    }
+    sum += (double)u * (double)u;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  if (ln == 0) sums[wave] = sum;
+  for (int i = threadIdx.x; i < 2 * kSmallSide * l / 8; i += kThreads)
+    *reinterpret_cast<u32x4*>((i < kSmallSide * l / 8 ? X.hi + i * 16 : X.lo + (i - kSmallSide * l / 8) * 16)) =
+        u32x4{0, 0, 0, 0};
+  __syncthreads();
+  sum = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) sum += sums[i];
+  const Scale sc(sqrt(sum) + (double)a.eps, scale);
+  for (int i = threadIdx.x, r = i / n, c = i - r * n; i < size; i += kThreads) {
+    float u = (float)g[i];
+    if (mom) u = update_of(a, mom[i], u);
+    f16 h, lo;
+    split((float)((double)u * sc.by), h, lo);
+    const int to = tall ? X.at(c, r) : X.at(r, c);
+    *reinterpret_cast<f16*>(X.hi + to) = h;
+    *reinterpret_cast<f16*>(X.lo + to) = lo;
+    r += kThreads / n;
+    c += kThreads % n;
+    if (c >= n) {
+      c -= n;
+      ++r;
+    }
+  }
+  __syncthreads();
+
+  const float unit = (float)(1.0 / scale);
+  for (int done = 0; done < a.steps;) {
+    const bool begin = done == 0, two = a.steps - done >= 2;
+    const float t = begin ? sc.first : unit;  // X = t X^
+    if (wave < 4) {
+      const int i0 = wave / 2 * 32, j0 = wave % 2 * 32, row = here(ln) & 31, col = 4 * (here(ln) >> 5);
+      const f32x16 r = lds_block<false>(X, X, i0, j0, l, ln);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v[4] = {t * t * r[4 * q], t * t * r[4 * q + 1], t * t * r[4 * q + 2], t * t * r[4 * q + 3]};
+        A.put(i0 + row, j0 + 8 * q + col, v);
+      }
+    }
+    __syncthreads();
+    lds_square<kSmallSide, true>(a, A, A, P, wave, ln);
+    if (two) {
+      lds_square<kSmallSide, false>(a, P, A, Y, wave, ln);
+      lds_square<kSmallSide, false>(a, P, Y, A, wave, ln);  // A'
+      lds_square<kSmallSide, true>(a, A, A, Y, wave, ln);   // P'
+      lds_square<kSmallSide, false>(a, Y, P, P, wave, ln);
+    }
+    done += two ? 2 : 1;
+    const bool last = done == a.steps;
+    const float f = last ? t : begin ? t * (float)scale : 1.f;
+    // block columns wave, wave + 8, .. of X, both block rows of each
+    const int row = here(ln) & 31, col = 4 * (here(ln) >> 5);
+    constexpr int EACH = (kSmallLong / 32 + kWaves - 1) / kWaves;
+    f32x16 r[EACH][2];
+#pragma unroll
+    for (int b = 0; b < EACH; ++b) {
+      const int j0 = (wave + b * kWaves) * 32;
+      if (j0 >= l) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) r[b][i] = f * lds_block<true>(P, X, i * 32, j0, kSmallSide, ln);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < EACH; ++b) {
+      const int j0 = (wave + b * kWaves) * 32;
+      if (j0 >= l) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int x = i * 32 + row, y = j0 + 8 * q + col;
+          float v[4] = {r[b][i][4 * q], r[b][i][4 * q + 1], r[b][i][4 * q + 2], r[b][i][4 * q + 3]};
+          if (!last) {
+            X.put(x, y, v);
+            continue;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int gr = tall ? y + k : x, gc = tall ? x : y + k;
+            if (gr >= m || gc >= n) continue;
+            TI* o = out + gr * n + gc;
+            *o = (TI)(a.momentum ? a.keep * (float)*o - a.rate * v[k] : v[k]);
+          }
+        }
+    }
+    __syncthreads();
+  }
 }
 
 // ---- host ------------------------------------------------------------------------------
@@ -738,6 +1031,10 @@ int terms_of(const OrthArgs& a) { return a.bf16 && (a.m < a.n ? a.m : a.n) > kOn
 // Most bytes of part sums: a round's tiles, of 256 rows one per CU.
 constexpr size_t kSumBytes = (size_t)kCus * 256 * 256 * sizeof(float);
 
+bool is_small(const OrthArgs& a) {
+  return (a.m <= kSmallSide || a.n <= kSmallSide) && a.m <= kSmallLong && a.n <= kSmallLong;
+}
+
 // Pieces of the workspace.
 struct Layout {
   int64_t rows, cols, side;  // padded
@@ -784,6 +1081,10 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
   // 2^k near the square root of the long side: X's values are of order 1 / sqrt(long side) at the end
   double scale = 1;
   while (scale * scale < (double)(a.m > a.n ? a.m : a.n)) scale *= 2;
+  if (is_small(a)) {
+    small_kernel<TI><<<a.E, kThreads, 0, s>>>(a, scale);
+    return hipGetLastError();
+  }
 
   square_kernel<TI><<<dim3(l.blocks, a.E), 256, 0, s>>>(a, aligned_in && a.m * a.n % 8 == 0, partial);
   hipError_t e = hipGetLastError();
@@ -828,9 +1129,18 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
     r.power = begin ? 2 : 0;
     r.f = begin ? 1.f : unit * unit;
     e = tall ? product<true, true, true, TERMS, kProduct, f16>(r, s) : product<false, false, true, TERMS, kProduct, f16>(r, s);
-    if (e == hipSuccess) e = symmetric(A, nullptr, P);
     const f16* Q = P;
-    if (two) {
+    if (l.side == kPad && TERMS == 2) {
+      if (e != hipSuccess) return e;
+      if ((tall ? a.n : a.m) <= 64)
+        polynomial_kernel<64><<<a.E, kThreads, 0, s>>>(a, two, A, P, kPad, sq_plane);
+      else
+        polynomial_kernel<kPad><<<a.E, kThreads, 0, s>>>(a, two, A, P, kPad, sq_plane);
+      e = hipGetLastError();
+    } else if (e == hipSuccess) {
+      e = symmetric(A, nullptr, P);
+    }
+    if (two && !(l.side == kPad && TERMS == 2)) {
       if (e == hipSuccess) e = symmetric(P, A, Y);
       if (e == hipSuccess) e = symmetric(P, Y, A);        // A'
       if (e == hipSuccess) e = symmetric(A, nullptr, Y);  // P'
