@@ -511,16 +511,16 @@ moe_status moe_layer_norm_backward(const moe_layer_norm_shape* shape, const void
  * its singular vectors.
  * Products are taken on the matrix cores in fp16 with fp32 sums, the matrices scaled so that
  * their values lie in fp16's range. What passes from one product to the next is, for
- *   bf16 matrices whose sides are both over 512, rounded to fp16 (2^-11 of a value at most). A
+ *   bf16 matrices whose sides are both over 128, rounded to fp16 (2^-11 of a value at most). A
  *     step multiplies small singular values by up to a, and with them what was rounded before
- *     it: matrices of full rank come out within about 2e-3 of their norm (and half a bf16 step),
- *     those of a rank r far below their sides within 0.15 / sqrt(r);
+ *     it: matrices of full rank come out within about 2e-3 of their norm, less than half a bf16
+ *     step of every value, those of a rank far below their sides within 2e-2;
  *   others, kept as two fp16 terms (22 bits), three products for one: as in fp32.
  * The coefficients are expected to keep the singular values below about 8 (beyond that a value may
  * leave fp16's range and come out infinite), and a not to be small beside b and c: a X carries the
- * small singular values, for which A is not kept to a relative precision. A matrix of zeros gives zeros; one that holds a value
- * that is not finite gives no finite ones; the others are not affected. Each matrix's scale is
- * found first, in fp64, so that every finite fp32 matrix has one. */
+ * small singular values, for which A is not kept to a relative precision. A matrix of zeros gives
+ * zeros; one that holds a value that is not finite gives no finite ones; the others are not
+ * affected. Each matrix's scale is found first, in fp64, so that every finite fp32 matrix has one. */
 typedef struct moe_orthogonalize_shape {
   int64_t m, n;      /* sides: 1 .. 2^18, the shorter one at most 16384 */
   int32_t E;         /* matrices, 1 .. 64 */

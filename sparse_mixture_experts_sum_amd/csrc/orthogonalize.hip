@@ -10,9 +10,13 @@
 // by itself would cancel where P is small, at the large singular values.
 //
 // Products: one workgroup of four waves per square tile, v_mfma_f32_32x32x16_f16, stages of 32 of the
-// summed axis through a ring of four LDS buffers, tile after tile as one stream (matmul_tile.h says
-// how operands lie in LDS). All matrices of the iteration are padded with zeros to multiples of
-// 128, so that a sum is a whole number of ring turns and no value of an operand has to be masked.
+// summed axis through a ring of four LDS buffers, tile after tile as one stream. All matrices of the
+// iteration are padded with zeros to multiples of 128, so that a sum is a whole number of ring turns
+// and no value of an operand has to be masked.
+// They are kept in panels of 32 columns, [columns / 32][rows][32]: what a load instruction of a stage
+// takes (16 rows of 64 bytes) is then one run of 1 KB of whole cache lines, whichever axis of the
+// matrix is summed over, and so is what a store leaves. With rows as they are, half lines, the L2s
+// gave a CU no more than the half (1.05 TB/s an XCD), and that bound the products.
 // Tiles that would leave most CUs without one in the last round have their sums in parts,
 // which a second kernel joins in order.
 //
@@ -44,7 +48,12 @@ constexpr int kColBlock = 4;        // columns of tiles walked together
 constexpr float kLo = 1.0f / 2048;  // scale of the second term
 constexpr int kNormBlocks = 256;    // most partial sums of a matrix's squares
 constexpr int kMaxParts = 16;       // of a product's sum
-constexpr int kOneTerm = 512;       // bf16 matrices with short sides past it are kept in one term
+constexpr int kOneTerm = 128;       // bf16 matrices with short sides past it are kept in one term
+
+// Place of a value of a matrix of the iteration: panels of 32 columns, each with all rows.
+__device__ __forceinline__ int64_t in_panels(int64_t rows, int64_t r, int64_t c) {
+  return ((c >> 5) * rows + r) * 32 + (c & 31);
+}
 
 // ---- the matrix in, and its norm -------------------------------------------------------
 // u, what is orthogonalised: g, or its momentum step, from g and the momentum before
@@ -160,7 +169,8 @@ struct Scale {
   }
 };
 
-// u 2^p in fp16 terms, padded with zeros to rows x cols, and each matrix's Scale::first.
+// u 2^p in fp16 terms, padded with zeros to rows x cols and in panels of 32 columns, and each matrix's
+// Scale::first. Eight threads take 64 columns of a row: whole lines of g, half lines of two panels.
 template <typename TI, int TERMS>
 __global__ __launch_bounds__(256) void scale_kernel(OrthArgs a, bool vec, const double* partial, int blocks,
                                                     double scale, f16* x, int64_t rows, int64_t cols,
@@ -170,12 +180,13 @@ __global__ __launch_bounds__(256) void scale_kernel(OrthArgs a, bool vec, const 
   const double sq = block_sum((int)threadIdx.x < blocks ? partial[(int64_t)e * blocks + threadIdx.x] : 0.0, sh);
   const Scale sc(sqrt(sq) + (double)a.eps, scale);
   if (blockIdx.x == 0 && threadIdx.x == 0) first[e] = sc.first;
-  const int64_t at = (int64_t)e * a.m * a.n, row_chunks = cols / 8, chunks = rows * row_chunks;
+  const int64_t at = (int64_t)e * a.m * a.n;
+  const uint32_t chunks = (uint32_t)rows * (uint32_t)(cols / 8), column = (uint32_t)rows * 8;  // (at most 2^31)
   const TI* g = static_cast<const TI*>(a.g) + at;
   const float* mom = a.momentum ? a.momentum + at : nullptr;
   f16* out = x + (int64_t)e * rows * cols;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / row_chunks, c = (i - r * row_chunks) * 8;
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < chunks; i += gridDim.x * 256) {
+    const int64_t r = i % column / 8, c = (int64_t)(i / column) * 64 + i % 8 * 8;
     const int n = r < a.m ? (int)max(min((int64_t)8, a.n - c), (int64_t)0) : 0;
     float u[8] = {};
     if (n > 0) {
@@ -195,24 +206,26 @@ __global__ __launch_bounds__(256) void scale_kernel(OrthArgs a, bool vec, const 
       hi[k] = h;
       lo[k] = l;
     }
-    *reinterpret_cast<f16x8*>(out + i * 8) = hi;
-    if constexpr (TERMS == 2) *reinterpret_cast<f16x8*>(out + plane + i * 8) = lo;
+    f16* to = out + in_panels(rows, r, c);
+    *reinterpret_cast<f16x8*>(to) = hi;
+    if constexpr (TERMS == 2) *reinterpret_cast<f16x8*>(to + plane) = lo;
   }
 }
 
 // ---- products --------------------------------------------------------------------------
-// d[i][j] = f sum_k A(i, k) B(j, k) (+ p c[i][j] + q I), f times first[e]^power, of E matrices. An
-// operand is K-contiguous ([i][k]) or K-strided ([k][i]). A matrix's fp16 terms are
-// `plane` values apart, its neighbours `mat` values.
+// Matrices of the iteration: rows x columns in panels, `mat` values each, their second terms
+// `plane` values behind the first ones.
 struct Operands {
   const f16* at;
   int64_t plane, mat;
-  int ld;
+  int rows;
 };
+// d[i][j] = f sum_k A(i, k) B(j, k) (+ p c[i][j] + q I), f times first[e]^power, of E matrices. An
+// operand is summed over its columns (A[i][k]) or over its rows (A[k][i]).
 struct ProductArgs {
   Operands a, b, c;
   int64_t K, rows, cols;  // padded
-  f16* d;                 // [rows][cols] in fp16 terms, or
+  f16* d;                 // rows x cols in fp16 terms, or
   int64_t d_plane;
   void* out;              // the result of the iteration, [m][n]
   int64_t m, n;
@@ -225,11 +238,47 @@ struct ProductArgs {
   float* sums;
 };
 
+// One operand's stage in LDS: X of its output axis by 32 of the summed axis, as rows of 64 bytes,
+// 16-byte chunk c of a row at c ^ swz(row): free of bank conflicts for both kinds of reads below. A
+// direct load instruction moves 16 rows, lane l into slot l.
+// Summed over columns (KS false): X rows of a panel. Summed over rows: 32 rows of each of X / 32 panels.
+template <bool KS_, int X_>
+struct Operand {
+  static constexpr bool KS = KS_;
+  static constexpr int X = X_, BYTES = X * 64, PW = BYTES / 1024 / 4;  // loads per wave and stage
+  static_assert(PW >= 1, "whole loads per wave");
+  static __device__ __forceinline__ int swz(int row) { return (row >> 2) & 3; }
+  // LDS row of load j of a wave for this lane, and the source chunk that goes into its slot
+  static __device__ __forceinline__ int row(int j, int wave, int ln) { return (wave * PW + j) * 16 + ln / 4; }
+  static __device__ __forceinline__ int chunk(int j, int wave, int ln) { return (ln % 4) ^ swz(row(j, wave, ln)); }
+  // byte offset of this lane's fragment of the 32 rows (columns) from x0 (substep 0)
+  static __device__ __forceinline__ int frag(int x0, int ln) {
+    if constexpr (!KS) {
+      const int m = x0 + (ln & 31);
+      return m * 64 + ((ln >> 5) ^ swz(m)) * 16;
+    } else {
+      const int g = ln >> 4, k = (g >> 1) * 8 + ((ln & 15) >> 2), n = (g & 1) * 16 + 4 * (ln & 3);
+      return (x0 + k) * 64 + ((n >> 3) ^ swz(k)) * 16 + ((n >> 2) & 1) * 8;
+    }
+  }
+  // The fragment of substep s, k = 16 s + 8 h .. + 7 (h = lane / 32); over rows by transposing reads.
+  static __device__ __forceinline__ u32x4 read(const char* st, int at, int s) {
+    if constexpr (!KS) {
+      return *reinterpret_cast<const u32x4*>(st + (at ^ (32 * s)));
+    } else {
+      // (swz of rows 4 on is that of these, which is even, and 1)
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(st + at + 1024 * s));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(st + (at ^ 16) + 256 + 1024 * s));
+      return __builtin_bit_cast(u32x4, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+    }
+  }
+};
+
 template <int BM_, bool AKS, bool BKS, int TERMS_>
 struct Tile {
   static constexpr int BM = BM_, BK = 32, TERMS = TERMS_;
-  typedef Operand<f16, AKS, BM, BK, 4> A;
-  typedef Operand<f16, BKS, BM, BK, 4> B;
+  typedef Operand<AKS, BM> A;
+  typedef Operand<BKS, BM> B;
   static constexpr int WM = BM / 2, MB = WM / 32, SUB = BK / 16;  // 2 x 2 waves
   // a stage: A's terms, then B's
   static constexpr int STAGE = TERMS * (A::BYTES + B::BYTES), LPS = TERMS * (A::PW + B::PW);
@@ -423,14 +472,15 @@ __device__ __forceinline__ void make_loader(const ProductArgs& a, const Item& t,
   const int ln = here(lane);
   auto side = [&](auto op, const Operands& o, int x0, int64_t size, const char*& base, uint32_t* v, int64_t& step) {
     typedef decltype(op) Op;
-    const int last = (int)size - 1 - x0;  // (256-row tiles: the last row or chunk again past the end)
-    step = (Op::KS ? (int64_t)o.ld : 1) * (G::BK * 2);
-    base = reinterpret_cast<const char*>(o.at + t.e * o.mat + (Op::KS ? (int64_t)x0 : (int64_t)x0 * o.ld)) +
+    const int last = (int)size - 1 - x0;  // (256-row tiles: the last row or panel again past the end)
+    step = Op::KS ? 32 * 64 : (int64_t)o.rows * 64;
+    base = reinterpret_cast<const char*>(o.at + t.e * o.mat + (Op::KS ? (int64_t)x0 * o.rows : (int64_t)x0 * 32)) +
            t.u0 * kStages * step;
 #pragma unroll
     for (int j = 0; j < Op::PW; ++j) {
-      const int row = Op::row(j, ld.wave, ln), chunk = Op::chunk(j, ld.wave, ln) * 8;
-      v[j] = Op::KS ? (uint32_t)(row * o.ld + min(chunk, last - 7)) * 2 : (uint32_t)(min(row, last) * o.ld + chunk) * 2;
+      const int row = Op::row(j, ld.wave, ln), chunk = Op::chunk(j, ld.wave, ln) * 16;
+      v[j] = Op::KS ? (uint32_t)(min(row >> 5, last >> 5) * o.rows + (row & 31)) * 64 + chunk
+                    : (uint32_t)min(row, last) * 64 + chunk;
     }
   };
   side(typename G::A{}, a.a, t.i * G::BM, a.rows, ld.a, ld.va, ld.sa);
@@ -450,7 +500,7 @@ template <int TERMS>
 struct Terms {
   u32x4 hi, lo;
   __device__ __forceinline__ void load(const Operands& o, int e, int64_t row, int64_t col) {
-    const f16* p = o.at + e * o.mat + row * o.ld + col;
+    const f16* p = o.at + e * o.mat + in_panels(o.rows, row, col);
     hi = ld16(p);
     if constexpr (TERMS == 2) lo = ld16(p + o.plane);
   }
@@ -468,12 +518,18 @@ enum { kProduct, kPolynomial, kLast };  // f S; f S + p c + q I; the result
 // 32 rows at a time go through a piece of LDS of the wave's own (16-byte chunk c of a row at
 // c ^ (row % chunks)) and leave as whole row segments; c's values are loaded a pass ahead.
 // The transposed tile leaves by the same piece of LDS, column by column.
+// (only: that pass alone)
+template <class G>
+struct Passes {
+  static constexpr int SEG = G::OUT_BYTES / 32, CHUNKS = SEG / 16, COLS = SEG / 4, BLOCKS = COLS / 32;
+  static constexpr int PER = COLS / 8, RPS = 64 / PER, N = 32 / RPS, ALL = G::MB * (G::MB / BLOCKS);
+};
 template <class G, bool SYM, int KIND, typename TO>
 __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, int wm, int wn, int lane, char* buf,
-                                           const Wave<G>& w) {
-  constexpr int TERMS = G::TERMS;
-  constexpr int SEG = G::OUT_BYTES / 32, CHUNKS = SEG / 16, COLS = SEG / 4, BLOCKS = COLS / 32;
-  constexpr int PER = COLS / 8, RPS = 64 / PER, N = 32 / RPS, PASSES = G::MB * (G::MB / BLOCKS);
+                                           const Wave<G>& w, int only = -1) {
+  typedef Passes<G> S;
+  constexpr int TERMS = G::TERMS, SEG = S::SEG, CHUNKS = S::CHUNKS, COLS = S::COLS, BLOCKS = S::BLOCKS;
+  constexpr int PER = S::PER, RPS = S::RPS, N = S::N, PASSES = S::ALL;
   const int ln = here(lane);
   const int64_t m0 = (int64_t)t.i * G::BM + wm * G::WM, n0 = (int64_t)t.j * G::BM + wn * G::WM;
   float f = a.f;
@@ -488,13 +544,17 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
       old[KIND == kPolynomial ? pass % 2 : 0][i].load(a.c, t.e, row_of(pass, i), col_of(pass));
     }
   };
-  if constexpr (KIND == kPolynomial) fetch(0);
+  if constexpr (KIND == kPolynomial) {
+    if (only < 0) fetch(0);
+  }
 #pragma unroll
   for (int pass = 0; pass < PASSES; ++pass) {
+    if (only >= 0 && pass != only) continue;
     __builtin_amdgcn_sched_barrier(0);  // (one pass's registers at a time)
     const int mb = pass / (G::MB / BLOCKS), nb0 = pass % (G::MB / BLOCKS) * BLOCKS, r = ln & 31;
     if constexpr (KIND == kPolynomial) {
-      if (pass + 1 < PASSES) fetch(pass + 1);
+      if (only >= 0) fetch(pass);
+      else if (pass + 1 < PASSES) fetch(pass + 1);
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -541,7 +601,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
           hi[i][k] = h;
           lo[i][k] = l;
         }
-        f16* d = a.d + (t.e * a.rows + gr) * a.cols + gc;
+        f16* d = a.d + t.e * a.rows * a.cols + in_panels(a.rows, gr, gc);
         *reinterpret_cast<f16x8*>(d) = hi[i];
         if constexpr (TERMS == 2) *reinterpret_cast<f16x8*>(d + a.d_plane) = lo[i];
       }
@@ -566,7 +626,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
             const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * COLS * 2));
             const s16x8 v{v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
             const int64_t gr = n0 + pass % (G::MB / BLOCKS) * COLS + 16 * i + (ln & 15), gc = m0 + mb * 32 + 8 * (ln >> 4);
-            st16(a.d + (t.e * a.rows + gr) * a.cols + gc + term * a.d_plane, __builtin_bit_cast(u32x4, v));
+            st16(a.d + t.e * a.rows * a.cols + in_panels(a.rows, gr, gc) + term * a.d_plane, __builtin_bit_cast(u32x4, v));
           }
         }
       }
@@ -674,32 +734,48 @@ __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs a) {
   wait_vmcnt<0>();  // the loads that nobody reads have landed before the LDS is given back
 }
 
-// The sums of the tiles that are in parts, in order: a quarter of a tile (what one of the product's
-// waves holds) per workgroup.
+// The sums of the tiles that are in parts, in order: one pass of what one of the product's waves
+// holds of a tile per workgroup.
 template <class G, bool SYM, int KIND, typename TO>
 __global__ __launch_bounds__(64, 1) void join_kernel(ProductArgs a) {
+  typedef Passes<G> S;
   __shared__ __attribute__((aligned(1024))) char buf[G::OUT_BYTES];
-  const int wave = blockIdx.x % 4, tile = blockIdx.x / 4 / kXcds, xcd = blockIdx.x / 4 % kXcds, ln = threadIdx.x;
+  const int pass = blockIdx.x % S::ALL, quarter = blockIdx.x / S::ALL, ln = threadIdx.x;
+  const int wave = quarter % 4, tile = quarter / 4 / kXcds, xcd = quarter / 4 % kXcds;
   const Share<G, SYM> share(a, xcd);
   if (a.whole + tile >= share.n) return;
   const Item t = share.locate(a, xcd, a.whole + tile * a.parts);
   if (idle<G, SYM>(a, t, wave / 2, wave % 2)) return;
   Wave<G> w;
-  w.clear();
-  for (int i = 0; i < a.parts; ++i) {
-    const float* p = part_at<G>(a, t.part + i, wave, ln);
 #pragma unroll
-    for (int nb = 0; nb < G::MB; ++nb)
+  for (int p = 0; p < S::ALL; ++p) {
+    if (p != pass) continue;
+    constexpr int WIDE = G::MB / S::BLOCKS, AHEAD = 8;  // (parts in flight: each waits for memory)
+    f32x4 sum[S::BLOCKS * 4] = {};
+    for (int i = 0; i < a.parts; i += AHEAD) {
+      f32x4 v[AHEAD][S::BLOCKS * 4];
 #pragma unroll
-      for (int mb = 0; mb < G::MB; ++mb)
+      for (int h = 0; h < AHEAD; ++h) {
+        const float* from = part_at<G>(a, t.part + min(i + h, a.parts - 1), wave, ln);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4 v = *reinterpret_cast<const f32x4*>(p + ((nb * G::MB + mb) * 4 + q) * 256);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w.acc[nb][mb][4 * q + k] += v[k];
+        for (int k = 0; k < S::BLOCKS * 4; ++k) {
+          const int block = (p % WIDE * S::BLOCKS + k / 4) * G::MB + p / WIDE;
+          v[h][k] = *reinterpret_cast<const f32x4*>(from + (block * 4 + k % 4) * 256);
         }
+      }
+#pragma unroll
+      for (int h = 0; h < AHEAD; ++h) {
+        if (i + h >= a.parts) continue;
+#pragma unroll
+        for (int k = 0; k < S::BLOCKS * 4; ++k) sum[k] += v[h][k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < S::BLOCKS * 4; ++k)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) w.acc[p % WIDE * S::BLOCKS + k / 4][p / WIDE][k % 4 * 4 + x] = sum[k][x];
   }
-  store_tile<G, SYM, KIND, TO>(a, t, wave / 2, wave % 2, ln, buf, w);
+  store_tile<G, SYM, KIND, TO>(a, t, wave / 2, wave % 2, ln, buf, w, pass);
 }
 
 // ---- small matrices --------------------------------------------------------------------
@@ -747,32 +823,45 @@ struct InLds {
   }
 };
 
-// Block of 32 rows of A from i0 and 32 columns from j0 of A B^T (or, COLUMNS, A B) over K: value
-// 4 q + t of lane l is row l % 32, column 8 q + 4 (l / 32) + t.
-template <bool COLUMNS>
-__device__ __forceinline__ f32x16 lds_block(const InLds& A, const InLds& B, int i0, int j0, int K, int lane) {
+// N blocks of 32 rows of A from i0 and 32 columns from j0 on, of A B^T (or, COLUMNS, A B) over K:
+// value 4 q + t of lane l is row l % 32, column 8 q + 4 (l / 32) + t of a block.
+template <bool COLUMNS, int N>
+__device__ __forceinline__ void lds_blocks(const InLds& A, const InLds& B, int i0, int j0, int K, int lane,
+                                           f32x16 (&out)[N]) {
   const int ln = here(lane);
-  f32x16 sum = {}, cross = {};
+  f32x16 cross[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    out[n] = f32x16{};
+    cross[n] = f32x16{};
+  }
   for (int k1 = 0; k1 < K; k1 += 64) {  // (sums of hi hi of 64 terms, as in the tiles above)
-    f32x16 acc = {};
+    f32x16 acc[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) acc[n] = f32x16{};
 #pragma unroll
     for (int k = 0; k < 64; k += 16) {
       const f16x8 ah = InLds::rows(A.hi, A, i0, k1 + k, ln), al = InLds::rows(A.lo, A, i0, k1 + k, ln);
-      f16x8 bh, bl;
-      if constexpr (COLUMNS) {
-        bh = InLds::columns(B.hi, B, j0, k1 + k, ln);
-        bl = InLds::columns(B.lo, B, j0, k1 + k, ln);
-      } else {
-        bh = InLds::rows(B.hi, B, j0, k1 + k, ln);
-        bl = InLds::rows(B.lo, B, j0, k1 + k, ln);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        f16x8 bh, bl;
+        if constexpr (COLUMNS) {
+          bh = InLds::columns(B.hi, B, j0 + 32 * n, k1 + k, ln);
+          bl = InLds::columns(B.lo, B, j0 + 32 * n, k1 + k, ln);
+        } else {
+          bh = InLds::rows(B.hi, B, j0 + 32 * n, k1 + k, ln);
+          bl = InLds::rows(B.lo, B, j0 + 32 * n, k1 + k, ln);
+        }
+        acc[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bh, ah, acc[n], 0, 0, 0);
+        cross[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bh, al, cross[n], 0, 0, 0);
+        cross[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bl, ah, cross[n], 0, 0, 0);
       }
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(bh, ah, acc, 0, 0, 0);
-      cross = __builtin_amdgcn_mfma_f32_32x32x16_f16(bh, al, cross, 0, 0, 0);
-      cross = __builtin_amdgcn_mfma_f32_32x32x16_f16(bl, ah, cross, 0, 0, 0);
     }
-    sum += acc;
+#pragma unroll
+    for (int n = 0; n < N; ++n) out[n] += acc[n];
   }
-  return sum + kLo * cross;
+#pragma unroll
+  for (int n = 0; n < N; ++n) out[n] += kLo * cross[n];
 }
 
 // d = u v, or a I + b u + c u^2 (POLY), of SIDE x SIDE symmetric matrices that commute; d may be u or v.
@@ -788,9 +877,9 @@ __device__ __forceinline__ void lds_square(const OrthArgs& a, const InLds& u, co
   auto j0 = [&](int n) { return (wave * EACH + n) % (SIDE / 32) * 32; };
   const int row = i0 + (ln & 31), col = 4 * (ln >> 5);
   if (mine) {
+    lds_blocks<false>(u, v, i0, j0(0), SIDE, ln, r);
 #pragma unroll
     for (int n = 0; n < EACH; ++n) {
-      r[n] = lds_block<false>(u, v, i0, j0(n), SIDE, ln);
       if constexpr (POLY) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) u.get(row, j0(n) + 8 * q + col, old[n][q]);
@@ -817,7 +906,7 @@ __device__ __forceinline__ void lds_square(const OrthArgs& a, const InLds& u, co
 }
 
 // Everything between a Gram matrix A and what X is multiplied by: P, or with `two` P' P. A and the
-// result in global memory, [side][side] in two terms; SIDE: what of it is not zero.
+// result in global memory, side x side in two terms; SIDE: what of it is not zero.
 template <int SIDE>
 __global__ __launch_bounds__(kThreads) void polynomial_kernel(OrthArgs a, bool two, const f16* A, f16* out, int side,
                                                               int64_t plane) {
@@ -829,8 +918,8 @@ __global__ __launch_bounds__(kThreads) void polynomial_kernel(OrthArgs a, bool t
 #pragma unroll
   for (int i = threadIdx.x; i < SIDE * CHUNKS; i += kThreads) {
     const int r = i / CHUNKS, c = i % CHUNKS * 8;
-    *reinterpret_cast<u32x4*>(U.hi + U.at(r, c)) = ld16(A + at + (int64_t)r * side + c);
-    *reinterpret_cast<u32x4*>(U.lo + U.at(r, c)) = ld16(A + plane + at + (int64_t)r * side + c);
+    *reinterpret_cast<u32x4*>(U.hi + U.at(r, c)) = ld16(A + at + in_panels(side, r, c));
+    *reinterpret_cast<u32x4*>(U.lo + U.at(r, c)) = ld16(A + plane + at + in_panels(side, r, c));
   }
   __syncthreads();
   lds_square<SIDE, true>(a, U, U, P, wave, ln);
@@ -844,8 +933,8 @@ __global__ __launch_bounds__(kThreads) void polynomial_kernel(OrthArgs a, bool t
     const int r = i / (side / 8), c = i % (side / 8) * 8;
     const bool in = r < SIDE && c < SIDE;
     const u32x4 zero = {0, 0, 0, 0};
-    st16(out + at + (int64_t)r * side + c, in ? *reinterpret_cast<const u32x4*>(P.hi + P.at(r, c)) : zero);
-    st16(out + plane + at + (int64_t)r * side + c, in ? *reinterpret_cast<const u32x4*>(P.lo + P.at(r, c)) : zero);
+    st16(out + at + in_panels(side, r, c), in ? *reinterpret_cast<const u32x4*>(P.hi + P.at(r, c)) : zero);
+    st16(out + plane + at + in_panels(side, r, c), in ? *reinterpret_cast<const u32x4*>(P.lo + P.at(r, c)) : zero);
   }
 }
 
@@ -912,10 +1001,12 @@ __global__ __launch_bounds__(kThreads) void small_kernel(OrthArgs a, double scal
     const float t = begin ? sc.first : unit;  // X = t X^
     if (wave < 4) {
       const int i0 = wave / 2 * 32, j0 = wave % 2 * 32, row = here(ln) & 31, col = 4 * (here(ln) >> 5);
-      const f32x16 r = lds_block<false>(X, X, i0, j0, l, ln);
+      f32x16 r[1];
+      lds_blocks<false>(X, X, i0, j0, l, ln, r);
+      r[0] *= t * t;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float v[4] = {t * t * r[4 * q], t * t * r[4 * q + 1], t * t * r[4 * q + 2], t * t * r[4 * q + 3]};
+        const float v[4] = {r[0][4 * q], r[0][4 * q + 1], r[0][4 * q + 2], r[0][4 * q + 3]};
         A.put(i0 + row, j0 + 8 * q + col, v);
       }
     }
@@ -939,7 +1030,11 @@ __global__ __launch_bounds__(kThreads) void small_kernel(OrthArgs a, double scal
       const int j0 = (wave + b * kWaves) * 32;
       if (j0 >= l) continue;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) r[b][i] = f * lds_block<true>(P, X, i * 32, j0, kSmallSide, ln);
+      for (int i = 0; i < 2; ++i) {
+        f32x16 one[1];
+        lds_blocks<true>(P, X, i * 32, j0, kSmallSide, ln, one);
+        r[b][i] = f * one[0];
+      }
     }
     __syncthreads();
 #pragma unroll
@@ -978,25 +1073,36 @@ int64_t tiles_of(const ProductArgs& a, int bm, bool sym) {
   return a.E * (sym ? mt * (mt + 1) / 2 : mt * nt);
 }
 
-// The tiles of a product and its sums' parts.
+// How a product is laid over the chip: whole tiles and parts of every XCD (ProductArgs), and
+// about how long it takes, in ns.
 struct Plan {
-  int bm;
   int whole, parts, rest;
+  double ns;
 };
-// Parts for the last round's tiles, where it would leave half of the chip without one: as many as
-// fill it, of two ring turns at least.
-Plan plan_of(const ProductArgs& a, int bm, int slots, bool sym) {
-  const int64_t all = tiles_of(a, bm, sym), turns = a.K / (kStages * 32);
-  Plan p{bm, (int)((all / kXcds) / slots * slots), 1, 0};
-  p.rest = (int)((all + kXcds - 1) / kXcds) - p.whole;
-  if (p.rest > 0) p.parts = (int)(slots / p.rest < turns / 2 ? slots / p.rest : turns / 2);
-  if (p.parts > kMaxParts) p.parts = kMaxParts;
-  return p;
-}
+// Parts where tiles do not fill the chip once, as many as do, of two ring turns at least.
 template <class G>
 Plan plan_for(const ProductArgs& a, bool sym) {
-  Plan p = plan_of(a, G::BM, G::SLOTS, sym);
-  if (a.K < 1024 || p.whole) p.parts = 1;
+  // ns of a tile's stage of 32, where a CU has few tiles and (the clock and the L2s' share gone down)
+  // many; of a tile's end, of a launch, and of a join
+  struct Cost {
+    double stage, busy, tile, launch, join;
+    int few;
+  };
+  constexpr Cost c = G::BM == 256    ? Cost{750, 850, 5000, 2000, 0, 1}
+                     : G::TERMS == 1 ? Cost{240, 340, 0, 5000, 7000, 8}
+                     : G::BM == 128  ? Cost{700, 800, 3000, 3000, 0, 1}
+                                     : Cost{200, 240, 0, 4000, 5000, 4};
+  constexpr int cus = kCus / kXcds;
+  const int64_t tiles = tiles_of(a, G::BM, sym), each = (tiles + kXcds - 1) / kXcds, turns = a.K / (kStages * G::BK);
+  const int64_t per_cu = (each + cus - 1) / cus;
+  const double sum = (double)(a.K / G::BK) * (per_cu > c.few ? c.busy : c.stage) + c.tile;
+  Plan p{(int)each, 1, 0, c.launch + sum * (double)per_cu};
+  if (c.join == 0 || each > G::SLOTS / 2) return p;
+  int parts = G::SLOTS / (int)each;
+  if (parts > turns / 2) parts = (int)(turns / 2);
+  if (parts > kMaxParts) parts = kMaxParts;
+  const double ns = c.launch + sum / parts * (double)((each * parts + cus - 1) / cus) + c.join;
+  if (parts > 1 && ns < p.ns) p = Plan{0, parts, (int)each, ns};
   return p;
 }
 
@@ -1004,32 +1110,39 @@ template <class G, bool SYM, int KIND, typename TO>
 hipError_t launch_tile(const ProductArgs& args, hipStream_t s) {
   ProductArgs a = args;
   const Plan p = plan_for<G>(a, SYM);
-  const int64_t each = (tiles_of(a, G::BM, SYM) + kXcds - 1) / kXcds;
   a.parts = p.parts;
   a.whole = p.whole;
   a.rest = p.rest;
-  const int64_t items = a.parts > 1 ? a.whole + (int64_t)a.rest * a.parts : each;
+  const int items = a.parts > 1 ? a.rest * a.parts : a.whole;
   product_kernel<G, SYM, KIND, TO><<<(unsigned)((items < G::SLOTS ? items : G::SLOTS) * kXcds), 256, 0, s>>>(a);
-  if (a.parts > 1) join_kernel<G, SYM, KIND, TO><<<(unsigned)(a.rest * kXcds * 4), 64, 0, s>>>(a);
+  if (a.parts > 1) join_kernel<G, SYM, KIND, TO><<<(unsigned)(a.rest * kXcds * 4 * Passes<G>::ALL), 64, 0, s>>>(a);
   return hipGetLastError();
 }
-// 256-row tiles
-bool wide(const ProductArgs& a, bool sym) { return tiles_of(a, 256, sym) >= kCus; }
-bool small(const ProductArgs& a, bool sym) { return tiles_of(a, 128, sym) < kCus / 2; }
 template <bool AKS, bool BKS, bool SYM, int TERMS, int KIND, typename TO>
 hipError_t product(const ProductArgs& a, hipStream_t s) {
-  if constexpr (TERMS == 1) {
-    if (wide(a, SYM)) return launch_tile<Tile<256, AKS, BKS, 1>, SYM, KIND, TO>(a, s);
-  } else {
-    if (small(a, SYM)) return launch_tile<Tile<64, AKS, BKS, 2>, SYM, KIND, TO>(a, s);
-  }
-  return launch_tile<Tile<128, AKS, BKS, TERMS>, SYM, KIND, TO>(a, s);
+  typedef Tile<TERMS == 1 ? 256 : 128, AKS, BKS, TERMS> Big;
+  typedef Tile<TERMS == 1 ? 128 : 64, AKS, BKS, TERMS> Small;
+  if (plan_for<Big>(a, SYM).ns < plan_for<Small>(a, SYM).ns) return launch_tile<Big, SYM, KIND, TO>(a, s);
+  return launch_tile<Small, SYM, KIND, TO>(a, s);
 }
 
 int terms_of(const OrthArgs& a) { return a.bf16 && (a.m < a.n ? a.m : a.n) > kOneTerm ? 1 : 2; }
 
 // Most bytes of part sums: a round's tiles, of 256 rows one per CU.
 constexpr size_t kSumBytes = (size_t)kCus * 256 * 256 * sizeof(float);
+
+// Whether the next two steps share a Gram matrix. In one term what was rounded in A is multiplied by
+// up to a^4 on the way to A', which costs most in the middle steps, where singular values of every size
+// are left: there single steps, unless the long side is twice the short one and pairs save a
+// fifth; then one single step between two pairs (off by, in 64-bit simulations of five steps with these
+// roundings, of gradients 512 x 2048 in 1e-3: pairs first 3.1, one between 0.9, all single 1.1; 512 x 512:
+// 2.4, 2.0, 1.3, and 1.0 with only the first two as a pair).
+bool pair_next(const OrthArgs& a, int terms, int done) {
+  const int left = a.steps - done;
+  if (left < 2 || terms == 2 || done == 0) return left >= 2;
+  const int64_t s = a.m < a.n ? a.m : a.n, l = a.m < a.n ? a.n : a.m;
+  return l >= 2 * s && left % 2 == 0;
+}
 
 bool is_small(const OrthArgs& a) {
   return (a.m <= kSmallSide || a.n <= kSmallSide) && a.m <= kSmallLong && a.n <= kSmallLong;
@@ -1095,7 +1208,7 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
   e = hipGetLastError();
   if (e != hipSuccess) return e;
 
-  auto big = [&](const f16* p) { return Operands{p, x_plane, l.rows * l.cols, (int)l.cols}; };
+  auto big = [&](const f16* p) { return Operands{p, x_plane, l.rows * l.cols, (int)l.rows}; };
   auto square = [&](const f16* p) { return Operands{p, sq_plane, l.side * l.side, (int)l.side}; };
   // of symmetric matrices that commute: d = u v, or a I + b u + c u^2
   auto symmetric = [&](const f16* u, const f16* v, f16* d) {
@@ -1115,7 +1228,7 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
   };
   f16 *A = sq[0], *P = sq[1], *Y = sq[2];
   for (int done = 0, at = 0; done < a.steps; at ^= 1) {
-    const bool begin = done == 0, two = a.steps - done >= 2;
+    const bool begin = done == 0, two = pair_next(a, TERMS, done);
     const float unit = (float)(1.0 / scale);  // X = unit X^ (the first X^: first[e] X^)
     ProductArgs r{};
     r.a = r.b = big(x[at]);
