@@ -905,23 +905,10 @@ __device__ __forceinline__ void lds_square(const OrthArgs& a, const InLds& u, co
   __syncthreads();
 }
 
-// Everything between a Gram matrix A and what X is multiplied by: P, or with `two` P' P. A and the
-// result in global memory, side x side in two terms; SIDE: what of it is not zero.
+// Everything between a Gram matrix, in U, and what X is multiplied by, to P: P(A), or with `two` P' P.
 template <int SIDE>
-__global__ __launch_bounds__(kThreads) void polynomial_kernel(OrthArgs a, bool two, const f16* A, f16* out, int side,
-                                                              int64_t plane) {
-  __shared__ __attribute__((aligned(1024))) char lds[2][2][SIDE * SIDE * 2];
-  const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const InLds U{lds[0][0], lds[0][1], SIDE * 2}, P{lds[1][0], lds[1][1], SIDE * 2};
-  const int64_t at = (int64_t)blockIdx.x * side * side;
-  constexpr int CHUNKS = SIDE / 8;
-#pragma unroll
-  for (int i = threadIdx.x; i < SIDE * CHUNKS; i += kThreads) {
-    const int r = i / CHUNKS, c = i % CHUNKS * 8;
-    *reinterpret_cast<u32x4*>(U.hi + U.at(r, c)) = ld16(A + at + in_panels(side, r, c));
-    *reinterpret_cast<u32x4*>(U.lo + U.at(r, c)) = ld16(A + plane + at + in_panels(side, r, c));
-  }
-  __syncthreads();
+__device__ __forceinline__ void lds_polynomial(const OrthArgs& a, bool two, const InLds& U, const InLds& P, int wave,
+                                               int ln) {
   lds_square<SIDE, true>(a, U, U, P, wave, ln);
   if (two) {
     lds_square<SIDE, false>(a, P, U, U, wave, ln);
@@ -929,32 +916,146 @@ __global__ __launch_bounds__(kThreads) void polynomial_kernel(OrthArgs a, bool t
     lds_square<SIDE, true>(a, U, U, U, wave, ln);   // P'
     lds_square<SIDE, false>(a, U, P, P, wave, ln);
   }
-  for (int i = threadIdx.x; i < side * (side / 8); i += kThreads) {
-    const int r = i / (side / 8), c = i % (side / 8) * 8;
-    const bool in = r < SIDE && c < SIDE;
-    const u32x4 zero = {0, 0, 0, 0};
-    st16(out + at + in_panels(side, r, c), in ? *reinterpret_cast<const u32x4*>(P.hi + P.at(r, c)) : zero);
-    st16(out + plane + at + in_panels(side, r, c), in ? *reinterpret_cast<const u32x4*>(P.lo + P.at(r, c)) : zero);
+}
+// The same from and to global memory, for short sides of 65 to 128.
+__global__ __launch_bounds__(kThreads) void polynomial_kernel(OrthArgs a, bool two, const f16* A, f16* out,
+                                                              int64_t plane) {
+  constexpr int SIDE = kPad;
+  __shared__ __attribute__((aligned(1024))) char lds[2][2][SIDE * SIDE * 2];
+  const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const InLds U{lds[0][0], lds[0][1], SIDE * 2}, P{lds[1][0], lds[1][1], SIDE * 2};
+  const int64_t at = (int64_t)blockIdx.x * SIDE * SIDE;
+  constexpr int CHUNKS = SIDE / 8;
+#pragma unroll
+  for (int i = threadIdx.x; i < SIDE * CHUNKS; i += kThreads) {
+    const int r = i / CHUNKS, c = i % CHUNKS * 8;
+    *reinterpret_cast<u32x4*>(U.hi + U.at(r, c)) = ld16(A + at + in_panels(SIDE, r, c));
+    *reinterpret_cast<u32x4*>(U.lo + U.at(r, c)) = ld16(A + plane + at + in_panels(SIDE, r, c));
+  }
+  __syncthreads();
+  lds_polynomial<SIDE>(a, two, U, P, wave, ln);
+#pragma unroll
+  for (int i = threadIdx.x; i < SIDE * CHUNKS; i += kThreads) {
+    const int r = i / CHUNKS, c = i % CHUNKS * 8;
+    st16(out + at + in_panels(SIDE, r, c), *reinterpret_cast<const u32x4*>(P.hi + P.at(r, c)));
+    st16(out + plane + at + in_panels(SIDE, r, c), *reinterpret_cast<const u32x4*>(P.lo + P.at(r, c)));
+  }
+}
+
+// X of up to 64 x 384 in LDS, of a matrix whose short side is at most 64, or of 384 of its longer side.
+constexpr int kSmallSide = 64, kSmallLong = 384;
+
+// Value (i, j) of X, i of the short side, is value (i, j) or (j, i) of the matrix.
+struct Shape {
+  int m, n;
+  bool tall;
+  __device__ __forceinline__ explicit Shape(const OrthArgs& a) : m((int)a.m), n((int)a.n), tall(a.m > a.n) {}
+  __device__ __forceinline__ int64_t at(int i, int j) const { return tall ? (int64_t)j * n + i : (int64_t)i * n + j; }
+};
+
+// Columns c0 .. c0 + w - 1 of X 2^p into LDS (of l columns, zeros behind w). All threads; ends with it whole.
+template <typename TI>
+__device__ __forceinline__ void lds_load(const OrthArgs& a, const Shape& sh, const TI* g, const float* mom, double by, int c0,
+                                         int w, int l, const InLds& X) {
+  for (int i = threadIdx.x; i < kSmallSide * l / 8; i += kThreads) {
+    *reinterpret_cast<u32x4*>(X.hi + i * 16) = u32x4{0, 0, 0, 0};
+    *reinterpret_cast<u32x4*>(X.lo + i * 16) = u32x4{0, 0, 0, 0};
+  }
+  __syncthreads();
+  // (along the matrix's rows)
+  const int s = sh.tall ? sh.n : sh.m, in = sh.tall ? s : w, size = s * w;
+  int r = threadIdx.x / in, c = threadIdx.x - r * in;
+  for (int k = threadIdx.x; k < size; k += kThreads) {
+    const int i = sh.tall ? c : r, j = sh.tall ? r : c;
+    const int64_t at = sh.at(i, c0 + j);
+    float u = (float)g[at];
+    if (mom) u = update_of(a, mom[at], u);
+    f16 h, lo;
+    split((float)((double)u * by), h, lo);
+    const int to = X.at(i, j);
+    *reinterpret_cast<f16*>(X.hi + to) = h;
+    *reinterpret_cast<f16*>(X.lo + to) = lo;
+    r += kThreads / in;
+    c += kThreads % in;
+    if (c >= in) {
+      c -= in;
+      ++r;
+    }
+  }
+  __syncthreads();
+}
+
+// f P X: the whole is computed, all waves wait for it, then put(i, j, values j .. j + 3).
+template <class Put>
+__device__ __forceinline__ void lds_times(const InLds& P, const InLds& X, int l, float f, int wave, int ln, Put put) {
+  // block columns wave, wave + 8, .. of X, both block rows of each
+  constexpr int EACH = (kSmallLong / 32 + kWaves - 1) / kWaves;
+  const int row = here(ln) & 31, col = 4 * (here(ln) >> 5);
+  f32x16 r[EACH][2];
+#pragma unroll
+  for (int b = 0; b < EACH; ++b) {
+    const int j0 = (wave + b * kWaves) * 32;
+    if (j0 >= l) continue;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f32x16 one[1];
+      lds_blocks<true>(P, X, i * 32, j0, kSmallSide, ln, one);
+      r[b][i] = f * one[0];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < EACH; ++b) {
+    const int j0 = (wave + b * kWaves) * 32;
+    if (j0 >= l) continue;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v[4] = {r[b][i][4 * q], r[b][i][4 * q + 1], r[b][i][4 * q + 2], r[b][i][4 * q + 3]};
+        put(i * 32 + row, j0 + 8 * q + col, v);
+      }
+  }
+}
+// X X^T, a block for each of four waves: put(i, j, values j .. j + 3).
+template <class Put>
+__device__ __forceinline__ void lds_gram(const InLds& X, int l, int wave, int ln, Put put) {
+  if (wave >= 4) return;
+  const int i0 = wave / 2 * 32, j0 = wave % 2 * 32, row = here(ln) & 31, col = 4 * (here(ln) >> 5);
+  f32x16 r[1];
+  lds_blocks<false>(X, X, i0, j0, l, ln, r);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float v[4] = {r[0][4 * q], r[0][4 * q + 1], r[0][4 * q + 2], r[0][4 * q + 3]};
+    put(i0 + row, j0 + 8 * q + col, v);
+  }
+}
+// Four values of the result, (i, j) on, to where they belong.
+template <typename TI>
+__device__ __forceinline__ void put_result(const OrthArgs& a, const Shape& sh, TI* out, int i, int j, const float (&v)[4]) {
+  const int s = sh.tall ? sh.n : sh.m, l = sh.tall ? sh.m : sh.n;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (i >= s || j + k >= l) continue;
+    TI* o = out + sh.at(i, j + k);
+    *o = (TI)(a.momentum ? a.keep * (float)*o - a.rate * v[k] : v[k]);
   }
 }
 
 // The whole of it for matrices of at most 64 x 384: X and the square matrices in LDS.
-constexpr int kSmallSide = 64, kSmallLong = 384;
 template <typename TI>
 __global__ __launch_bounds__(kThreads) void small_kernel(OrthArgs a, double scale) {
   __shared__ __attribute__((aligned(1024))) char xs[2][kSmallSide * kSmallLong * 2];
-  __shared__ __attribute__((aligned(1024))) char sq[3][2][kSmallSide * kSmallSide * 2];
+  __shared__ __attribute__((aligned(1024))) char sq[2][2][kSmallSide * kSmallSide * 2];
   __shared__ double sums[kWaves];
   const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m = (int)a.m, n = (int)a.n, size = m * n, l = (max(m, n) + 63) / 64 * 64;
-  const bool tall = m > n;
+  const Shape sh(a);
+  const int size = sh.m * sh.n, w = max(sh.m, sh.n), l = (w + 63) / 64 * 64;
   const int64_t at = (int64_t)blockIdx.x * size;
   const TI* g = static_cast<const TI*>(a.g) + at;
   TI* out = static_cast<TI*>(a.out) + at;
   float* mom = a.momentum ? a.momentum + at : nullptr;
-  const InLds X{xs[0], xs[1], l * 2};
-  const InLds A{sq[0][0], sq[0][1], kSmallSide * 2}, P{sq[1][0], sq[1][1], kSmallSide * 2},
-      Y{sq[2][0], sq[2][1], kSmallSide * 2};
+  const InLds X{xs[0], xs[1], l * 2}, A{sq[0][0], sq[0][1], kSmallSide * 2}, P{sq[1][0], sq[1][1], kSmallSide * 2};
 
   double sum = 0;
 #pragma unroll 4
@@ -970,97 +1071,142 @@ __global__ __launch_bounds__(kThreads) void small_kernel(OrthArgs a, double scal
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
   if (ln == 0) sums[wave] = sum;
-  for (int i = threadIdx.x; i < 2 * kSmallSide * l / 8; i += kThreads)
-    *reinterpret_cast<u32x4*>((i < kSmallSide * l / 8 ? X.hi + i * 16 : X.lo + (i - kSmallSide * l / 8) * 16)) =
-        u32x4{0, 0, 0, 0};
-  __syncthreads();
+  __syncthreads();  // (and the momentum is written, which other threads read below)
   sum = 0;
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) sum += sums[i];
   const Scale sc(sqrt(sum) + (double)a.eps, scale);
-  for (int i = threadIdx.x, r = i / n, c = i - r * n; i < size; i += kThreads) {
-    float u = (float)g[i];
-    if (mom) u = update_of(a, mom[i], u);
-    f16 h, lo;
-    split((float)((double)u * sc.by), h, lo);
-    const int to = tall ? X.at(c, r) : X.at(r, c);
-    *reinterpret_cast<f16*>(X.hi + to) = h;
-    *reinterpret_cast<f16*>(X.lo + to) = lo;
-    r += kThreads / n;
-    c += kThreads % n;
-    if (c >= n) {
-      c -= n;
-      ++r;
-    }
-  }
-  __syncthreads();
+  lds_load(a, sh, g, mom, sc.by, 0, w, l, X);
 
   const float unit = (float)(1.0 / scale);
   for (int done = 0; done < a.steps;) {
     const bool begin = done == 0, two = a.steps - done >= 2;
     const float t = begin ? sc.first : unit;  // X = t X^
-    if (wave < 4) {
-      const int i0 = wave / 2 * 32, j0 = wave % 2 * 32, row = here(ln) & 31, col = 4 * (here(ln) >> 5);
-      f32x16 r[1];
-      lds_blocks<false>(X, X, i0, j0, l, ln, r);
-      r[0] *= t * t;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float v[4] = {r[0][4 * q], r[0][4 * q + 1], r[0][4 * q + 2], r[0][4 * q + 3]};
-        A.put(i0 + row, j0 + 8 * q + col, v);
-      }
-    }
+    lds_gram(X, l, wave, ln, [&](int i, int j, const float(&v)[4]) {
+      const float r[4] = {t * t * v[0], t * t * v[1], t * t * v[2], t * t * v[3]};
+      A.put(i, j, r);
+    });
     __syncthreads();
-    lds_square<kSmallSide, true>(a, A, A, P, wave, ln);
-    if (two) {
-      lds_square<kSmallSide, false>(a, P, A, Y, wave, ln);
-      lds_square<kSmallSide, false>(a, P, Y, A, wave, ln);  // A'
-      lds_square<kSmallSide, true>(a, A, A, Y, wave, ln);   // P'
-      lds_square<kSmallSide, false>(a, Y, P, P, wave, ln);
-    }
+    lds_polynomial<kSmallSide>(a, two, A, P, wave, ln);
     done += two ? 2 : 1;
-    const bool last = done == a.steps;
-    const float f = last ? t : begin ? t * (float)scale : 1.f;
-    // block columns wave, wave + 8, .. of X, both block rows of each
-    const int row = here(ln) & 31, col = 4 * (here(ln) >> 5);
-    constexpr int EACH = (kSmallLong / 32 + kWaves - 1) / kWaves;
-    f32x16 r[EACH][2];
+    if (done == a.steps)
+      lds_times(P, X, l, t, wave, ln, [&](int i, int j, const float(&v)[4]) { put_result(a, sh, out, i, j, v); });
+    else
+      lds_times(P, X, l, begin ? t * (float)scale : 1.f, wave, ln,
+                [&](int i, int j, const float(&v)[4]) { X.put(i, j, v); });
+    __syncthreads();
+  }
+}
+
+// Matrices of at most 64 x 12288: workgroup (c, e) has up to 384 columns of X in LDS. Between two launches of
+// this kernel the Gram matrix's parts, one of every workgroup, are joined and P is computed.
+// first: X from g (else X <- f P X from the one that the launch before left); last: X is the result
+// (else it is left for the next launch, with its part of the Gram matrix).
+struct ThinArgs {
+  const double* partial;  // of the squares, `blocks` per matrix
+  float* first;           // per matrix
+  char* x;                // [E][columns / each][2][64 x 384], as in LDS
+  const char* P;          // [E][2][64 x 64], as in LDS
+  float* parts;           // [E][columns / each][64][64]
+  double scale;
+  int each;               // columns of a workgroup
+  int blocks, power;
+  float f;                // times first^power
+};
+constexpr int kThinLong = 32 * kSmallLong;
+template <typename TI, bool FIRST, bool LAST>
+__global__ __launch_bounds__(kThreads) void thin_kernel(OrthArgs a, ThinArgs t) {
+  __shared__ __attribute__((aligned(1024))) char xs[2][kSmallSide * kSmallLong * 2];
+  __shared__ __attribute__((aligned(1024))) char sq[2][kSmallSide * kSmallSide * 2];
+  __shared__ double sums[kWaves];
+  const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Shape sh(a);
+  const int e = blockIdx.y, all = max(sh.m, sh.n), c0 = blockIdx.x * t.each, w = min(all - c0, t.each);
+  const int l = (w + 63) / 64 * 64, bytes = kSmallSide * l * 2;
+  const int64_t at = (int64_t)e * a.m * a.n, part = (int64_t)e * gridDim.x + blockIdx.x;
+  const InLds X{xs[0], xs[1], l * 2}, P{sq[0], sq[1], kSmallSide * 2};
+  char* image = t.x + part * (2 * kSmallSide * kSmallLong * 2);
+  if constexpr (FIRST) {
+    double v = (int)threadIdx.x < t.blocks ? t.partial[(int64_t)e * t.blocks + threadIdx.x] : 0.0;
 #pragma unroll
-    for (int b = 0; b < EACH; ++b) {
-      const int j0 = (wave + b * kWaves) * 32;
-      if (j0 >= l) continue;
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    if (ln == 0) sums[wave] = v;
+    __syncthreads();
+    v = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        f32x16 one[1];
-        lds_blocks<true>(P, X, i * 32, j0, kSmallSide, ln, one);
-        r[b][i] = f * one[0];
-      }
+    for (int i = 0; i < kWaves; ++i) v += sums[i];
+    const Scale sc(sqrt(v) + (double)a.eps, t.scale);
+    if (blockIdx.x == 0 && threadIdx.x == 0) t.first[e] = sc.first;
+    lds_load(a, sh, static_cast<const TI*>(a.g) + at, a.momentum ? a.momentum + at : nullptr, sc.by, c0, w, l, X);
+  } else {
+    const char* from = t.P + (int64_t)e * (2 * kSmallSide * kSmallSide * 2);
+#pragma unroll
+    for (int i = threadIdx.x * 16; i < kSmallSide * kSmallSide * 2; i += kThreads * 16) {
+      *reinterpret_cast<u32x4*>(P.hi + i) = ld16(from + i);
+      *reinterpret_cast<u32x4*>(P.lo + i) = ld16(from + kSmallSide * kSmallSide * 2 + i);
+    }
+    for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16) {
+      *reinterpret_cast<u32x4*>(X.hi + i) = ld16(image + i);
+      *reinterpret_cast<u32x4*>(X.lo + i) = ld16(image + bytes + i);
     }
     __syncthreads();
-#pragma unroll
-    for (int b = 0; b < EACH; ++b) {
-      const int j0 = (wave + b * kWaves) * 32;
-      if (j0 >= l) continue;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int x = i * 32 + row, y = j0 + 8 * q + col;
-          float v[4] = {r[b][i][4 * q], r[b][i][4 * q + 1], r[b][i][4 * q + 2], r[b][i][4 * q + 3]};
-          if (!last) {
-            X.put(x, y, v);
-            continue;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int gr = tall ? y + k : x, gc = tall ? x : y + k;
-            if (gr >= m || gc >= n) continue;
-            TI* o = out + gr * n + gc;
-            *o = (TI)(a.momentum ? a.keep * (float)*o - a.rate * v[k] : v[k]);
-          }
-        }
+    const float f = t.power ? t.f * t.first[e] : t.f;
+    if constexpr (LAST) {
+      TI* out = static_cast<TI*>(a.out) + at;
+      lds_times(P, X, l, f, wave, ln, [&](int i, int j, const float(&v)[4]) { put_result(a, sh, out, i, c0 + j, v); });
+    } else {
+      lds_times(P, X, l, f, wave, ln, [&](int i, int j, const float(&v)[4]) { X.put(i, j, v); });
+      __syncthreads();
     }
-    __syncthreads();
+  }
+  if constexpr (!LAST) {
+    float* to = t.parts + part * (kSmallSide * kSmallSide);
+    lds_gram(X, l, wave, ln, [&](int i, int j, const float(&v)[4]) {
+      *reinterpret_cast<f32x4*>(to + i * kSmallSide + j) = f32x4{v[0], v[1], v[2], v[3]};
+    });
+    for (int i = threadIdx.x * 16; i < bytes; i += kThreads * 16) {
+      st16(image + i, *reinterpret_cast<const u32x4*>(X.hi + i));
+      st16(image + bytes + i, *reinterpret_cast<const u32x4*>(X.lo + i));
+    }
+  }
+}
+// The sum of the parts, in order, times f (times first^power), and what X is multiplied by.
+__global__ __launch_bounds__(kThreads) void thin_polynomial_kernel(OrthArgs a, ThinArgs t, int parts, bool two, char* out) {
+  __shared__ __attribute__((aligned(1024))) char sq[2][2][kSmallSide * kSmallSide * 2];
+  const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const InLds A{sq[0][0], sq[0][1], kSmallSide * 2}, P{sq[1][0], sq[1][1], kSmallSide * 2};
+  float f = t.f;
+  for (int i = 0; i < t.power; ++i) f *= t.first[blockIdx.x];
+  constexpr int N = kSmallSide * kSmallSide, EACH = N / 4 / kThreads, AHEAD = 8;
+  const float* from = t.parts + (int64_t)blockIdx.x * parts * N + threadIdx.x * 4;
+  f32x4 sum[EACH] = {};
+  for (int i = 0; i < parts; i += AHEAD) {
+    f32x4 v[AHEAD][EACH];
+#pragma unroll
+    for (int h = 0; h < AHEAD; ++h)
+#pragma unroll
+      for (int k = 0; k < EACH; ++k)
+        v[h][k] = *reinterpret_cast<const f32x4*>(from + (int64_t)min(i + h, parts - 1) * N + k * kThreads * 4);
+#pragma unroll
+    for (int h = 0; h < AHEAD; ++h) {
+      if (i + h >= parts) continue;
+#pragma unroll
+      for (int k = 0; k < EACH; ++k) sum[k] += v[h][k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    const int i = threadIdx.x * 4 + k * kThreads * 4;
+    const float v[4] = {f * sum[k][0], f * sum[k][1], f * sum[k][2], f * sum[k][3]};
+    A.put(i / kSmallSide, i % kSmallSide, v);
+  }
+  __syncthreads();
+  lds_polynomial<kSmallSide>(a, two, A, P, wave, ln);
+  char* to = out + (int64_t)blockIdx.x * (2 * kSmallSide * kSmallSide * 2);
+#pragma unroll
+  for (int i = threadIdx.x * 16; i < kSmallSide * kSmallSide * 2; i += kThreads * 16) {
+    st16(to + i, *reinterpret_cast<const u32x4*>(P.hi + i));
+    st16(to + kSmallSide * kSmallSide * 2 + i, *reinterpret_cast<const u32x4*>(P.lo + i));
   }
 }
 
@@ -1144,9 +1290,20 @@ bool pair_next(const OrthArgs& a, int terms, int done) {
   return l >= 2 * s && left % 2 == 0;
 }
 
-bool is_small(const OrthArgs& a) {
-  return (a.m <= kSmallSide || a.n <= kSmallSide) && a.m <= kSmallLong && a.n <= kSmallLong;
+// Matrices of one launch, and of workgroups that keep 384 columns.
+int64_t long_side(const OrthArgs& a) { return a.m > a.n ? a.m : a.n; }
+bool is_small(const OrthArgs& a) { return (a.m <= kSmallSide || a.n <= kSmallSide) && long_side(a) <= kSmallLong; }
+bool is_thin(const OrthArgs& a) {
+  return (a.m <= kSmallSide || a.n <= kSmallSide) && !is_small(a) && long_side(a) <= kThinLong;
 }
+// Columns of a workgroup: few, so that it has soon done, but so that a matrix has no more than 24
+// parts of its Gram matrix and all workgroups are on the chip at once.
+int thin_columns(const OrthArgs& a) {
+  for (int w = 128; w < kSmallLong; w += 128)
+    if (long_side(a) <= 24 * w && a.E * ((long_side(a) + w - 1) / w) <= kCus) return w;
+  return kSmallLong;
+}
+int64_t thin_groups(const OrthArgs& a) { return (long_side(a) + thin_columns(a) - 1) / thin_columns(a); }
 
 // Pieces of the workspace.
 struct Layout {
@@ -1168,14 +1325,58 @@ Layout layout_of(const OrthArgs& a) {
     at += aligned(n);
     return p;
   };
+  if (is_small(a)) {  // (everything is in LDS)
+    l.bytes = 256;
+    return l;
+  }
   l.partial = take((size_t)a.E * l.blocks * sizeof(double));
   l.first = take((size_t)a.E * sizeof(float));
+  if (is_thin(a)) {
+    const size_t groups = (size_t)a.E * (size_t)thin_groups(a);
+    l.sums = take(groups * kSmallSide * kSmallSide * sizeof(float));
+    l.x[0] = take(groups * kSmallSide * kSmallLong * 4);
+    l.sq[0] = take((size_t)a.E * kSmallSide * kSmallSide * 4);
+    l.bytes = at;
+    return l;
+  }
   l.sums = take(kSumBytes);
   const size_t x = (size_t)a.E * l.rows * l.cols * terms * 2, sq = (size_t)a.E * l.side * l.side * terms * 2;
   for (int i = 0; i < 2; ++i) l.x[i] = i == 0 || a.steps > 2 ? take(x) : 0;
   for (int i = 0; i < 3; ++i) l.sq[i] = i < 2 || a.steps > 1 ? take(sq) : 0;
   l.bytes = at;
   return l;
+}
+
+template <typename TI>
+hipError_t run_thin(const OrthArgs& a, const Layout& l, double scale, hipStream_t s) {
+  ThinArgs t{};
+  t.partial = reinterpret_cast<const double*>(a.ws + l.partial);
+  t.first = reinterpret_cast<float*>(a.ws + l.first);
+  t.x = a.ws + l.x[0];
+  t.P = a.ws + l.sq[0];
+  t.parts = reinterpret_cast<float*>(a.ws + l.sums);
+  t.scale = scale;
+  t.blocks = l.blocks;
+  const dim3 grid((unsigned)thin_groups(a), a.E);
+  t.each = thin_columns(a);
+  const float unit = (float)(1.0 / scale);
+  thin_kernel<TI, true, false><<<grid, kThreads, 0, s>>>(a, t);
+  for (int done = 0; done < a.steps;) {
+    const bool begin = done == 0, two = a.steps - done >= 2;
+    t.power = begin ? 2 : 0;
+    t.f = begin ? 1.f : unit * unit;
+    thin_polynomial_kernel<<<a.E, kThreads, 0, s>>>(a, t, (int)grid.x, two, a.ws + l.sq[0]);
+    done += two ? 2 : 1;
+    t.power = begin ? 1 : 0;
+    if (done == a.steps) {
+      t.f = begin ? 1.f : unit;
+      thin_kernel<TI, false, true><<<grid, kThreads, 0, s>>>(a, t);
+    } else {
+      t.f = begin ? (float)scale : 1.f;
+      thin_kernel<TI, false, false><<<grid, kThreads, 0, s>>>(a, t);
+    }
+  }
+  return hipGetLastError();
 }
 
 template <typename TI, int TERMS>
@@ -1202,6 +1403,7 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
   square_kernel<TI><<<dim3(l.blocks, a.E), 256, 0, s>>>(a, aligned_in && a.m * a.n % 8 == 0, partial);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  if (TERMS == 2 && is_thin(a)) return run_thin<TI>(a, l, scale, s);
   const int64_t chunks = (l.rows * l.cols / 8 + 255) / 256, most = (4096 + a.E - 1) / a.E;
   scale_kernel<TI, TERMS><<<dim3((unsigned)(chunks < most ? chunks : most), a.E), 256, 0, s>>>(
       a, aligned_in && a.n % 8 == 0, partial, l.blocks, scale, x[0], l.rows, l.cols, x_plane, first);
@@ -1245,10 +1447,7 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
     const f16* Q = P;
     if (l.side == kPad && TERMS == 2) {
       if (e != hipSuccess) return e;
-      if ((tall ? a.n : a.m) <= 64)
-        polynomial_kernel<64><<<a.E, kThreads, 0, s>>>(a, two, A, P, kPad, sq_plane);
-      else
-        polynomial_kernel<kPad><<<a.E, kThreads, 0, s>>>(a, two, A, P, kPad, sq_plane);
+      polynomial_kernel<<<a.E, kThreads, 0, s>>>(a, two, A, P, sq_plane);
       e = hipGetLastError();
     } else if (e == hipSuccess) {
       e = symmetric(A, nullptr, P);

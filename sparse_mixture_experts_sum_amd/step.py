@@ -62,10 +62,8 @@ def moe_layer_norm(x, gamma, beta=None, *, y=None, residual_scale=1.0, eps=1e-5,
         pout = out.data_ptr()
     u = torch.empty_like(x)
     if want_stats:
-        stats = torch.empty(2, T, dtype=_F32, device=dev)
-        mean, rstd = stats.unbind(0)
-        pm = stats.data_ptr()
-        pr = pm + 4 * T
+        mean, rstd = torch.empty(T, dtype=_F32, device=dev), torch.empty(T, dtype=_F32, device=dev)
+        pm, pr = mean.data_ptr(), rstd.data_ptr()
     _call("moe_layer_norm", dev, s, px, py, pg, pb, pout, u.data_ptr(), pm, pr)
     return {"out": x if y is None else out, "u": u, "mean": mean, "rstd": rstd}
 

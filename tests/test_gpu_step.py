@@ -333,7 +333,7 @@ def terms_of(m, n, dt):
 
 SIZES = [(1, 1, 1), (2, 1, 300), (3, 300, 1), (2, 16, 16), (5, 31, 33), (8, 64, 128), (3, 128, 64), (1, 127, 129),
          (2, 129, 1000), (2, 200, 333), (2, 333, 200), (1, 512, 513), (1, 513, 640), (2, 640, 520), (1, 520, 2056),
-         (1, 2056, 520), (64, 24, 40)]
+         (1, 2056, 520), (64, 24, 40), (3, 64, 384), (2, 64, 385), (2, 17, 1000), (3, 1531, 33), (1, 64, 12288), (1, 9, 12289)]
 
 
 @pytest.mark.parametrize("dt", [BF16, FP32])
