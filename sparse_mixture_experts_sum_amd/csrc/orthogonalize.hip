@@ -229,7 +229,7 @@ struct ProductArgs {
   int64_t d_plane;
   void* out;              // the result of the iteration, [m][n]
   int64_t m, n;
-  int E, power, vec, update;
+  int E, power, vec;
   float f, p, q, keep, rate;
   const float* first;
   // set by the launch: of every XCD's tiles, how many are whole; the others' sums are in `parts`
@@ -284,7 +284,7 @@ struct Tile {
   static constexpr int STAGE = TERMS * (A::BYTES + B::BYTES), LPS = TERMS * (A::PW + B::PW);
   static constexpr int OUT_BYTES = BM == 64 ? 4096 : 32 * WM * 2;  // LDS of each wave for its output
   static constexpr int LDS = kStages * STAGE + 4 * OUT_BYTES, PER_CU = 160 * 1024 / LDS;
-  static constexpr int SLOTS = PER_CU * kCus / kXcds;  // workgroups of an XCD that are resident
+  static constexpr int SLOTS = PER_CU * (kCus / kXcds);  // workgroups of an XCD that are resident
   static constexpr int MFMAS = TERMS == 2 ? 3 : 1;     // per pair of fragments
 };
 
@@ -511,12 +511,27 @@ struct Terms {
   }
 };
 
+// A chunk of 8 of the weights, where its row is whole chunks.
+template <typename TO>
+struct Weights {
+  u32x4 v[sizeof(TO) / 2];
+  __device__ __forceinline__ void load(const TO* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(TO) / 2; ++i) v[i] = ld16(p + i * (16 / sizeof(TO)));
+  }
+  __device__ __forceinline__ float value(int k) const {
+    if constexpr (sizeof(TO) == 2) return (float)__builtin_bit_cast(bf16x8, v[0])[k];
+    else return __builtin_bit_cast(f32x4, v[k / 4])[k % 4];
+  }
+};
+
 // What a product does with its sums.
-enum { kProduct, kPolynomial, kLast };  // f S; f S + p c + q I; the result
+enum { kProduct, kPolynomial, kLast, kUpdate };  // f S; f S + p c + q I; the result; it into the weights
 
 // acc[nb][mb][4 q + i] is row lane % 32 of block mb, column 8 q + 4 (lane / 32) + i of block nb.
 // 32 rows at a time go through a piece of LDS of the wave's own (16-byte chunk c of a row at
-// c ^ (row % chunks)) and leave as whole row segments; c's values are loaded a pass ahead.
+// c ^ (row % chunks)) and leave as whole row segments; c's values, and the weights that the result is
+// applied to, are loaded a pass ahead.
 // The transposed tile leaves by the same piece of LDS, column by column.
 // (only: that pass alone)
 template <class G>
@@ -535,16 +550,24 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
   float f = a.f;
   for (int i = 0; i < a.power; ++i) f *= a.first[t.e];
   const int r0 = ln / PER, c0 = ln % PER;
+  constexpr bool AHEAD = KIND == kPolynomial || KIND == kUpdate;
   Terms<TERMS> old[KIND == kPolynomial ? 2 : 1][N];
+  Weights<TO> weights[KIND == kUpdate ? 2 : 1][N];
   auto row_of = [&](int pass, int i) { return m0 + pass / (G::MB / BLOCKS) * 32 + i * RPS + r0; };
   auto col_of = [&](int pass) { return n0 + pass % (G::MB / BLOCKS) * COLS + c0 * 8; };
   auto fetch = [&](int pass) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      old[KIND == kPolynomial ? pass % 2 : 0][i].load(a.c, t.e, row_of(pass, i), col_of(pass));
+      const int64_t row = row_of(pass, i), col = col_of(pass);
+      if constexpr (KIND == kPolynomial) old[pass % 2][i].load(a.c, t.e, row, col);
+      if constexpr (KIND == kUpdate) {
+        // (past the end the first ones, which nobody takes)
+        const bool in = row < a.m && col < a.n;
+        if (a.vec) weights[pass % 2][i].load(static_cast<const TO*>(a.out) + (in ? ((int64_t)t.e * a.m + row) * a.n + col : 0));
+      }
     }
   };
-  if constexpr (KIND == kPolynomial) {
+  if constexpr (AHEAD) {
     if (only < 0) fetch(0);
   }
 #pragma unroll
@@ -552,7 +575,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
     if (only >= 0 && pass != only) continue;
     __builtin_amdgcn_sched_barrier(0);  // (one pass's registers at a time)
     const int mb = pass / (G::MB / BLOCKS), nb0 = pass % (G::MB / BLOCKS) * BLOCKS, r = ln & 31;
-    if constexpr (KIND == kPolynomial) {
+    if constexpr (AHEAD) {
       if (only >= 0) fetch(pass);
       else if (pass + 1 < PASSES) fetch(pass + 1);
       __builtin_amdgcn_sched_barrier(0);
@@ -582,15 +605,15 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
         if constexpr (KIND == kPolynomial)
           v[k] += a.p * old[pass % 2][i].value(k) + (gr == gc + k ? a.q : 0.f);
       }
-      if constexpr (KIND == kLast) {
+      if constexpr (KIND >= kLast) {
         if (gr >= a.m || gc >= a.n) continue;
         const int n = (int)min((int64_t)8, a.n - gc);
         TO* o = static_cast<TO*>(a.out) + ((int64_t)t.e * a.m + gr) * a.n + gc;
-        if (a.update) {
-          float old[8];
-          load_row(o, n, a.vec, old);
+        if constexpr (KIND == kUpdate) {
+          float w[8];
+          if (!a.vec) load_row(o, n, false, w);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = a.keep * old[k] - a.rate * v[k];
+          for (int k = 0; k < 8; ++k) v[k] = a.keep * (a.vec ? weights[pass % 2][i].value(k) : w[k]) - a.rate * v[k];
         }
         store_row(o, n, a.vec, v);
       } else {
@@ -606,7 +629,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
         if constexpr (TERMS == 2) *reinterpret_cast<f16x8*>(d + a.d_plane) = lo[i];
       }
     }
-    if constexpr (SYM && KIND != kLast) {
+    if constexpr (SYM && KIND < kLast) {
       if (m0 != n0) {
         // [32 rows][columns] of fp16, chunk c of a row at c ^ swz(row), and out of there in columns
         // by transposing reads: 16 columns at a time, lane l with rows 8 (l / 16) .. + 7 of column l % 16
@@ -1261,21 +1284,38 @@ hipError_t launch_tile(const ProductArgs& args, hipStream_t s) {
   a.rest = p.rest;
   const int items = a.parts > 1 ? a.rest * a.parts : a.whole;
   product_kernel<G, SYM, KIND, TO><<<(unsigned)((items < G::SLOTS ? items : G::SLOTS) * kXcds), 256, 0, s>>>(a);
-  if (a.parts > 1) join_kernel<G, SYM, KIND, TO><<<(unsigned)(a.rest * kXcds * 4 * Passes<G>::ALL), 64, 0, s>>>(a);
+  if (a.parts > 1)
+    join_kernel<G, SYM, KIND, TO><<<(unsigned)(a.rest * kXcds * 4 * Passes<G>::ALL), 64, 0, s>>>(a);
   return hipGetLastError();
+}
+// The larger of the two tiles there are for one or two terms, or the smaller one.
+template <bool AKS, bool BKS, int TERMS>
+using Big = Tile<TERMS == 1 ? 256 : 128, AKS, BKS, TERMS>;
+template <bool AKS, bool BKS, int TERMS>
+using Small = Tile<TERMS == 1 ? 128 : 64, AKS, BKS, TERMS>;
+template <int TERMS>
+bool big(const ProductArgs& a, bool sym) {
+  return plan_for<Big<false, false, TERMS>>(a, sym).ns < plan_for<Small<false, false, TERMS>>(a, sym).ns;
 }
 template <bool AKS, bool BKS, bool SYM, int TERMS, int KIND, typename TO>
 hipError_t product(const ProductArgs& a, hipStream_t s) {
-  typedef Tile<TERMS == 1 ? 256 : 128, AKS, BKS, TERMS> Big;
-  typedef Tile<TERMS == 1 ? 128 : 64, AKS, BKS, TERMS> Small;
-  if (plan_for<Big>(a, SYM).ns < plan_for<Small>(a, SYM).ns) return launch_tile<Big, SYM, KIND, TO>(a, s);
-  return launch_tile<Small, SYM, KIND, TO>(a, s);
+  if (big<TERMS>(a, SYM)) return launch_tile<Big<AKS, BKS, TERMS>, SYM, KIND, TO>(a, s);
+  return launch_tile<Small<AKS, BKS, TERMS>, SYM, KIND, TO>(a, s);
+}
+// Bytes of its parts' sums.
+template <int TERMS>
+size_t sum_bytes(int E, int64_t K, int64_t rows, int64_t cols, bool sym) {
+  typedef Small<false, false, TERMS> G;  // (the larger tiles have no parts)
+  ProductArgs a{};
+  a.E = E;
+  a.K = K;
+  a.rows = rows;
+  a.cols = cols;
+  const Plan p = plan_for<G>(a, sym);
+  return big<TERMS>(a, sym) || p.parts == 1 ? 0 : (size_t)kXcds * p.rest * p.parts * G::BM * G::BM * sizeof(float);
 }
 
 int terms_of(const OrthArgs& a) { return a.bf16 && (a.m < a.n ? a.m : a.n) > kOneTerm ? 1 : 2; }
-
-// Most bytes of part sums: a round's tiles, of 256 rows one per CU.
-constexpr size_t kSumBytes = (size_t)kCus * 256 * 256 * sizeof(float);
 
 // Whether the next two steps share a Gram matrix. In one term what was rounded in A is multiplied by
 // up to a^4 on the way to A', which costs most in the middle steps, where singular values of every size
@@ -1339,7 +1379,16 @@ Layout layout_of(const OrthArgs& a) {
     l.bytes = at;
     return l;
   }
-  l.sums = take(kSumBytes);
+  const int64_t longer = l.rows < l.cols ? l.cols : l.rows;
+  size_t sums = 0;
+  auto product = [&](int64_t K, int64_t rows, int64_t cols, bool sym) {
+    const size_t n = terms == 1 ? sum_bytes<1>(a.E, K, rows, cols, sym) : sum_bytes<2>(a.E, K, rows, cols, sym);
+    if (n > sums) sums = n;
+  };
+  product(longer, l.side, l.side, true);
+  product(l.side, l.side, l.side, true);
+  product(l.side, l.rows, l.cols, false);
+  l.sums = take(sums);
   const size_t x = (size_t)a.E * l.rows * l.cols * terms * 2, sq = (size_t)a.E * l.side * l.side * terms * 2;
   for (int i = 0; i < 2; ++i) l.x[i] = i == 0 || a.steps > 2 ? take(x) : 0;
   for (int i = 0; i < 3; ++i) l.sq[i] = i < 2 || a.steps > 1 ? take(sq) : 0;
@@ -1478,10 +1527,14 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
       g.m = a.m;
       g.n = a.n;
       g.vec = aligned16(a.out) && a.n % 8 == 0;
-      g.update = a.momentum != nullptr;
       g.keep = a.keep;
       g.rate = a.rate;
-      e = tall ? product<false, false, false, TERMS, kLast, TI>(g, s) : product<false, true, false, TERMS, kLast, TI>(g, s);
+      if (a.momentum)
+        e = tall ? product<false, false, false, TERMS, kUpdate, TI>(g, s)
+                 : product<false, true, false, TERMS, kUpdate, TI>(g, s);
+      else
+        e = tall ? product<false, false, false, TERMS, kLast, TI>(g, s)
+                 : product<false, true, false, TERMS, kLast, TI>(g, s);
     } else {
       g.f = begin ? (float)scale : 1.f;
       g.d = x[at ^ 1];
