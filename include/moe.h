@@ -488,7 +488,7 @@ moe_status moe_layer_norm(const moe_layer_norm_shape* shape, const void* x, cons
                           const float* gamma, const float* beta, void* out, void* u, float* mean,
                           float* rstd, hipStream_t stream);
 
-/* Bytes of workspace moe_layer_norm_backward needs. Host only. */
+/* Bytes of workspace moe_layer_norm_backward needs: 0 (and a NULL workspace) for few rows. Host only. */
 moe_status moe_layer_norm_backward_workspace_size(const moe_layer_norm_shape* shape, size_t* bytes);
 
 /* Its gradient, with z = (out - mean) rstd and dz = d_u gamma:

@@ -9,7 +9,9 @@
 // Gradient: z = (out - mean) r, dz = d_u gamma, D = d_out + r (dz - mean(dz) - z mean(dz z)),
 // dx = rs D, dy = D; both row means in one reduction. The column sums (dgamma, dbeta) stay in
 // registers while a workgroup walks its rows and go out once per workgroup as partial sums,
-// which a second kernel adds in workgroup order: no atomics, one fixed order.
+// which a second kernel adds in workgroup order: no atomics, one fixed order. They need the row's
+// mean and rstd alone, which are inputs: where rows are few, workgroups of their own take them in the
+// same launch, 64 columns of all rows each.
 // All values and sums are fp32; outputs are rounded once.
 #include "step_kernels.h"
 #include "train_common.h"
@@ -190,22 +192,68 @@ __global__ __launch_bounds__(R::THREADS) void layer_norm_kernel(LayerNormArgs a)
   }
 }
 
+// dgamma and dbeta of 64 columns from c0 on: thread i takes columns c0 + 8 (i % 8) .. + 7 of every
+// THREADS / 8th row, and the threads' sums are added in order.
+template <typename TI, int THREADS>
+__device__ __forceinline__ void column_sums(const LayerNormGradArgs& a, int c0) {
+  constexpr int LANES = THREADS / 8;
+  __shared__ __attribute__((aligned(16))) float cols[LANES][64];
+  const int c = c0 + threadIdx.x % 8 * 8, lane = threadIdx.x / 8;
+  float acc[2][8] = {};
+  if (c < a.d) {
+#pragma unroll 4
+    for (int t = lane; t < a.T; t += LANES) {
+      const size_t at = (size_t)t * a.d + c;
+      float z[8], du[8];
+      load8(static_cast<const TI*>(a.out) + at, z);
+      load8(static_cast<const TI*>(a.d_u) + at, du);
+      const float mean = a.mean[t], r = a.rstd[t];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        acc[0][e] += du[e] * ((z[e] - mean) * r);
+        acc[1][e] += du[e];
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    float* out = s == 0 ? a.dgamma : a.dbeta;
+    if (!out) continue;
+    store8(&cols[lane][threadIdx.x % 8 * 8], acc[s]);
+    __syncthreads();
+    if (threadIdx.x < 64 && c0 + (int)threadIdx.x < a.d) {
+      float v = cols[0][threadIdx.x];
+#pragma unroll 8
+      for (int i = 1; i < LANES; ++i) v += cols[i][threadIdx.x];
+      out[c0 + threadIdx.x] = v;
+    }
+    __syncthreads();
+  }
+}
+
 // Gradient. acc[0], acc[1]: this thread's column sums of dgamma and dbeta over its rows, which
-// the workgroup writes to partial[workgroup][2][d], those that are asked for.
-template <typename TI, class R>
-__global__ __launch_bounds__(R::THREADS) void layer_norm_grad_kernel(LayerNormGradArgs a) {
+// the workgroup writes to partial[workgroup][2][d], those that are asked for. FEW: workgroups from
+// `groups` on take the column sums.
+template <typename TI, class R, bool FEW>
+__global__ __launch_bounds__(R::THREADS) void layer_norm_grad_kernel(LayerNormGradArgs a, int groups) {
   constexpr int TPR = R::TPR, CH = R::CH, ROWS = R::ROWS;
   __shared__ float sh[2 * R::WAVES];
+  if constexpr (FEW) {
+    if ((int)blockIdx.x >= groups) {
+      column_sums<TI, R::THREADS>(a, ((int)blockIdx.x - groups) * 64);
+      return;
+    }
+  }
   const int tid = threadIdx.x % TPR, nch = a.d / 8;
   const float inv_d = 1.0f / (float)a.d;
   float gm[CH][8];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i = tid + c * TPR;
-    if (i < nch && a.T > 0) load8(a.gamma + i * 8, gm[c]);
+    if (i < nch) load8(a.gamma + i * 8, gm[c]);
   }
   float acc[2][CH][8] = {};
-  for (int64_t t0 = (int64_t)blockIdx.x * ROWS; t0 < a.T; t0 += (int64_t)gridDim.x * ROWS) {
+  for (int64_t t0 = (int64_t)blockIdx.x * ROWS; t0 < a.T; t0 += (int64_t)groups * ROWS) {
     const int64_t mine = t0 + threadIdx.x / TPR, t = ROWS > 1 && mine >= a.T ? a.T - 1 : mine;
     const bool real = ROWS == 1 || mine < a.T;
     const size_t row = (size_t)t * a.d;
@@ -222,7 +270,7 @@ __global__ __launch_bounds__(R::THREADS) void layer_norm_grad_kernel(LayerNormGr
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         z[c][e] = (z[c][e] - mean) * r;
-        if (real) {
+        if (!FEW && real) {
           acc[0][c][e] += dz[c][e] * z[c][e];
           acc[1][c][e] += dz[c][e];
         }
@@ -250,6 +298,7 @@ __global__ __launch_bounds__(R::THREADS) void layer_norm_grad_kernel(LayerNormGr
       if (a.dy) store8(static_cast<TI*>(a.dy) + row + i * 8, D[c]);
     }
   }
+  if constexpr (FEW) return;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     if (s == 0 ? !a.dgamma : !a.dbeta) continue;
@@ -336,9 +385,19 @@ hipError_t launch_fwd(const LayerNormArgs& a, hipStream_t s) {
   return fwd<TI, Row<1024, 2>>(a, s);
 }
 
+// Rows so few that the column sums are taken in the same launch.
+constexpr int64_t kFewRows = 512;
+
 template <typename TI, class R>
 hipError_t bwd(const LayerNormGradArgs& a, int64_t groups, hipStream_t s) {
-  layer_norm_grad_kernel<TI, R><<<(unsigned)groups, R::THREADS, 0, s>>>(a);
+  if (a.T <= kFewRows) {
+    const int64_t rows = a.dx || a.dy ? (a.T + R::ROWS - 1) / R::ROWS : 0;
+    const int64_t columns = a.dgamma || a.dbeta ? (a.d + 63) / 64 : 0;
+    if (rows + columns == 0) return hipSuccess;
+    layer_norm_grad_kernel<TI, R, true><<<(unsigned)(rows + columns), R::THREADS, 0, s>>>(a, (int)rows);
+  } else {
+    layer_norm_grad_kernel<TI, R, false><<<(unsigned)groups, R::THREADS, 0, s>>>(a, (int)groups);
+  }
   return hipGetLastError();
 }
 template <typename TI>
@@ -352,14 +411,16 @@ hipError_t launch_bwd(const LayerNormGradArgs& a, hipStream_t s) {
                        : a.d <= 4096     ? bwd<TI, Row<512, 1>>(a, n, s)
                        : a.d <= 8192     ? bwd<TI, Row<1024, 1>>(a, n, s)
                                          : bwd<TI, Row<1024, 2>>(a, n, s);
-  if (e != hipSuccess || (!a.dgamma && !a.dbeta)) return e;
+  if (e != hipSuccess || a.T <= kFewRows || (!a.dgamma && !a.dbeta)) return e;
   layer_norm_sum_kernel<<<dim3((a.d + 63) / 64, 2), 64 * kSumParts, 0, s>>>(a.partial, n, a.d, a.dgamma, a.dbeta);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t layer_norm_grad_workspace(int64_t T, int d) { return (size_t)grad_groups(T, d) * 2 * (size_t)d; }
+size_t layer_norm_grad_workspace(int64_t T, int d) {
+  return T <= kFewRows ? 0 : (size_t)grad_groups(T, d) * 2 * (size_t)d;
+}
 
 hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s) {
   return a.bf16 ? launch_fwd<bf16>(a, s) : launch_fwd<float>(a, s);

@@ -118,7 +118,7 @@ moe_status moe_layer_norm_backward(const moe_layer_norm_shape* shape, const void
   const moe_layer_norm_shape& s = *shape;
   if (!all_aligned16(out, d_u, d_out, gamma, dx, dy, ws)) return MOE_ERR_MISALIGNED;
   if (s.T > 0 && (!out || !d_u || !mean || !rstd || !gamma)) return MOE_ERR_NULL_ARG;
-  if (!ws) return MOE_ERR_NULL_ARG;
+  if (need && !ws) return MOE_ERR_NULL_ARG;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   LayerNormGradArgs m{};
   m.out = out;

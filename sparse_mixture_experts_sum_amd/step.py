@@ -13,7 +13,7 @@ import struct
 
 import torch
 
-from .training import _F32, _call, _matrix, _pointers, _scratch, _type
+from .training import _F32, _call, _matrix, _pointers, _scratch, _type, _workspace_bytes
 
 # the structs of include/moe.h, native alignment
 _NORM_SHAPE = struct.Struct("@qqiff0q").pack
@@ -81,12 +81,16 @@ def moe_layer_norm_backward(out, d_u, mean, rstd, gamma, *, d_out=None, residual
     po, pdu, pdo, pm, pr, pg = _pointers(
         ((out, "out", rows, dtype), (d_u, "d_u", rows, dtype), (d_out, "d_out", rows, dtype),
          (mean, "mean", (T,), _F32), (rstd, "rstd", (T,), _F32), (gamma, "gamma", (d,), _F32)), dev)
-    ws, ws_bytes = _scratch("moe_layer_norm_backward_workspace_size", s, dev, workspace)
+    ws = pws = None
+    ws_bytes = _workspace_bytes("moe_layer_norm_backward_workspace_size", s)
+    if ws_bytes:
+        ws, ws_bytes = _scratch("moe_layer_norm_backward_workspace_size", s, dev, workspace)
+        pws = ws.data_ptr()
     dx = torch.empty_like(out)
     dy = torch.empty_like(out) if want_dy else None
     dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
     _call("moe_layer_norm_backward", dev, s, po, pdu, pdo, pm, pr, pg, dx.data_ptr(),
-          None if dy is None else dy.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws_bytes)
+          None if dy is None else dy.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), pws, ws_bytes)
     return {"dx": dx, "dy": dy, "dgamma": dgamma, "dbeta": dbeta}
 
 

@@ -113,7 +113,7 @@ WIDTHS = [8, 64, 120, 128, 136, 256, 264, 512, 520, 1000, 1024, 1032, 2048, 2056
 @pytest.mark.parametrize("dt", [BF16, FP32])
 @pytest.mark.parametrize("d", WIDTHS)
 def test_layer_norm_and_gradient(moe, d, dt):
-    for T, y, beta in ((1, True, True), (37, False, False), (533, True, True)):
+    for T, y, beta in ((1, True, True), (37, False, False), (512, True, True), (533, True, True)):
         say("layer norm", T, d, dt)
         x, gm, bt, yy, du, do = norm_inputs(T, d, dt, y, beta)
         scale, eps = (0.75 if y else 1.0), 1e-5
@@ -217,11 +217,12 @@ def test_layer_norm_sum_and_norm_are_two_calls(moe):
     assert moe.moe_layer_norm(x, gm, want_stats=False)["mean"] is None
 
 
-def test_layer_norm_c_outputs_left_out_and_in_place(moe):
+@pytest.mark.parametrize("T", [77, 601])
+def test_layer_norm_c_outputs_left_out_and_in_place(moe, T):
     from sparse_mixture_experts_sum_amd import step as ST
-    x, gm, bt, y, du, do = (t.cuda() for t in norm_inputs(77, 520, BF16, True, True))
+    x, gm, bt, y, du, do = (t.cuda() for t in norm_inputs(T, 520, BF16, True, True))
     ref = moe.moe_layer_norm(x, gm, bt, y=y, residual_scale=0.5)
-    shape = ST._NORM_SHAPE(77, 520, 1, 1e-5, 0.5)
+    shape = ST._NORM_SHAPE(T, 520, 1, 1e-5, 0.5)
     xx, u = x.clone(), torch.empty_like(x)
     ST._call("moe_layer_norm", x.device, shape, xx.data_ptr(), y.data_ptr(), gm.data_ptr(), bt.data_ptr(), xx.data_ptr(),
              u.data_ptr(), None, None)

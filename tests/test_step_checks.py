@@ -161,11 +161,11 @@ def test_c_layer_norm_arguments(lib):
     assert fwd(T=0, x=None, u=None, gamma=None) == OK
 
     n = ctypes.c_size_t(0)
-    assert lib.moe_layer_norm_backward_workspace_size(norm_shape(), ctypes.byref(n)) == OK and n.value >= 2 * 64 * 4
+    assert lib.moe_layer_norm_backward_workspace_size(norm_shape(T=10000), ctypes.byref(n)) == OK and n.value >= 2 * 64 * 4
     assert lib.moe_layer_norm_backward_workspace_size(norm_shape(), None) == NULL_ARG
 
     def bwd(out=A, d_u=B, mean=C, rstd=C, gamma=D, dx=U, ws=U, ws_bytes=n.value):
-        return lib.moe_layer_norm_backward(norm_shape(), out, d_u, None, mean, rstd, gamma, dx, None, None, None, ws,
+        return lib.moe_layer_norm_backward(norm_shape(T=10000), out, d_u, None, mean, rstd, gamma, dx, None, None, None, ws,
                                            ws_bytes, None)
     assert bwd(out=None) == bwd(d_u=None) == bwd(mean=None) == bwd(rstd=None) == bwd(gamma=None) == bwd(ws=None) == NULL_ARG
     assert bwd(dx=U + 8) == MISALIGNED
