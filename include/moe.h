@@ -496,7 +496,7 @@ moe_status moe_layer_norm_backward_workspace_size(const moe_layer_norm_shape* sh
  *   dx = residual_scale D,  dy = D,  dgamma = sum_t d_u z,  dbeta = sum_t d_u
  *   out [T, d] dtype (the forward's rounded sum; x where it had no y, with residual_scale 1),
  *   d_u, d_out [T, d] dtype, mean, rstd [T], gamma [d] fp32
- *   dx, dy [T, d] dtype, dgamma, dbeta [d] fp32: NULL to skip. dx may be d_out or d_u.
+ *   dx, dy [T, d] dtype, dgamma, dbeta [d] fp32: NULL to skip. dx and dy may be d_out or d_u.
  * With T = 0 dgamma and dbeta are zero. eps is not looked at. */
 moe_status moe_layer_norm_backward(const moe_layer_norm_shape* shape, const void* out,
                                    const void* d_u, const void* d_out, const float* mean,
@@ -533,7 +533,7 @@ typedef struct moe_orthogonalize_shape {
 /* Bytes of workspace moe_orthogonalize and moe_muon_update need. Host only. */
 moe_status moe_orthogonalize_workspace_size(const moe_orthogonalize_shape* shape, size_t* bytes);
 
-/*   g, out [E, m, n] dtype, row-major; out may be g. ws 256-byte aligned; g and out need no
+/*   g, out [E, m, n] dtype, row-major; out is g or apart from it. ws 256-byte aligned; g and out need no
  *   alignment beyond their type's (rows of whole 16 bytes, 16-byte aligned, are faster). */
 moe_status moe_orthogonalize(const moe_orthogonalize_shape* shape, const void* g, void* out,
                              void* ws, size_t ws_bytes, hipStream_t stream);
@@ -547,7 +547,7 @@ typedef struct moe_muon_params {
   int32_t nesterov;                         /* 0 or 1 */
 } moe_muon_params;
 
-/*   w, g [E, m, n] dtype, m [E, m, n] fp32. */
+/*   w, g [E, m, n] dtype, m [E, m, n] fp32: three tensors that share no memory. */
 moe_status moe_muon_update(const moe_orthogonalize_shape* shape, const moe_muon_params* params,
                            void* w, const void* g, float* m, void* ws, size_t ws_bytes,
                            hipStream_t stream);

@@ -590,7 +590,10 @@ class SparseMoE:
         and W_down, in place, from ``backward``'s dW_gate, dW_up and dW_down. Each expert's update
         is scaled by sqrt(max(1, its columns / its rows)), the ratio of its output's width to its
         input's. The momentum (fp32, zeros before the first step) is kept in ``self.momentum``; so is a
-        workspace, which the steps of one layer share: they run one after another."""
+        workspace, which the steps of one layer share: they run one after another. The first step, or
+        filling ``self.momentum`` with a tensor for each weight, comes before a capture."""
+        if len(self.momentum) < 3 and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("muon_update's first step makes the momentum: take it before the capture")
         for name in ("W_gate", "W_up", "W_down"):
             w = getattr(self, name)
             m = self.momentum.get(name)

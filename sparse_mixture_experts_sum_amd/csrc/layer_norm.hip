@@ -391,7 +391,8 @@ hipError_t launch_fwd(const LayerNormArgs& a, hipStream_t s) {
   return fwd<TI, Row<1024, 2>>(a, s);
 }
 
-// Rows so few that the column sums are taken in the same launch.
+// Rows so few that the column sums are taken in the same launch; in one before it where the rows'
+// results go over what the sums read.
 constexpr int64_t kFewRows = 512;
 
 template <typename TI, class R>
@@ -400,7 +401,13 @@ hipError_t bwd(const LayerNormGradArgs& a, int64_t groups, hipStream_t s) {
     const int64_t rows = a.dx || a.dy ? (a.T + R::ROWS - 1) / R::ROWS : 0;
     const int64_t columns = a.dgamma || a.dbeta ? (a.d + 63) / 64 : 0;
     if (rows + columns == 0) return hipSuccess;
-    layer_norm_grad_kernel<TI, R, true><<<(unsigned)(rows + columns), R::THREADS, 0, s>>>(a, (int)rows);
+    auto over = [&](const void* p) { return p && (p == a.d_u || p == a.out); };
+    if (columns && (over(a.dx) || over(a.dy))) {
+      layer_norm_grad_kernel<TI, R, true><<<(unsigned)columns, R::THREADS, 0, s>>>(a, 0);
+      if (rows) layer_norm_grad_kernel<TI, R, true><<<(unsigned)rows, R::THREADS, 0, s>>>(a, (int)rows);
+    } else {
+      layer_norm_grad_kernel<TI, R, true><<<(unsigned)(rows + columns), R::THREADS, 0, s>>>(a, (int)rows);
+    }
   } else {
     layer_norm_grad_kernel<TI, R, false><<<(unsigned)groups, R::THREADS, 0, s>>>(a, (int)groups);
   }

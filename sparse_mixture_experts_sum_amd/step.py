@@ -107,6 +107,12 @@ def _matrices(t, name):
     return E, m, n
 
 
+def _overlap(a, b):
+    """Whether two contiguous tensors share memory."""
+    pa, pb = a.data_ptr(), b.data_ptr()
+    return pa < pb + b.numel() * b.element_size() and pb < pa + a.numel() * a.element_size()
+
+
 def _orth_shape(t, E, m, n, steps, coefficients, eps):
     if len(coefficients) != 3:
         raise ValueError("coefficients are three numbers: a, b, c")
@@ -132,6 +138,8 @@ def moe_orthogonalize(g, *, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, out=N
     dev = g.device
     s = _orth_shape(g, E, m, n, steps, coefficients, eps)
     pg, pout = _pointers(((g, "g", g.shape, g.dtype), (out, "out", g.shape, g.dtype)), dev)
+    if out is not None and pout != pg and _overlap(g, out):
+        raise ValueError("out must be g itself or apart from it")
     ws, ws_bytes = _scratch("moe_orthogonalize_workspace_size", s, dev, workspace)
     if out is None:
         out = torch.empty_like(g)
@@ -157,8 +165,8 @@ def moe_muon_update(w, g, m, *, lr, momentum=0.95, nesterov=True, weight_decay=0
         raise ValueError("moe_muon_update needs g and m")
     s = _orth_shape(w, E, rows, cols, steps, coefficients, eps)
     pw, pg, pm = _pointers(((w, "w", w.shape, dtype), (g, "g", w.shape, dtype), (m, "m", w.shape, _F32)), dev)
-    if pw == pg or pw == pm or pg == pm:
-        raise ValueError("w, g and m must be three tensors")
+    if _overlap(w, g) or _overlap(w, m) or _overlap(g, m):
+        raise ValueError("w, g and m must be three tensors that share no memory")
     ws, ws_bytes = _scratch("moe_orthogonalize_workspace_size", s, dev, workspace)
     _call("moe_muon_update", dev, s, _MUON_PARAMS(lr, momentum, weight_decay, scale, 1 if nesterov else 0),
           pw, pg, pm, ws.data_ptr(), ws_bytes)

@@ -248,6 +248,27 @@ def test_layer_norm_c_outputs_left_out_and_in_place(moe, T):
         assert torch.equal(to, full["dx"])
 
 
+@pytest.mark.parametrize("T,d", [(1, 64), (300, 1024), (512, 8200), (513, 1024)])
+def test_layer_norm_gradient_over_its_inputs(moe, T, d):
+    """Every output, dx or dy over d_u or d_out: the column sums are those of the d_u that was given."""
+    from sparse_mixture_experts_sum_amd import step as ST
+    from sparse_mixture_experts_sum_amd.training import _scratch
+    x, gm, _, _, du, do = (t.cuda() if t is not None else None for t in norm_inputs(T, d, BF16, False, False))
+    f = moe.moe_layer_norm(x, gm)
+    want = moe.moe_layer_norm_backward(x, du, f["mean"], f["rstd"], gm, d_out=do, residual_scale=0.5, want_dy=True)
+    shape = ST._NORM_SHAPE(T, d, 1, 1e-5, 0.5)
+    ws, n = _scratch("moe_layer_norm_backward_workspace_size", shape, x.device, None)
+    for over in ("dx", "dy", "both"):
+        a, b = du.clone(), do.clone()
+        dx, dy = (a, b) if over == "both" else (a, torch.empty_like(a)) if over == "dx" else (torch.empty_like(a), a)
+        dg, db = torch.empty_like(gm), torch.empty_like(gm)
+        ST._call("moe_layer_norm_backward", x.device, shape, x.data_ptr(), a.data_ptr(), b.data_ptr(), f["mean"].data_ptr(),
+                 f["rstd"].data_ptr(), gm.data_ptr(), dx.data_ptr(), dy.data_ptr(), dg.data_ptr(), db.data_ptr(),
+                 ws.data_ptr(), n)
+        for k, v in zip(("dx", "dy", "dgamma", "dbeta"), (dx, dy, dg, db)):
+            assert torch.equal(v, want[k]), (over, k)
+
+
 # ---- orthogonalisation ---------------------------------------------------------------------
 def plain(g, steps, co=NS, eps=1e-7, dtype=torch.float64):
     """The definition, matrix by matrix of the last two dimensions."""
@@ -396,6 +417,37 @@ def test_orthogonalize_scales_exactly(moe):
     check_orth(small, g * 2.0 ** -40, 5, 2)
 
 
+@pytest.mark.parametrize("m,n,dt", [(262144, 8200, BF16), (8200, 262144, FP32)])
+def test_orthogonalize_past_2_31_values(moe, m, n, dt):
+    """One step of a matrix with the longest side there is and more than 2^31 values, 256 of its long side
+    at a time against P X with P in 64 bits. Four directions hold four fifths of it (singular values of
+    0.45: P is far from a I). Tolerance, of each of these parts' norm: half a step of the result; where one term is
+    kept 2^-9 for P's rounding of 2^-11 and the products, and A's in fp16's last steps (values of
+    1 / s lie among them), 2^-25 s of its norm at most, times |b| + 2 |c|."""
+    tall, s, l = m > n, min(m, n), max(m, n)
+    g = torch.empty(m, n, device="cuda", dtype=dt)
+    side = (lambda t, i, w: t[i:i + w].t()) if tall else (lambda t, i, w: t[:, i:i + w])
+    r = torch.Generator(device="cuda").manual_seed(11)
+    u = torch.randn(s, 4, device="cuda", generator=r)
+    for i in range(0, l, 8192):
+        x = torch.randn(s, 8192, device="cuda", generator=r) + u @ torch.randn(4, 8192, device="cuda", generator=r)
+        side(g, i, 8192).copy_(x)
+    got = moe.moe_orthogonalize(g, steps=1)
+    A = torch.zeros(s, s, device="cuda")
+    for i in range(0, l, 8192):  # (sums of 8192 fp32 terms, and of 32 of these)
+        x = side(g, i, 8192).float().contiguous()
+        A += x @ x.t()
+    t = A.diagonal().double().sum().sqrt() + 1e-7  # the norm
+    A = A.double() / t ** 2
+    for i in (0, 128, 131072 - 64, l - 512, l - 256):
+        x = side(g, i, 256).double().contiguous() / t
+        Ax = A @ x
+        want = NS[0] * x + NS[1] * Ax + NS[2] * (A @ Ax)
+        off = side(got, i, 256).double() - want
+        tol = HALF[dt] + (2.0 ** -9 + 2.0 ** -25 * s * (abs(NS[1]) + 2 * abs(NS[2])) if dt is BF16 else 1e-5)
+        assert float(off.norm() / want.norm()) <= tol, i
+
+
 @pytest.mark.parametrize("dt", [BF16, FP32])
 def test_orthogonalize_special_matrices(moe, dt):
     """Zeros give zeros; a value that is not finite spoils its own matrix and no other."""
@@ -471,6 +523,18 @@ def test_orthogonalize_on_two_streams(moe):
         got.append((oa, ob))
     torch.cuda.synchronize()
     assert all(torch.equal(x, wa) and torch.equal(y, wb) for x, y in got)
+
+
+def test_shared_memory_is_refused(moe):
+    buf = torch.randn(4, 40, 72, device="cuda")
+    a, b, c = buf[:2], buf[1:3], buf[2:]
+    with pytest.raises(ValueError, match="apart"):
+        moe.moe_orthogonalize(a, out=b)
+    assert torch.equal(moe.moe_orthogonalize(a, out=c), moe.moe_orthogonalize(a))
+    m = torch.zeros(2, 40, 72, device="cuda")
+    for w, g, mom in ((a, a, m), (a, b, m), (a, m, b), (m, a, a), (m, b, a)):
+        with pytest.raises(ValueError, match="share no memory"):
+            moe.moe_muon_update(w, g, mom, lr=0.1)
 
 
 # ---- the update step -------------------------------------------------------------------------
@@ -615,6 +679,22 @@ def test_training_step_captured(moe):
         assert torch.equal(out, w)
     for n in ("W_gate", "W_up", "W_down"):
         assert torch.equal(getattr(held, n), getattr(eager, n)) and torch.equal(held.momentum[n], eager.momentum[n])
+
+
+def test_first_update_in_a_capture_is_refused(moe):
+    """A momentum made by the captured call would be zeroed again by every replay."""
+    block, _, _, x = layer(moe, BF16)
+    block(x.cuda())
+    grads = block.backward(draw(gen(1), *x.shape).cuda())
+    before = block.W_up.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="before the capture"):
+            block.muon_update(grads, lr=0.02)
+    assert not block.momentum and torch.equal(block.W_up, before)
+    block.muon_update(grads, lr=0.02)
+    assert not torch.equal(block.W_up, before)
 
 
 def test_layer_with_one_norm_of_the_two(moe):
