@@ -31,6 +31,8 @@
 // 2048, then hi hi.
 #include <math.h>
 
+#include <type_traits>
+
 #include "matmul_tile.h"
 #include "step_kernels.h"
 #include "train_common.h"
@@ -53,6 +55,12 @@ constexpr int kOneTerm = 128;       // bf16 matrices with short sides past it ar
 // Place of a value of a matrix of the iteration: panels of 32 columns, each with all rows.
 __device__ __forceinline__ int64_t in_panels(int64_t rows, int64_t r, int64_t c) {
   return ((c >> 5) * rows + r) * 32 + (c & 31);
+}
+
+// The same for matrices that are loaded as fragments: of 32 rows and 16 columns one run of 1 KB, lane l's
+// 16 bytes (row l % 32, columns 8 (l / 32) ..) at 16 l.
+__device__ __forceinline__ int64_t in_fragments(int64_t rows, int64_t r, int64_t c) {
+  return (((c >> 4) * (rows >> 5) + (r >> 5)) * 64 + (c >> 3 & 1) * 32 + (r & 31)) * 8 + (c & 7);
 }
 
 // ---- the matrix in, and its norm -------------------------------------------------------
@@ -169,11 +177,11 @@ struct Scale {
   }
 };
 
-// u 2^p in fp16 terms, padded with zeros to rows x cols and in panels of 32 columns, and each matrix's
-// Scale::first. Eight threads take 64 columns of a row: whole lines of g, half lines of two panels.
+// u 2^p in fp16 terms, padded with zeros to rows x cols and in panels of 32 columns (and in `frags`, where
+// given, as fragments), and each matrix's Scale::first. Eight threads take 64 columns of a row: whole lines of g, half lines of two panels.
 template <typename TI, int TERMS>
 __global__ __launch_bounds__(256) void scale_kernel(OrthArgs a, bool vec, const double* partial, int blocks,
-                                                    double scale, f16* x, int64_t rows, int64_t cols,
+                                                    double scale, f16* x, f16* frags, int64_t rows, int64_t cols,
                                                     int64_t plane, float* first) {
   __shared__ double sh[4];
   const int e = blockIdx.y;
@@ -209,6 +217,11 @@ __global__ __launch_bounds__(256) void scale_kernel(OrthArgs a, bool vec, const 
     f16* to = out + in_panels(rows, r, c);
     *reinterpret_cast<f16x8*>(to) = hi;
     if constexpr (TERMS == 2) *reinterpret_cast<f16x8*>(to + plane) = lo;
+    if (frags) {
+      to = frags + (int64_t)e * rows * cols + in_fragments(rows, r, c);
+      *reinterpret_cast<f16x8*>(to) = hi;
+      if constexpr (TERMS == 2) *reinterpret_cast<f16x8*>(to + plane) = lo;
+    }
   }
 }
 
@@ -525,8 +538,8 @@ struct Weights {
   }
 };
 
-// What a product does with its sums.
-enum { kProduct, kPolynomial, kLast, kUpdate };  // f S; f S + p c + q I; the result; it into the weights
+// What a product does with its sums: f S, as fragments; f S; f S + p c + q I; the result; it into the weights.
+enum { kFragments, kProduct, kPolynomial, kLast, kUpdate };
 
 // acc[nb][mb][4 q + i] is row lane % 32 of block mb, column 8 q + 4 (lane / 32) + i of block nb.
 // 32 rows at a time go through a piece of LDS of the wave's own (16-byte chunk c of a row at
@@ -553,6 +566,9 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
   constexpr bool AHEAD = KIND == kPolynomial || KIND == kUpdate;
   Terms<TERMS> old[KIND == kPolynomial ? 2 : 1][N];
   Weights<TO> weights[KIND == kUpdate ? 2 : 1][N];
+  auto place = [&](int64_t r, int64_t c) {
+    return KIND == kFragments ? in_fragments(a.rows, r, c) : in_panels(a.rows, r, c);
+  };
   auto row_of = [&](int pass, int i) { return m0 + pass / (G::MB / BLOCKS) * 32 + i * RPS + r0; };
   auto col_of = [&](int pass) { return n0 + pass % (G::MB / BLOCKS) * COLS + c0 * 8; };
   auto fetch = [&](int pass) {
@@ -624,7 +640,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
           hi[i][k] = h;
           lo[i][k] = l;
         }
-        f16* d = a.d + t.e * a.rows * a.cols + in_panels(a.rows, gr, gc);
+        f16* d = a.d + t.e * a.rows * a.cols + place(gr, gc);
         *reinterpret_cast<f16x8*>(d) = hi[i];
         if constexpr (TERMS == 2) *reinterpret_cast<f16x8*>(d + a.d_plane) = lo[i];
       }
@@ -649,7 +665,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const Item& t, 
             const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * COLS * 2));
             const s16x8 v{v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
             const int64_t gr = n0 + pass % (G::MB / BLOCKS) * COLS + 16 * i + (ln & 15), gc = m0 + mb * 32 + 8 * (ln >> 4);
-            st16(a.d + t.e * a.rows * a.cols + in_panels(a.rows, gr, gc) + term * a.d_plane, __builtin_bit_cast(u32x4, v));
+            st16(a.d + t.e * a.rows * a.cols + place(gr, gc) + term * a.d_plane, __builtin_bit_cast(u32x4, v));
           }
         }
       }
@@ -1233,6 +1249,251 @@ __global__ __launch_bounds__(kThreads) void thin_polynomial_kernel(OrthArgs a, T
   }
 }
 
+// ---- short sides of 129 to 256 -----------------------------------------------------------
+// Where launches are what counts, a step is two: the Gram matrix by the tiles above, and this one, which
+// takes 32 rows of P and, without leaving LDS, their product with 128 columns of X (every workgroup of
+// a row of them computes the same rows of P). X is kept with its long side along the rows, [long][256],
+// wide matrices turned: then both products' right operands are rows, whose fragments only one wave
+// uses. It loads them itself, those of A into registers and those of X into its own piece of LDS while
+// it computes P; A, and X a second time, are kept as those fragments. 5 of 201 x 333 fp32: 12 us a launch,
+// twelve launches in place of nineteen.
+constexpr int kStrip = 256;      // the padded short side
+constexpr int kStripRows = 32;   // of P, of a workgroup
+constexpr int kStripLong = 128;  // of the long side, of a workgroup
+
+// u 2^p in fp16 terms as scale_kernel leaves it, of the transposed matrix: 32 x 64 of it by way of LDS.
+template <typename TI, int TERMS>
+__global__ __launch_bounds__(256) void scale_turned_kernel(OrthArgs a, bool vec, const double* partial, int blocks,
+                                                           double scale, f16* x, f16* frags, int64_t rows, int64_t plane,
+                                                           float* first) {
+  __shared__ double sh[4];
+  __shared__ __attribute__((aligned(16))) f16 tile[TERMS][64][40];
+  const int e = blockIdx.y;
+  const double sq = block_sum((int)threadIdx.x < blocks ? partial[(int64_t)e * blocks + threadIdx.x] : 0.0, sh);
+  const Scale sc(sqrt(sq) + (double)a.eps, scale);
+  if (blockIdx.x == 0 && threadIdx.x == 0) first[e] = sc.first;
+  const int64_t r0 = (int64_t)(blockIdx.x % (kStrip / 32)) * 32, c0 = (int64_t)(blockIdx.x / (kStrip / 32)) * 64;
+  const int64_t r = r0 + threadIdx.x / 8, c = c0 + threadIdx.x % 8 * 8, at = ((int64_t)e * a.m + r) * a.n + c;
+  const int n = r < a.m ? (int)max(min((int64_t)8, a.n - c), (int64_t)0) : 0;
+  float u[8] = {};
+  if (n > 0) {
+    load_row(static_cast<const TI*>(a.g) + at, n, vec, u);
+    if (a.momentum) {
+      float m[8];
+      load_row(a.momentum + at, n, vec, m);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = update_of(a, m[k], u[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    f16 h, l;
+    split((float)((double)u[k] * sc.by), h, l);
+    tile[0][c - c0 + k][r - r0] = h;
+    if constexpr (TERMS == 2) tile[1][c - c0 + k][r - r0] = l;
+  }
+  __syncthreads();
+  const int64_t mat = (int64_t)e * rows * kStrip, i = c0 + threadIdx.x / 4, j = r0 + threadIdx.x % 4 * 8;
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) {
+    const f16x8 v = *reinterpret_cast<const f16x8*>(&tile[t][threadIdx.x / 4][threadIdx.x % 4 * 8]);
+    *reinterpret_cast<f16x8*>(x + mat + in_panels(rows, i, j) + t * plane) = v;
+    *reinterpret_cast<f16x8*>(frags + mat + in_fragments(rows, i, j) + t * plane) = v;
+  }
+}
+
+struct StripArgs {
+  const f16* A;  // [E][256 x 256], as fragments
+  const f16* x;  // [E][rows x 256], as fragments
+  f16 *to, *panels;  // the next X, as fragments and in panels
+  const float* first;
+  int64_t a_plane, x_plane;
+  int rows, power;
+  float f;  // times first^power
+};
+
+// A product with 32 rows in LDS, of N steps of 16 from k0 on: lane l has row l % 32 of those in LDS and
+// columns 8 q + 4 (l / 32) + t, or, TURNED, a row of the other operand and those columns of LDS's rows.
+// frag(term, k): the other operand's fragments.
+template <int TERMS, bool TURNED, int N, class Frag>
+__device__ __forceinline__ f32x16 strip_times(const InLds& m, int k0, int lane, Frag frag) {
+  const int ln = here(lane);
+  auto mfma = [](f16x8 lds, f16x8 reg, f32x16 to) {
+    return TURNED ? __builtin_amdgcn_mfma_f32_32x32x16_f16(lds, reg, to, 0, 0, 0)
+                  : __builtin_amdgcn_mfma_f32_32x32x16_f16(reg, lds, to, 0, 0, 0);
+  };
+  f32x16 sum{}, cross{}, acc{};
+  f16x8 hi[2], lo[2];  // (of one step ahead)
+  auto read = [&](int k) {
+    hi[k % 2] = InLds::rows(m.hi, m, 0, k0 + 16 * k, ln);
+    if constexpr (TERMS == 2) lo[k % 2] = InLds::rows(m.lo, m, 0, k0 + 16 * k, ln);
+  };
+  read(0);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const f16x8 h = frag(0, k), l = TERMS == 2 ? frag(1, k) : h;
+    if (k + 1 < N) read(k + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    acc = mfma(hi[k % 2], h, acc);
+    if constexpr (TERMS == 2) {
+      cross = mfma(lo[k % 2], h, cross);
+      cross = mfma(hi[k % 2], l, cross);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (k % 4 == 3) {  // (sums of hi hi of 64 terms, as above)
+      sum += acc;
+      acc = f32x16{};
+    }
+  }
+  if constexpr (TERMS == 2) sum += kLo * cross;
+  return sum;
+}
+
+template <typename TI, int TERMS, bool LAST>
+__global__ __launch_bounds__(kThreads) void strip_kernel(OrthArgs a, StripArgs t) {
+  constexpr int STRIPS = kStrip / kStripRows, STEPS = kStrip / 16, BLOCKS = kStripLong / 32;
+  // rows of A, then of P; and each wave's part of X: 32 rows, half of the summed axis
+  __shared__ __attribute__((aligned(1024))) char ps[TERMS][kStripRows * kStrip * 2];
+  __shared__ __attribute__((aligned(1024))) char xs[kWaves][TERMS][STEPS / 2][1024];
+  const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = ln >> 5;
+  // the workgroups of the same rows of X are on one XCD
+  const int chunks = t.rows / kStripLong, group = blockIdx.x / kXcds;
+  const int chunk = group / STRIPS * kXcds + blockIdx.x % kXcds, e = chunk / chunks;
+  if (e >= a.E) return;
+  const int i0 = group % STRIPS * kStripRows, l0 = chunk % chunks * kStripLong + wave % BLOCKS * 32;
+  const int k0 = wave / BLOCKS * (STEPS / 2);
+  const InLds P{ps[0], ps[TERMS - 1], kStrip * 2};
+  const f16* const mat = t.A + (int64_t)e * kStrip * kStrip;
+  constexpr int EACH = kStripRows * kStrip / 8 / kThreads;
+  auto place = [&](int n, int& r, int& c) {
+    const int i = threadIdx.x + n * kThreads;
+    r = i % kStripRows;
+    c = i / kStripRows * 8;
+  };
+  u32x4 rows[TERMS][EACH];
+  int r, c;
+#pragma unroll
+  for (int n = 0; n < EACH; ++n) {
+    place(n, r, c);
+#pragma unroll
+    for (int term = 0; term < TERMS; ++term) rows[term][n] = ld16(mat + term * t.a_plane + in_fragments(kStrip, i0 + r, c));
+  }
+  f16x8 own[TERMS][STEPS];  // this wave's 32 columns of A (which is its own transpose)
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+    for (int term = 0; term < TERMS; ++term)
+      own[term][k] = __builtin_bit_cast(f16x8, ld16(mat + term * t.a_plane + in_fragments(kStrip, wave * 32, 16 * k) + ln * 8));
+  const f16* const x = t.x + (int64_t)e * t.rows * kStrip;
+#pragma unroll
+  for (int k = 0; k < STEPS / 2; ++k)
+#pragma unroll
+    for (int term = 0; term < TERMS; ++term)
+      __builtin_amdgcn_global_load_lds(x + term * t.x_plane + in_fragments(t.rows, l0, 16 * (k0 + k)) + ln * 8,
+                                       (lds_void*)xs[wave][term][k], 16, 0, 0);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int n = 0; n < EACH; ++n) {
+    place(n, r, c);
+#pragma unroll
+    for (int term = 0; term < TERMS; ++term) *reinterpret_cast<u32x4*>(ps[term] + P.at(r, c)) = rows[term][n];
+  }
+  __syncthreads();
+  const f32x16 sq = strip_times<TERMS, false, STEPS>(P, 0, ln, [&](int term, int k) { return own[term][k]; });
+  __syncthreads();  // (everyone has read A)
+  r = ln & 31;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    c = wave * 32 + 8 * q + 4 * half;
+    f16x4* const at[2] = {reinterpret_cast<f16x4*>(P.hi + P.at(r, c)), reinterpret_cast<f16x4*>(P.lo + P.at(r, c))};
+    const f16x4 h = *at[0], l = *at[1];
+    f16x4 ph, pl;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float old = TERMS == 2 ? (float)h[k] + kLo * (float)l[k] : (float)h[k];
+      f16 v0, v1;
+      split(a.c * sq[4 * q + k] + a.b * old + (i0 + r == c + k ? a.a : 0.f), v0, v1);
+      ph[k] = v0;
+      pl[k] = v1;
+    }
+    *at[0] = ph;
+    if constexpr (TERMS == 2) *at[1] = pl;
+  }
+  wait_vmcnt<0>();  // X
+  __syncthreads();
+  const bool tall = a.m > a.n, turned = !LAST || tall;
+  auto times = [&](auto flag) {
+    return strip_times<TERMS, decltype(flag)::value, STEPS / 2>(P, 16 * k0, ln, [&](int term, int k) {
+      return *reinterpret_cast<const f16x8*>(xs[wave][term][k] + ln * 16);
+    });
+  };
+  f32x16 v = turned ? times(std::true_type{}) : times(std::false_type{});
+  // Two waves have half of each sum: each takes half of the values.
+  const bool upper = wave >= BLOCKS;
+  {
+    f32x4* const to = reinterpret_cast<f32x4*>(xs[wave][0][0]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      f32x4 w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = upper ? v[4 * q + k] : v[4 * (q + 2) + k];
+      to[q * 64 + ln] = w;
+    }
+    __syncthreads();
+    const f32x4* const from = reinterpret_cast<const f32x4*>(xs[wave ^ BLOCKS][0][0]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const f32x4 w = from[q * 64 + ln];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[4 * q + k] = (upper ? v[4 * (q + 2) + k] : v[4 * q + k]) + w[k];
+    }
+  }
+  float by = t.f;
+  for (int i = 0; i < t.power; ++i) by *= t.first[e];
+  const int j0 = (upper ? 16 : 0) + 4 * half;  // of value 0; value 4 q + k is 8 q + k behind it
+  if constexpr (!LAST) {
+    const int64_t at = (int64_t)e * t.rows * kStrip;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      f16x4 h, l;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f16 v0, v1;
+        split(by * v[4 * q + k], v0, v1);
+        h[k] = v0;
+        l[k] = v1;
+      }
+      const int64_t row = l0 + (ln & 31), col = i0 + j0 + 8 * q;
+      f16 *to = t.to + at + in_fragments(t.rows, row, col), *panel = t.panels + at + in_panels(t.rows, row, col);
+      *reinterpret_cast<f16x4*>(to) = h;
+      *reinterpret_cast<f16x4*>(panel) = h;
+      if constexpr (TERMS == 2) {
+        *reinterpret_cast<f16x4*>(to + t.x_plane) = l;
+        *reinterpret_cast<f16x4*>(panel + t.x_plane) = l;
+      }
+    }
+  } else {
+    const int row = (tall ? l0 : i0) + (ln & 31), col = (tall ? i0 : l0) + j0;
+    if (row >= a.m) return;
+    TI* out = static_cast<TI*>(a.out) + ((int64_t)e * a.m + row) * a.n + col;
+    float w[2][4] = {};
+    if (a.momentum) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (col + 8 * q + k < a.n) w[q][k] = (float)out[8 * q + k];
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float u = by * v[4 * q + k];
+        if (col + 8 * q + k < a.n) out[8 * q + k] = (TI)(a.momentum ? a.keep * w[q][k] - a.rate * u : u);
+      }
+  }
+}
+
 // ---- host ------------------------------------------------------------------------------
 int64_t padded(int64_t n) { return (n + kPad - 1) / kPad * kPad; }
 size_t aligned(size_t n) { return (n + 255) / 256 * 256; }
@@ -1345,11 +1606,22 @@ int thin_columns(const OrthArgs& a) {
 }
 int64_t thin_groups(const OrthArgs& a) { return (long_side(a) + thin_columns(a) - 1) / thin_columns(a); }
 
+// Matrices whose steps are two launches each: those whose workgroups are a quarter of what the chip holds (us,
+// before and so: 2 of 200 x 1000 bf16 129, 94; 2 of 1500 x 200 bf16 135, 101; 5 of 201 x 333 fp32 113, 104; past it 8 of
+// 256 x 1024 bf16 132, 127; 16 of 160 x 800 bf16 135, 161; 16 of 256 x 256 fp32 105, 118). What they read of
+// L2, 192 KB a term of each workgroup, is the time then.
+int64_t strip_groups(const OrthArgs& a) {
+  return (int64_t)a.E * (kStrip / kStripRows) * (padded(long_side(a)) / kStripLong);
+}
+bool is_strip(const OrthArgs& a) {
+  return padded(a.m < a.n ? a.m : a.n) == kStrip && strip_groups(a) * terms_of(a) <= kCus;
+}
+
 // Pieces of the workspace.
 struct Layout {
   int64_t rows, cols, side;  // padded
   int blocks;                // partial sums per matrix
-  size_t partial, first, sums, x[2], sq[3], bytes;
+  size_t partial, first, sums, x[3], sq[3], bytes;
 };
 Layout layout_of(const OrthArgs& a) {
   Layout l;
@@ -1386,12 +1658,19 @@ Layout layout_of(const OrthArgs& a) {
     if (n > sums) sums = n;
   };
   product(longer, l.side, l.side, true);
-  product(l.side, l.side, l.side, true);
-  product(l.side, l.rows, l.cols, false);
+  const bool strip = is_strip(a);
+  if (strip) {
+    l.rows = longer;
+    l.cols = l.side;
+  } else {
+    product(l.side, l.side, l.side, true);
+    product(l.side, l.rows, l.cols, false);
+  }
   l.sums = take(sums);
   const size_t x = (size_t)a.E * l.rows * l.cols * terms * 2, sq = (size_t)a.E * l.side * l.side * terms * 2;
-  for (int i = 0; i < 2; ++i) l.x[i] = i == 0 || a.steps > 2 ? take(x) : 0;
-  for (int i = 0; i < 3; ++i) l.sq[i] = i < 2 || a.steps > 1 ? take(sq) : 0;
+  // (strips: X in panels, and as fragments before and after a step)
+  for (int i = 0; i < 3; ++i) l.x[i] = i == 0 || (strip ? i == 1 || a.steps > 1 : i == 1 && a.steps > 2) ? take(x) : 0;
+  for (int i = 0; i < 3; ++i) l.sq[i] = i == 0 || (!strip && (i == 1 || a.steps > 1)) ? take(sq) : 0;
   l.bytes = at;
   return l;
 }
@@ -1429,6 +1708,59 @@ hipError_t run_thin(const OrthArgs& a, const Layout& l, double scale, hipStream_
 }
 
 template <typename TI, int TERMS>
+hipError_t run_strip(const OrthArgs& a, const Layout& l, double scale, bool aligned_in, hipStream_t s) {
+  const double* partial = reinterpret_cast<const double*>(a.ws + l.partial);
+  float* first = reinterpret_cast<float*>(a.ws + l.first);
+  const int64_t x_plane = a.E * l.rows * l.cols, a_plane = (int64_t)a.E * kStrip * kStrip;
+  f16* panels = reinterpret_cast<f16*>(a.ws + l.x[0]);
+  f16* x[2] = {reinterpret_cast<f16*>(a.ws + l.x[1]), reinterpret_cast<f16*>(a.ws + l.x[2])};
+  f16* A = reinterpret_cast<f16*>(a.ws + l.sq[0]);
+  const bool vec = aligned_in && a.n % 8 == 0;
+  if (a.m > a.n)
+    scale_kernel<TI, TERMS><<<dim3((unsigned)(l.rows * l.cols / 8 / 256), a.E), 256, 0, s>>>(
+        a, vec, partial, l.blocks, scale, panels, x[0], l.rows, l.cols, x_plane, first);
+  else
+    scale_turned_kernel<TI, TERMS><<<dim3((unsigned)(kStrip / 32 * (l.rows / 64)), a.E), 256, 0, s>>>(
+        a, vec, partial, l.blocks, scale, panels, x[0], l.rows, x_plane, first);
+  hipError_t e = hipGetLastError();
+  const float unit = (float)(1.0 / scale);
+  const int64_t chunks = strip_groups(a) / (kStrip / kStripRows);
+  const unsigned grid = (unsigned)((chunks + kXcds - 1) / kXcds * kXcds * (kStrip / kStripRows));
+  for (int done = 0; done < a.steps && e == hipSuccess; ++done) {
+    const bool begin = done == 0;
+    ProductArgs r{};
+    r.a = r.b = Operands{panels, x_plane, l.rows * l.cols, (int)l.rows};
+    r.K = l.rows;
+    r.rows = r.cols = kStrip;
+    r.E = a.E;
+    r.sums = reinterpret_cast<float*>(a.ws + l.sums);
+    r.d = A;
+    r.d_plane = a_plane;
+    r.first = first;
+    r.power = begin ? 2 : 0;
+    r.f = begin ? 1.f : unit * unit;
+    e = product<true, true, true, TERMS, kFragments, f16>(r, s);
+    if (e != hipSuccess) return e;
+    const bool last = done + 1 == a.steps;
+    StripArgs t{};
+    t.A = A;
+    t.x = x[done & 1];
+    t.to = x[(done + 1) & 1];
+    t.panels = panels;
+    t.first = first;
+    t.a_plane = a_plane;
+    t.x_plane = x_plane;
+    t.rows = (int)l.rows;
+    t.power = begin ? 1 : 0;
+    t.f = last ? (begin ? 1.f : unit) : begin ? (float)scale : 1.f;
+    if (last) strip_kernel<TI, TERMS, true><<<grid, kThreads, 0, s>>>(a, t);
+    else strip_kernel<TI, TERMS, false><<<grid, kThreads, 0, s>>>(a, t);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+template <typename TI, int TERMS>
 hipError_t run(const OrthArgs& a, hipStream_t s) {
   const Layout l = layout_of(a);
   double* partial = reinterpret_cast<double*>(a.ws + l.partial);
@@ -1453,9 +1785,10 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (TERMS == 2 && is_thin(a)) return run_thin<TI>(a, l, scale, s);
+  if (is_strip(a)) return run_strip<TI, TERMS>(a, l, scale, aligned_in, s);
   const int64_t chunks = (l.rows * l.cols / 8 + 255) / 256, most = (4096 + a.E - 1) / a.E;
   scale_kernel<TI, TERMS><<<dim3((unsigned)(chunks < most ? chunks : most), a.E), 256, 0, s>>>(
-      a, aligned_in && a.n % 8 == 0, partial, l.blocks, scale, x[0], l.rows, l.cols, x_plane, first);
+      a, aligned_in && a.n % 8 == 0, partial, l.blocks, scale, x[0], nullptr, l.rows, l.cols, x_plane, first);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
 

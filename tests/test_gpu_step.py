@@ -284,6 +284,11 @@ def plain(g, steps, co=NS, eps=1e-7, dtype=torch.float64):
     return x.transpose(1, 2) if tall else x
 
 
+def in_strips(E, s, l, terms):
+    """Whether a matrix's steps are two launches each: none share a Gram matrix."""
+    return 128 < s <= 256 and 8 * E * -(-l // 128) * terms <= 256
+
+
 def rounded(g, steps, terms, co=NS, eps=1e-7):
     """The iteration as the operator takes it, in 64 bits but for the roundings of what it keeps."""
     a, b, c = co
@@ -304,7 +309,7 @@ def rounded(g, steps, terms, co=NS, eps=1e-7):
     done = 0
     while done < steps:
         left = steps - done
-        two = left >= 2 and (terms == 2 or done == 0 or (g.shape[2] >= 2 * g.shape[1] and left % 2 == 0))
+        two = left >= 2 and not in_strips(*g.shape, terms) and (terms == 2 or done == 0 or (g.shape[2] >= 2 * g.shape[1] and left % 2 == 0))
         A = keep(unit ** 2 * (x @ x.transpose(1, 2).contiguous()))
         P = keep(a * eye + b * A + c * (A @ A))
         if two:
@@ -354,7 +359,7 @@ def terms_of(m, n, dt):
 
 
 SIZES = [(1, 1, 1), (2, 1, 300), (3, 300, 1), (2, 16, 16), (5, 31, 33), (8, 64, 128), (3, 128, 64), (1, 127, 129),
-         (2, 129, 1000), (2, 200, 333), (2, 333, 200), (1, 512, 513), (1, 513, 640), (2, 640, 520), (1, 520, 2056),
+         (2, 129, 1000), (5, 201, 333), (1, 250, 4090), (1, 1500, 200), (3, 256, 256), (2, 200, 333), (2, 333, 200), (1, 512, 513), (1, 513, 640), (2, 640, 520), (1, 520, 2056),
          (1, 2056, 520), (64, 24, 40), (3, 64, 384), (2, 64, 385), (2, 17, 1000), (3, 1531, 33), (1, 64, 12288), (1, 9, 12289)]
 
 
@@ -451,7 +456,7 @@ def test_orthogonalize_past_2_31_values(moe, m, n, dt):
 @pytest.mark.parametrize("dt", [BF16, FP32])
 def test_orthogonalize_special_matrices(moe, dt):
     """Zeros give zeros; a value that is not finite spoils its own matrix and no other."""
-    for m, n in ((72, 200), (600, 530)):
+    for m, n in ((72, 200), (600, 530), (140, 200)):
         g = stack(5, m, n, dt)
         ref = moe.moe_orthogonalize(g)
         bad = g.clone()
@@ -469,7 +474,7 @@ def test_orthogonalize_special_matrices(moe, dt):
 def test_orthogonalize_buffers(moe, dt):
     """In place, a workspace full of garbage or larger than needed, matrices at odd addresses,
     one matrix without its stack's dimension."""
-    for m, n in ((70, 201), (530, 640)):
+    for m, n in ((70, 201), (530, 640), (201, 130)):
         g = stack(3, m, n, dt)
         ref = moe.moe_orthogonalize(g)
         same = g.clone()
@@ -487,7 +492,7 @@ def test_orthogonalize_buffers(moe, dt):
 
 def test_orthogonalize_is_reproducible_and_captured(moe):
     """The same bits again; captured and replayed on new values, with eager work between."""
-    for m, n, dt in ((90, 130, FP32), (640, 700, BF16)):
+    for m, n, dt in ((90, 130, FP32), (640, 700, BF16), (150, 260, FP32)):
         g = stack(2, m, n, dt)
         others = [stack(2, m, n, dt, seed=s) for s in (1, 2, 3)]
         want = [moe.moe_orthogonalize(t) for t in others]
@@ -540,7 +545,7 @@ def test_shared_memory_is_refused(moe):
 # ---- the update step -------------------------------------------------------------------------
 @pytest.mark.parametrize("nesterov", [True, False])
 @pytest.mark.parametrize("size,dt", [((3, 70, 201), FP32), ((3, 70, 201), BF16), ((2, 640, 536), BF16), ((2, 536, 640), BF16),
-                                     ((1, 1, 9), FP32)])
+                                     ((5, 201, 333), FP32), ((2, 200, 1501), BF16), ((2, 1501, 200), BF16), ((1, 1, 9), FP32)])
 def test_muon_update(moe, size, dt, nesterov):
     E, m, n = size
     say("muon", size, dt, nesterov)
