@@ -49,6 +49,17 @@ __device__ __forceinline__ void store8(TI* p, const float (&v)[8]) {
   }
 }
 
+// 8 elements as they are stored, loaded before they are needed.
+template <typename TI>
+struct Stored8 {
+  f32x4 v[sizeof(TI) / 2];
+  __device__ __forceinline__ void load(const TI* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(TI) / 2; ++i) v[i] = reinterpret_cast<const f32x4*>(p)[i];
+  }
+  __device__ __forceinline__ void get(float (&o)[8]) const { load8(reinterpret_cast<const TI*>(v), o); }
+};
+
 // Sum over the L lanes of a row's part in one wave.
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -255,20 +266,58 @@ __global__ __launch_bounds__(R::THREADS) void layer_norm_grad_kernel(LayerNormGr
     if (i < nch) load8(a.gamma + i * 8, gm[c]);
   }
   float acc[2][CH][8] = {};
-  for (int64_t t0 = (int64_t)blockIdx.x * ROWS; t0 < a.T; t0 += (int64_t)groups * ROWS) {
+  // Where a CU holds one workgroup of a row, the next row's values are loaded while this one is worked on (8192
+  // rows of 6000 bf16 105, so 96 us; 2000 of 8192 36, 33; where several are resident they do that for each
+  // other, and the registers cost more: 16384 of 4096 129, 135).
+  constexpr bool AHEAD = !FEW && TPR == 1024 && CH == 1;
+  Stored8<TI> so[CH], su[CH], sd[CH];
+  float s_mean = 0.f, s_rstd = 0.f;
+  auto fetch = [&](int64_t t) {
+    const size_t row = (size_t)t * a.d;
+    s_mean = a.mean[t];
+    s_rstd = a.rstd[t];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = tid + c * TPR;
+      if (i >= nch) continue;
+      so[c].load(static_cast<const TI*>(a.out) + row + i * 8);
+      su[c].load(static_cast<const TI*>(a.d_u) + row + i * 8);
+      if (a.d_out) sd[c].load(static_cast<const TI*>(a.d_out) + row + i * 8);
+    }
+  };
+  const int64_t step = (int64_t)groups * ROWS;
+  int64_t t0 = (int64_t)blockIdx.x * ROWS;
+  if (AHEAD && t0 < a.T) fetch(t0);
+  for (; t0 < a.T; t0 += step) {
     const int64_t mine = t0 + threadIdx.x / TPR, t = ROWS > 1 && mine >= a.T ? a.T - 1 : mine;
     const bool real = ROWS == 1 || mine < a.T;
     const size_t row = (size_t)t * a.d;
-    const float mean = a.mean[t], r = a.rstd[t];
+    float mean = s_mean, r = s_rstd;
+    if constexpr (!AHEAD) {
+      mean = a.mean[t];
+      r = a.rstd[t];
+    }
     float z[CH][8], dz[CH][8], D[CH][8];
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if (tid + c * TPR >= nch) continue;
+        so[c].get(z[c]);
+        su[c].get(dz[c]);
+        if (a.d_out) sd[c].get(D[c]);
+      }
+      if (t0 + step < a.T) fetch(t0 + step);
+    }
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = tid + c * TPR;
       if (i >= nch) continue;
-      load8(static_cast<const TI*>(a.out) + row + i * 8, z[c]);
-      load8(static_cast<const TI*>(a.d_u) + row + i * 8, dz[c]);
-      if (a.d_out) load8(static_cast<const TI*>(a.d_out) + row + i * 8, D[c]);
+      if constexpr (!AHEAD) {
+        load8(static_cast<const TI*>(a.out) + row + i * 8, z[c]);
+        load8(static_cast<const TI*>(a.d_u) + row + i * 8, dz[c]);
+        if (a.d_out) load8(static_cast<const TI*>(a.d_out) + row + i * 8, D[c]);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         z[c][e] = (z[c][e] - mean) * r;
