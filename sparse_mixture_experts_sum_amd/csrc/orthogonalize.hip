@@ -817,6 +817,15 @@ __global__ __launch_bounds__(64, 1) void join_kernel(ProductArgs a) {
   store_tile<G, SYM, KIND, TO>(a, t, wave / 2, wave % 2, ln, buf, w, pass);
 }
 
+// Whether the next two steps of a matrix kept in two terms share a Gram matrix. Of few singular values
+// a rounding of A is not averaged away, and the first pair multiplies it most: with up to kFewValues of
+// them an odd step comes first, alone (off by, in 1e-7 of the norm, pairs first and so: 16 x 680 30, 13;
+// 24 x 2000 13, 12; but 32 x 380 9, 12; 64 x 128 11, 17; plain fp32 13, 10, 11, 12).
+constexpr int kFewValues = 24;
+__host__ __device__ inline bool pair_in_two_terms(int64_t side, int left) {
+  return side > kFewValues ? left >= 2 : left > 0 && left % 2 == 0;
+}
+
 // ---- small matrices --------------------------------------------------------------------
 // Products of matrices that stay in LDS, by one workgroup of eight waves per matrix: what a launch
 // of its own for every product costs (5 us where nothing else counts) would be most of their time.
@@ -1081,7 +1090,8 @@ __device__ __forceinline__ void put_result(const OrthArgs& a, const Shape& sh, T
   }
 }
 
-// The whole of it for matrices of at most 64 x 384: X and the square matrices in LDS.
+// The whole of it for matrices of at most 64 x 384: X and the square matrices in LDS. Few singular values:
+// single steps (16 x 16: off by 0.8 in 1e-6, pairs 1.4), which cost nothing here where a side is short.
 template <typename TI>
 __global__ __launch_bounds__(kThreads) void small_kernel(OrthArgs a, double scale) {
   __shared__ __attribute__((aligned(1024))) char xs[2][kSmallSide * kSmallLong * 2];
@@ -1119,7 +1129,7 @@ __global__ __launch_bounds__(kThreads) void small_kernel(OrthArgs a, double scal
 
   const float unit = (float)(1.0 / scale);
   for (int done = 0; done < a.steps;) {
-    const bool begin = done == 0, two = a.steps - done >= 2;
+    const bool begin = done == 0, two = min(sh.m, sh.n) > kFewValues && a.steps - done >= 2;
     const float t = begin ? sc.first : unit;  // X = t X^
     lds_gram(X, l, wave, ln, [&](int i, int j, const float(&v)[4]) {
       const float r[4] = {t * t * v[0], t * t * v[1], t * t * v[2], t * t * v[3]};
@@ -1586,8 +1596,9 @@ int terms_of(const OrthArgs& a) { return a.bf16 && (a.m < a.n ? a.m : a.n) > kOn
 // 2.4, 2.0, 1.3, and 1.0 with only the first two as a pair).
 bool pair_next(const OrthArgs& a, int terms, int done) {
   const int left = a.steps - done;
-  if (left < 2 || terms == 2 || done == 0) return left >= 2;
   const int64_t s = a.m < a.n ? a.m : a.n, l = a.m < a.n ? a.n : a.m;
+  if (terms == 2) return pair_in_two_terms(s, left);
+  if (left < 2 || done == 0) return left >= 2;
   return l >= 2 * s && left % 2 == 0;
 }
 
@@ -1690,7 +1701,7 @@ hipError_t run_thin(const OrthArgs& a, const Layout& l, double scale, hipStream_
   const float unit = (float)(1.0 / scale);
   thin_kernel<TI, true, false><<<grid, kThreads, 0, s>>>(a, t);
   for (int done = 0; done < a.steps;) {
-    const bool begin = done == 0, two = a.steps - done >= 2;
+    const bool begin = done == 0, two = pair_in_two_terms(a.m < a.n ? a.m : a.n, a.steps - done);
     t.power = begin ? 2 : 0;
     t.f = begin ? 1.f : unit * unit;
     thin_polynomial_kernel<<<a.E, kThreads, 0, s>>>(a, t, (int)grid.x, two, a.ws + l.sq[0]);
