@@ -24,7 +24,8 @@
 // two near the square root of its long side; A and P as they are, of order 1). G itself enters
 // as G 2^p, exact for bf16, and the rest of its norm as a factor of the first products' sums.
 // bf16 matrices: one fp16 term (2^-11 of a value at most; with bf16 terms a full-rank matrix would be
-// off by 1%, not by 0.2%). fp32 matrices, and bf16 ones of short sides (few large singular values,
+// off by 1%, not by 0.2%), for as many steps as bear it: each multiplies what was rounded before it.
+// fp32 matrices, bf16 ones of more steps (one_term_bears) and bf16 ones of short sides (few large singular values,
 // whose roundings do not average out: 64 x 128 is 0.7% off with one term, 700 x 700 0.2%; the products
 // are too small there to be what counts): two terms, hi + lo / 2048 (22 bits; lo is scaled so that
 // it stays normal where hi is), and three products: lo hi and hi lo first, their sum divided by
@@ -53,7 +54,9 @@ constexpr int kColBlock = 4;        // columns of tiles walked together
 constexpr float kLo = 1.0f / 2048;  // scale of the second term
 constexpr int kNormBlocks = 256;    // most partial sums of a matrix's squares
 constexpr int kMaxParts = 16;       // of a product's sum
-constexpr int kOneTerm = 128;       // bf16 matrices with short sides past it are kept in one term
+constexpr int kOneTerm = 128;       // bf16 matrices with short sides past it may be kept in one term (terms_of)
+constexpr double kMostGrowth = 256;  // what steps in one term may multiply a rounding by, added over the steps
+constexpr double kMostValue = 1.25;  // singular values that they may reach
 
 // Place of a value of a matrix of the iteration: panels of 32 columns, each with all rows.
 __device__ __forceinline__ int64_t in_panels(int64_t rows, int64_t r, int64_t c) {
@@ -219,11 +222,13 @@ __global__ __launch_bounds__(256) void scale_kernel(OrthArgs a, bool vec, const 
     }
     f16* to = out + in_panels(rows, r, c);
     *reinterpret_cast<f16x8*>(to) = hi;
-    if constexpr (TERMS == 2) *reinterpret_cast<f16x8*>(to + plane) = lo;
-    if (frags) {
-      to = frags + (int64_t)e * rows * cols + in_fragments(rows, r, c);
-      *reinterpret_cast<f16x8*>(to) = hi;
-      if constexpr (TERMS == 2) *reinterpret_cast<f16x8*>(to + plane) = lo;
+    if constexpr (TERMS == 2) {
+      *reinterpret_cast<f16x8*>(to + plane) = lo;
+      if (frags) {
+        to = frags + (int64_t)e * rows * cols + in_fragments(rows, r, c);
+        *reinterpret_cast<f16x8*>(to) = hi;
+        *reinterpret_cast<f16x8*>(to + plane) = lo;
+      }
     }
   }
 }
@@ -1277,12 +1282,12 @@ constexpr int kStripRows = 32;   // of P, of a workgroup
 constexpr int kStripLong = 128;  // of the long side, of a workgroup
 
 // u 2^p in fp16 terms as scale_kernel leaves it, of the transposed matrix: 32 x 64 of it by way of LDS.
-template <typename TI, int TERMS>
+template <typename TI>
 __global__ __launch_bounds__(256) void scale_turned_kernel(OrthArgs a, bool vec, const double* partial, int blocks,
                                                            double scale, f16* x, f16* frags, int64_t rows, int64_t plane,
                                                            float* first) {
   __shared__ double sh[4];
-  __shared__ __attribute__((aligned(16))) f16 tile[TERMS][64][40];
+  __shared__ __attribute__((aligned(16))) f16 tile[2][64][40];
   const int e = blockIdx.y;
   const double sq = block_sum((int)threadIdx.x < blocks ? partial[(int64_t)e * blocks + threadIdx.x] : 0.0, sh);
   const Scale sc(sqrt(sq) + (double)a.eps, scale);
@@ -1305,12 +1310,12 @@ __global__ __launch_bounds__(256) void scale_turned_kernel(OrthArgs a, bool vec,
     f16 h, l;
     split((float)((double)u[k] * sc.by), h, l);
     tile[0][c - c0 + k][r - r0] = h;
-    if constexpr (TERMS == 2) tile[1][c - c0 + k][r - r0] = l;
+    tile[1][c - c0 + k][r - r0] = l;
   }
   __syncthreads();
   const int64_t mat = (int64_t)e * rows * kStrip, i = c0 + threadIdx.x / 4, j = r0 + threadIdx.x % 4 * 8;
 #pragma unroll
-  for (int t = 0; t < TERMS; ++t) {
+  for (int t = 0; t < 2; ++t) {
     const f16x8 v = *reinterpret_cast<const f16x8*>(&tile[t][threadIdx.x / 4][threadIdx.x % 4 * 8]);
     *reinterpret_cast<f16x8*>(x + mat + in_panels(rows, i, j) + t * plane) = v;
     *reinterpret_cast<f16x8*>(frags + mat + in_fragments(rows, i, j) + t * plane) = v;
@@ -1330,7 +1335,7 @@ struct StripArgs {
 // A product with 32 rows in LDS, of N steps of 16 from k0 on: lane l has row l % 32 of those in LDS and
 // columns 8 q + 4 (l / 32) + t, or, TURNED, a row of the other operand and those columns of LDS's rows.
 // frag(term, k): the other operand's fragments.
-template <int TERMS, bool TURNED, int N, class Frag>
+template <bool TURNED, int N, class Frag>
 __device__ __forceinline__ f32x16 strip_times(const InLds& m, int k0, int lane, Frag frag) {
   const int ln = here(lane);
   auto mfma = [](f16x8 lds, f16x8 reg, f32x16 to) {
@@ -1341,35 +1346,32 @@ __device__ __forceinline__ f32x16 strip_times(const InLds& m, int k0, int lane, 
   f16x8 hi[2], lo[2];  // (of one step ahead)
   auto read = [&](int k) {
     hi[k % 2] = InLds::rows(m.hi, m, 0, k0 + 16 * k, ln);
-    if constexpr (TERMS == 2) lo[k % 2] = InLds::rows(m.lo, m, 0, k0 + 16 * k, ln);
+    lo[k % 2] = InLds::rows(m.lo, m, 0, k0 + 16 * k, ln);
   };
   read(0);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    const f16x8 h = frag(0, k), l = TERMS == 2 ? frag(1, k) : h;
+    const f16x8 h = frag(0, k), l = frag(1, k);
     if (k + 1 < N) read(k + 1);
     __builtin_amdgcn_sched_barrier(0);
     acc = mfma(hi[k % 2], h, acc);
-    if constexpr (TERMS == 2) {
-      cross = mfma(lo[k % 2], h, cross);
-      cross = mfma(hi[k % 2], l, cross);
-    }
+    cross = mfma(lo[k % 2], h, cross);
+    cross = mfma(hi[k % 2], l, cross);
     __builtin_amdgcn_sched_barrier(0);
     if (k % 4 == 3) {  // (sums of hi hi of 64 terms, as above)
       sum += acc;
       acc = f32x16{};
     }
   }
-  if constexpr (TERMS == 2) sum += kLo * cross;
-  return sum;
+  return sum + kLo * cross;
 }
 
-template <typename TI, int TERMS, bool LAST>
+template <typename TI, bool LAST>
 __global__ __launch_bounds__(kThreads) void strip_kernel(OrthArgs a, StripArgs t) {
   constexpr int STRIPS = kStrip / kStripRows, STEPS = kStrip / 16, BLOCKS = kStripLong / 32;
   // rows of A, then of P; and each wave's part of X: 32 rows, half of the summed axis
-  __shared__ __attribute__((aligned(1024))) char ps[TERMS][kStripRows * kStrip * 2];
-  __shared__ __attribute__((aligned(1024))) char xs[kWaves][TERMS][STEPS / 2][1024];
+  __shared__ __attribute__((aligned(1024))) char ps[2][kStripRows * kStrip * 2];
+  __shared__ __attribute__((aligned(1024))) char xs[kWaves][2][STEPS / 2][1024];
   const int ln = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = ln >> 5;
   // the workgroups of the same rows of X are on one XCD
   const int chunks = t.rows / kStripLong, group = blockIdx.x / kXcds;
@@ -1377,7 +1379,7 @@ __global__ __launch_bounds__(kThreads) void strip_kernel(OrthArgs a, StripArgs t
   if (e >= a.E) return;
   const int i0 = group % STRIPS * kStripRows, l0 = chunk % chunks * kStripLong + wave % BLOCKS * 32;
   const int k0 = wave / BLOCKS * (STEPS / 2);
-  const InLds P{ps[0], ps[TERMS - 1], kStrip * 2};
+  const InLds P{ps[0], ps[1], kStrip * 2};
   const f16* const mat = t.A + (int64_t)e * kStrip * kStrip;
   constexpr int EACH = kStripRows * kStrip / 8 / kThreads;
   auto place = [&](int n, int& r, int& c) {
@@ -1385,25 +1387,25 @@ __global__ __launch_bounds__(kThreads) void strip_kernel(OrthArgs a, StripArgs t
     r = i % kStripRows;
     c = i / kStripRows * 8;
   };
-  u32x4 rows[TERMS][EACH];
+  u32x4 rows[2][EACH];
   int r, c;
 #pragma unroll
   for (int n = 0; n < EACH; ++n) {
     place(n, r, c);
 #pragma unroll
-    for (int term = 0; term < TERMS; ++term) rows[term][n] = ld16(mat + term * t.a_plane + in_fragments(kStrip, i0 + r, c));
+    for (int term = 0; term < 2; ++term) rows[term][n] = ld16(mat + term * t.a_plane + in_fragments(kStrip, i0 + r, c));
   }
-  f16x8 own[TERMS][STEPS];  // this wave's 32 columns of A (which is its own transpose)
+  f16x8 own[2][STEPS];  // this wave's 32 columns of A (which is its own transpose)
 #pragma unroll
   for (int k = 0; k < STEPS; ++k)
 #pragma unroll
-    for (int term = 0; term < TERMS; ++term)
+    for (int term = 0; term < 2; ++term)
       own[term][k] = __builtin_bit_cast(f16x8, ld16(mat + term * t.a_plane + in_fragments(kStrip, wave * 32, 16 * k) + ln * 8));
   const f16* const x = t.x + (int64_t)e * t.rows * kStrip;
 #pragma unroll
   for (int k = 0; k < STEPS / 2; ++k)
 #pragma unroll
-    for (int term = 0; term < TERMS; ++term)
+    for (int term = 0; term < 2; ++term)
       __builtin_amdgcn_global_load_lds(x + term * t.x_plane + in_fragments(t.rows, l0, 16 * (k0 + k)) + ln * 8,
                                        (lds_void*)xs[wave][term][k], 16, 0, 0);
   __builtin_amdgcn_sched_barrier(0);
@@ -1411,10 +1413,10 @@ __global__ __launch_bounds__(kThreads) void strip_kernel(OrthArgs a, StripArgs t
   for (int n = 0; n < EACH; ++n) {
     place(n, r, c);
 #pragma unroll
-    for (int term = 0; term < TERMS; ++term) *reinterpret_cast<u32x4*>(ps[term] + P.at(r, c)) = rows[term][n];
+    for (int term = 0; term < 2; ++term) *reinterpret_cast<u32x4*>(ps[term] + P.at(r, c)) = rows[term][n];
   }
   __syncthreads();
-  const f32x16 sq = strip_times<TERMS, false, STEPS>(P, 0, ln, [&](int term, int k) { return own[term][k]; });
+  const f32x16 sq = strip_times<false, STEPS>(P, 0, ln, [&](int term, int k) { return own[term][k]; });
   __syncthreads();  // (everyone has read A)
   r = ln & 31;
 #pragma unroll
@@ -1425,20 +1427,20 @@ __global__ __launch_bounds__(kThreads) void strip_kernel(OrthArgs a, StripArgs t
     f16x4 ph, pl;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float old = TERMS == 2 ? (float)h[k] + kLo * (float)l[k] : (float)h[k];
+      const float old = (float)h[k] + kLo * (float)l[k];
       f16 v0, v1;
       split(a.c * sq[4 * q + k] + a.b * old + (i0 + r == c + k ? a.a : 0.f), v0, v1);
       ph[k] = v0;
       pl[k] = v1;
     }
     *at[0] = ph;
-    if constexpr (TERMS == 2) *at[1] = pl;
+    *at[1] = pl;
   }
   wait_vmcnt<0>();  // X
   __syncthreads();
   const bool tall = a.m > a.n, turned = !LAST || tall;
   auto times = [&](auto flag) {
-    return strip_times<TERMS, decltype(flag)::value, STEPS / 2>(P, 16 * k0, ln, [&](int term, int k) {
+    return strip_times<decltype(flag)::value, STEPS / 2>(P, 16 * k0, ln, [&](int term, int k) {
       return *reinterpret_cast<const f16x8*>(xs[wave][term][k] + ln * 16);
     });
   };
@@ -1482,10 +1484,8 @@ __global__ __launch_bounds__(kThreads) void strip_kernel(OrthArgs a, StripArgs t
       f16 *to = t.to + at + in_fragments(t.rows, row, col), *panel = t.panels + at + in_panels(t.rows, row, col);
       *reinterpret_cast<f16x4*>(to) = h;
       *reinterpret_cast<f16x4*>(panel) = h;
-      if constexpr (TERMS == 2) {
-        *reinterpret_cast<f16x4*>(to + t.x_plane) = l;
-        *reinterpret_cast<f16x4*>(panel + t.x_plane) = l;
-      }
+      *reinterpret_cast<f16x4*>(to + t.x_plane) = l;
+      *reinterpret_cast<f16x4*>(panel + t.x_plane) = l;
     }
   } else {
     const int row = (tall ? l0 : i0) + (ln & 31), col = (tall ? i0 : l0) + j0;
@@ -1591,22 +1591,6 @@ size_t sum_bytes(int E, int64_t K, int64_t rows, int64_t cols, bool sym) {
   return big<TERMS>(a, sym) || p.parts == 1 ? 0 : (size_t)kXcds * p.rest * p.parts * G::BM * G::BM * sizeof(float);
 }
 
-int terms_of(const OrthArgs& a) { return a.bf16 && (a.m < a.n ? a.m : a.n) > kOneTerm ? 1 : 2; }
-
-// Whether the next two steps share a Gram matrix. In one term what was rounded in A is multiplied by
-// up to a^4 on the way to A', which costs most in the middle steps, where singular values of every size
-// are left: there single steps, unless the long side is twice the short one and pairs save a
-// fifth; then one single step between two pairs (off by, in 64-bit simulations of five steps with these
-// roundings, of gradients 512 x 2048 in 1e-3: pairs first 3.1, one between 0.9, all single 1.1; 512 x 512:
-// 2.4, 2.0, 1.3, and 1.0 with only the first two as a pair).
-bool pair_next(const OrthArgs& a, int terms, int done) {
-  const int left = a.steps - done;
-  const int64_t s = a.m < a.n ? a.m : a.n, l = a.m < a.n ? a.n : a.m;
-  if (terms == 2) return pair_in_two_terms(s, left);
-  if (left < 2 || done == 0) return left >= 2;
-  return l >= 2 * s && left % 2 == 0;
-}
-
 // Matrices of one launch, and of workgroups that keep 384 columns.
 int64_t long_side(const OrthArgs& a) { return a.m > a.n ? a.m : a.n; }
 bool is_small(const OrthArgs& a) { return (a.m <= kSmallSide || a.n <= kSmallSide) && long_side(a) <= kSmallLong; }
@@ -1622,15 +1606,49 @@ int thin_columns(const OrthArgs& a) {
 }
 int64_t thin_groups(const OrthArgs& a) { return (long_side(a) + thin_columns(a) - 1) / thin_columns(a); }
 
-// Matrices whose steps are two launches each: those whose workgroups are a quarter of what the chip holds (us,
-// before and so: 2 of 200 x 1000 bf16 129, 94; 2 of 1500 x 200 bf16 135, 101; 5 of 201 x 333 fp32 113, 104; past it 8 of
-// 256 x 1024 bf16 132, 127; 16 of 160 x 800 bf16 135, 161; 16 of 256 x 256 fp32 105, 118). What they read of
-// L2, 192 KB a term of each workgroup, is the time then.
+// Matrices whose steps are two launches each: those whose workgroups are at most half of what the chip holds, in two
+// terms whatever their type (us, by the tiles above and so: 5 of 201 x 333 fp32 113, 98; 2 of 200 x 1000 bf16 129 in one
+// term, 109; past it 16 of 256 x 256 fp32 105, 118). What they read of L2, 384 KB of each workgroup, is the time
+// then. (One term would be 92 for 109, but every step is a single one and rounds X: off by up to 3.7% of the norm at
+// ranks of 1 to 64, where tiles, with pairs, are off by 1.2%.)
 int64_t strip_groups(const OrthArgs& a) {
   return (int64_t)a.E * (kStrip / kStripRows) * (padded(long_side(a)) / kStripLong);
 }
 bool is_strip(const OrthArgs& a) {
-  return padded(a.m < a.n ? a.m : a.n) == kStrip && strip_groups(a) * terms_of(a) <= kCus;
+  return padded(a.m < a.n ? a.m : a.n) == kStrip && strip_groups(a) * 2 <= kCus;
+}
+
+// Whether `steps` steps bear the roundings of one term: what a step is off by is multiplied in every later one by
+// |p'| at most, p(s) = a s + b s^3 + c s^5, whose largest magnitude over the singular values there are is mostly a's, at
+// 0 (the default coefficients' 3.44, which makes that 198 for five steps and 683 for six; off by up to 1.5% and 4.4%
+// of the norm at ranks of 1 to 128, eight steps up to 51%). Singular values well past 1 are left to two terms.
+bool one_term_bears(const OrthArgs& a) {
+  double growth = 0, most = 0;
+  for (int i = 0; i <= 64; ++i) {
+    const double s = i / 64.0, t = s * s, d = fabs(a.a + t * (3.0 * a.b + t * 5.0 * a.c)), v = fabs(s * (a.a + t * (a.b + t * a.c)));
+    growth = growth > d ? growth : d;
+    most = most > v ? most : v;
+  }
+  double sum = 0;
+  for (int i = 0; i < a.steps && sum <= kMostGrowth; ++i) sum = sum * growth + 1;
+  return most <= kMostValue && sum <= kMostGrowth;
+}
+int terms_of(const OrthArgs& a) {
+  return a.bf16 && (a.m < a.n ? a.m : a.n) > kOneTerm && !is_strip(a) && one_term_bears(a) ? 1 : 2;
+}
+
+// Whether the next two steps share a Gram matrix. In one term what was rounded in A is multiplied by
+// up to a^4 on the way to A', which costs most in the middle steps, where singular values of every size
+// are left: there single steps, unless the long side is twice the short one and pairs save a
+// fifth; then one single step between two pairs (off by, in 64-bit simulations of five steps with these
+// roundings, of gradients 512 x 2048 in 1e-3: pairs first 3.1, one between 0.9, all single 1.1; 512 x 512:
+// 2.4, 2.0, 1.3, and 1.0 with only the first two as a pair).
+bool pair_next(const OrthArgs& a, int terms, int done) {
+  const int left = a.steps - done;
+  const int64_t s = a.m < a.n ? a.m : a.n, l = a.m < a.n ? a.n : a.m;
+  if (terms == 2) return pair_in_two_terms(s, left);
+  if (left < 2 || done == 0) return left >= 2;
+  return l >= 2 * s && left % 2 == 0;
 }
 
 // Pieces of the workspace.
@@ -1723,7 +1741,7 @@ hipError_t run_thin(const OrthArgs& a, const Layout& l, double scale, hipStream_
   return hipGetLastError();
 }
 
-template <typename TI, int TERMS>
+template <typename TI>
 hipError_t run_strip(const OrthArgs& a, const Layout& l, double scale, bool aligned_in, hipStream_t s) {
   const double* partial = reinterpret_cast<const double*>(a.ws + l.partial);
   float* first = reinterpret_cast<float*>(a.ws + l.first);
@@ -1733,10 +1751,10 @@ hipError_t run_strip(const OrthArgs& a, const Layout& l, double scale, bool alig
   f16* A = reinterpret_cast<f16*>(a.ws + l.sq[0]);
   const bool vec = aligned_in && a.n % 8 == 0;
   if (a.m > a.n)
-    scale_kernel<TI, TERMS><<<dim3((unsigned)(l.rows * l.cols / 8 / 256), a.E), 256, 0, s>>>(
+    scale_kernel<TI, 2><<<dim3((unsigned)(l.rows * l.cols / 8 / 256), a.E), 256, 0, s>>>(
         a, vec, partial, l.blocks, scale, panels, x[0], l.rows, l.cols, x_plane, first);
   else
-    scale_turned_kernel<TI, TERMS><<<dim3((unsigned)(kStrip / 32 * (l.rows / 64)), a.E), 256, 0, s>>>(
+    scale_turned_kernel<TI><<<dim3((unsigned)(kStrip / 32 * (l.rows / 64)), a.E), 256, 0, s>>>(
         a, vec, partial, l.blocks, scale, panels, x[0], l.rows, x_plane, first);
   hipError_t e = hipGetLastError();
   const float unit = (float)(1.0 / scale);
@@ -1755,7 +1773,7 @@ hipError_t run_strip(const OrthArgs& a, const Layout& l, double scale, bool alig
     r.first = first;
     r.power = begin ? 2 : 0;
     r.f = begin ? 1.f : unit * unit;
-    e = product<true, true, true, TERMS, kFragments, f16>(r, s);
+    e = product<true, true, true, 2, kFragments, f16>(r, s);
     if (e != hipSuccess) return e;
     const bool last = done + 1 == a.steps;
     StripArgs t{};
@@ -1769,8 +1787,8 @@ hipError_t run_strip(const OrthArgs& a, const Layout& l, double scale, bool alig
     t.rows = (int)l.rows;
     t.power = begin ? 1 : 0;
     t.f = last ? (begin ? 1.f : unit) : begin ? (float)scale : 1.f;
-    if (last) strip_kernel<TI, TERMS, true><<<grid, kThreads, 0, s>>>(a, t);
-    else strip_kernel<TI, TERMS, false><<<grid, kThreads, 0, s>>>(a, t);
+    if (last) strip_kernel<TI, true><<<grid, kThreads, 0, s>>>(a, t);
+    else strip_kernel<TI, false><<<grid, kThreads, 0, s>>>(a, t);
     e = hipGetLastError();
   }
   return e;
@@ -1800,8 +1818,10 @@ hipError_t run(const OrthArgs& a, hipStream_t s) {
   square_kernel<TI><<<dim3(l.blocks, a.E), 256, 0, s>>>(a, aligned_in && a.m * a.n % 8 == 0, partial);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (TERMS == 2 && is_thin(a)) return run_thin<TI>(a, l, scale, s);
-  if (is_strip(a)) return run_strip<TI, TERMS>(a, l, scale, aligned_in, s);
+  if constexpr (TERMS == 2) {
+    if (is_thin(a)) return run_thin<TI>(a, l, scale, s);
+    if (is_strip(a)) return run_strip<TI>(a, l, scale, aligned_in, s);
+  }
   const int64_t chunks = (l.rows * l.cols / 8 + 255) / 256, most = (4096 + a.E - 1) / a.E;
   scale_kernel<TI, TERMS><<<dim3((unsigned)(chunks < most ? chunks : most), a.E), 256, 0, s>>>(
       a, aligned_in && a.n % 8 == 0, partial, l.blocks, scale, x[0], nullptr, l.rows, l.cols, x_plane, first);

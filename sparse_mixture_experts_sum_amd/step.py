@@ -131,9 +131,10 @@ def moe_orthogonalize(g, *, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, out=N
     X = g / (|g| + eps), then `steps` times  X = a X + (b A + c A^2) X with A = X X^T
 
     (of the transpose where m > n). `out` (g itself may be given) takes the result, of g's type.
-    bf16 matrices whose sides are both over 128 are computed in fp16 with fp32 sums: within about
-    2e-3 of the norm (less than the result's own rounding), at a rank far below the sides within
-    2e-2. Others are computed as in fp32."""
+    bf16 matrices whose sides are both over 128 may be computed in fp16 with fp32 sums: within
+    2e-3 of the norm (less than the result's own rounding), at a rank below the sides within
+    2e-2. Others, and those of more steps than the bound allows (five of the default coefficients), are
+    computed as in fp32."""
     E, m, n = _matrices(g, "g")
     dev = g.device
     s = _orth_shape(g, E, m, n, steps, coefficients, eps)
