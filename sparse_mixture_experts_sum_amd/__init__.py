@@ -591,15 +591,21 @@ class SparseMoE:
         is scaled by sqrt(max(1, its columns / its rows)), the ratio of its output's width to its
         input's. The momentum (fp32, zeros before the first step) is kept in ``self.momentum``; so is a
         workspace, which the steps of one layer share: they run one after another. The first step, or
-        filling ``self.momentum`` with a tensor for each weight, comes before a capture."""
-        if len(self.momentum) < 3 and torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("muon_update's first step makes the momentum: take it before the capture")
-        for name in ("W_gate", "W_up", "W_down"):
-            w = getattr(self, name)
-            m = self.momentum.get(name)
-            if m is None:
-                m = self.momentum[name] = torch.zeros_like(w, dtype=torch.float32)
+        filling ``self.momentum`` with a tensor for each weight, comes before a capture. All three updates are
+        checked before the first begins: a refused call changes nothing."""
+        names = ("W_gate", "W_up", "W_down")
+        missing = [n for n in names if self.momentum.get(n) is None]
+        if missing and self.W_gate.is_cuda:
+            with torch.cuda.device(self.W_gate.device):
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("muon_update's first step makes the momentum: take it before the capture")
+        made = {n: torch.zeros_like(getattr(self, n), dtype=torch.float32) for n in missing}
+        updates = []
+        for n in names:
+            w = getattr(self, n)
             rows, cols = w.shape[-2:]
-            self._update_ws = moe_muon_update(
-                w, grads["d" + name], m, lr=lr, momentum=momentum, nesterov=nesterov, weight_decay=weight_decay,
-                scale=max(1.0, cols / rows) ** 0.5, workspace=self._update_ws, **kw)
+            updates.append((w, grads["d" + n], made[n] if n in made else self.momentum[n],
+                            max(1.0, cols / rows) ** 0.5))
+        self._update_ws = step._muon_updates(updates, lr=lr, momentum=momentum, nesterov=nesterov,
+                                            weight_decay=weight_decay, workspace=self._update_ws, **kw)
+        self.momentum.update(made)

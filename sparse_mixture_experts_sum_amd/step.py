@@ -149,15 +149,8 @@ def moe_orthogonalize(g, *, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, out=N
     return out
 
 
-def moe_muon_update(w, g, m, *, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=1.0, steps=5,
-                    coefficients=NEWTON_SCHULZ, eps=1e-7, workspace=None) -> torch.Tensor:
-    """One step of orthogonalised updates with momentum, in place, of a matrix or a stack of them:
-
-    m = momentum * m + g;  u = g + momentum * m (nesterov) or m
-    w = (1 - lr * weight_decay) * w - lr * scale * moe_orthogonalize(u)
-
-    w, g [m,n] or [E,m,n] bf16 or fp32, m fp32 of their shape. The update is rounded with w alone.
-    Returns the workspace, for the next call."""
+def _muon_args(w, g, m, lr, momentum, nesterov, weight_decay, scale, steps, coefficients, eps):
+    """An update's tensors and numbers, checked: (shape, arguments of the call before its workspace)."""
     E, rows, cols = _matrices(w, "w")
     dev, dtype = w.device, w.dtype
     if not all(math.isfinite(v) for v in (lr, momentum, weight_decay, scale)):
@@ -168,7 +161,37 @@ def moe_muon_update(w, g, m, *, lr, momentum=0.95, nesterov=True, weight_decay=0
     pw, pg, pm = _pointers(((w, "w", w.shape, dtype), (g, "g", w.shape, dtype), (m, "m", w.shape, _F32)), dev)
     if _overlap(w, g) or _overlap(w, m) or _overlap(g, m):
         raise ValueError("w, g and m must be three tensors that share no memory")
-    ws, ws_bytes = _scratch("moe_orthogonalize_workspace_size", s, dev, workspace)
-    _call("moe_muon_update", dev, s, _MUON_PARAMS(lr, momentum, weight_decay, scale, 1 if nesterov else 0),
-          pw, pg, pm, ws.data_ptr(), ws_bytes)
+    return s, (dev, s, _MUON_PARAMS(lr, momentum, weight_decay, scale, 1 if nesterov else 0), pw, pg, pm)
+
+
+def moe_muon_update(w, g, m, *, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=1.0, steps=5,
+                    coefficients=NEWTON_SCHULZ, eps=1e-7, workspace=None) -> torch.Tensor:
+    """One step of orthogonalised updates with momentum, in place, of a matrix or a stack of them:
+
+    m = momentum * m + g;  u = g + momentum * m (nesterov) or m
+    w = (1 - lr * weight_decay) * w - lr * scale * moe_orthogonalize(u)
+
+    w, g [m,n] or [E,m,n] bf16 or fp32, m fp32 of their shape. The update is rounded with w alone.
+    Returns the workspace, for the next call."""
+    s, args = _muon_args(w, g, m, lr, momentum, nesterov, weight_decay, scale, steps, coefficients, eps)
+    ws, ws_bytes = _scratch("moe_orthogonalize_workspace_size", s, w.device, workspace)
+    _call("moe_muon_update", *args, ws.data_ptr(), ws_bytes)
+    return ws
+
+
+def _muon_updates(updates, *, lr, momentum=0.95, nesterov=True, weight_decay=0.0, steps=5, coefficients=NEWTON_SCHULZ,
+                  eps=1e-7, workspace=None) -> torch.Tensor:
+    """moe_muon_update of each (w, g, m, scale), on one workspace, which it returns: all are checked and the
+    workspace is there before the first is launched, so that a refused call changes nothing."""
+    calls = [_muon_args(w, g, m, lr, momentum, nesterov, weight_decay, scale, steps, coefficients, eps)
+             for w, g, m, scale in updates]
+    dev = calls[0][1][0]
+    if any(args[0] != dev for _, args in calls):
+        raise ValueError("the weights must be on one device")
+    largest = max((s for s, _ in calls), key=lambda s: _workspace_bytes("moe_orthogonalize_workspace_size", s))
+    ws, ws_bytes = _scratch("moe_orthogonalize_workspace_size", largest, dev, workspace)
+    if ws.data_ptr() % 256:
+        raise ValueError("workspace must be 256-byte aligned")
+    for _, args in calls:
+        _call("moe_muon_update", *args, ws.data_ptr(), ws_bytes)
     return ws

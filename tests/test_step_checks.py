@@ -219,3 +219,21 @@ def test_c_orthogonalize_arguments(lib):
     for bad in ((float("nan"), 0.9, 0.0, 1.0, 1), (0.1, float("inf"), 0.0, 1.0, 1), (0.1, 0.9, float("nan"), 1.0, 1),
                 (0.1, 0.9, 0.0, float("inf"), 1), (0.1, 0.9, 0.0, 1.0, 2)):
         assert muon(p=ST._MUON_PARAMS(*bad)) == BAD_SHAPE
+
+
+# ---- the layer's update ------------------------------------------------------------------
+@pytest.mark.parametrize("kw,error", [
+    (dict(dW_gate=None), ValueError), (dict(dW_gate=z(4, 64, 95)), ValueError), (dict(), TypeError),
+    (dict(dW_up=z(4, 64, 96, dtype=F32)), TypeError), (dict(lr=float("nan")), ValueError), (dict(steps=0), ValueError),
+    (dict(drop="dW_down"), KeyError), (dict(scale=2.0), TypeError)])
+def test_refused_update_of_a_layer_keeps_no_momentum(kw, error):
+    block = M.SparseMoE(z(64, 4), z(4, 64, 96), z(4, 64, 96), z(4, 96, 64))
+    grads = {"d" + n: torch.ones_like(getattr(block, n)) for n in ("W_gate", "W_up", "W_down")}
+    drop, args = kw.get("drop"), dict(lr=0.1)
+    for n, t in kw.items():
+        (grads if n.startswith("dW") else args)[n] = t
+    args.pop("drop", None)
+    grads.pop(drop, None)
+    with pytest.raises(error):
+        block.muon_update(grads, **args)
+    assert block.momentum == {} and block._update_ws is None
