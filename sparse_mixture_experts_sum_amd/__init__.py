@@ -441,7 +441,7 @@ class SparseMoE:
     a capacity, no training noise). It reads that call's x, u, y and workspace, and the
     weights: none of them must have been changed since. Calls of one layer share its
     workspace, captured ones too: they run one after another, each with its backward before
-    the next call.
+    the next call. What a captured call used is kept for as long as the layer is.
 
     ``muon_update(grads, lr=...)`` takes an optimiser's step on the experts' weights."""
 
@@ -465,7 +465,15 @@ class SparseMoE:
         self.norm, self.pre_beta, self.post_beta = norm, pre_beta, post_beta
         self.momentum = {}  # muon_update's, by weight
         self._ws = self._update_ws = None
+        self._captured = []  # workspaces that a graph writes to, also once a larger one has taken their place
         self.last = None
+
+    def _keep_captured(self, ws):
+        if any(ws is t for t in self._captured):
+            return
+        with torch.cuda.device(ws.device):
+            if torch.cuda.is_current_stream_capturing():
+                self._captured.append(ws)
 
     def __call__(self, x, **kw):
         _need(x, "x")
@@ -482,6 +490,7 @@ class SparseMoE:
                           self.W_down, k=self.k, mode=self.mode, capacity_factor=self.cf,
                           renormalize=self.renormalize, workspace=self._ws, **kw)
         self._ws = out["workspace"]
+        self._keep_captured(self._ws)
         out["x"], out["u"], out["noise"] = x2, u, kw.get("eps") is not None
         out["rstd"] = None if pre is None else pre["rstd"]
         out["mean"] = pre["mean"] if pre is not None and layer_norm else None
@@ -609,3 +618,4 @@ class SparseMoE:
         self._update_ws = step._muon_updates(updates, lr=lr, momentum=momentum, nesterov=nesterov,
                                             weight_decay=weight_decay, workspace=self._update_ws, **kw)
         self.momentum.update(made)
+        self._keep_captured(self._update_ws)

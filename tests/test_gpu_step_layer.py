@@ -49,3 +49,56 @@ def test_refused_update_changes_nothing(moe, name, steps):  # noqa: F811
     torch.cuda.synchronize()
     assert all(torch.equal(getattr(block, n), weights[n]) for n in NAMES)
     assert all(torch.equal(kept[n], momentum[n]) for n in kept) and len(block.momentum) == len(kept)
+
+
+def test_workspaces_of_a_captured_step_outlive_larger_ones(moe):  # noqa: F811
+    """A graph holds the addresses of the workspaces that the eager step before it made. Calls of more rows and of
+    updates by more steps put larger ones in their place; what is allocated then is not what the graph writes to."""
+    eager, _, _, x = layer(moe, BF16)
+    held, _, _, _ = layer(moe, BF16)
+    rows = [draw(gen(40 + i), *x.shape).to(BF16).cuda() for i in range(4)]
+    many = draw(gen(50), 4096, x.shape[1]).to(BF16).cuda()
+    d_out = draw(gen(51), *x.shape).to(BF16).cuda()
+
+    def one(block, r):
+        y = block(r)
+        block.muon_update(block.backward(d_out), lr=0.02, steps=2)
+        return y
+
+    def large(block):
+        block(many)
+        return block.backward(many)
+    want = []
+    for i, r in enumerate(rows):
+        want.append(one(eager, r).clone())
+        if i:
+            eager.muon_update(large(eager), lr=0.02)
+    buf = rows[0].clone()
+    assert torch.equal(one(held, buf), want[0])
+    torch.cuda.synchronize()
+    before = held._ws, held._update_ws
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = one(held, buf)
+    assert held._ws is before[0] and held._update_ws is before[1]
+    assert all(any(t is c for c in held._captured) for t in before)
+    at = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in before]
+    del before
+    for r, w in zip(rows[1:], want[1:]):
+        buf.copy_(r)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, w)
+        held.muon_update(large(held), lr=0.02)
+        other = [torch.full((b - a,), 1, dtype=torch.uint8, device="cuda") for a, b in at]
+        for t in other + [held._ws, held._update_ws]:
+            assert all(t.data_ptr() >= b or t.data_ptr() + t.numel() <= a for a, b in at)
+    assert all(torch.equal(getattr(held, n), getattr(eager, n)) for n in NAMES)
+    assert all(torch.equal(held.momentum[n], eager.momentum[n]) for n in NAMES)
+    assert held._captured and len(held._captured) == 2
+
+
+def test_layer_with_one_workspace_keeps_none_without_a_capture(moe):  # noqa: F811
+    block, grads = trained(moe, FP32)
+    block.muon_update(grads, lr=0.02)
+    assert block._captured == []
