@@ -1658,7 +1658,7 @@ struct Layout {
   size_t partial, first, sums, x[3], sq[3], bytes;
 };
 Layout layout_of(const OrthArgs& a) {
-  Layout l;
+  Layout l{};  // (pieces that a path does not have: at 0, which nothing looks at)
   const int terms = terms_of(a);
   l.rows = padded(a.m);
   l.cols = padded(a.n);
