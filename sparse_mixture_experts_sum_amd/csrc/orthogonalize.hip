@@ -253,9 +253,8 @@ struct ProductArgs {
   int E, power, vec;
   float f, p, q, keep, rate;
   const float* first;
-  // set by the launch: of every XCD's tiles, how many are whole; the others' sums are in `parts`
-  // parts, of which there are at most `rest` tiles an XCD
-  int whole, parts, rest;
+  // set by the launch: the parts that a tile's sum is in, and the most tiles that an XCD has
+  int parts, rest;
   float* sums;
 };
 
@@ -467,21 +466,19 @@ struct Share {
     n = (int)(all * (xcd + 1) / kXcds) - lo;
     turns = (int)(a.K / (kStages * G::BK));
   }
-  // items: the whole tiles, then the others' parts
-  __device__ __forceinline__ int items(const ProductArgs& a) const {
-    return a.parts > 1 ? a.whole + (n - a.whole) * a.parts : n;
-  }
+  // items: the tiles, or their parts, a tile's one after another
+  __device__ __forceinline__ int items(const ProductArgs& a) const { return n * a.parts; }
   __device__ __forceinline__ Item locate(const ProductArgs& a, int xcd, int at) const {
     Item t;
     t.part = -1;
     t.u0 = 0;
     t.u1 = turns;
-    if (a.parts > 1 && at >= a.whole) {
-      const int in = at - a.whole, tile = in / a.parts, part = in - tile * a.parts;
+    if (a.parts > 1) {
+      const int tile = at / a.parts, part = at - tile * a.parts;
       t.u0 = turns * part / a.parts;
       t.u1 = turns * (part + 1) / a.parts;
       t.part = (xcd * a.rest + tile) * a.parts + part;
-      at = a.whole + tile;
+      at = tile;
     }
     locate_tile<SYM>(lo + at, Mt, Nt, t);
     return t;
@@ -790,8 +787,8 @@ __global__ __launch_bounds__(64, 1) void join_kernel(ProductArgs a) {
   const int pass = blockIdx.x % S::ALL, quarter = blockIdx.x / S::ALL, ln = threadIdx.x;
   const int wave = quarter % 4, tile = quarter / 4 / kXcds, xcd = quarter / 4 % kXcds;
   const Share<G, SYM> share(a, xcd);
-  if (a.whole + tile >= share.n) return;
-  const Item t = share.locate(a, xcd, a.whole + tile * a.parts);
+  if (tile >= share.n) return;
+  const Item t = share.locate(a, xcd, tile * a.parts);
   if (idle<G, SYM>(a, t, wave / 2, wave % 2)) return;
   Wave<G> w;
 #pragma unroll
@@ -1518,10 +1515,10 @@ int64_t tiles_of(const ProductArgs& a, int bm, bool sym) {
   return a.E * (sym ? mt * (mt + 1) / 2 : mt * nt);
 }
 
-// How a product is laid over the chip: whole tiles and parts of every XCD (ProductArgs), and
+// How a product is laid over the chip: parts of a tile and tiles of an XCD (ProductArgs), and
 // about how long it takes, in ns.
 struct Plan {
-  int whole, parts, rest;
+  int parts, rest;
   double ns;
 };
 // Parts where tiles do not fill the chip once, as many as do, of two ring turns at least.
@@ -1541,13 +1538,13 @@ Plan plan_for(const ProductArgs& a, bool sym) {
   const int64_t tiles = tiles_of(a, G::BM, sym), each = (tiles + kXcds - 1) / kXcds, turns = a.K / (kStages * G::BK);
   const int64_t per_cu = (each + cus - 1) / cus;
   const double sum = (double)(a.K / G::BK) * (per_cu > c.few ? c.busy : c.stage) + c.tile;
-  Plan p{(int)each, 1, 0, c.launch + sum * (double)per_cu};
+  Plan p{1, (int)each, c.launch + sum * (double)per_cu};
   if (c.join == 0 || each > G::SLOTS / 2) return p;
   int parts = G::SLOTS / (int)each;
   if (parts > turns / 2) parts = (int)(turns / 2);
   if (parts > kMaxParts) parts = kMaxParts;
   const double ns = c.launch + sum / parts * (double)((each * parts + cus - 1) / cus) + c.join;
-  if (parts > 1 && ns < p.ns) p = Plan{0, parts, (int)each, ns};
+  if (parts > 1 && ns < p.ns) p = Plan{parts, (int)each, ns};
   return p;
 }
 
@@ -1556,9 +1553,8 @@ hipError_t launch_tile(const ProductArgs& args, hipStream_t s) {
   ProductArgs a = args;
   const Plan p = plan_for<G>(a, SYM);
   a.parts = p.parts;
-  a.whole = p.whole;
   a.rest = p.rest;
-  const int items = a.parts > 1 ? a.rest * a.parts : a.whole;
+  const int items = a.rest * a.parts;
   product_kernel<G, SYM, KIND, TO><<<(unsigned)((items < G::SLOTS ? items : G::SLOTS) * kXcds), 256, 0, s>>>(a);
   if (a.parts > 1)
     join_kernel<G, SYM, KIND, TO><<<(unsigned)(a.rest * kXcds * 4 * Passes<G>::ALL), 64, 0, s>>>(a);
