@@ -512,11 +512,13 @@ moe_status moe_layer_norm_backward(const moe_layer_norm_shape* shape, const void
  * Products are taken on the matrix cores in fp16 with fp32 sums, the matrices scaled so that
  * their values lie in fp16's range. What passes from one product to the next is, for
  *   bf16 matrices whose sides are both over 128, where the steps bear it, rounded to fp16 (2^-11 of a
- *     value at most): matrices of full rank come out within 2e-3 of their norm, less than half a bf16
- *     step of every value, those of any rank within 2e-2, beside the result's own rounding. A step
- *     multiplies small singular values by up to a, and with them what was rounded before it; the steps
- *     bear it where a rounding in each of them, so multiplied, adds up to at most 256 of it: up to five
- *     steps of (3.4445, -4.7750, 2.0315). Not where the short side is at most 256 and E ceil(long / 128) <= 16;
+ *     value at most, 2^-25 below 2^-14): matrices of full rank come out within 2e-3 of their norm, those
+ *     of any rank within 2e-2, beside the result's own rounding. That is of the whole: X's values are of
+ *     the order of 1 / sqrt(short side), and rows or columns 1e-4 times the size of the others are off
+ *     by 1% of themselves, at 1e-5 by 7%. A step multiplies small singular values by up to a, and with
+ *     them what was rounded before it; the steps bear it where a rounding in each of them, so multiplied,
+ *     adds up to at most 256 of it: up to five steps of (3.4445, -4.7750, 2.0315). Not where the short
+ *     side is at most 256 and E ceil(long / 128) <= 16;
  *   others, kept as two fp16 terms (22 bits), three products for one: as in fp32.
  * The coefficients are expected to keep the singular values below about 8 (beyond that a value may
  * leave fp16's range and come out infinite), and a not to be small beside b and c: a X carries the

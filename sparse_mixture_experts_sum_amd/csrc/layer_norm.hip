@@ -13,7 +13,8 @@
 // which a second kernel adds in workgroup order: no atomics, one fixed order. They need the row's
 // mean and rstd alone, which are inputs: where rows are few, workgroups of their own take them in the
 // same launch, 64 columns of all rows each. bf16, 16384 x 4096 with d_out and dy: 130 us, 5.1 TB/s; fp32,
-// 8191 x 2048: 54-59 us (52 at a copy's rate); 4096 x 1024: 14 us in two launches (6.5); 300 x 2048: 5 us.
+// 8191 x 2048: 49-57 us (52 at a copy's rate); 4096 x 1024: 14.6 us in two launches (6.5): one wave a SIMD,
+// whose four rows' loads wait for each other; 300 x 2048: 5 us.
 // All values and sums are fp32; outputs are rounded once.
 #include "step_kernels.h"
 #include "train_common.h"

@@ -22,8 +22,10 @@
 //
 // What is kept between products: fp16, of values scaled to lie in its range (X times a power of
 // two near the square root of its long side; A and P as they are, of order 1). G itself enters
-// as G 2^p, exact for bf16, and the rest of its norm as a factor of the first products' sums.
-// bf16 matrices: one fp16 term (2^-11 of a value at most; with bf16 terms a full-rank matrix would be
+// as G 2^p (bf16 values of 2^-14 and more then exactly, smaller ones to 2^-25, and so what the momentum makes of
+// them in fp32 to 2^-11 of a value), and the rest of its norm as a factor of the first products' sums.
+// bf16 matrices: one fp16 term (2^-11 of a value at most, 2^-25 below 2^-14, where values are 1 / sqrt(short side)
+// at the start: rows 1e-5 times the others are off by 7% of themselves; with bf16 terms a full-rank matrix would be
 // off by 1%, not by 0.2%), for as many steps as bear it: each multiplies what was rounded before it.
 // fp32 matrices, bf16 ones of more steps (one_term_bears) and bf16 ones of short sides (few large singular values,
 // whose roundings do not average out: 64 x 128 is 0.7% off with one term, 700 x 700 0.2%; the products
@@ -699,7 +701,9 @@ __device__ __forceinline__ void put_part(const ProductArgs& a, int part, int wav
 }
 
 // Workgroups take their XCD's items in strides of the XCD's workgroups, as one stream of
-// stages: the last ring turn of an item loads the first one of the next.
+// stages: the last ring turn of an item loads the first one of the next. The 256-row tiles take all 512 registers:
+// six of them keep one value in scratch, read at a tile's end, and the one of operands summed over rows five,
+// in the last turn of a tile; the turns before it have no scratch accesses.
 template <class G, bool SYM, int KIND, typename TO>
 __global__ __launch_bounds__(256, 1) void product_kernel(ProductArgs a) {
   // (an array of its own for each stage: the compiler then sees that the reads of one stage
@@ -1525,7 +1529,10 @@ struct Plan {
 template <class G>
 Plan plan_for(const ProductArgs& a, bool sym) {
   // ns of a tile's stage of 32, where a CU has few tiles and (the clock and the L2s' share gone down)
-  // many; of a tile's end, of a launch, and of a join
+  // many; of a tile's end, of a launch, and of a join. Fitted to kernel traces (us so, and measured: 256 rows: 8 of 4096 squared
+  // 571, 541, times 4096 x 14336 3188, 3107; 128 rows in one term: 8 of 1024 squared 20.4, 21.6, 4 of 512 8.8, 10.2;
+  // in two: 2048 squared times itself 50.8, 58.6, 64 of 2048 x 640 by 640 383, 360; 64 rows: 8 of 1024 squared 42.4, 42.8,
+  // 4 of 512 7.2, 8.5, 2 of 384 over 8064 in ten parts with the join 19, 24.6); they choose, no result depends on them.
   struct Cost {
     double stage, busy, tile, launch, join;
     int few;
@@ -1593,8 +1600,9 @@ bool is_small(const OrthArgs& a) { return (a.m <= kSmallSide || a.n <= kSmallSid
 bool is_thin(const OrthArgs& a) {
   return (a.m <= kSmallSide || a.n <= kSmallSide) && !is_small(a) && long_side(a) <= kThinLong;
 }
-// Columns of a workgroup: few, so that it has soon done, but so that a matrix has no more than 24
-// parts of its Gram matrix and all workgroups are on the chip at once.
+// Columns of a workgroup: 128 or 256, so that it has soon done, where a matrix then has no more than 24
+// parts of its Gram matrix and all workgroups are on the chip at once; else 384 (at most 32 parts, of 12288
+// columns, and as many rounds of workgroups as there are).
 int thin_columns(const OrthArgs& a) {
   for (int w = 128; w < kSmallLong; w += 128)
     if (long_side(a) <= 24 * w && a.E * ((long_side(a) + w - 1) / w) <= kCus) return w;

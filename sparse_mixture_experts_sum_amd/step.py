@@ -132,8 +132,8 @@ def moe_orthogonalize(g, *, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, out=N
 
     (of the transpose where m > n). `out` (g itself may be given) takes the result, of g's type.
     bf16 matrices whose sides are both over 128 may be computed in fp16 with fp32 sums: within
-    2e-3 of the norm (less than the result's own rounding), at a rank below the sides within
-    2e-2. Others, and those of more steps than the bound allows (five of the default coefficients), are
+    2e-3 of the norm beside the result's own rounding, at a rank below the sides within 2e-2 (rows
+    or columns far smaller than the others may be off by more of themselves). Others, and those of more steps than the bound allows (five of the default coefficients), are
     computed as in fp32."""
     E, m, n = _matrices(g, "g")
     dev = g.device

@@ -39,9 +39,10 @@ def in_fp32(g, steps, co, E):
     """What an iteration that keeps 22 bits may be off by, of two kinds. Against plain fp32: a rounding is 4 times
     its at most, a pair of steps takes twice as many, and plain fp32 (one draw of its roundings) counts twice.
     And by itself, where plain fp32 rounds less than usual (few different values, a power of two as the rank): half a
-    step is 2^-23 of a value, 0.58 of that on the average; it is multiplied by up to a in every later step where
-    the singular values are 0, and what a step brings there of X, A and P (norms 1, 1 and at most a) is 1, |b + c| and
-    a times it: 0.58 sqrt(1 + 2.74^2 + 3.44^2) = 2.6 for the default coefficients, taken as 4."""
+    step is 2^-22 of a value at most, 0.4 of that on the average (0.58, of values between 1 and 2); it is multiplied by
+    up to a in every later step where the singular values are 0, and what a step brings there of X, A and P (norms 1, 1
+    and at most a) is 1, |b + c| and a times it: 0.4 sqrt(1 + 2.74^2 + 3.44^2) 2^-22 = 3.6 2^-23 for the default
+    coefficients, taken as 4 2^-23."""
     grown = sum(co[0] ** i for i in range(steps))
     return 16 * norm(plain(g, steps, co, 1e-7, FP32) - E) + (2.0 ** -20 + 4 * 2.0 ** -23 * grown) * norm(E)
 
@@ -108,3 +109,24 @@ def test_full_rank_in_bf16_is_within_2e_3(moe, size):  # noqa: F811
         say("full rank", size, steps)
         check(moe, stack(*size, BF16), steps, 2e-3)
         check(moe, torch.randn(*size, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(BF16), steps, 2e-3)
+
+
+@pytest.mark.parametrize("size", [(1, 512, 1024), (1, 1024, 4096), (1, 2048, 1408)], ids=lambda s: "x".join(map(str, s)))
+def test_small_rows_among_others(moe, size):  # noqa: F811
+    """Every other row (column of a tall matrix) 1e-2 to 1e-5 times the others. In one term values below 2^-14 are
+    rounded to 2^-25, where X's, scaled, are k / sqrt(short side) or more: 0.58 2^-25 sqrt(short side) / k of such rows
+    on the average; in the first step X, A X and P X carry it, 1 + |b| + 2 |c| = 9.8 times at most. In two terms to 2^-36."""
+    s = min(size[1:])
+    for k in (1e-2, 1e-3, 1e-4, 1e-5):
+        g = torch.randn(*size, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+        part = (slice(None), slice(0, None, 2)) if size[1] < size[2] else (slice(None), slice(None), slice(0, None, 2))
+        g[part] *= k
+        g = g.to(BF16)
+        say("small rows", size, k)
+        E = plain(g, 5)
+        for dt, share, bits in ((BF16, 2e-3, 25), (FP32, 1e-5, 36)):
+            off = moe.moe_orthogonalize(g.to(dt)).double() - E
+            own = E.to(dt).double() - E
+            assert bool((norm(off) <= share * norm(E) + 1.25 * norm(own)).all())
+            most = share + 9.8 * 0.58 * 2.0 ** -bits * s ** 0.5 / k
+            assert bool((norm(off[part]) <= most * norm(E[part]) + 1.25 * norm(own[part])).all()), (k, dt)
