@@ -518,7 +518,7 @@ moe_status moe_layer_norm_backward(const moe_layer_norm_shape* shape, const void
  *     by 1% of themselves, at 1e-5 by 7%. A step multiplies small singular values by up to a, and with
  *     them what was rounded before it; the steps bear it where a rounding in each of them, so multiplied,
  *     adds up to at most 256 of it: up to five steps of (3.4445, -4.7750, 2.0315). Not where the short
- *     side is at most 256 and E ceil(long / 128) <= 16;
+ *     side is at most 256 and E ceil(long / 128) <= 32;
  *   others, kept as two fp16 terms (22 bits), three products for one: as in fp32.
  * The coefficients are expected to keep the singular values below about 8 (beyond that a value may
  * leave fp16's range and come out infinite), and a not to be small beside b and c: a X carries the

@@ -1614,13 +1614,14 @@ int64_t thin_groups(const OrthArgs& a) { return (long_side(a) + thin_columns(a) 
 // terms whatever their type (us, by the tiles above and so: 5 of 201 x 333 fp32 113, 98; 2 of 200 x 1000 bf16 129 in one
 // term, 109; past it 16 of 256 x 256 fp32 105, 118). What they read of L2, 384 KB of each workgroup, is the time
 // then. (One term would be 92 for 109, but every step is a single one and rounds X: off by up to 3.7% of the norm at
-// ranks of 1 to 64, where tiles, with pairs, are off by 1.2%.)
+// ranks of 1 to 64, where tiles, with pairs, are off by 1.2%.) Up to twice as many workgroups bf16 matrices are kept in
+// two terms as well: their smaller tiles fill more of the chip (us by tiles, one term and two: 8 of 440 x 168 122, 104; 2 of
+// 1500 x 200 133, 117; 1 of 200 x 4096 145, 131; past it 32 of 130 x 256 117, 139; 40 of 160 x 800 164, 214).
 int64_t strip_groups(const OrthArgs& a) {
   return (int64_t)a.E * (kStrip / kStripRows) * (padded(long_side(a)) / kStripLong);
 }
-bool is_strip(const OrthArgs& a) {
-  return padded(a.m < a.n ? a.m : a.n) == kStrip && strip_groups(a) * 2 <= kCus;
-}
+bool are_few(const OrthArgs& a) { return padded(a.m < a.n ? a.m : a.n) == kStrip && strip_groups(a) <= kCus; }
+bool is_strip(const OrthArgs& a) { return are_few(a) && strip_groups(a) * 2 <= kCus; }
 
 // Whether `steps` steps bear the roundings of one term: what a step is off by is multiplied in every later one by
 // |p'| at most, p(s) = a s + b s^3 + c s^5, whose largest magnitude over the singular values there are is mostly a's, at
@@ -1638,7 +1639,7 @@ bool one_term_bears(const OrthArgs& a) {
   return most <= kMostValue && sum <= kMostGrowth;
 }
 int terms_of(const OrthArgs& a) {
-  return a.bf16 && (a.m < a.n ? a.m : a.n) > kOneTerm && !is_strip(a) && one_term_bears(a) ? 1 : 2;
+  return a.bf16 && (a.m < a.n ? a.m : a.n) > kOneTerm && !are_few(a) && one_term_bears(a) ? 1 : 2;
 }
 
 // Whether the next two steps share a Gram matrix. In one term what was rounded in A is multiplied by
